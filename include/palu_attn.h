@@ -414,6 +414,121 @@ palu_status_t palu_project_latents(palu_attn_t h, const void* W, palu_dtype_t w_
                                    const void* x, const palu_cache* cache, const int32_t* dst_slot, int batch,
                                    int n_new, palu_stream_t stream);
 
+/*
+ * Paged dense KV cache: rotation and norm of queries and keys, append, and attention of new tokens.
+ *
+ * Layers kept dense, and the dense sink and window tokens of palu_decode_hybrid, need a standard KV
+ * cache filled with rotated keys ("PuzzleKV" section 3: the sink page and the window stay dense;
+ * "Palu" method section, RoPE paragraph: keys are rotated at their own positions) and attention of
+ * prompts, chunks and single tokens over it. The pages give no layout; this library's is
+ *   k, v   [n_pages][page_size][n_kv_heads][head_dim] elements of desc->dtype
+ * A batch row's token t lies in page page_table[row][t / page_size] at offset t % page_size. Without
+ * a page table row b is page b, which is the layout of palu_dense_cache (capacity = page_size).
+ *
+ * A handle of its own (palu_kv_create) holds the shape, the rotation's frequencies and the workspace
+ * (error word, split partials, counters), with the rules of palu_attn_t: host memory only, calls on
+ * one handle share the workspace, so calls that may overlap on the GPU (two streams, two captured
+ * graphs) need a handle each. No call but palu_kv_check synchronises; all can be captured into a
+ * graph. The calls run on the workspace's device and leave the thread's current device as it was.
+ */
+typedef struct palu_kv_desc {
+  int abi_version;        /* must be PALU_ABI_VERSION */
+  int n_heads;            /* query heads */
+  int n_kv_heads;         /* key/value heads; n_heads % n_kv_heads == 0, n_heads / n_kv_heads <= 64. Query
+                             head i reads key/value head i / (n_heads / n_kv_heads) */
+  int head_dim;           /* 64 or 128 */
+  palu_dtype_t dtype;     /* pages, rotated queries and keys, attention output: F16 or BF16 (F32: palu_norm_rope
+                             and palu_append_kv only) */
+  palu_dtype_t x_dtype;   /* unrotated queries, keys, values and norm weights: F32, F16 or BF16 */
+  double rope_theta;      /* RoPE base, 0 for no rotation (convention in the file header: rotate-half) */
+  double norm_eps;        /* added to the mean square by the norm; >= 0 */
+  int max_batch;          /* largest batch of a call, <= 65535 */
+  int64_t max_tokens;     /* largest n_tokens of a call, < 2^31 */
+} palu_kv_desc;
+
+typedef struct palu_kv* palu_kv_t;
+
+palu_status_t palu_kv_workspace_size(const palu_kv_desc* desc, size_t* bytes);
+palu_status_t palu_kv_create(const palu_kv_desc* desc, void* workspace, size_t workspace_bytes, palu_stream_t stream,
+                             palu_kv_t* out);
+/* As palu_destroy and palu_attn_check. */
+palu_status_t palu_kv_destroy(palu_kv_t h);
+palu_status_t palu_kv_check(palu_kv_t h, palu_stream_t stream);
+
+/* The pages: caller-owned device memory, 16-byte aligned; n_pages * page_size < 2^31. */
+typedef struct palu_kv_pages {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int page_size;          /* tokens of a page, any positive number */
+} palu_kv_pages;
+
+/*
+ * The new tokens of a batch, packed: row b's are row_start[b] .. row_start[b + 1] - 1 of the token
+ * arrays (row_start does not decrease). kv_len[b] counts the row's cached tokens with the new ones,
+ * which are the last: new token i of n_b has slot kv_len[b] - n_b + i. Rows without new tokens are
+ * fine. Token array rows that belong to no batch row are neither read nor written.
+ */
+typedef struct palu_kv_rows {
+  const int32_t* row_start;   /* device [batch + 1] */
+  const int32_t* kv_len;      /* device [batch] */
+  const int32_t* page_table;  /* device [batch][table_pages], or NULL (row b is page b; batch <= n_pages) */
+  int64_t table_pages;        /* pages per row of the table */
+  const int32_t* positions;   /* device [n_tokens] rotation positions for palu_append_kv, or NULL: the slots */
+  int batch;
+  int64_t n_tokens;           /* host: rows of the packed token arrays */
+  int max_new;                /* host: bound on a row's new tokens */
+  int64_t max_kv_len;         /* host: bound on kv_len; <= table_pages * page_size (page_size without a table) */
+} palu_kv_rows;
+
+/*
+ * Norm and rotation of the queries and keys of n_tokens tokens in one pass:
+ *   y = R(pos) (x * rsqrt(mean(x^2) + norm_eps) * w)  per head, R of the file header's convention.
+ *   q, k            device [n_tokens][heads][head_dim] in x_dtype, heads and elements contiguous, tokens
+ *                   q_stride / k_stride elements apart (a column block of a fused projection); 16-byte
+ *                   aligned, strides in multiples of 16 bytes. k may be NULL
+ *   q_norm, k_norm  device [head_dim] weights in x_dtype, 16-byte aligned, or NULL: no norm
+ *   positions       device [n_tokens], any int32; may be NULL when the handle rotates nothing
+ *   q_out, k_out    device, dtype, same layout and rules; may be q and k themselves where dtype = x_dtype and
+ *                   the strides agree. Other overlaps are not allowed
+ * fp32 arithmetic, one rounding to dtype at the end; angles are reduced exactly at any position.
+ */
+palu_status_t palu_norm_rope(palu_kv_t h, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* q_norm, const void* k_norm, const int32_t* positions, int64_t n_tokens,
+                             void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                             palu_stream_t stream);
+
+/*
+ * Append the new tokens' keys, normed and rotated as by palu_norm_rope, and their values to the pages,
+ * and norm and rotate their queries into q_out, in one launch. k, v (and q) as q, k above with
+ * n_kv_heads heads; q and q_out (device [n_tokens][n_heads][head_dim] contiguous, dtype) may both be
+ * NULL. Rotation positions are rows->positions, or the slots. A token whose slot is negative, lies past
+ * the page table or in a page outside the pool is recorded in the error word and not stored. Two
+ * tokens that fall on one slot (a page shared by two rows that both append to it) leave either's.
+ */
+palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu_kv_rows* rows, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const void* q_norm, const void* k_norm, void* q_out, palu_stream_t stream);
+
+/*
+ * Attention of the new tokens over the pages, causal: new token i of row b attends to the slots
+ * 0 .. kv_len[b] - n_b + i (its own included; palu_append_kv comes first). Score scale
+ * 1/sqrt(head_dim).
+ *   q    device [n_tokens][n_heads][head_dim] in dtype, rotated, 16-byte aligned, tokens q_stride elements apart
+ *        (a multiple of 8)
+ *   out  device [n_tokens][n_heads][head_dim] in dtype, contiguous, 16-byte aligned
+ *   lse  device [n_tokens][n_heads] float32 natural log-sum-exp of the scaled scores, or NULL
+ * A token that sees no slot (kv_len[b] < n_b) yields 0 and lse = -inf. Slots at or past kv_len[b] are
+ * not read and may hold anything; the slots below it must be finite. fp32 scores, softmax statistics
+ * and accumulation; the softmax weights are rounded to dtype for the product with the values. A
+ * length outside [0, max_kv_len], a row with more than max_new new tokens (both clamped), a decreasing
+ * row_start (the row is skipped) and a page outside the pool (read as zeros) are recorded in the
+ * error word. The result does not depend on timing: the same call gives the same bits.
+ * PALU_ERR_UNSUPPORTED for F32 handles.
+ */
+palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu_kv_rows* rows, const void* q,
+                             int64_t q_stride, void* out, float* lse, palu_stream_t stream);
+
 /* Free the host handle. Does not synchronise: no work on it may be in flight. NULL is fine. */
 palu_status_t palu_destroy(palu_attn_t h);
 

@@ -7,7 +7,8 @@ there is no CPU fallback.
 
 Low-level functions carry the C names and take raw integers (device pointers,
 stream handles); ``PaluAttention`` and ``LatentCache`` wrap them for torch
-tensors.
+tensors, and ``PagedAttention``, ``KVPages`` and ``KVRows`` those of the paged
+dense KV cache.
 """
 from __future__ import annotations
 
@@ -36,7 +37,8 @@ EXPORTS = ("palu_attn_workspace_size", "palu_attn_create", "palu_append_latents"
            "palu_debug_int4_operand", "palu_debug_int4_dp2a", "palu_attn_trace_times",
            "palu_fuse_value_output", "palu_output_proj_workspace_size", "palu_output_proj",
            "palu_down_proj_size", "palu_prepare_down_proj", "palu_project_latents", "palu_decode_hybrid",
-           "palu_decode_paged")
+           "palu_decode_paged", "palu_kv_workspace_size", "palu_kv_create", "palu_kv_destroy", "palu_kv_check",
+           "palu_norm_rope", "palu_append_kv", "palu_attend_kv")
 PALU_TRACE_CAPACITY = 4096
 
 
@@ -62,6 +64,24 @@ class palu_dense_cache(ctypes.Structure):
 class palu_page_cache(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_void_p), ("capacity", ctypes.c_int64),
                 ("page_size", ctypes.c_int), ("rank", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class palu_kv_desc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int), ("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("x_dtype", ctypes.c_int),
+                ("rope_theta", ctypes.c_double), ("norm_eps", ctypes.c_double), ("max_batch", ctypes.c_int),
+                ("max_tokens", ctypes.c_int64)]
+
+
+class palu_kv_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int)]
+
+
+class palu_kv_rows(ctypes.Structure):
+    _fields_ = [("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_pages", ctypes.c_int64), ("positions", ctypes.c_void_p), ("batch", ctypes.c_int),
+                ("n_tokens", ctypes.c_int64), ("max_new", ctypes.c_int), ("max_kv_len", ctypes.c_int64)]
 
 
 class PaluError(RuntimeError):
@@ -102,6 +122,14 @@ def _load():
                                    ctypes.POINTER(palu_dense_cache), P, P, P, P]),
         "palu_decode_paged": (I, [P, P, ctypes.POINTER(palu_page_cache), P, I, I64,
                                   ctypes.POINTER(palu_dense_cache), P, P, P, P]),
+        "palu_kv_workspace_size": (I, [ctypes.POINTER(palu_kv_desc), ctypes.POINTER(SZ)]),
+        "palu_kv_create": (I, [ctypes.POINTER(palu_kv_desc), P, SZ, P, ctypes.POINTER(P)]),
+        "palu_kv_destroy": (I, [P]),
+        "palu_kv_check": (I, [P, P]),
+        "palu_norm_rope": (I, [P, P, I64, P, I64, P, P, P, I64, P, I64, P, I64, P]),
+        "palu_append_kv": (I, [P, ctypes.POINTER(palu_kv_pages), ctypes.POINTER(palu_kv_rows), P, I64, P, I64, P, I64,
+                               P, P, P, P]),
+        "palu_attend_kv": (I, [P, ctypes.POINTER(palu_kv_pages), ctypes.POINTER(palu_kv_rows), P, I64, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -243,6 +271,43 @@ def palu_decode_hybrid(h, q: int, cache: palu_cache, seq_lens: int, positions, q
                        stream: int) -> int:
     return _lib.palu_decode_hybrid(h, q, ctypes.byref(cache), seq_lens, positions, q_pos, batch, max_seq_len,
                                    ctypes.byref(dense), out, out_dense, lse, stream)
+
+
+def palu_kv_workspace_size(desc: palu_kv_desc):
+    n = ctypes.c_size_t(0)
+    st = _lib.palu_kv_workspace_size(ctypes.byref(desc), ctypes.byref(n))
+    return st, n.value
+
+
+def palu_kv_create(desc: palu_kv_desc, ws_ptr: int, ws_bytes: int, stream: int):
+    h = ctypes.c_void_p()
+    st = _lib.palu_kv_create(ctypes.byref(desc), ws_ptr, ws_bytes, stream, ctypes.byref(h))
+    return st, h.value
+
+
+def palu_kv_destroy(h) -> int:
+    return _lib.palu_kv_destroy(h)
+
+
+def palu_kv_check(h, stream: int) -> int:
+    return _lib.palu_kv_check(h, stream)
+
+
+def palu_norm_rope(h, q: int, q_stride: int, k, k_stride: int, q_norm, k_norm, positions, n_tokens: int, q_out: int,
+                   q_out_stride: int, k_out, k_out_stride: int, stream: int) -> int:
+    return _lib.palu_norm_rope(h, q, q_stride, k, k_stride, q_norm, k_norm, positions, n_tokens, q_out, q_out_stride,
+                               k_out, k_out_stride, stream)
+
+
+def palu_append_kv(h, pages: palu_kv_pages, rows: palu_kv_rows, q, q_stride: int, k: int, k_stride: int, v: int,
+                   v_stride: int, q_norm, k_norm, q_out, stream: int) -> int:
+    return _lib.palu_append_kv(h, ctypes.byref(pages), ctypes.byref(rows), q, q_stride, k, k_stride, v, v_stride,
+                               q_norm, k_norm, q_out, stream)
+
+
+def palu_attend_kv(h, pages: palu_kv_pages, rows: palu_kv_rows, q: int, q_stride: int, out: int, lse,
+                   stream: int) -> int:
+    return _lib.palu_attend_kv(h, ctypes.byref(pages), ctypes.byref(rows), q, q_stride, out, lse, stream)
 
 
 def check(status: int, what: str = "palu") -> None:
@@ -500,3 +565,186 @@ class OutputProjection:
         check(palu_output_proj(_ptr(self.w), self.w_dtype, self.k_dim, self.d_model, _ptr(o), B, _ptr(y),
                                self.ws_ptr, self.ws_bytes, _stream_handle(stream)), "palu_output_proj")
         return y
+
+
+# ---------------------------------------------------------------------------
+# Paged dense KV cache
+# ---------------------------------------------------------------------------
+
+class KVPages:
+    """The pages of a dense KV cache: k and v [n_pages][page_size][n_kv_heads][head_dim] device tensors. A contiguous
+    cache [rows][capacity][heads][head_dim], such as the dense segment of decode_hybrid, is one page a row."""
+
+    def __init__(self, k, v):
+        _require_contiguous(k=k, v=v)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be [n_pages][page_size][n_kv_heads][head_dim] of one dtype and device")
+        self.k, self.v = k, v
+        self.n_pages, self.page_size = int(k.shape[0]), int(k.shape[1])
+        self.heads, self.dtype = tuple(k.shape[2:]), k.dtype
+        self._c = palu_kv_pages(_ptr(k), _ptr(v), self.n_pages, self.page_size)
+
+    def c_struct(self) -> palu_kv_pages:
+        return self._c
+
+
+class KVRows:
+    """The new tokens of a batch and its rows' caches, as palu_kv_rows describes them: device int32 tensors
+    row_start [batch + 1], kv_len [batch], page_table [batch][pages] (or None: row b is page b) and positions
+    [n_tokens] (or None), and the host's bounds. One object serves every layer of a step; the tensors may be
+    overwritten between steps."""
+
+    def __init__(self, row_start, kv_len, *, n_tokens, max_new, max_kv_len, page_table=None, positions=None):
+        torch = _torch()
+        given = {"row_start": row_start, "kv_len": kv_len, "page_table": page_table, "positions": positions}
+        _require_contiguous(**given)
+        for name, t in given.items():
+            if t is not None and (t.dtype != torch.int32 or t.device != row_start.device):
+                raise ValueError(f"{name} must be an int32 tensor on row_start's device")
+        batch = int(kv_len.shape[0])
+        if kv_len.dim() != 1 or row_start.shape != (batch + 1,):
+            raise ValueError("row_start must hold batch + 1 and kv_len batch entries")
+        if page_table is not None and (page_table.dim() != 2 or page_table.shape[0] != batch):
+            raise ValueError("page_table must be [batch][pages]")
+        if positions is not None and positions.shape != (n_tokens,):
+            raise ValueError("positions must hold n_tokens entries")
+        self.tensors, self.device = (row_start, kv_len, page_table, positions), row_start.device
+        self.batch, self.n_tokens = batch, int(n_tokens)
+        self._c = palu_kv_rows(_ptr(row_start), _ptr(kv_len), _ptr(page_table),
+                               0 if page_table is None else int(page_table.shape[1]), _ptr(positions), batch,
+                               self.n_tokens, int(max_new), int(max_kv_len))
+
+    def c_struct(self) -> palu_kv_rows:
+        return self._c
+
+
+class PagedAttention:
+    """One layer's paged dense KV cache operators: norm_rope, append and attend. Owns one handle and its
+    torch-allocated workspace; calls that may overlap on the GPU need an object each."""
+
+    def __init__(self, *, n_heads, n_kv_heads, head_dim, dtype, x_dtype=None, rope_theta=10000.0, norm_eps=1e-6,
+                 max_batch=1, max_tokens=1, device="cuda", stream=None):
+        torch = _torch()
+        names = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+        x_dtype = x_dtype or dtype
+        self.desc = palu_kv_desc(PALU_ABI_VERSION, n_heads, n_kv_heads, head_dim, DTYPES[dtype], DTYPES[x_dtype],
+                                 float(rope_theta), float(norm_eps), max_batch, max_tokens)
+        st, nbytes = palu_kv_workspace_size(self.desc)
+        check(st, "palu_kv_workspace_size")
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
+        self.dtype, self.x_dtype = names[dtype], names[x_dtype]
+        self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        self.device = self.workspace.device
+        base = int(self.workspace.data_ptr())
+        st, self.handle = palu_kv_create(self.desc, base + (-base) % 256, nbytes, self._stream(stream))
+        check(st, "palu_kv_create")
+
+    def close(self):
+        if getattr(self, "handle", None):
+            palu_kv_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _stream(self, stream) -> int:
+        if stream is None:
+            stream = _torch().cuda.current_stream(self.device)
+        return stream.cuda_stream
+
+    def _view(self, name, t, heads, dtype, n_tokens):
+        """(pointer, token stride) of a [n_tokens][heads][head_dim] tensor whose tokens may lie apart."""
+        if t.dtype != dtype or t.device != self.device:
+            raise ValueError(f"{name} must be a {dtype} tensor on {self.device}")
+        if t.shape != (n_tokens, heads, self.head_dim):
+            raise ValueError(f"{name} must be [{n_tokens}][{heads}][{self.head_dim}]")
+        s = t.stride()
+        if s[2] != 1 or (heads > 1 and s[1] != self.head_dim):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        return t.data_ptr(), (s[0] if n_tokens > 1 else heads * self.head_dim)
+
+    def _weight(self, name, t):
+        if t is None:
+            return None
+        if t.dtype != self.x_dtype or t.device != self.device or t.shape != (self.head_dim,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{self.head_dim}] {self.x_dtype} tensor on {self.device}")
+        return t.data_ptr()
+
+    def _batch(self, pages, rows):
+        if pages.heads != (self.n_kv_heads, self.head_dim) or pages.dtype != self.dtype:
+            raise ValueError(f"pages must hold {self.n_kv_heads} heads of {self.head_dim} {self.dtype} values")
+        if pages.k.device != self.device or rows.device != self.device:
+            raise ValueError(f"pages and rows must be on {self.device}")
+
+    def norm_rope(self, q, k=None, positions=None, *, q_weight=None, k_weight=None, q_out=None, k_out=None,
+                  stream=None):
+        """Norm (where a weight is given) and rotation of q [n_tokens][n_heads][head_dim] and k [n_tokens]
+        [n_kv_heads][head_dim] at positions [n_tokens]. Returns (q_out, k_out); outputs may be the inputs."""
+        torch = _torch()
+        N = int(q.shape[0])
+        if q_out is None:
+            q_out = torch.empty((N, self.n_heads, self.head_dim), dtype=self.dtype, device=self.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty((N, self.n_kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
+        if positions is not None and (positions.dtype != torch.int32 or positions.shape != (N,) or
+                                      positions.device != self.device or not positions.is_contiguous()):
+            raise ValueError(f"positions must be a contiguous [{N}] int32 tensor on {self.device}")
+        qp, qs = self._view("q", q, self.n_heads, self.x_dtype, N)
+        qo, qos = self._view("q_out", q_out, self.n_heads, self.dtype, N)
+        kp = ks = ko = kos = None
+        if k is not None:
+            kp, ks = self._view("k", k, self.n_kv_heads, self.x_dtype, N)
+            ko, kos = self._view("k_out", k_out, self.n_kv_heads, self.dtype, N)
+        check(_lib.palu_norm_rope(self.handle, qp, qs, kp, ks or 0, self._weight("q_weight", q_weight),
+                                  self._weight("k_weight", k_weight), _ptr(positions), N, qo, qos, ko, kos or 0,
+                                  self._stream(stream)), "palu_norm_rope")
+        return q_out, k_out
+
+    def append(self, pages: KVPages, rows: KVRows, k, v, *, q=None, q_weight=None, k_weight=None, q_out=None,
+               stream=None):
+        """Writes the new tokens' keys (normed where k_weight is given, rotated at rows' positions or their slots)
+        and values [n_tokens][n_kv_heads][head_dim] into the pages, and norms and rotates q into q_out in the same
+        launch. Returns q_out, or None without q."""
+        self._batch(pages, rows)
+        N = rows.n_tokens
+        kp, ks = self._view("k", k, self.n_kv_heads, self.x_dtype, N)
+        vp, vs = self._view("v", v, self.n_kv_heads, self.x_dtype, N)
+        qp, qs, qo = None, 0, None
+        if q is not None:
+            if q_out is None:
+                q_out = _torch().empty((N, self.n_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            qp, qs = self._view("q", q, self.n_heads, self.x_dtype, N)
+            qo, qos = self._view("q_out", q_out, self.n_heads, self.dtype, N)
+            if qos != self.n_heads * self.head_dim:
+                raise ValueError("q_out must be contiguous")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        check(_lib.palu_append_kv(self.handle, pages._c, rows._c, qp, qs, kp, ks, vp, vs,
+                                  self._weight("q_weight", q_weight), self._weight("k_weight", k_weight), qo,
+                                  self._stream(stream)), "palu_append_kv")
+        return q_out
+
+    def attend(self, pages: KVPages, rows: KVRows, q, *, out=None, lse=None, stream=None):
+        """Causal attention of the new tokens' rotated queries q [n_tokens][n_heads][head_dim] over the pages.
+        Returns out, of q's shape; lse, when given, is [n_tokens][n_heads] float32."""
+        torch = _torch()
+        self._batch(pages, rows)
+        N = rows.n_tokens
+        qp, qs = self._view("q", q, self.n_heads, self.dtype, N)
+        if out is None:
+            out = torch.empty((N, self.n_heads, self.head_dim), dtype=self.dtype, device=self.device)
+        op, os_ = self._view("out", out, self.n_heads, self.dtype, N)
+        if os_ != self.n_heads * self.head_dim:
+            raise ValueError("out must be contiguous")
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (N, self.n_heads) or
+                                lse.device != self.device or not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous [{N}][{self.n_heads}] float32 tensor on {self.device}")
+        check(_lib.palu_attend_kv(self.handle, pages._c, rows._c, qp, qs, op, _ptr(lse), self._stream(stream)),
+              "palu_attend_kv")
+        return out
+
+    def check_device(self, stream=None):
+        check(palu_kv_check(self.handle, self._stream(stream)), "palu_kv_check")
