@@ -45,6 +45,36 @@ __device__ __forceinline__ int64_t kv_slot(const KvRows& r, const KvPages& p, in
   return (int64_t)page * p.page_size + (t - pg * p.page_size);
 }
 
+// Row b's first packed token, new tokens and cached length, clamped to the call's bounds; false where the row
+// is skipped. `bad`: what to record (an ErrWhere), or 0.
+__device__ __forceinline__ bool kv_row(const KvRows& r, int b, int& q0, int& n, int& L, unsigned& bad) {
+  q0 = r.row_start[b];
+  const int q1 = r.row_start[b + 1];
+  const int len = r.kv_len[b];
+  const bool skip = q0 < 0 || q1 < q0 || q1 > r.n_tokens;
+  n = skip ? 0 : q1 - q0;
+  bad = skip || n > r.max_new ? kErrRows : len < 0 || len > r.max_kv_len ? kErrSeqLen : 0u;
+  n = min(n, r.max_new);
+  L = max(0, min(len, r.max_kv_len));
+  return !skip;
+}
+
+// 2^x by the special function unit (relative error 2^-22; 2^-inf = 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool BF16> __device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
 // norm_rope and append: one kernel over packed tokens and the heads of q, k and (append) v
 struct KvRopeArgs {
   const void* src[3];          // q, k, v (nullptr: absent)
@@ -78,14 +108,41 @@ struct KvAttendArgs {
   int head_dim;
   int bf16;
   float scale_log2;            // log2(e) / sqrt(d)
-  int n_splits;                // ranges a row's cached tokens are cut into
-  float* part_o;               // [unit][n_splits][16][d] fp32 partial outputs, normalised by nothing
-  float2* part_ml;             // [unit][n_splits][16]: running maximum (log2 units) and sum
+  int n_splits;                // few rows: ranges a row's cached tokens are cut into, at most
+  float* part_o;               // fp32 partial outputs, not yet divided by their sums
+  float2* part_ml;             // their running maxima (log2 units) and sums
   unsigned* counters;          // [unit], zero between calls
   ErrWord* err;
 };
 constexpr int kKvFewRows = 16;           // query rows (token, head of the group) of a unit
 constexpr int kKvFewStep = 128;          // cached tokens the unit's warps take together
 cudaError_t launch_kv_attend_few(const KvAttendArgs& a, cudaStream_t st);
+
+// Work list of the tensor-core kernel, in the workspace.
+constexpr int kKvTcRows = 128;           // query rows of a tile
+struct KvItem {      // one or two tiles of a row's query tokens over cached steps [kv0, kv1) of 128 tokens
+  int b, q0, n, L;   // row; its first packed token, new tokens, cached length
+  int tok0, tiles;   // first new token; tiles of per_tile tokens
+  int kv0, kv1;
+  int split;         // number of the item among those that were cut, or -1: it writes the output itself
+  int pad[3];
+};
+struct KvJoin {      // a cut item's pieces: numbers slot .. slot + pieces - 1
+  int q0, n, tok0, tiles, slot, pieces, pad[2];
+};
+struct KvPlanHead {
+  int n_items, n_joins;
+  unsigned next;     // the next item to take
+};
+struct KvTcPlan {
+  KvPlanHead* head;
+  KvItem* items;     // [tile_cap + slots]
+  KvJoin* joins;     // [slots]
+  int* row_base;     // [batch + 1]: tiles before each row
+  int tile_cap;      // most tiles the call's packed tokens can make
+  int slots;         // most pieces x key/value heads whose partials the workspace holds
+  int sm_count;
+};
+cudaError_t launch_kv_attend_tc(const KvAttendArgs& a, const KvTcPlan& t, cudaStream_t st);
 
 }  // namespace palu

@@ -51,23 +51,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <bool BF16> __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
-// 2^x by the special function unit; 2^-inf = 0
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int DH> struct Sm {
   static constexpr int kRow = DH * 2;                       // bytes of a token's head row
   static constexpr int kTile = kTok * kRow;                 // one warp's K (or V) stage
@@ -95,16 +78,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
   const int h = uy % a.n_kv, rt = uy / a.n_kv, b = blockIdx.y;
   const KvRows& R = a.rows;
 
-  // the row's new tokens and length, clamped to the call's bounds
-  const int q0 = R.row_start[b], q1 = R.row_start[b + 1];
-  int n = q1 - q0, L = R.kv_len[b];
-  const bool bad_rows = q0 < 0 || q1 < q0 || q1 > R.n_tokens || n > R.max_new;
-  const bool bad_len = L < 0 || L > R.max_kv_len;
-  if ((bad_rows || bad_len) && split == 0 && uy == 0 && threadIdx.x == 0)
-    record_error(a.err, kCodeDevice, bad_rows ? kErrRows : kErrSeqLen, bad_rows ? q0 : L, b);
-  if (q0 < 0 || q1 < q0 || q1 > R.n_tokens) return;      // the row is skipped
-  n = min(n, R.max_new);
-  L = max(0, min(L, R.max_kv_len));
+  int q0, n, L;
+  unsigned bad;
+  const bool use = kv_row(R, b, q0, n, L, bad);
+  if (bad && split == 0 && uy == 0 && threadIdx.x == 0) record_error(a.err, kCodeDevice, bad, b, b);
+  if (!use) return;
   const int rows = min(n * a.g - rt * kKvFewRows, kKvFewRows);
   if (rows <= 0) return;
   const int i_last = (rt * kKvFewRows + rows - 1) / a.g;           // the unit's last new token

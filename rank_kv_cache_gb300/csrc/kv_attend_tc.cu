@@ -1,0 +1,823 @@
+// Attention of many new tokens over a paged KV cache on the tcgen05 tensor cores: prompts, chunks of
+// prompts, and batches that mix them with decode steps.
+//
+//   o = softmax(q K^T / sqrt(d)) V over slots 0 .. L - n + i of the query's row,  lse = ln sum e^s.
+//
+// Query rows. The g query heads of a key/value head are rows of one tile: row i g + j is new token i
+// under head j, floor(128 / g) tokens fill a 128-row tile, and K and V are read once for the group. A
+// work item is (row of the batch, key/value head, one or two tiles, a range of the cached tokens).
+//
+// Three launches. kv_plan_kernel lists the items from the lengths on the device: the longest first
+// within a row, and cut along the cached tokens where whole tiles would leave SMs idle (few rows, long
+// caches). kv_attend_tc_kernel is persistent, one CTA an SM, and takes items off the list by an atomic
+// counter (which item runs where does not change any sum). kv_join_kernel joins the ranges of items
+// that were cut, in their order.
+//
+// One CTA: two softmax warpgroups, a loader warp and an MMA warp.
+//   * The loader gathers the cached rows of 128 tokens by TMA, four a copy, at the slots that the page
+//     table gives, into a ring of K and V tiles (128-byte swizzle). Tokens past the row's length are
+//     rows outside the tensor map: they arrive as zeros, so pages of any size may end anywhere and
+//     what lies behind the length is never read.
+//   * The MMA thread issues S = Q K^T (both operands in shared memory) and O += P V (P in tensor
+//     memory, V as stored, along the head dimension), alternating between two units, so that one
+//     unit's product runs while the other's softmax does.
+//   * A unit is a warpgroup with a 128-row S and O accumulator in tensor memory; a thread owns a query
+//     row. P overwrites S in place. The running maximum is only raised when a score exceeds it by more
+//     than 2^8, so that the output in tensor memory is rarely rescaled; p then stays below 2^8, and the
+//     sum and the output share the same factor.
+//   With two tiles the units are the tiles, over the same K and V; with one, the units take the cached
+//   tiles in turn (even, odd) and are joined through shared memory at the end.
+//
+// Sums, maxima, S and O are fp32; the weights p are rounded to the cache's type, as the product takes
+// them; l is the sum of the unrounded p.
+//
+// Every wait is bounded; one that gives up records PALU_ERR_TIMEOUT, and all roles wait for their own
+// copies and products in flight before tensor memory is freed.
+#include "kv.h"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace palu {
+namespace {
+
+constexpr int kTile = 128;               // query rows of a tile, cached tokens of a step
+constexpr int kThreads = 384;            // two softmax warpgroups; loader, MMA and two idle warps
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanTiles = 4096;         // tiles the plan weighs for cutting; longer lists are not cut
+// Registers: launched with 168 a thread (65536 / 384, in eights); 2 * 128 * 208 + 128 * 88 = 384 * 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr float kRaise = 8.f;            // log2 by which a score may exceed the running maximum
+
+template <int DH> struct Lay {
+  static constexpr int kHalf = kTile * 128;             // 64 elements of 128 rows
+  static constexpr int kTileB = kHalf * (DH / 64);
+  static constexpr int kStages = DH == 128 ? 5 : 10;
+  static constexpr int kOffKv = 2 * kTileB;             // behind two query tiles
+  static constexpr int kOffBar = kOffKv + kStages * kTileB;
+  static constexpr int kSmem = kOffBar + 2048 + 1024;   // barriers, items, the units' exchange; alignment
+  static constexpr uint32_t kColO = 2 * kTile;          // tensor memory: S (and P) of the units, then O
+};
+
+struct Item {
+  int q0, n, L, tok0, tiles, kv0, kv1, split, h;
+};
+
+struct Shared {
+  uint64_t full[10], empty[10];
+  uint64_t q_full, q_empty, x_full, drained;
+  uint64_t s_full[2], o_full[2], p_full[2][2];
+  uint64_t item_full[2], item_empty[2];
+  Item item[2];
+  uint32_t tmem;
+  int abort_flag;
+  float2 ml[kTile];
+};
+static_assert(sizeof(Shared) <= 2048, "shared block");
+
+struct TcParams {
+  KvAttendArgs a;
+  KvTcPlan plan;
+  int per_tile;        // tokens of a 128-row tile: floor(128 / g)
+  int64_t oob_row;     // a row index outside the tensor maps
+  uint64_t wait_ns;
+};
+
+// ------------------------------------------------------------------------------------------- plan
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {   // exclusive, kPlanThreads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  total = warp_sums[31];
+  return x - v + (warp ? warp_sums[warp - 1] : 0);
+}
+
+// cut a tile of c steps into pieces of at most `target`: their number, and their length
+__device__ __forceinline__ int cut(int c, int target, int* len) {
+  if (c <= target) {
+    *len = c;
+    return 1;
+  }
+  const int p = (c + target - 1) / target;
+  *len = (c + p - 1) / p;
+  return (c + *len - 1) / *len;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P) {
+  __shared__ int cost[kPlanTiles];
+  __shared__ int sums[32];
+  __shared__ int tops[32];
+  __shared__ float est_s[32];
+  __shared__ int target_s;
+  const KvAttendArgs& a = P.a;
+  const KvRows& R = a.rows;
+  const KvTcPlan& plan = P.plan;
+  int* base = plan.row_base;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = P.per_tile, tile_cap = plan.tile_cap, slots = plan.slots, sms = plan.sm_count;
+
+  // tiles (or pairs) of each row, and their running number
+  int T = 0;
+  for (int b0 = 0; b0 < R.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int w = 0;
+    if (b < R.batch) {
+      int q0, n, L;
+      unsigned bad;
+      if (kv_row(R, b, q0, n, L, bad)) w = ((n + per - 1) / per + 1) / 2;
+      if (bad) record_error(a.err, kCodeDevice, bad, b, b);
+    }
+    int total;
+    const int at = block_scan(w, sums, total);
+    if (b < R.batch) base[b] = T + at;
+    T += total;
+  }
+  if (tid == 0) base[R.batch] = T;
+  if (T > tile_cap) {   // rows that overlap in the packed arrays: more tiles than tokens
+    if (tid == 0) record_error(a.err, kCodeDevice, kErrRows, T, 0);
+    T = tile_cap;
+  }
+  __syncthreads();
+
+  auto tile_of = [&](int i, KvItem& it) -> int {   // fills the item of tile i, uncut; its steps
+    int lo = 0, hi = R.batch;                      // the last row with base[row] <= i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (base[mid] <= i) lo = mid; else hi = mid;
+    }
+    unsigned bad;
+    kv_row(R, lo, it.q0, it.n, it.L, bad);
+    it.b = lo;
+    it.tok0 = (base[lo + 1] - 1 - i) * 2 * per;    // the last tokens, which see most, first
+    it.tiles = it.n - it.tok0 > per ? 2 : 1;
+    const int last = min(it.n, it.tok0 + it.tiles * per) - 1;
+    const int seen = max(0, min(it.L, it.L - it.n + last + 1));
+    return (seen + kTile - 1) / kTile;
+  };
+
+  int top = 0, total_c = 0;
+  for (int i = tid; i < T; i += kPlanThreads) {
+    KvItem it;
+    const int c = tile_of(i, it);
+    if (i < kPlanTiles) cost[i] = c;
+    top = max(top, c);
+    total_c += c;
+  }
+  int all_c;
+  block_scan(total_c, sums, all_c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+  top = tops[0];
+  for (int k = 1; k < 32; ++k) top = max(top, tops[k]);
+  top = max(top, 1);
+
+  // Each warp weighs one way to cut: the longest tile into s pieces, the others into pieces as long. The
+  // time is estimated as the waves of items times their mean length and start-up, at least the longest
+  // item, and the join of what was cut (in steps of 128 tokens).
+  if (T <= kPlanTiles) {
+    const int s = warp < 16 ? warp + 1 : warp < 24 ? 16 + (warp - 15) * 4 : 48 + (warp - 23) * 13;
+    const int target = max(1, (top + s - 1) / s);
+    int items = 0, cut_items = 0;
+    for (int i = lane; i < T; i += 32) {
+      int len;
+      const int p = cut(cost[i], target, &len);
+      items += p;
+      if (p > 1) cut_items += p;
+    }
+    items = __reduce_add_sync(0xffffffffu, items);
+    cut_items = __reduce_add_sync(0xffffffffu, cut_items);
+    const float waves = ceilf(float(items) * a.n_kv / sms);
+    float est = fmaxf(waves * (float(all_c) / max(items, 1) + 2.f), target + 2.f) + (cut_items ? 4.f : 0.f);
+    if ((int64_t)cut_items * a.n_kv > slots) est = INFINITY;
+    if (lane == 0) est_s[warp] = est;
+    __syncthreads();
+    if (tid == 0) {
+      int best = 0;
+      for (int k = 1; k < 32; ++k)
+        if (est_s[k] < est_s[best]) best = k;
+      const int sb = best < 16 ? best + 1 : best < 24 ? 16 + (best - 15) * 4 : 48 + (best - 23) * 13;
+      target_s = max(1, (top + sb - 1) / sb);
+    }
+  } else if (tid == 0) {
+    target_s = top;
+  }
+  __syncthreads();
+  const int target = target_s;
+
+  int n_items = 0, n_cut = 0, n_joins = 0;
+  for (int i0 = 0; i0 < T; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    KvItem it{};
+    int p = 0, len = 0, c = 0;
+    if (i < T) {
+      c = tile_of(i, it);
+      p = cut(c, target, &len);
+    }
+    int tot_p, tot_c, tot_j;
+    const int at = n_items + block_scan(p, sums, tot_p);
+    const int slot = n_cut + block_scan(p > 1 ? p : 0, sums, tot_c);
+    const int join = n_joins + block_scan(p > 1 ? 1 : 0, sums, tot_j);
+    for (int k = 0; k < p; ++k) {
+      it.kv0 = k * len;
+      it.kv1 = min(c, it.kv0 + len);
+      it.split = p > 1 ? slot + k : -1;
+      plan.items[at + k] = it;
+    }
+    if (p > 1) plan.joins[join] = KvJoin{it.q0, it.n, it.tok0, it.tiles, slot, p, {0, 0}};
+    n_items += tot_p;
+    n_cut += tot_c;
+    n_joins += tot_j;
+  }
+  if (tid == 0) {
+    plan.head->n_items = n_items;
+    plan.head->n_joins = n_joins;
+    plan.head->next = 0;
+  }
+}
+
+// ------------------------------------------------------------------------------------------- join
+// A warp takes 32 query rows of a cut tile, a lane one row: o = sum_k o_k 2^(m_k - M) / L.
+template <int DH, bool BF16> __global__ void __launch_bounds__(128) kv_join_kernel(const TcParams P) {
+  const KvAttendArgs& a = P.a;
+  const KvTcPlan& plan = P.plan;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kParts = 4;                                // column parts of a row, one a warp
+  const int units = plan.head->n_joins * a.n_kv * 8;            // two tiles of four 32-row parts
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const KvJoin J = plan.joins[u / 8 / a.n_kv];
+    const int h = u / 8 % a.n_kv, tile = u / 4 % 2, r = (u % 4) * 32 + lane;
+    if (tile >= J.tiles) continue;
+    const int i = J.tok0 + tile * P.per_tile + r / a.g;
+    if (r >= P.per_tile * a.g || i >= J.n) continue;
+    const int64_t s0 = ((int64_t)J.slot * a.n_kv + h) * 2 + tile, step = 2 * a.n_kv;
+    const float2* ml = a.part_ml + s0 * kTile + r;
+    float M = -INFINITY;
+    for (int k = 0; k < J.pieces; ++k) M = fmaxf(M, ml[k * step * kTile].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int k = 0; k < J.pieces; ++k) L = fmaf(ml[k * step * kTile].y, exp2f(ml[k * step * kTile].x - base), L);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int head = h * a.g + r % a.g;
+    const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + head;
+    if (warp == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994531f;
+    constexpr int kCols = DH / 4 / kParts;                 // float4 columns of this warp
+    float4 acc[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + warp * kCols) * kTile + r;
+    for (int k = 0; k < J.pieces; ++k) {
+      const float w = exp2f(ml[k * step * kTile].x - base);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const float4 v = po[(k * step * (DH / 4) + c) * kTile];
+        acc[c].x = fmaf(v.x, w, acc[c].x);
+        acc[c].y = fmaf(v.y, w, acc[c].y);
+        acc[c].z = fmaf(v.z, w, acc[c].z);
+        acc[c].w = fmaf(v.w, w, acc[c].w);
+      }
+    }
+    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * DH + warp * kCols * 4);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+      out[c] = make_uint2(pack2<BF16>(acc[c].x * inv, acc[c].y * inv), pack2<BF16>(acc[c].z * inv, acc[c].w * inv));
+  }
+}
+
+// ------------------------------------------------------------------------------------------- attend
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// steps of unit u of an item (its cached tiles), and the tile of its step k
+__device__ __forceinline__ int unit_steps(const Item& it, int u, int per) {
+  if (it.tiles == 1) return (it.kv1 - it.kv0 + 1 - u) / 2;
+  if (u == 1) return it.kv1 - it.kv0;
+  const int seen = max(0, min(it.L, it.L - it.n + it.tok0 + per));   // the first tile sees less than the second
+  return max(0, min(it.kv1, (seen + kTile - 1) / kTile) - it.kv0);
+}
+__device__ __forceinline__ int unit_tile(const Item& it, int u, int k) {
+  return it.tiles == 1 ? it.kv0 + u + 2 * k : it.kv0 + k;
+}
+
+template <int DH, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const TcParams P) {
+  using Y = Lay<DH>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared& S = *reinterpret_cast<Shared*>(smem + Y::kOffBar);
+  volatile int* abort_flag = &S.abort_flag;
+  const KvAttendArgs& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Y::kStages; ++i) {
+      tc::mbar_init(&S.full[i], 1);
+      tc::mbar_init(&S.empty[i], 1);
+    }
+    tc::mbar_init(&S.q_full, 1);
+    tc::mbar_init(&S.q_empty, 5);              // the products that read the queries; warpgroup 0's warps
+    tc::mbar_init(&S.x_full, 4);
+    tc::mbar_init(&S.drained, 1);
+    for (int u = 0; u < 2; ++u) {
+      tc::mbar_init(&S.s_full[u], 1);
+      tc::mbar_init(&S.o_full[u], 1);
+      for (int k = 0; k < 2; ++k) tc::mbar_init(&S.p_full[u][k], 4);
+      tc::mbar_init(&S.item_full[u], 1);
+      tc::mbar_init(&S.item_empty[u], 9);      // eight softmax warps, the MMA thread
+    }
+    S.abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&S.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = S.tmem;
+
+  if (warp >= 8) {
+    tc::regs_shrink<kRegsOther>();
+    if (warp == 8) {
+      // ------------------------------------------------------------------ loader
+      const int total = P.plan.head->n_items * a.n_kv;
+      const int oob = int(P.oob_row);
+      int seq = 0, loads_q = 0;
+      bool ok = true;
+      if (lane == 0) {
+        tc::tma_prefetch(&tm_q);
+        tc::tma_prefetch(&tm_k);
+        tc::tma_prefetch(&tm_v);
+      }
+      for (int i = 0; ok; ++i) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, P.wait_ns));
+        if (!ok) break;
+        int idx = 0;
+        if (lane == 0) idx = (int)atomicAdd(&P.plan.head->next, 1u);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+        Item it{};
+        int b = 0;
+        if (idx < total) {
+          const KvItem e = P.plan.items[idx / a.n_kv];
+          it = Item{e.q0, e.n, e.L, e.tok0, e.tiles, e.kv0, e.kv1, e.split, idx % a.n_kv};
+          b = e.b;
+        }
+        if (lane == 0) {
+          S.item[i & 1] = it;
+          tc::mbar_arrive(&S.item_full[i & 1]);
+        }
+        if (idx >= total) break;
+        if (it.kv1 == it.kv0) continue;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.q_empty, (loads_q & 1) ^ 1, abort_flag, P.wait_ns));
+        if (!ok) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(it.tiles) * P.per_tile * a.g * DH * 2);
+          for (int t = 0; t < it.tiles; ++t)
+            for (int c = 0; c < DH / 64; ++c)
+              tc::tma_load_3d(smem + t * Y::kTileB + c * Y::kHalf, &tm_q, &S.q_full, c * 64, it.h * a.g,
+                              it.q0 + it.tok0 + t * P.per_tile);
+        }
+        ++loads_q;
+        __syncwarp();
+        auto load = [&](const CUtensorMap* m, int j) {
+          int r[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = j * kTile + lane * 4 + e;
+            r[e] = oob;
+            if (t < it.L) {
+              const int64_t s = kv_slot(a.rows, a.pages, b, t);
+              if (s >= 0) r[e] = int(s) * a.n_kv + it.h;
+              else record_error(a.err, kCodeDevice, kErrPage, t, b);
+            }
+          }
+          const int st = seq % Y::kStages;
+          ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.empty[st], ((seq / Y::kStages) & 1) ^ 1, abort_flag, P.wait_ns));
+          if (!ok) return;
+          if (lane == 0) tc::mbar_arrive_expect_tx(&S.full[st], Y::kTileB);
+          __syncwarp();
+          uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB + lane * 512;
+#pragma unroll
+          for (int c = 0; c < DH / 64; ++c)
+            tc::tma_gather4(dst + c * Y::kHalf, m, &S.full[st], c * 64, r[0], r[1], r[2], r[3]);
+          ++seq;
+        };
+        // the order in which the products take them: K runs one tile ahead of V, two where the units alternate
+        const int lead = it.tiles == 1 ? 2 : 1;
+        for (int j = it.kv0; ok && j < min(it.kv0 + lead, it.kv1); ++j) load(&tm_k, j);
+        for (int j = it.kv0; ok && j < it.kv1; ++j) {
+          load(&tm_v, j);
+          if (ok && j + lead < it.kv1) load(&tm_k, j + lead);
+        }
+      }
+      if (!ok) {   // copies still in flight must land before the CTA exits
+        volatile int quiet = 0;
+        for (int s = max(0, seq - Y::kStages); s < seq; ++s)
+          tc::mbar_wait_bounded(&S.full[s % Y::kStages], (s / Y::kStages) & 1, &quiet, P.wait_ns / 10);
+        if (loads_q) tc::mbar_wait_bounded(&S.q_full, (loads_q - 1) & 1, &quiet, P.wait_ns / 10);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------------ MMA
+      if (lane == 0) {
+        const uint32_t id_qk = tc::idesc_f16(kTile, kTile, BF16), id_pv = tc::idesc_f16(kTile, DH, BF16) | tc::kIdescBMajorMN;
+        const uint32_t base = tc::smem_addr(smem);
+        int seq = 0, loads_q = 0, np[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t par) {
+          if (ok) ok = tc::mbar_wait_bounded(bar, par, abort_flag, P.wait_ns);
+          tc::tc_fence_after();
+          return ok;
+        };
+        for (int i = 0; ok; ++i) {
+          if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
+          const Item it = S.item[i & 1];
+          tc::mbar_arrive(&S.item_empty[i & 1]);
+          if (it.tiles == 0) break;
+          if (it.kv1 == it.kv0) continue;
+          if (!wait(&S.q_full, loads_q & 1)) break;
+          ++loads_q;
+          const int steps[2] = {unit_steps(it, 0, P.per_tile), unit_steps(it, 1, P.per_tile)};
+          auto qk = [&](int u, int st) {
+            const uint32_t qa = base + (it.tiles == 2 ? u * Y::kTileB : 0), ka = base + Y::kOffKv + st * Y::kTileB;
+#pragma unroll
+            for (int k = 0; k < DH / 16; ++k) {
+              const uint32_t off = (k / 4) * Y::kHalf + (k % 4) * 32;
+              tc::umma_f16(tmem + u * kTile, tc::sdesc_k_sw128(qa + off), tc::sdesc_k_sw128(ka + off), id_qk, k != 0);
+            }
+            tc::umma_commit(&S.s_full[u]);
+          };
+          auto pv = [&](int u, int st, bool first) {
+            const uint32_t va = base + Y::kOffKv + st * Y::kTileB;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (!wait(&S.p_full[u][half], np[u] & 1)) return;
+#pragma unroll
+              for (int k = half * 4; k < half * 4 + 4; ++k)
+                tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8,
+                                tc::sdesc_mn_sw128(va + k * 2048, Y::kHalf), id_pv, !first || k != 0);
+            }
+            ++np[u];
+          };
+          auto free_stage = [&](int st) { tc::umma_commit(&S.empty[st]); };
+          auto done = [&](int u) { tc::umma_commit(&S.o_full[u]); };
+          auto stage_wait = [&]() -> int {
+            const int st = seq % Y::kStages;
+            wait(&S.full[st], (seq / Y::kStages) & 1);
+            return st;
+          };
+          if (it.tiles == 2) {
+            int st = stage_wait();
+            if (!ok) break;
+            if (steps[0] > 0) qk(0, st);
+            qk(1, st);
+            free_stage(st);
+            ++seq;
+            for (int k = 0; k < steps[1]; ++k) {
+              const bool more = k + 1 < steps[1];
+              const int sv = stage_wait();
+              ++seq;
+              if (!ok) break;
+              int sk = -1;
+              if (k < steps[0]) {
+                pv(0, sv, k == 0);
+                if (!ok) break;
+                if (k + 1 < steps[0]) {
+                  sk = stage_wait();
+                  if (!ok) break;
+                  qk(0, sk);
+                } else {
+                  done(0);
+                }
+              }
+              pv(1, sv, k == 0);
+              if (!ok) break;
+              free_stage(sv);
+              if (more) {
+                sk = stage_wait();
+                if (!ok) break;
+                qk(1, sk);
+                free_stage(sk);
+                ++seq;
+              } else {
+                done(1);
+              }
+            }
+          } else {
+            const int n = it.kv1 - it.kv0;
+            for (int k = 0; k < min(n, 2) && ok; ++k) {
+              const int st = stage_wait();
+              if (!ok) break;
+              qk(k, st);
+              free_stage(st);
+              ++seq;
+            }
+            for (int k = 0; k < n && ok; ++k) {
+              const int u = k & 1;
+              const int sv = stage_wait();
+              ++seq;
+              if (!ok) break;
+              pv(u, sv, k < 2);
+              if (!ok) break;
+              free_stage(sv);
+              if (k + 2 < n) {
+                const int sk = stage_wait();
+                if (!ok) break;
+                qk(u, sk);
+                free_stage(sk);
+                ++seq;
+              } else {
+                done(u);
+              }
+            }
+          }
+          if (!ok) break;
+          tc::umma_commit(&S.q_empty);
+        }
+        // every product issued has completed once this commit lands
+        volatile int quiet = 0;
+        tc::umma_commit(&S.drained);
+        tc::mbar_wait_bounded(&S.drained, 0, &quiet, P.wait_ns);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    tc::regs_grow<kRegsSoftmax>();
+    const int u = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;                        // query row of the tile = lane of tensor memory
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + u * kTile, t_o = tmem + lanes + Y::kColO + u * DH;
+    const float c = a.scale_log2;
+    const uint64_t c2 = pair(c, c);
+    int n_s = 0, n_o = 0, n_x = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t par) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, par, abort_flag, P.wait_ns));
+      tc::tc_fence_after();
+      return ok;
+    };
+    for (int i = 0; ok; ++i) {
+      if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
+      const Item it = S.item[i & 1];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&S.item_empty[i & 1]);
+      if (it.tiles == 0) break;
+      const int tile = it.tiles == 2 ? u : 0;
+      const int first_tok = it.tok0 + tile * P.per_tile;
+      const int tok = first_tok + r / a.g;
+      const bool live = r < P.per_tile * a.g && tok < it.n;
+      const int vis = it.L - it.n + tok;                         // last slot this row sees
+      const int vis_min = it.L - it.n + first_tok;               // every row of the tile sees slots up to here
+      const int steps = unit_steps(it, u, P.per_tile);
+      const bool any = it.kv1 > it.kv0;
+      // queries are free for the next item once warpgroup 0 needs nothing of their space either
+      const bool exchange = it.tiles == 1 && it.kv1 - it.kv0 > 1;
+      if (any && !exchange && u == 0 && lane == 0) tc::mbar_arrive(&S.q_empty);
+
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < steps; ++k) {
+        if (!wait(&S.s_full[u], n_s & 1)) break;
+        ++n_s;
+        const int t0 = unit_tile(it, u, k) * kTile;
+        float s[kTile];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tc::tmem_ld32_nowait(t_s + x * 32, reinterpret_cast<uint32_t*>(s) + x * 32);
+        tc::tmem_ld_wait();
+        if (t0 + kTile - 1 > vis_min) {
+          const int lim = vis - t0;
+#pragma unroll
+          for (int x = 0; x < kTile; ++x) s[x] = x > lim ? -INFINITY : s[x];
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int x = 4; x < kTile; x += 8) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mx[y] = x + 4 + y < kTile ? fmaxf(mx[y], fmaxf(s[x + y], s[x + 4 + y])) : fmaxf(mx[y], s[x + y]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool raise = top > m + kRaise;                     // true on the first finite score
+        if (__any_sync(0xffffffffu, raise)) {
+          const float mn = raise ? top : m;
+          const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - mn);
+          m = mn;
+          l *= f;
+          if (k > 0) {   // s_full also says that the product before it, into O, has completed
+#pragma unroll
+            for (int x = 0; x < DH / 32; ++x) {
+              uint32_t o[32];
+              tc::tmem_ld32_nowait(t_o + x * 32, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tc::tmem_st32(t_o + x * 32, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;             // nothing seen yet: every p is 2^-inf = 0
+        const uint64_t n2 = pair(neg, neg);
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t p[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            const float2 e = unpair(fma2(pair(s[x * 32 + 2 * y], s[x * 32 + 2 * y + 1]), c2, n2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            sum2[y & 1] = add2(sum2[y & 1], pair(p0, p1));
+            p[y] = pack2<BF16>(p0, p1);
+          }
+          tc::tmem_st16(t_s + x * 16, p);
+          if (x & 1) {                                           // 64 tokens' weights: the product may begin
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&S.p_full[u][x >> 1]);
+          }
+        }
+        const float2 z = unpair(add2(sum2[0], sum2[1]));
+        l += z.x + z.y;
+      }
+      if (!ok) break;
+
+      // the unit's row: O / l, or its partial
+      if (steps > 0) {
+        if (!wait(&S.o_full[u], n_o & 1)) break;
+        ++n_o;
+      }
+      float* xs = reinterpret_cast<float*>(smem);                // [d / 4][128 rows][4] in the queries' space
+      if (exchange && u == 1) {
+#pragma unroll
+        for (int x = 0; x < DH / 32; ++x) {
+          uint32_t o[32];
+          tc::tmem_ld32_nowait(t_o + x * 32, o);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            *reinterpret_cast<uint4*>(xs + ((x * 8 + y) * kTile + r) * 4) =
+                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
+        S.ml[r] = make_float2(m, l);
+        tc::fence_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.x_full);
+        continue;
+      }
+      if (it.tiles == 1 && u == 1) continue;                     // a single step: unit 0 has all of it
+      float f0 = 1.f, f1 = 0.f;
+      if (exchange) {
+        if (!wait(&S.x_full, n_x & 1)) break;
+        ++n_x;
+        const float2 o1 = S.ml[r];
+        const float mn = fmaxf(m, o1.x), b0 = mn == -INFINITY ? 0.f : mn;
+        f0 = exp2f(m - b0);
+        f1 = exp2f(o1.x - b0);
+        l = fmaf(l, f0, o1.y * f1);
+        m = mn;
+      }
+      const int64_t row = (int64_t)(it.q0 + tok) * a.n_heads + it.h * a.g + r % a.g;
+      const int64_t slot = ((int64_t)it.split * a.n_kv + it.h) * 2 + tile;
+      if (it.split < 0) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        f0 *= inv;
+        f1 *= inv;
+        if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      } else {
+        a.part_ml[slot * kTile + r] = make_float2(m, l);
+      }
+#pragma unroll
+      for (int x = 0; x < DH / 32; ++x) {
+        float o[32];
+        if (steps > 0) {
+          tc::tmem_ld32_nowait(t_o + x * 32, reinterpret_cast<uint32_t*>(o));
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] *= f0;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0.f;
+        }
+        if (exchange) {
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const float4 v = *reinterpret_cast<const float4*>(xs + ((x * 8 + y) * kTile + r) * 4);
+            o[4 * y] = fmaf(v.x, f1, o[4 * y]);
+            o[4 * y + 1] = fmaf(v.y, f1, o[4 * y + 1]);
+            o[4 * y + 2] = fmaf(v.z, f1, o[4 * y + 2]);
+            o[4 * y + 3] = fmaf(v.w, f1, o[4 * y + 3]);
+          }
+        }
+        if (it.split >= 0) {
+          float4* po = reinterpret_cast<float4*>(a.part_o) + (slot * (DH / 4) + x * 8) * kTile + r;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) po[y * kTile] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        } else if (live) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * DH + x * 32);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            out[y] = make_uint4(pack2<BF16>(o[8 * y], o[8 * y + 1]), pack2<BF16>(o[8 * y + 2], o[8 * y + 3]),
+                                pack2<BF16>(o[8 * y + 4], o[8 * y + 5]), pack2<BF16>(o[8 * y + 6], o[8 * y + 7]));
+        }
+      }
+      tc::tc_fence_before();
+      if (exchange) {                                            // the queries' space is read: TMA may fill it again
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.q_empty);
+      }
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (threadIdx.x == 0 && *abort_flag) record_error(a.err, kCodeTimeout, kErrWait, blockIdx.x, 0);
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const KvTcPlan& t, cudaStream_t st) {
+  const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  TcParams P{};
+  P.a = a;
+  P.plan = t;
+  P.per_tile = kTile / a.g;
+  const int64_t rows = a.pages.n_pages * a.pages.page_size * a.n_kv;
+  P.oob_row = rows;
+  P.wait_ns = 1000000000ull;
+  CUtensorMap tm_q, tm_k, tm_v;
+  {
+    // queries [token][head][d]: boxes of 64 columns, one group's heads, a tile's tokens
+    const cuuint64_t dims[3] = {DH, (cuuint64_t)a.n_heads, (cuuint64_t)a.rows.n_tokens};
+    const cuuint64_t strides[2] = {DH * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)P.per_tile};
+    if (!tma_encode(&tm_q, dt, 3, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  }
+  {
+    // cached head rows [slot][kv head][d] as one list of rows, gathered four at a time
+    const cuuint64_t dims[2] = {DH, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {DH * 2};
+    const cuuint32_t box[2] = {64, 1};
+    if (!tma_encode(&tm_k, dt, 2, a.pages.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    if (!tma_encode(&tm_v, dt, 2, a.pages.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  }
+  auto kern = kv_attend_tc_kernel<DH, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DH>::kSmem);
+  if (e != cudaSuccess) return e;
+  kv_plan_kernel<<<1, kPlanThreads, 0, st>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
+  kern<<<(unsigned)(most < t.sm_count ? most : t.sm_count), kThreads, Lay<DH>::kSmem, st>>>(tm_q, tm_k, tm_v, P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  kv_join_kernel<DH, BF16><<<2 * t.sm_count, 128, 0, st>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attend_tc(const KvAttendArgs& a, const KvTcPlan& t, cudaStream_t st) {
+  if (!tma_available()) return cudaErrorNotSupported;
+  if (a.head_dim == 128) return a.bf16 ? launch_tc<128, true>(a, t, st) : launch_tc<128, false>(a, t, st);
+  return a.bf16 ? launch_tc<64, true>(a, t, st) : launch_tc<64, false>(a, t, st);
+}
+
+}  // namespace palu

@@ -12,13 +12,21 @@ namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Split partials of a call: a unit that is cut into ranges takes one slot a range. Plans keep to
-// kPartSlots in all (a few waves of CTAs on any current GPU), so the workspace does not grow with the call.
-constexpr int kPartSlots = 2048;
+// Split partials of a call: a unit that is cut into ranges takes one slot a range. Plans keep to these
+// numbers (a few waves of CTAs), so the workspace does not grow with the call. The two kernels' partials
+// share the space.
+constexpr int kPartSlots = 2048;   // few rows: ranges of 16 query rows
+constexpr int kTcSlots = 456;      // tensor-core kernel: pieces x key/value heads, of two 128-row tiles
 
 struct KvLayout {
-  size_t err, counters, part_ml, part_o, total;
+  size_t err, counters, part_ml, part_o, head, items, joins, row_base, total;
 };
+
+// tiles (or pairs of tiles) that n_tokens packed new tokens of `batch` rows make at most
+int64_t tc_tile_cap(const palu_kv_desc& d, int64_t n_tokens, int64_t batch) {
+  const int64_t per = 2 * (kKvTcRows / (d.n_heads / d.n_kv_heads));
+  return (n_tokens + per - 1) / per + batch;
+}
 
 KvLayout kv_layout(const palu_kv_desc& d) {
   KvLayout L{};
@@ -26,12 +34,23 @@ KvLayout kv_layout(const palu_kv_desc& d) {
   L.err = off;
   off = align256(off + 256);
   if (d.dtype != PALU_F32) {
+    const size_t few = (size_t)kPartSlots * kKvFewRows, tc = (size_t)kTcSlots * 2 * kKvTcRows;
+    const size_t rows = few > tc ? few : tc;
+    const size_t cap = (size_t)tc_tile_cap(d, d.max_tokens, d.max_batch);
     L.counters = off;
     off = align256(off + kPartSlots * sizeof(unsigned));
     L.part_ml = off;
-    off = align256(off + (size_t)kPartSlots * kKvFewRows * sizeof(float2));
+    off = align256(off + rows * sizeof(float2));
     L.part_o = off;
-    off = align256(off + (size_t)kPartSlots * kKvFewRows * d.head_dim * sizeof(float));
+    off = align256(off + rows * d.head_dim * sizeof(float));
+    L.head = off;
+    off = align256(off + sizeof(KvPlanHead));
+    L.items = off;
+    off = align256(off + (cap + kTcSlots) * sizeof(KvItem));
+    L.joins = off;
+    off = align256(off + kTcSlots * sizeof(KvJoin));
+    L.row_base = off;
+    off = align256(off + ((size_t)d.max_batch + 1) * sizeof(int));
   }
   L.total = off;
   return L;
@@ -307,23 +326,39 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
   a.part_ml = reinterpret_cast<float2*>(h->ws + h->L.part_ml);
   a.counters = reinterpret_cast<unsigned*>(h->ws + h->L.counters);
   a.err = reinterpret_cast<ErrWord*>(h->ws + h->L.err);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // One 16-row tile holds every row's queries: the few-row kernel streams the cache once. More rows: the
+  // tensor-core kernel (see there for the sizes at which each was measured).
+  const int64_t cached_rows = a.pages.n_pages * a.pages.page_size * a.n_kv;
+  if ((int64_t)a.rows.max_new * a.g > kKvFewRows && cached_rows < (int64_t(1) << 31) - 1) {
+    KvTcPlan t{};
+    t.head = reinterpret_cast<KvPlanHead*>(h->ws + h->L.head);
+    t.items = reinterpret_cast<KvItem*>(h->ws + h->L.items);
+    t.joins = reinterpret_cast<KvJoin*>(h->ws + h->L.joins);
+    t.row_base = reinterpret_cast<int*>(h->ws + h->L.row_base);
+    t.tile_cap = (int)tc_tile_cap(d, rows->n_tokens, rows->batch);
+    t.slots = kTcSlots;
+    t.sm_count = h->sm_count;
+    const cudaError_t e = launch_kv_attend_tc(a, t, s);
+    return e == cudaSuccess ? PALU_OK : e == cudaErrorNotSupported ? PALU_ERR_UNSUPPORTED : PALU_ERR_CUDA;
+  }
   // Ranges of a unit: enough CTAs to fill the GPU in whole waves, each range worth its start and join.
   const int64_t units = (((int64_t)a.rows.max_new * a.g + kKvFewRows - 1) / kKvFewRows) * a.n_kv * a.rows.batch;
   if (units >= (int64_t(1) << 31)) return PALU_ERR_UNSUPPORTED;
   const int64_t steps = (a.rows.max_kv_len + kKvFewStep - 1) / kKvFewStep;
   int64_t best = 1;
   double least = 1e300;
-  for (int64_t s = 1; s <= steps && s * units <= kPartSlots; ++s) {
-    const int64_t per = (steps + s - 1) / s;
-    if ((steps + per - 1) / per != s) continue;
-    const double est = double((units * s + h->sm_count - 1) / h->sm_count) * double(per + 2);
+  for (int64_t k = 1; k <= steps && k * units <= kPartSlots; ++k) {
+    const int64_t per = (steps + k - 1) / k;
+    if ((steps + per - 1) / per != k) continue;
+    const double est = double((units * k + h->sm_count - 1) / h->sm_count) * double(per + 2);
     if (est < least - 1e-9) {
       least = est;
-      best = s;
+      best = k;
     }
   }
   a.n_splits = (int)best;
-  const cudaError_t e = launch_kv_attend_few(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv_attend_few(a, s);
   return e == cudaSuccess ? PALU_OK : PALU_ERR_CUDA;
 }
 
