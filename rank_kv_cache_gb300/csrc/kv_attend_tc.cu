@@ -78,7 +78,9 @@ struct TcParams {
   KvAttendArgs a;
   KvTcPlan plan;
   int per_tile;        // tokens of a 128-row tile: floor(128 / g)
-  int64_t oob_row;     // a row index outside the tensor maps
+  int box;             // cached tokens a TMA box takes: 8 .. 128, a power of two; 0: rows are gathered
+  int64_t oob_row;     // a row index outside the gather maps, and a slot outside the box maps
+  int64_t oob_slot;
   uint64_t wait_ns;
 };
 
@@ -337,7 +339,8 @@ __device__ __forceinline__ int unit_tile(const Item& it, int u, int k) {
 template <int DH, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const TcParams P) {
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kb,
+                        const __grid_constant__ CUtensorMap tm_vb, const TcParams P) {
   using Y = Lay<DH>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       // ------------------------------------------------------------------ loader
       const int total = P.plan.head->n_items * a.n_kv;
-      const int oob = int(P.oob_row);
+      const int oob = int(P.oob_row), box = P.box, n_box = box ? kTile / box : 0;
       int seq = 0, loads_q = 0;
       bool ok = true;
       if (lane == 0) {
@@ -417,35 +420,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++loads_q;
         __syncwarp();
-        auto load = [&](const CUtensorMap* m, int j) {
+        // One tile of 128 cached tokens: boxes of `box` tokens where they lie in one page below the length, and
+        // rows gathered four at a time where not (the box that holds the length's end; pages of odd sizes).
+        auto load = [&](const CUtensorMap* m, const CUtensorMap* mb, int j) {
+          const int t0 = j * kTile;
+          int slot = -1;                       // this lane's box
+          const int tb = t0 + lane * box;
+          if (lane < n_box && tb < it.L) {
+            slot = int(kv_slot(a.rows, a.pages, b, tb));
+            if (slot < 0) record_error(a.err, kCodeDevice, kErrPage, tb, b);
+          }
+          // the rows to gather: all without boxes, else those of the box that the length ends in
+          const int g0 = box == 0 ? t0 : it.L / box * box, g1 = box == 0 ? t0 + kTile : it.L % box ? g0 + box : g0;
+          const bool gather = g0 < g1 && g0 < t0 + kTile && g1 > t0;
           int r[4];
+          if (gather) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = j * kTile + lane * 4 + e;
-            r[e] = oob;
-            if (t < it.L) {
-              const int64_t s = kv_slot(a.rows, a.pages, b, t);
-              if (s >= 0) r[e] = int(s) * a.n_kv + it.h;
-              else record_error(a.err, kCodeDevice, kErrPage, t, b);
+            for (int e = 0; e < 4; ++e) {
+              const int t = g0 + lane * 4 + e;
+              r[e] = oob;
+              if (t < g1 && t < it.L) {
+                const int64_t s = kv_slot(a.rows, a.pages, b, t);
+                if (s >= 0) r[e] = int(s) * a.n_kv + it.h;
+                else record_error(a.err, kCodeDevice, kErrPage, t, b);
+              }
             }
           }
           const int st = seq % Y::kStages;
-          ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.empty[st], ((seq / Y::kStages) & 1) ^ 1, abort_flag, P.wait_ns));
+          ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.empty[st], ((seq / Y::kStages) & 1) ^ 1, abort_flag,
+                                                             P.wait_ns));
           if (!ok) return;
           if (lane == 0) tc::mbar_arrive_expect_tx(&S.full[st], Y::kTileB);
           __syncwarp();
-          uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB + lane * 512;
+          uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB;
+          if (lane < n_box && !(gather && tb == g0)) {
 #pragma unroll
-          for (int c = 0; c < DH / 64; ++c)
-            tc::tma_gather4(dst + c * Y::kHalf, m, &S.full[st], c * 64, r[0], r[1], r[2], r[3]);
+            for (int c = 0; c < DH / 64; ++c)
+              tc::tma_load_3d(dst + c * Y::kHalf + lane * box * 128, mb, &S.full[st], c * 64, it.h,
+                              slot < 0 ? int(P.oob_slot) : slot);
+          }
+          if (gather && g0 + lane * 4 < g1) {
+#pragma unroll
+            for (int c = 0; c < DH / 64; ++c)
+              tc::tma_gather4(dst + c * Y::kHalf + (g0 - t0 + lane * 4) * 128, m, &S.full[st], c * 64, r[0], r[1], r[2],
+                              r[3]);
+          }
           ++seq;
         };
         // the order in which the products take them: K runs one tile ahead of V, two where the units alternate
         const int lead = it.tiles == 1 ? 2 : 1;
-        for (int j = it.kv0; ok && j < min(it.kv0 + lead, it.kv1); ++j) load(&tm_k, j);
+        for (int j = it.kv0; ok && j < min(it.kv0 + lead, it.kv1); ++j) load(&tm_k, &tm_kb, j);
         for (int j = it.kv0; ok && j < it.kv1; ++j) {
-          load(&tm_v, j);
-          if (ok && j + lead < it.kv1) load(&tm_k, j + lead);
+          load(&tm_v, &tm_vb, j);
+          if (ok && j + lead < it.kv1) load(&tm_k, &tm_kb, j + lead);
         }
       }
       if (!ok) {   // copies still in flight must land before the CTA exits
@@ -782,7 +809,7 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
   const int64_t rows = a.pages.n_pages * a.pages.page_size * a.n_kv;
   P.oob_row = rows;
   P.wait_ns = 1000000000ull;
-  CUtensorMap tm_q, tm_k, tm_v;
+  CUtensorMap tm_q, tm_k, tm_v, tm_kb, tm_vb;
   {
     // queries [token][head][d]: boxes of 64 columns, one group's heads, a tile's tokens
     const cuuint64_t dims[3] = {DH, (cuuint64_t)a.n_heads, (cuuint64_t)a.rows.n_tokens};
@@ -795,6 +822,17 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
     const cuuint64_t dims[2] = {DH, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {DH * 2};
     const cuuint32_t box[2] = {64, 1};
+    P.oob_slot = a.pages.n_pages * a.pages.page_size;
+    const cuuint64_t bdims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)P.oob_slot};
+    const cuuint64_t bstrides[2] = {DH * 2, (cuuint64_t)a.n_kv * DH * 2};
+    // a box must lie in one page: without a table a row is one page, else the largest power of two that divides it
+    int box_tokens = a.rows.page_table ? a.pages.page_size & -a.pages.page_size : kTile;
+    box_tokens = box_tokens > kTile ? kTile : box_tokens;
+    P.box = box_tokens >= 8 ? box_tokens : 0;
+    const cuuint32_t bbox[3] = {64, 1, (cuuint32_t)(P.box ? P.box : 8)};
+    if (!tma_encode(&tm_kb, dt, 3, a.pages.k, bdims, bstrides, bbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tma_encode(&tm_vb, dt, 3, a.pages.v, bdims, bstrides, bbox, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
     if (!tma_encode(&tm_k, dt, 2, a.pages.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     if (!tma_encode(&tm_v, dt, 2, a.pages.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
   }
@@ -805,7 +843,7 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
-  kern<<<(unsigned)(most < t.sm_count ? most : t.sm_count), kThreads, Lay<DH>::kSmem, st>>>(tm_q, tm_k, tm_v, P);
+  kern<<<(unsigned)(most < t.sm_count ? most : t.sm_count), kThreads, Lay<DH>::kSmem, st>>>(tm_q, tm_k, tm_v, tm_kb, tm_vb, P);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   kv_join_kernel<DH, BF16><<<2 * t.sm_count, 128, 0, st>>>(P);
