@@ -13,12 +13,13 @@
 // counter (which item runs where does not change any sum). kv_join_kernel joins the ranges of items
 // that were cut, in their order.
 //
-// One CTA: two softmax warpgroups, a loader warp and an MMA warp.
-//   * The loader gathers the cached rows of 128 tokens by TMA, four a copy, at the slots that the page
-//     table gives, into a ring of K and V tiles (128-byte swizzle). Tokens past the row's length are
-//     rows outside the tensor map: they arrive as zeros, so pages of any size may end anywhere and
-//     what lies behind the length is never read.
-//   * The MMA thread issues S = Q K^T (both operands in shared memory) and O += P V (P in tensor
+// One CTA: two softmax warpgroups, two loader warps and an MMA warp.
+//   * The loaders bring 128 cached tokens at a time by TMA into a ring of K and V tiles (128-byte
+//     swizzle): boxes of the tokens of a page, at the slots that the page table gives, and around the
+//     row's length rows gathered four a copy. Tokens past the length are rows outside the tensor map:
+//     they arrive as zeros, so pages of any size may end anywhere and what lies behind the length is
+//     never read.
+//   * The MMA warp issues S = Q K^T (both operands in shared memory) and O += P V (P in tensor
 //     memory, V as stored, along the head dimension), alternating between two units, so that one
 //     unit's product runs while the other's softmax does.
 //   * A unit is a warpgroup with a 128-row S and O accumulator in tensor memory; a thread owns a query
@@ -41,7 +42,7 @@ namespace palu {
 namespace {
 
 constexpr int kTile = 128;               // query rows of a tile, cached tokens of a step
-constexpr int kThreads = 384;            // two softmax warpgroups; loader, MMA and two idle warps
+constexpr int kThreads = 384;            // two softmax warpgroups; two loader warps, MMA and an idle warp
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTiles = 4096;         // tiles the plan weighs for cutting; longer lists are not cut
 // Registers: launched with 168 a thread (65536 / 384, in eights); 2 * 128 * 208 + 128 * 88 = 384 * 168.
@@ -59,7 +60,7 @@ template <int DH> struct Lay {
 };
 
 struct Item {
-  int q0, n, L, tok0, tiles, kv0, kv1, split, h;
+  int q0, n, L, tok0, tiles, kv0, kv1, split, h, b;
 };
 
 struct Shared {
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&S.o_full[u], 1);
       for (int k = 0; k < 2; ++k) tc::mbar_init(&S.p_full[u][k], 4);
       tc::mbar_init(&S.item_full[u], 1);
-      tc::mbar_init(&S.item_empty[u], 9);      // eight softmax warps, the MMA thread
+      tc::mbar_init(&S.item_empty[u], 10);     // eight softmax warps, the MMA warp, the value loader
     }
     S.abort_flag = 0;
     tc::fence_barrier_init();
@@ -379,59 +380,79 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     tc::regs_shrink<kRegsOther>();
-    if (warp == 8) {
-      // ------------------------------------------------------------------ loader
+    if (warp == 8 || warp == 10) {
+      // ------------------------------------------------------------------ loaders
+      // Warp 8 takes the items and loads Q and K, warp 10 V. Both count every stage of the ring, in the order
+      // in which the products take them: K runs one tile ahead of V, two where the units alternate. Copies are
+      // issued by one lane with uniform operands: 32 lanes issuing their own took 90 ns a copy.
+      const bool keys = warp == 8;
+      const CUtensorMap* rows_map = keys ? &tm_k : &tm_v;
+      const CUtensorMap* box_map = keys ? &tm_kb : &tm_vb;
       const int total = P.plan.head->n_items * a.n_kv;
       const int oob = int(P.oob_row), box = P.box, n_box = box ? kTile / box : 0;
-      int seq = 0, loads_q = 0;
+      int st = 0, loads_q = 0, seq = 0;    // the ring's next stage; stages counted
+      uint32_t par = 1, mine = 0;          // what `empty` is waited for; which of the last stages this warp filled
       bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, phase, abort_flag, P.wait_ns));
+        return ok;
+      };
       if (lane == 0) {
-        tc::tma_prefetch(&tm_q);
-        tc::tma_prefetch(&tm_k);
-        tc::tma_prefetch(&tm_v);
+        if (keys) tc::tma_prefetch(&tm_q);
+        tc::tma_prefetch(rows_map);
+        tc::tma_prefetch(box_map);
       }
       for (int i = 0; ok; ++i) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.item_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, P.wait_ns));
-        if (!ok) break;
-        int idx = 0;
-        if (lane == 0) idx = (int)atomicAdd(&P.plan.head->next, 1u);
-        idx = __shfl_sync(0xffffffffu, idx, 0);
         Item it{};
-        int b = 0;
-        if (idx < total) {
-          const KvItem e = P.plan.items[idx / a.n_kv];
-          it = Item{e.q0, e.n, e.L, e.tok0, e.tiles, e.kv0, e.kv1, e.split, idx % a.n_kv};
-          b = e.b;
+        if (keys) {
+          if (!wait(&S.item_empty[i & 1], ((i >> 1) & 1) ^ 1)) break;
+          int idx = 0;
+          if (lane == 0) idx = (int)atomicAdd(&P.plan.head->next, 1u);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
+          if (idx < total) {
+            const KvItem e = P.plan.items[idx / a.n_kv];
+            it = Item{e.q0, e.n, e.L, e.tok0, e.tiles, e.kv0, e.kv1, e.split, idx % a.n_kv, e.b};
+          }
+          if (lane == 0) {
+            S.item[i & 1] = it;
+            tc::mbar_arrive(&S.item_full[i & 1]);
+          }
+        } else {
+          if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
+          it = S.item[i & 1];
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&S.item_empty[i & 1]);
         }
-        if (lane == 0) {
-          S.item[i & 1] = it;
-          tc::mbar_arrive(&S.item_full[i & 1]);
+        const int b = __shfl_sync(0xffffffffu, it.b, 0), L = __shfl_sync(0xffffffffu, it.L, 0);
+        const int h = __shfl_sync(0xffffffffu, it.h, 0), tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+        const int kv0 = __shfl_sync(0xffffffffu, it.kv0, 0), kv1 = __shfl_sync(0xffffffffu, it.kv1, 0);
+        if (tiles == 0) break;
+        if (kv1 == kv0) continue;
+        if (keys) {
+          if (!wait(&S.q_empty, (loads_q & 1) ^ 1)) break;
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(tiles) * P.per_tile * a.g * DH * 2);
+            for (int t = 0; t < tiles; ++t)
+              for (int c = 0; c < DH / 64; ++c)
+                tc::tma_load_3d(smem + t * Y::kTileB + c * Y::kHalf, &tm_q, &S.q_full, c * 64, h * a.g,
+                                it.q0 + it.tok0 + t * P.per_tile);
+          }
+          ++loads_q;
+          __syncwarp();
         }
-        if (idx >= total) break;
-        if (it.kv1 == it.kv0) continue;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.q_empty, (loads_q & 1) ^ 1, abort_flag, P.wait_ns));
-        if (!ok) break;
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(it.tiles) * P.per_tile * a.g * DH * 2);
-          for (int t = 0; t < it.tiles; ++t)
-            for (int c = 0; c < DH / 64; ++c)
-              tc::tma_load_3d(smem + t * Y::kTileB + c * Y::kHalf, &tm_q, &S.q_full, c * 64, it.h * a.g,
-                              it.q0 + it.tok0 + t * P.per_tile);
-        }
-        ++loads_q;
-        __syncwarp();
         // One tile of 128 cached tokens: boxes of `box` tokens where they lie in one page below the length, and
         // rows gathered four at a time where not (the box that holds the length's end; pages of odd sizes).
-        auto load = [&](const CUtensorMap* m, const CUtensorMap* mb, int j) {
+        auto load = [&](int j) {
           const int t0 = j * kTile;
-          int slot = -1;                       // this lane's box
+          int slot = int(P.oob_slot);            // of this lane's box
           const int tb = t0 + lane * box;
-          if (lane < n_box && tb < it.L) {
-            slot = int(kv_slot(a.rows, a.pages, b, tb));
-            if (slot < 0) record_error(a.err, kCodeDevice, kErrPage, tb, b);
+          if (lane < n_box && tb < L) {
+            const int64_t s = kv_slot(a.rows, a.pages, b, tb);
+            if (s >= 0) slot = int(s);
+            else record_error(a.err, kCodeDevice, kErrPage, tb, b);
           }
           // the rows to gather: all without boxes, else those of the box that the length ends in
-          const int g0 = box == 0 ? t0 : it.L / box * box, g1 = box == 0 ? t0 + kTile : it.L % box ? g0 + box : g0;
+          const int g0 = box == 0 ? t0 : L / box * box, g1 = box == 0 ? t0 + kTile : L % box ? g0 + box : g0;
           const bool gather = g0 < g1 && g0 < t0 + kTile && g1 > t0;
           int r[4];
           if (gather) {
@@ -439,170 +460,200 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) {
               const int t = g0 + lane * 4 + e;
               r[e] = oob;
-              if (t < g1 && t < it.L) {
+              if (t < g1 && t < L) {
                 const int64_t s = kv_slot(a.rows, a.pages, b, t);
-                if (s >= 0) r[e] = int(s) * a.n_kv + it.h;
+                if (s >= 0) r[e] = int(s) * a.n_kv + h;
                 else record_error(a.err, kCodeDevice, kErrPage, t, b);
               }
             }
           }
-          const int st = seq % Y::kStages;
-          ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&S.empty[st], ((seq / Y::kStages) & 1) ^ 1, abort_flag,
-                                                             P.wait_ns));
-          if (!ok) return;
-          if (lane == 0) tc::mbar_arrive_expect_tx(&S.full[st], Y::kTileB);
-          __syncwarp();
+          if (!wait(&S.empty[st], par)) return;
           uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB;
-          if (lane < n_box && !(gather && tb == g0)) {
+          if (tc::elect_one()) tc::mbar_arrive_expect_tx(&S.full[st], Y::kTileB);
+          __syncwarp();
+          const int skip = gather && box ? (g0 - t0) / box : -1;
+          for (int x = 0; x < n_box; ++x) {
+            const int sx = __shfl_sync(0xffffffffu, slot, x);
+            if (x != skip && tc::elect_one()) {
 #pragma unroll
-            for (int c = 0; c < DH / 64; ++c)
-              tc::tma_load_3d(dst + c * Y::kHalf + lane * box * 128, mb, &S.full[st], c * 64, it.h,
-                              slot < 0 ? int(P.oob_slot) : slot);
+              for (int c = 0; c < DH / 64; ++c)
+                tc::tma_load_3d(dst + c * Y::kHalf + x * box * 128, box_map, &S.full[st], c * 64, h, sx);
+            }
+            __syncwarp();
           }
-          if (gather && g0 + lane * 4 < g1) {
+          if (gather) {
+            uint8_t* gd = dst + (g0 - t0) * 128;
+            for (int x = 0; x < (g1 - g0) / 4; ++x) {
+              const int r0 = __shfl_sync(0xffffffffu, r[0], x), r1 = __shfl_sync(0xffffffffu, r[1], x);
+              const int r2 = __shfl_sync(0xffffffffu, r[2], x), r3 = __shfl_sync(0xffffffffu, r[3], x);
+              if (tc::elect_one()) {
 #pragma unroll
-            for (int c = 0; c < DH / 64; ++c)
-              tc::tma_gather4(dst + c * Y::kHalf + (g0 - t0 + lane * 4) * 128, m, &S.full[st], c * 64, r[0], r[1], r[2],
-                              r[3]);
+                for (int c = 0; c < DH / 64; ++c)
+                  tc::tma_gather4(gd + c * Y::kHalf + x * 512, rows_map, &S.full[st], c * 64, r0, r1, r2, r3);
+              }
+              __syncwarp();
+            }
           }
-          ++seq;
+          mine |= 1u;
         };
-        // the order in which the products take them: K runs one tile ahead of V, two where the units alternate
-        const int lead = it.tiles == 1 ? 2 : 1;
-        for (int j = it.kv0; ok && j < min(it.kv0 + lead, it.kv1); ++j) load(&tm_k, &tm_kb, j);
-        for (int j = it.kv0; ok && j < it.kv1; ++j) {
-          load(&tm_v, &tm_vb, j);
-          if (ok && j + lead < it.kv1) load(&tm_k, &tm_kb, j + lead);
+        auto step = [&](bool k_tile, int j) {
+          mine <<= 1;
+          ++seq;
+          if (k_tile == keys) load(j);
+          if (++st == Y::kStages) {
+            st = 0;
+            par ^= 1;
+          }
+        };
+        const int lead = min(tiles == 1 ? 2 : 1, kv1 - kv0);
+        for (int j = kv0; ok && j < kv0 + lead; ++j) step(true, j);
+        for (int j = kv0; ok && j < kv1; ++j) {
+          step(false, j);
+          if (ok && j + lead < kv1) step(true, j + lead);
         }
       }
       if (!ok) {   // copies still in flight must land before the CTA exits
         volatile int quiet = 0;
-        for (int s = max(0, seq - Y::kStages); s < seq; ++s)
-          tc::mbar_wait_bounded(&S.full[s % Y::kStages], (s / Y::kStages) & 1, &quiet, P.wait_ns / 10);
+        for (int d = 0; d < Y::kStages && d < seq; ++d) {
+          const int p = seq - 1 - d;
+          if (mine >> d & 1u) tc::mbar_wait_bounded(&S.full[p % Y::kStages], (p / Y::kStages) & 1, &quiet, P.wait_ns / 10);
+        }
         if (loads_q) tc::mbar_wait_bounded(&S.q_full, (loads_q - 1) & 1, &quiet, P.wait_ns / 10);
       }
     } else if (warp == 9) {
       // ------------------------------------------------------------------ MMA
-      if (lane == 0) {
-        const uint32_t id_qk = tc::idesc_f16(kTile, kTile, BF16), id_pv = tc::idesc_f16(kTile, DH, BF16) | tc::kIdescBMajorMN;
-        const uint32_t base = tc::smem_addr(smem);
-        int seq = 0, loads_q = 0, np[2] = {0, 0};
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t par) {
-          if (ok) ok = tc::mbar_wait_bounded(bar, par, abort_flag, P.wait_ns);
-          tc::tc_fence_after();
-          return ok;
-        };
-        for (int i = 0; ok; ++i) {
-          if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
-          const Item it = S.item[i & 1];
-          tc::mbar_arrive(&S.item_empty[i & 1]);
-          if (it.tiles == 0) break;
-          if (it.kv1 == it.kv0) continue;
-          if (!wait(&S.q_full, loads_q & 1)) break;
-          ++loads_q;
-          const int steps[2] = {unit_steps(it, 0, P.per_tile), unit_steps(it, 1, P.per_tile)};
-          auto qk = [&](int u, int st) {
-            const uint32_t qa = base + (it.tiles == 2 ? u * Y::kTileB : 0), ka = base + Y::kOffKv + st * Y::kTileB;
+      // The whole warp walks the loop, so that stages and descriptors stay in uniform registers, and one lane
+      // issues: from a branch of one thread each product took 80 cycles to issue, longer than it runs.
+      const uint32_t id_qk = tc::idesc_f16(kTile, kTile, BF16);
+      const uint32_t id_pv = tc::idesc_f16(kTile, DH, BF16) | tc::kIdescBMajorMN;
+      const uint32_t base = tc::smem_addr(smem);
+      const uint64_t dq = tc::sdesc_k_sw128(base), dk = tc::sdesc_k_sw128(base + Y::kOffKv);
+      const uint64_t dv = tc::sdesc_mn_sw128(base + Y::kOffKv, Y::kHalf);
+      int st = 0, loads_q = 0;           // the ring's stage that comes next
+      uint32_t par = 0, np[2] = {0, 0};  // its phase; the weights' phases of the units
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, phase, abort_flag, P.wait_ns));
+        tc::tc_fence_after();
+        return ok;
+      };
+      auto stage = [&]() -> int {        // waits for the next stage of the ring and takes it
+        const int s = st;
+        wait(&S.full[s], par);
+        if (++st == Y::kStages) {
+          st = 0;
+          par ^= 1;
+        }
+        return s;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (tc::elect_one()) tc::umma_commit(bar);
+      };
+      auto qk = [&](int u, uint64_t q, int s) {                  // S_u = Q K^T
+        const uint64_t k0 = dk + uint64_t(s) * (Y::kTileB >> 4);
+        if (tc::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < DH / 16; ++k) {
-              const uint32_t off = (k / 4) * Y::kHalf + (k % 4) * 32;
-              tc::umma_f16(tmem + u * kTile, tc::sdesc_k_sw128(qa + off), tc::sdesc_k_sw128(ka + off), id_qk, k != 0);
-            }
-            tc::umma_commit(&S.s_full[u]);
-          };
-          auto pv = [&](int u, int st, bool first) {
-            const uint32_t va = base + Y::kOffKv + st * Y::kTileB;
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint64_t off = ((k / 4) * Y::kHalf + (k % 4) * 32) >> 4;
+            tc::umma_f16(tmem + u * kTile, q + off, k0 + off, id_qk, k != 0);
+          }
+          tc::umma_commit(&S.s_full[u]);
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int u, int s, bool first) {                  // O_u += P_u V, the first half's weights first
+        const uint64_t v0 = dv + uint64_t(s) * (Y::kTileB >> 4);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!wait(&S.p_full[u][half], np[u] & 1)) return;
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(&S.p_full[u][half], np[u])) return;
+          if (tc::elect_one()) {
 #pragma unroll
-              for (int k = half * 4; k < half * 4 + 4; ++k)
-                tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8,
-                                tc::sdesc_mn_sw128(va + k * 2048, Y::kHalf), id_pv, !first || k != 0);
-            }
-            ++np[u];
-          };
-          auto free_stage = [&](int st) { tc::umma_commit(&S.empty[st]); };
-          auto done = [&](int u) { tc::umma_commit(&S.o_full[u]); };
-          auto stage_wait = [&]() -> int {
-            const int st = seq % Y::kStages;
-            wait(&S.full[st], (seq / Y::kStages) & 1);
-            return st;
-          };
-          if (it.tiles == 2) {
-            int st = stage_wait();
+            for (int k = half * 4; k < half * 4 + 4; ++k)
+              tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, v0 + ((k * 2048) >> 4), id_pv,
+                              !first || k != 0);
+          }
+          __syncwarp();
+        }
+        np[u] ^= 1;
+      };
+      for (int i = 0; ok; ++i) {
+        if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
+        Item it = S.item[i & 1];
+        it.L = __shfl_sync(0xffffffffu, it.L, 0);
+        it.n = __shfl_sync(0xffffffffu, it.n, 0);
+        it.tok0 = __shfl_sync(0xffffffffu, it.tok0, 0);
+        it.tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+        it.kv0 = __shfl_sync(0xffffffffu, it.kv0, 0);
+        it.kv1 = __shfl_sync(0xffffffffu, it.kv1, 0);
+        if (lane == 0) tc::mbar_arrive(&S.item_empty[i & 1]);
+        if (it.tiles == 0) break;
+        const int n = it.kv1 - it.kv0;
+        if (n == 0) continue;
+        if (!wait(&S.q_full, loads_q & 1)) break;
+        ++loads_q;
+        if (it.tiles == 2) {
+          // both units over each tile; unit 0 may see fewer (it stops first)
+          const int n0 = unit_steps(it, 0, P.per_tile);
+          const uint64_t dq1 = dq + (Y::kTileB >> 4);
+          int s = stage();
+          if (!ok) break;
+          if (n0 > 0) qk(0, dq, s);
+          qk(1, dq1, s);
+          commit(&S.empty[s]);
+          for (int k = 0; k < n; ++k) {
+            const int sv = stage();
             if (!ok) break;
-            if (steps[0] > 0) qk(0, st);
-            qk(1, st);
-            free_stage(st);
-            ++seq;
-            for (int k = 0; k < steps[1]; ++k) {
-              const bool more = k + 1 < steps[1];
-              const int sv = stage_wait();
-              ++seq;
+            if (k < n0) pv(0, sv, k == 0);
+            if (!ok) break;
+            if (k + 1 == n0) commit(&S.o_full[0]);
+            if (k + 1 < n) {
+              s = stage();
               if (!ok) break;
-              int sk = -1;
-              if (k < steps[0]) {
-                pv(0, sv, k == 0);
-                if (!ok) break;
-                if (k + 1 < steps[0]) {
-                  sk = stage_wait();
-                  if (!ok) break;
-                  qk(0, sk);
-                } else {
-                  done(0);
-                }
-              }
-              pv(1, sv, k == 0);
-              if (!ok) break;
-              free_stage(sv);
-              if (more) {
-                sk = stage_wait();
-                if (!ok) break;
-                qk(1, sk);
-                free_stage(sk);
-                ++seq;
-              } else {
-                done(1);
-              }
+              if (k + 1 < n0) qk(0, dq, s);
             }
-          } else {
-            const int n = it.kv1 - it.kv0;
-            for (int k = 0; k < min(n, 2) && ok; ++k) {
-              const int st = stage_wait();
-              if (!ok) break;
-              qk(k, st);
-              free_stage(st);
-              ++seq;
-            }
-            for (int k = 0; k < n && ok; ++k) {
-              const int u = k & 1;
-              const int sv = stage_wait();
-              ++seq;
-              if (!ok) break;
-              pv(u, sv, k < 2);
-              if (!ok) break;
-              free_stage(sv);
-              if (k + 2 < n) {
-                const int sk = stage_wait();
-                if (!ok) break;
-                qk(u, sk);
-                free_stage(sk);
-                ++seq;
-              } else {
-                done(u);
-              }
+            pv(1, sv, k == 0);
+            if (!ok) break;
+            commit(&S.empty[sv]);
+            if (k + 1 < n) {
+              qk(1, dq1, s);
+              commit(&S.empty[s]);
             }
           }
           if (!ok) break;
-          tc::umma_commit(&S.q_empty);
+          commit(&S.o_full[1]);
+        } else {
+          // the units take the tiles in turn
+          for (int k = 0; k < min(n, 2) && ok; ++k) {
+            const int s = stage();
+            if (!ok) break;
+            qk(k, dq, s);
+            commit(&S.empty[s]);
+          }
+          for (int k = 0; k < n && ok; ++k) {
+            const int u = k & 1;
+            const int sv = stage();
+            if (!ok) break;
+            pv(u, sv, k < 2);
+            if (!ok) break;
+            commit(&S.empty[sv]);
+            if (k + 2 < n) {
+              const int s = stage();
+              if (!ok) break;
+              qk(u, dq, s);
+              commit(&S.empty[s]);
+            } else {
+              commit(&S.o_full[u]);
+            }
+          }
         }
-        // every product issued has completed once this commit lands
-        volatile int quiet = 0;
-        tc::umma_commit(&S.drained);
-        tc::mbar_wait_bounded(&S.drained, 0, &quiet, P.wait_ns);
+        if (!ok) break;
+        commit(&S.q_empty);
       }
+      // every product issued has completed once this commit lands
+      volatile int quiet = 0;
+      commit(&S.drained);
+      __syncwarp();
+      tc::mbar_wait_bounded(&S.drained, 0, &quiet, P.wait_ns);
     }
   } else {
     // ------------------------------------------------------------------ softmax
