@@ -21,7 +21,7 @@
 //     never read.
 //   * The MMA warp issues S = Q K^T (both operands in shared memory) and O += P V (P in tensor
 //     memory, V as stored, along the head dimension), alternating between two units, so that one
-//     unit's product runs while the other's softmax does.
+//     unit's products run while the other's softmax does.
 //   * A unit is a warpgroup with a 128-row S and O accumulator in tensor memory; a thread owns a query
 //     row. P overwrites S in place. The running maximum is only raised when a score exceeds it by more
 //     than 2^8, so that the output in tensor memory is rarely rescaled; p then stays below 2^8, and the
@@ -326,6 +326,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // steps of unit u of an item (its cached tiles), and the tile of its step k
 __device__ __forceinline__ int unit_steps(const Item& it, int u, int per) {
   if (it.tiles == 1) return (it.kv1 - it.kv0 + 1 - u) / 2;
@@ -390,11 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* box_map = keys ? &tm_kb : &tm_vb;
       const int total = P.plan.head->n_items * a.n_kv;
       const int oob = int(P.oob_row), box = P.box, n_box = box ? kTile / box : 0;
+      const int ps = a.pages.page_size, tile_pages = kTile / ps, tile_rest = kTile % ps;
+      const int table_pages = int(a.rows.table_pages);
       int st = 0, loads_q = 0, seq = 0;    // the ring's next stage; stages counted
       uint32_t par = 1, mine = 0;          // what `empty` is waited for; which of the last stages this warp filled
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t phase) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, phase, abort_flag, P.wait_ns));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, phase, abort_flag, P.wait_ns));
         return ok;
       };
       if (lane == 0) {
@@ -428,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kv0 = __shfl_sync(0xffffffffu, it.kv0, 0), kv1 = __shfl_sync(0xffffffffu, it.kv1, 0);
         if (tiles == 0) break;
         if (kv1 == kv0) continue;
+        const int32_t* table = a.rows.page_table ? a.rows.page_table + (int64_t)b * table_pages : nullptr;
         if (keys) {
           if (!wait(&S.q_empty, (loads_q & 1) ^ 1)) break;
           if (lane == 0) {
@@ -442,25 +451,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // One tile of 128 cached tokens: boxes of `box` tokens where they lie in one page below the length, and
         // rows gathered four at a time where not (the box that holds the length's end; pages of odd sizes).
-        auto load = [&](int j) {
-          const int t0 = j * kTile;
-          int slot = int(P.oob_slot);            // of this lane's box
-          const int tb = t0 + lane * box;
+        // A lane looks up the slot of its box one tile ahead: the next tile's is 128 tokens on.
+        const int g0 = box ? L & -box : 0, g1 = box && g0 < L ? g0 + box : g0;   // the box with the length's end
+        int tb = kv0 * kTile + lane * box;
+        int pg = tb / ps, off = tb - pg * ps;
+        auto look = [&]() -> int {
+          int page = table ? -1 : b;
+          if (lane < n_box && tb < L && table && pg < table_pages) page = table[pg];
+          int s = int(P.oob_slot);
           if (lane < n_box && tb < L) {
-            const int64_t s = kv_slot(a.rows, a.pages, b, tb);
-            if (s >= 0) slot = int(s);
+            if (page >= 0 && page < a.pages.n_pages) s = page * ps + off;
             else record_error(a.err, kCodeDevice, kErrPage, tb, b);
           }
-          // the rows to gather: all without boxes, else those of the box that the length ends in
-          const int g0 = box == 0 ? t0 : L / box * box, g1 = box == 0 ? t0 + kTile : L % box ? g0 + box : g0;
-          const bool gather = g0 < g1 && g0 < t0 + kTile && g1 > t0;
+          tb += kTile;
+          pg += tile_pages;
+          off += tile_rest;
+          if (off >= ps) {
+            off -= ps;
+            ++pg;
+          }
+          return s;
+        };
+        int next_slot = box ? look() : 0;
+        auto load = [&](int j) {
+          const int t0 = j * kTile, slot = next_slot;
+          const int lo = box ? g0 : t0, hi = box ? g1 : t0 + kTile;   // the rows to gather
+          const bool gather = lo < hi && lo < t0 + kTile && hi > t0;
           int r[4];
           if (gather) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int t = g0 + lane * 4 + e;
+              const int t = lo + lane * 4 + e;
               r[e] = oob;
-              if (t < g1 && t < L) {
+              if (t < hi && t < L) {
                 const int64_t s = kv_slot(a.rows, a.pages, b, t);
                 if (s >= 0) r[e] = int(s) * a.n_kv + h;
                 else record_error(a.err, kCodeDevice, kErrPage, t, b);
@@ -471,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB;
           if (tc::elect_one()) tc::mbar_arrive_expect_tx(&S.full[st], Y::kTileB);
           __syncwarp();
-          const int skip = gather && box ? (g0 - t0) / box : -1;
+          const int skip = gather && box ? (lo - t0) / box : -1;
           for (int x = 0; x < n_box; ++x) {
             const int sx = __shfl_sync(0xffffffffu, slot, x);
             if (x != skip && tc::elect_one()) {
@@ -482,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (gather) {
-            uint8_t* gd = dst + (g0 - t0) * 128;
-            for (int x = 0; x < (g1 - g0) / 4; ++x) {
+            uint8_t* gd = dst + (lo - t0) * 128;
+            for (int x = 0; x < (hi - lo) / 4; ++x) {
               const int r0 = __shfl_sync(0xffffffffu, r[0], x), r1 = __shfl_sync(0xffffffffu, r[1], x);
               const int r2 = __shfl_sync(0xffffffffu, r[2], x), r3 = __shfl_sync(0xffffffffu, r[3], x);
               if (tc::elect_one()) {
@@ -495,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           mine |= 1u;
+          if (box) next_slot = look();
         };
         auto step = [&](bool k_tile, int j) {
           mine <<= 1;
@@ -523,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
       // ------------------------------------------------------------------ MMA
       // The whole warp walks the loop, so that stages and descriptors stay in uniform registers, and one lane
-      // issues: from a branch of one thread each product took 80 cycles to issue, longer than it runs.
+      // issues: from a branch of one thread each product took 80 cycles to issue, longer than it runs. One warp
+      // issues for both units, in turn: with a warp each, the units fell into step and waited together.
       const uint32_t id_qk = tc::idesc_f16(kTile, kTile, BF16);
       const uint32_t id_pv = tc::idesc_f16(kTile, DH, BF16) | tc::kIdescBMajorMN;
       const uint32_t base = tc::smem_addr(smem);
@@ -531,11 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dv = tc::sdesc_mn_sw128(base + Y::kOffKv, Y::kHalf);
       int st = 0, loads_q = 0;           // the ring's stage that comes next
       uint32_t par = 0, np[2] = {0, 0};  // its phase; the weights' phases of the units
-      bool ok = true;
+      // A wait that gives up only raises the abort flag, at which every later wait gives up at once; the loop
+      // looks at the flag once a tile, so that a wait that need not wait costs little more than its test.
       auto wait = [&](uint64_t* bar, uint32_t phase) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, phase, abort_flag, P.wait_ns));
-        tc::tc_fence_after();
-        return ok;
+        if (!tc::mbar_try_wait(bar, phase)) tc::mbar_wait_short(bar, phase, abort_flag, P.wait_ns);
       };
       auto stage = [&]() -> int {        // waits for the next stage of the ring and takes it
         const int s = st;
@@ -546,38 +570,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return s;
       };
-      auto commit = [&](uint64_t* bar) {
-        if (tc::elect_one()) tc::umma_commit(bar);
-      };
-      auto qk = [&](int u, uint64_t q, int s) {                  // S_u = Q K^T
-        const uint64_t k0 = dk + uint64_t(s) * (Y::kTileB >> 4);
+      auto qk = [&](int u, uint64_t q, int s, bool free) {       // S_u = Q K^T of key stage s
+        const uint64_t kd = dk + uint64_t(s) * (Y::kTileB >> 4);
+        __syncwarp();
+        tc::tc_fence_after();
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < DH / 16; ++k) {
             const uint64_t off = ((k / 4) * Y::kHalf + (k % 4) * 32) >> 4;
-            tc::umma_f16(tmem + u * kTile, q + off, k0 + off, id_qk, k != 0);
+            tc::umma_f16(tmem + u * kTile, q + off, kd + off, id_qk, k != 0);
           }
           tc::umma_commit(&S.s_full[u]);
+          if (free) tc::umma_commit(&S.empty[s]);
         }
-        __syncwarp();
       };
-      auto pv = [&](int u, int s, bool first) {                  // O_u += P_u V, the first half's weights first
-        const uint64_t v0 = dv + uint64_t(s) * (Y::kTileB >> 4);
+      // O_u += P_u V of value stage s, the first half's weights first; `last`: the item's last for the unit
+      auto pv = [&](int u, int s, bool first, bool free, bool last) {
+        const uint64_t vd = dv + uint64_t(s) * (Y::kTileB >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!wait(&S.p_full[u][half], np[u])) return;
+          wait(&S.p_full[u][half], np[u]);
+          __syncwarp();
+          tc::tc_fence_after();
           if (tc::elect_one()) {
 #pragma unroll
             for (int k = half * 4; k < half * 4 + 4; ++k)
-              tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, v0 + ((k * 2048) >> 4), id_pv,
+              tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, vd + ((k * 2048) >> 4), id_pv,
                               !first || k != 0);
+            if (half == 1 && free) tc::umma_commit(&S.empty[s]);
+            if (half == 1 && last) tc::umma_commit(&S.o_full[u]);
           }
-          __syncwarp();
         }
         np[u] ^= 1;
       };
-      for (int i = 0; ok; ++i) {
-        if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
+      auto dead = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
+      for (int i = 0;; ++i) {
+        wait(&S.item_full[i & 1], (i >> 1) & 1);
+        if (dead()) break;
         Item it = S.item[i & 1];
         it.L = __shfl_sync(0xffffffffu, it.L, 0);
         it.n = __shfl_sync(0xffffffffu, it.n, 0);
@@ -589,69 +618,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it.tiles == 0) break;
         const int n = it.kv1 - it.kv0;
         if (n == 0) continue;
-        if (!wait(&S.q_full, loads_q & 1)) break;
+        wait(&S.q_full, loads_q & 1);
         ++loads_q;
         if (it.tiles == 2) {
           // both units over each tile; unit 0 may see fewer (it stops first)
           const int n0 = unit_steps(it, 0, P.per_tile);
           const uint64_t dq1 = dq + (Y::kTileB >> 4);
-          int s = stage();
-          if (!ok) break;
-          if (n0 > 0) qk(0, dq, s);
-          qk(1, dq1, s);
-          commit(&S.empty[s]);
+          int sk = stage();
+          if (n0 > 0) qk(0, dq, sk, false);
+          qk(1, dq1, sk, true);
           for (int k = 0; k < n; ++k) {
+            if (dead()) break;
             const int sv = stage();
-            if (!ok) break;
-            if (k < n0) pv(0, sv, k == 0);
-            if (!ok) break;
-            if (k + 1 == n0) commit(&S.o_full[0]);
+            if (k < n0) pv(0, sv, k == 0, false, k + 1 == n0);
             if (k + 1 < n) {
-              s = stage();
-              if (!ok) break;
-              if (k + 1 < n0) qk(0, dq, s);
+              sk = stage();
+              if (k + 1 < n0) qk(0, dq, sk, false);
             }
-            pv(1, sv, k == 0);
-            if (!ok) break;
-            commit(&S.empty[sv]);
-            if (k + 1 < n) {
-              qk(1, dq1, s);
-              commit(&S.empty[s]);
-            }
+            pv(1, sv, k == 0, true, k + 1 == n);
+            if (k + 1 < n) qk(1, dq1, sk, true);
           }
-          if (!ok) break;
-          commit(&S.o_full[1]);
         } else {
           // the units take the tiles in turn
-          for (int k = 0; k < min(n, 2) && ok; ++k) {
+          for (int k = 0; k < min(n, 2); ++k) {
             const int s = stage();
-            if (!ok) break;
-            qk(k, dq, s);
-            commit(&S.empty[s]);
+            qk(k, dq, s, true);
           }
-          for (int k = 0; k < n && ok; ++k) {
-            const int u = k & 1;
+          for (int k = 0; k < n; ++k) {
+            if (dead()) break;
             const int sv = stage();
-            if (!ok) break;
-            pv(u, sv, k < 2);
-            if (!ok) break;
-            commit(&S.empty[sv]);
+            pv(k & 1, sv, k < 2, true, k + 2 >= n);
             if (k + 2 < n) {
-              const int s = stage();
-              if (!ok) break;
-              qk(u, dq, s);
-              commit(&S.empty[s]);
-            } else {
-              commit(&S.o_full[u]);
+              const int sk = stage();
+              qk(k & 1, dq, sk, true);
             }
           }
         }
-        if (!ok) break;
-        commit(&S.q_empty);
+        __syncwarp();
+        if (tc::elect_one()) tc::umma_commit(&S.q_empty);
       }
+      __syncwarp();
       // every product issued has completed once this commit lands
       volatile int quiet = 0;
-      commit(&S.drained);
+      if (tc::elect_one()) tc::umma_commit(&S.drained);
       __syncwarp();
       tc::mbar_wait_bounded(&S.drained, 0, &quiet, P.wait_ns);
     }
@@ -664,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = tmem + lanes + u * kTile, t_o = tmem + lanes + Y::kColO + u * DH;
     const float c = a.scale_log2;
     const uint64_t c2 = pair(c, c);
-    int n_s = 0, n_o = 0, n_x = 0;
+    int n_s = 0, n_o = 0, n_o0 = 0, n_x = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t par) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, par, abort_flag, P.wait_ns));
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, par, abort_flag, P.wait_ns));
       tc::tc_fence_after();
       return ok;
     };
@@ -703,12 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < kTile; ++x) s[x] = x > lim ? -INFINITY : s[x];
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        float mx[4];
 #pragma unroll
-        for (int x = 4; x < kTile; x += 8) {
+        for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s[y], s[y + 4]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            mx[y] = x + 4 + y < kTile ? fmaxf(mx[y], fmaxf(s[x + y], s[x + 4 + y])) : fmaxf(mx[y], s[x + y]);
+        for (int x = 8; x < kTile; x += 8) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[x + y], s[x + 4 + y]);
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         const bool raise = top > m + kRaise;                     // true on the first finite score
@@ -761,7 +771,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_o;
       }
       float* xs = reinterpret_cast<float*>(smem);                // [d / 4][128 rows][4] in the queries' space
+      if (u == 1 && unit_steps(it, 0, P.per_tile) > 0) ++n_o0;
       if (exchange && u == 1) {
+        if (!wait(&S.o_full[0], (n_o0 - 1) & 1)) break;          // unit 0's products read the queries too
 #pragma unroll
         for (int x = 0; x < DH / 32; ++x) {
           uint32_t o[32];

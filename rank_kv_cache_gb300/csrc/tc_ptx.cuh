@@ -44,6 +44,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* b, uint32_t parity) {
   return ok != 0;
 }
 
+// whether the phase has completed, without waiting
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // try_wait with a suspend-time hint: the thread sleeps until the phase completes or the
 // hint (ns) elapses, instead of spinning and taking issue slots from the warps that work.
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* b, uint32_t parity, uint32_t hint_ns) {
@@ -77,6 +88,26 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
   return ok != 0;
+}
+
+// The same for short waits between the roles of one CTA: the clock, whose reading takes longer than such a wait, is
+// only read after 32 tries without success.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                                uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(b, parity)) return true;
+    if (i % 32 == 0) {
+      if (*abort_flag) return false;
+      const uint64_t t = globaltimer();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > limit_ns) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- TMA
