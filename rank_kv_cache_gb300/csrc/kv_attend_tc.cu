@@ -45,11 +45,13 @@ constexpr int kTile = 128;               // query rows of a tile, cached tokens 
 constexpr int kThreads = 384;            // two softmax warpgroups; two loader warps, MMA and an idle warp
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTiles = 4096;         // tiles the plan weighs for cutting; longer lists are not cut
-// Registers: launched with 168 a thread (65536 / 384, in eights); 2 * 128 * 208 + 128 * 88 = 384 * 168.
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+// Registers: launched with 168 a thread (65536 / 384, in eights); 2 * 128 * 200 + 128 * 104 = 384 * 168.
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr float kRaise = 8.f;            // log2 by which a score may exceed the running maximum
 
 template <int DH> struct Lay {
+  // All tiles: 64 elements (128 bytes) of all rows, then the next 64. (Groups of eight tokens with both blocks
+  // side by side, which one TMA box can bring, were 3 to 5% slower.)
   static constexpr int kHalf = kTile * 128;             // 64 elements of 128 rows
   static constexpr int kTileB = kHalf * (DH / 64);
   static constexpr int kStages = DH == 128 ? 5 : 10;
@@ -80,35 +82,33 @@ struct TcParams {
   KvTcPlan plan;
   int per_tile;        // tokens of a 128-row tile: floor(128 / g)
   int box;             // cached tokens a TMA box takes: 8 .. 128, a power of two; 0: rows are gathered
-  int64_t oob_row;     // a row index outside the gather maps, and a slot outside the box maps
-  int64_t oob_slot;
+  int64_t oob_row;     // a row index outside the gather maps
   uint64_t wait_ns;
 };
 
 // ------------------------------------------------------------------------------------------- plan
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {   // exclusive, kPlanThreads
+// exclusive sums over the block of values packed into one 64-bit word; kPlanThreads
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, uint64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  uint64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
+  uint64_t s = warp_sums[lane];      // every warp sums the warps for itself
+  const uint64_t own = s;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  __syncthreads();
-  total = warp_sums[31];
-  return x - v + (warp ? warp_sums[warp - 1] : 0);
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const uint64_t before = __shfl_sync(0xffffffffu, s - own, warp);
+  __syncthreads();                   // warp_sums may be written again
+  return x - v + before;
 }
 
 // cut a tile of c steps into pieces of at most `target`: their number, and their length
@@ -124,14 +124,15 @@ __device__ __forceinline__ int cut(int c, int target, int* len) {
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P) {
   __shared__ int cost[kPlanTiles];
-  __shared__ int sums[32];
+  __shared__ int row_base_s[kPlanThreads + 1];
+  __shared__ uint64_t sums[32];
   __shared__ int tops[32];
   __shared__ float est_s[32];
-  __shared__ int target_s;
   const KvAttendArgs& a = P.a;
   const KvRows& R = a.rows;
   const KvTcPlan& plan = P.plan;
-  int* base = plan.row_base;
+  // tiles before each row: in shared memory where the batch fits
+  int* base = R.batch <= kPlanThreads ? row_base_s : plan.row_base;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = P.per_tile, tile_cap = plan.tile_cap, slots = plan.slots, sms = plan.sm_count;
 
@@ -146,10 +147,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P)
       if (kv_row(R, b, q0, n, L, bad)) w = ((n + per - 1) / per + 1) / 2;
       if (bad) record_error(a.err, kCodeDevice, bad, b, b);
     }
-    int total;
-    const int at = block_scan(w, sums, total);
+    uint64_t total;
+    const int at = int(block_scan(uint64_t(w), sums, total));
     if (b < R.batch) base[b] = T + at;
-    T += total;
+    T += int(total);
   }
   if (tid == 0) base[R.batch] = T;
   if (T > tile_cap) {   // rows that overlap in the packed arrays: more tiles than tokens
@@ -174,30 +175,35 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P)
     return (seen + kTile - 1) / kTile;
   };
 
-  int top = 0, total_c = 0;
+  KvItem mine{};                                   // tile `tid`, kept for the list
+  int mine_c = 0, top = 0, sum = 0;
   for (int i = tid; i < T; i += kPlanThreads) {
-    KvItem it;
+    KvItem it{};
     const int c = tile_of(i, it);
     if (i < kPlanTiles) cost[i] = c;
+    if (i == tid) {
+      mine = it;
+      mine_c = c;
+    }
     top = max(top, c);
-    total_c += c;
+    sum += c;
   }
-  int all_c;
-  block_scan(total_c, sums, all_c);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) tops[warp] = top;
+  top = __reduce_max_sync(0xffffffffu, top);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) {
+    tops[warp] = top;
+    sums[warp] = uint64_t(sum);
+  }
   __syncthreads();
-  top = tops[0];
-  for (int k = 1; k < 32; ++k) top = max(top, tops[k]);
-  top = max(top, 1);
+  top = max(1, __reduce_max_sync(0xffffffffu, tops[lane]));
+  const int all_c = __reduce_add_sync(0xffffffffu, int(sums[lane]));
 
   // Each warp weighs one way to cut: the longest tile into s pieces, the others into pieces as long. The
   // time is estimated as the waves of items times their mean length and start-up, at least the longest
   // item, and the join of what was cut (in steps of 128 tokens).
+  const int s_way = warp < 16 ? warp + 1 : warp < 24 ? 16 + (warp - 15) * 4 : 48 + (warp - 23) * 13;
   if (T <= kPlanTiles) {
-    const int s = warp < 16 ? warp + 1 : warp < 24 ? 16 + (warp - 15) * 4 : 48 + (warp - 23) * 13;
-    const int target = max(1, (top + s - 1) / s);
+    const int target = max(1, (top + s_way - 1) / s_way);
     int items = 0, cut_items = 0;
     for (int i = lane; i < T; i += 32) {
       int len;
@@ -211,33 +217,30 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P)
     float est = fmaxf(waves * (float(all_c) / max(items, 1) + 2.f), target + 2.f) + (cut_items ? 4.f : 0.f);
     if ((int64_t)cut_items * a.n_kv > slots) est = INFINITY;
     if (lane == 0) est_s[warp] = est;
-    __syncthreads();
-    if (tid == 0) {
-      int best = 0;
-      for (int k = 1; k < 32; ++k)
-        if (est_s[k] < est_s[best]) best = k;
-      const int sb = best < 16 ? best + 1 : best < 24 ? 16 + (best - 15) * 4 : 48 + (best - 23) * 13;
-      target_s = max(1, (top + sb - 1) / sb);
-    }
-  } else if (tid == 0) {
-    target_s = top;
+  } else if (lane == 0) {
+    est_s[warp] = warp == 0 ? 0.f : INFINITY;
   }
   __syncthreads();
-  const int target = target_s;
+  // the best way, the fewest pieces among equals; estimates are not negative, so their bits order them
+  const unsigned e = __float_as_uint(est_s[lane]);
+  const int best = __ffs(__ballot_sync(0xffffffffu, e == __reduce_min_sync(0xffffffffu, e))) - 1;
+  const int s_best = best < 16 ? best + 1 : best < 24 ? 16 + (best - 15) * 4 : 48 + (best - 23) * 13;
+  const int target = max(1, (top + s_best - 1) / s_best);
 
   int n_items = 0, n_cut = 0, n_joins = 0;
   for (int i0 = 0; i0 < T; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    KvItem it{};
-    int p = 0, len = 0, c = 0;
+    KvItem it = mine;
+    int p = 0, len = 0, c = mine_c;
     if (i < T) {
-      c = tile_of(i, it);
+      if (i0 > 0) c = tile_of(i, it);
       p = cut(c, target, &len);
     }
-    int tot_p, tot_c, tot_j;
-    const int at = n_items + block_scan(p, sums, tot_p);
-    const int slot = n_cut + block_scan(p > 1 ? p : 0, sums, tot_c);
-    const int join = n_joins + block_scan(p > 1 ? 1 : 0, sums, tot_j);
+    // items (28 bits), cut items (18) and joins (18) in one scan; slots bounds the last two
+    uint64_t tot;
+    const uint64_t sc = block_scan(uint64_t(p) | uint64_t(p > 1 ? p : 0) << 28 | uint64_t(p > 1) << 46, sums, tot);
+    const int at = n_items + int(sc & 0xfffffff), slot = n_cut + int(sc >> 28 & 0x3ffff);
+    const int join = n_joins + int(sc >> 46);
     for (int k = 0; k < p; ++k) {
       it.kv0 = k * len;
       it.kv1 = min(c, it.kv0 + len);
@@ -245,9 +248,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P)
       plan.items[at + k] = it;
     }
     if (p > 1) plan.joins[join] = KvJoin{it.q0, it.n, it.tok0, it.tiles, slot, p, {0, 0}};
-    n_items += tot_p;
-    n_cut += tot_c;
-    n_joins += tot_j;
+    n_items += int(tot & 0xfffffff);
+    n_cut += int(tot >> 28 & 0x3ffff);
+    n_joins += int(tot >> 46);
   }
   if (tid == 0) {
     plan.head->n_items = n_items;
@@ -257,50 +260,82 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P)
 }
 
 // ------------------------------------------------------------------------------------------- join
-// A warp takes 32 query rows of a cut tile, a lane one row: o = sum_k o_k 2^(m_k - M) / L.
-template <int DH, bool BF16> __global__ void __launch_bounds__(128) kv_join_kernel(const TcParams P) {
+// A block takes eight query rows of a cut tile: o = sum_k 2^(m_k - M) o_k / L over its pieces. The weights are
+// formed once, then a thread sums four columns of a row, eight pieces' loads in flight at a time (from L2: one
+// piece after the other took a microsecond each).
+constexpr int kJoinRows = 8;
+template <int DH, bool BF16>
+__global__ void __launch_bounds__(kJoinRows * DH / 4) kv_join_kernel(const TcParams P, int max_pieces) {
+  extern __shared__ float wgt[];                           // [pieces][8 rows]
+  __shared__ float inv_s[kJoinRows];
   const KvAttendArgs& a = P.a;
   const KvTcPlan& plan = P.plan;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kParts = 4;                                // column parts of a row, one a warp
-  const int units = plan.head->n_joins * a.n_kv * 8;            // two tiles of four 32-row parts
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const KvJoin J = plan.joins[u / 8 / a.n_kv];
-    const int h = u / 8 % a.n_kv, tile = u / 4 % 2, r = (u % 4) * 32 + lane;
-    if (tile >= J.tiles) continue;
-    const int i = J.tok0 + tile * P.per_tile + r / a.g;
-    if (r >= P.per_tile * a.g || i >= J.n) continue;
+  const int r8 = threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kGroups = kTile / kJoinRows;
+  const int heads = plan.head->n_joins * a.n_kv;
+  // the row groups run slowest, so that the tiles' live rows spread over the blocks
+  for (int u = blockIdx.x; u < heads * 2 * kGroups; u += gridDim.x) {
+    const KvJoin J = plan.joins[u % heads / a.n_kv];
+    const int h = u % heads % a.n_kv, tile = u / heads % 2, row0 = u / heads / 2 * kJoinRows;
+    if (tile >= J.tiles || row0 >= P.per_tile * a.g || J.tok0 + tile * P.per_tile + row0 / a.g >= J.n) continue;
+    const int pieces = min(J.pieces, max_pieces);
     const int64_t s0 = ((int64_t)J.slot * a.n_kv + h) * 2 + tile, step = 2 * a.n_kv;
-    const float2* ml = a.part_ml + s0 * kTile + r;
-    float M = -INFINITY;
-    for (int k = 0; k < J.pieces; ++k) M = fmaxf(M, ml[k * step * kTile].x);
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int k = 0; k < J.pieces; ++k) L = fmaf(ml[k * step * kTile].y, exp2f(ml[k * step * kTile].x - base), L);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int head = h * a.g + r % a.g;
-    const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + head;
-    if (warp == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994531f;
-    constexpr int kCols = DH / 4 / kParts;                 // float4 columns of this warp
-    float4 acc[kCols];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + warp * kCols) * kTile + r;
-    for (int k = 0; k < J.pieces; ++k) {
-      const float w = exp2f(ml[k * step * kTile].x - base);
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const float4 v = po[(k * step * (DH / 4) + c) * kTile];
-        acc[c].x = fmaf(v.x, w, acc[c].x);
-        acc[c].y = fmaf(v.y, w, acc[c].y);
-        acc[c].z = fmaf(v.z, w, acc[c].z);
-        acc[c].w = fmaf(v.w, w, acc[c].w);
+    auto query = [&](int r, int& i) {                      // the row's token; whether it is one
+      i = J.tok0 + tile * P.per_tile + r / a.g;
+      return r < P.per_tile * a.g && i < J.n;
+    };
+    for (int x = warp; x < kJoinRows; x += blockDim.x / 32) {
+      int i;
+      const int r = row0 + x;
+      if (!query(r, i)) continue;
+      const float2* ml = a.part_ml + s0 * kTile + r;
+      float M = -INFINITY, L = 0.f;
+      for (int k = lane; k < pieces; k += 32) M = fmaxf(M, ml[k * step * kTile].x);
+      M = warp_max(M);
+      const float base = M == -INFINITY ? 0.f : M;
+      for (int k = lane; k < pieces; k += 32) {
+        const float2 v = ml[k * step * kTile];
+        const float w = exp2f(v.x - base);
+        wgt[k * kJoinRows + x] = w;
+        L = fmaf(v.y, w, L);
+      }
+      L = warp_sum(L);
+      if (lane == 0) {
+        inv_s[x] = L == 0.f ? 0.f : 1.f / L;
+        if (a.lse)
+          a.lse[(int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g] =
+              L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994531f;
       }
     }
-    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * DH + warp * kCols * 4);
+    __syncthreads();
+    int i;
+    const int r = row0 + r8;
+    if (query(r, i)) {
+      const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + c4) * kTile + r;
+      const int64_t pitch = step * (DH / 4) * kTile;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < pieces; k0 += 8) {
+        float4 v[8];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c)
-      out[c] = make_uint2(pack2<BF16>(acc[c].x * inv, acc[c].y * inv), pack2<BF16>(acc[c].z * inv, acc[c].w * inv));
+        for (int x = 0; x < 8; ++x)
+          if (k0 + x < pieces) v[x] = po[(k0 + x) * pitch];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (k0 + x < pieces) {
+            const float w = wgt[(k0 + x) * kJoinRows + r8];
+            acc.x = fmaf(v[x].x, w, acc.x);
+            acc.y = fmaf(v[x].y, w, acc.y);
+            acc.z = fmaf(v[x].z, w, acc.z);
+            acc.w = fmaf(v[x].w, w, acc.w);
+          }
+      }
+      const float inv = inv_s[r8];
+      const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * DH + c4 * 4) =
+          make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
   }
 }
 
@@ -330,6 +365,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// one 32-byte sector
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // steps of unit u of an item (its cached tiles), and the tile of its step k
@@ -397,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int total = P.plan.head->n_items * a.n_kv;
       const int oob = int(P.oob_row), box = P.box, n_box = box ? kTile / box : 0;
       const int ps = a.pages.page_size, tile_pages = kTile / ps, tile_rest = kTile % ps;
-      const int table_pages = int(a.rows.table_pages);
+      const int table_pages = int(a.rows.table_pages), n_pages = int(a.pages.n_pages);
+      const int oob_slot = n_pages * ps;
       int st = 0, loads_q = 0, seq = 0;    // the ring's next stage; stages counted
       uint32_t par = 1, mine = 0;          // what `empty` is waited for; which of the last stages this warp filled
       bool ok = true;
@@ -454,15 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A lane looks up the slot of its box one tile ahead: the next tile's is 128 tokens on.
         const int g0 = box ? L & -box : 0, g1 = box && g0 < L ? g0 + box : g0;   // the box with the length's end
         int tb = kv0 * kTile + lane * box;
-        int pg = tb / ps, off = tb - pg * ps;
-        auto look = [&]() -> int {
-          int page = table ? -1 : b;
-          if (lane < n_box && tb < L && table && pg < table_pages) page = table[pg];
-          int s = int(P.oob_slot);
-          if (lane < n_box && tb < L) {
-            if (page >= 0 && page < a.pages.n_pages) s = page * ps + off;
-            else record_error(a.err, kCodeDevice, kErrPage, tb, b);
-          }
+        int pg = tb / ps, off = tb - pg * ps;   // without a table ps is not exceeded: pg is 0
+        int next_page = -1, next_off = 0, next_t = 0;
+        auto look = [&]() {
+          next_page = table ? -1 : b;
+          if (lane < n_box && tb < L && table && pg < table_pages) next_page = table[pg];
+          next_off = off;
+          next_t = tb;
           tb += kTile;
           pg += tile_pages;
           off += tile_rest;
@@ -470,11 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             off -= ps;
             ++pg;
           }
-          return s;
         };
-        int next_slot = box ? look() : 0;
+        if (box) look();
         auto load = [&](int j) {
-          const int t0 = j * kTile, slot = next_slot;
+          const int t0 = j * kTile;
+          int slot = oob_slot;                   // of this lane's box; outside the pool: zeros
+          if (lane < n_box && next_t < L) {
+            if (next_page >= 0 && next_page < n_pages) slot = next_page * ps + next_off;
+            else record_error(a.err, kCodeDevice, kErrPage, next_t, b);
+          }
           const int lo = box ? g0 : t0, hi = box ? g1 : t0 + kTile;   // the rows to gather
           const bool gather = lo < hi && lo < t0 + kTile && hi > t0;
           int r[4];
@@ -518,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           mine |= 1u;
-          if (box) next_slot = look();
+          if (box) look();
         };
         auto step = [&](bool k_tile, int j) {
           mine <<= 1;
@@ -552,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_qk = tc::idesc_f16(kTile, kTile, BF16);
       const uint32_t id_pv = tc::idesc_f16(kTile, DH, BF16) | tc::kIdescBMajorMN;
       const uint32_t base = tc::smem_addr(smem);
-      const uint64_t dq = tc::sdesc_k_sw128(base), dk = tc::sdesc_k_sw128(base + Y::kOffKv);
-      const uint64_t dv = tc::sdesc_mn_sw128(base + Y::kOffKv, Y::kHalf);
+      const uint64_t dq = tc::sdesc_sw128(base, 16, 1024), dk = tc::sdesc_sw128(base + Y::kOffKv, 16, 1024);
+      const uint64_t dv = tc::sdesc_sw128(base + Y::kOffKv, Y::kHalf, 1024);
       int st = 0, loads_q = 0;           // the ring's stage that comes next
       uint32_t par = 0, np[2] = {0, 0};  // its phase; the weights' phases of the units
       // A wait that gives up only raises the abort flag, at which every later wait gives up at once; the loop
@@ -570,7 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return s;
       };
-      auto qk = [&](int u, uint64_t q, int s, bool free) {       // S_u = Q K^T of key stage s
+      // S_u = Q K^T of key stage s; `last`: the item's last product that reads the queries
+      auto qk = [&](int u, uint64_t q, int s, bool free, bool last) {
         const uint64_t kd = dk + uint64_t(s) * (Y::kTileB >> 4);
         __syncwarp();
         tc::tc_fence_after();
@@ -582,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc::umma_commit(&S.s_full[u]);
           if (free) tc::umma_commit(&S.empty[s]);
+          if (last) tc::umma_commit(&S.q_empty);
         }
       };
       // O_u += P_u V of value stage s, the first half's weights first; `last`: the item's last for the unit
@@ -625,24 +672,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n0 = unit_steps(it, 0, P.per_tile);
           const uint64_t dq1 = dq + (Y::kTileB >> 4);
           int sk = stage();
-          if (n0 > 0) qk(0, dq, sk, false);
-          qk(1, dq1, sk, true);
+          if (n0 > 0) qk(0, dq, sk, false, false);
+          qk(1, dq1, sk, true, n == 1);
           for (int k = 0; k < n; ++k) {
             if (dead()) break;
             const int sv = stage();
             if (k < n0) pv(0, sv, k == 0, false, k + 1 == n0);
             if (k + 1 < n) {
               sk = stage();
-              if (k + 1 < n0) qk(0, dq, sk, false);
+              if (k + 1 < n0) qk(0, dq, sk, false, false);
             }
             pv(1, sv, k == 0, true, k + 1 == n);
-            if (k + 1 < n) qk(1, dq1, sk, true);
+            if (k + 1 < n) qk(1, dq1, sk, true, k + 2 == n);
           }
         } else {
           // the units take the tiles in turn
           for (int k = 0; k < min(n, 2); ++k) {
             const int s = stage();
-            qk(k, dq, s, true);
+            qk(k, dq, s, true, k + 1 == n);
           }
           for (int k = 0; k < n; ++k) {
             if (dead()) break;
@@ -650,12 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             pv(k & 1, sv, k < 2, true, k + 2 >= n);
             if (k + 2 < n) {
               const int sk = stage();
-              qk(k & 1, dq, sk, true);
+              qk(k & 1, dq, sk, true, k + 3 == n);
             }
           }
         }
         __syncwarp();
-        if (tc::elect_one()) tc::umma_commit(&S.q_empty);
       }
       __syncwarp();
       // every product issued has completed once this commit lands
@@ -703,15 +749,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&S.s_full[u], n_s & 1)) break;
         ++n_s;
         const int t0 = unit_tile(it, u, k) * kTile;
+        if (t0 + kTile - 1 > vis_min) {
+          // tokens that a row does not see: masked in tensor memory, so that the common tile's code stays short
+          const int lim = vis - t0;
+#pragma unroll 1
+          for (int x = 0; x < kTile; x += 32) {
+            uint32_t w[32];
+            tc::tmem_ld32_nowait(t_s + x, w);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) w[y] = x + y > lim ? 0xff800000u : w[y];
+            tc::tmem_st32(t_s + x, w);
+          }
+          tc::tmem_st_wait();
+        }
         float s[kTile];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tc::tmem_ld32_nowait(t_s + x * 32, reinterpret_cast<uint32_t*>(s) + x * 32);
         tc::tmem_ld_wait();
-        if (t0 + kTile - 1 > vis_min) {
-          const int lim = vis - t0;
-#pragma unroll
-          for (int x = 0; x < kTile; ++x) s[x] = x > lim ? -INFINITY : s[x];
-        }
         float mx[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s[y], s[y + 4]);
@@ -728,14 +783,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mn;
           l *= f;
           if (k > 0) {   // s_full also says that the product before it, into O, has completed
-#pragma unroll
-            for (int x = 0; x < DH / 32; ++x) {
-              uint32_t o[32];
-              tc::tmem_ld32_nowait(t_o + x * 32, o);
+#pragma unroll 1
+            for (int x = 0; x < DH; x += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16_nowait(t_o + x, o);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tc::tmem_st32(t_o + x * 32, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tc::tmem_st16(t_o + x, o);
             }
           }
         }
@@ -774,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u == 1 && unit_steps(it, 0, P.per_tile) > 0) ++n_o0;
       if (exchange && u == 1) {
         if (!wait(&S.o_full[0], (n_o0 - 1) & 1)) break;          // unit 0's products read the queries too
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < DH / 32; ++x) {
           uint32_t o[32];
           tc::tmem_ld32_nowait(t_o + x * 32, o);
@@ -811,9 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 *= inv;
         if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
       } else {
-        a.part_ml[slot * kTile + r] = make_float2(m, l);
+        if (live) a.part_ml[slot * kTile + r] = make_float2(m, l);
       }
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < DH / 32; ++x) {
         float o[32];
         if (steps > 0) {
@@ -835,16 +890,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[4 * y + 3] = fmaf(v.w, f1, o[4 * y + 3]);
           }
         }
-        if (it.split >= 0) {
+        if (it.split >= 0 && live) {
           float4* po = reinterpret_cast<float4*>(a.part_o) + (slot * (DH / 4) + x * 8) * kTile + r;
 #pragma unroll
           for (int y = 0; y < 8; ++y) po[y * kTile] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-        } else if (live) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * DH + x * 32);
+        } else if (it.split < 0 && live) {
+          uint16_t* out = static_cast<uint16_t*>(a.out) + row * DH + x * 32;
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            out[y] = make_uint4(pack2<BF16>(o[8 * y], o[8 * y + 1]), pack2<BF16>(o[8 * y + 2], o[8 * y + 3]),
-                                pack2<BF16>(o[8 * y + 4], o[8 * y + 5]), pack2<BF16>(o[8 * y + 6], o[8 * y + 7]));
+          for (int y = 0; y < 2; ++y) {
+            uint32_t w[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) w[z] = pack2<BF16>(o[16 * y + 2 * z], o[16 * y + 2 * z + 1]);
+            store32(out + 16 * y, w);
+          }
         }
       }
       tc::tc_fence_before();
@@ -885,8 +943,7 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
     const cuuint64_t dims[2] = {DH, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {DH * 2};
     const cuuint32_t box[2] = {64, 1};
-    P.oob_slot = a.pages.n_pages * a.pages.page_size;
-    const cuuint64_t bdims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)P.oob_slot};
+    const cuuint64_t bdims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)(a.pages.n_pages * a.pages.page_size)};
     const cuuint64_t bstrides[2] = {DH * 2, (cuuint64_t)a.n_kv * DH * 2};
     // a box must lie in one page: without a table a row is one page, else the largest power of two that divides it
     int box_tokens = a.rows.page_table ? a.pages.page_size & -a.pages.page_size : kTile;
@@ -909,7 +966,9 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
   kern<<<(unsigned)(most < t.sm_count ? most : t.sm_count), kThreads, Lay<DH>::kSmem, st>>>(tm_q, tm_k, tm_v, tm_kb, tm_vb, P);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kv_join_kernel<DH, BF16><<<2 * t.sm_count, 128, 0, st>>>(P);
+  // a cut makes slots / n_kv pieces at most
+  const int max_pieces = t.slots / a.n_kv > 1 ? t.slots / a.n_kv : 1;
+  kv_join_kernel<DH, BF16><<<8 * t.sm_count, kJoinRows * DH / 4, max_pieces * kJoinRows * sizeof(float), st>>>(P, max_pieces);
   return cudaGetLastError();
 }
 

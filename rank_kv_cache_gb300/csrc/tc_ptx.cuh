@@ -90,24 +90,23 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-// The same for short waits between the roles of one CTA: the clock, whose reading takes longer than such a wait, is
-// only read after 32 tries without success.
+// The same for short waits between the roles of one CTA: the thread sleeps at once (polling warps take issue slots
+// from those that work), and the clock, whose reading takes longer than such a wait, is only read after a sleep that
+// was not ended by the phase.
 __device__ __forceinline__ bool mbar_wait_short(uint64_t* b, uint32_t parity, volatile int* abort_flag,
                                                 uint64_t limit_ns) {
   uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(b, parity)) return true;
-    if (i % 32 == 0) {
-      if (*abort_flag) return false;
-      const uint64_t t = globaltimer();
-      if (t0 == 0) {
-        t0 = t;
-      } else if (t - t0 > limit_ns) {
-        *abort_flag = 1;
-        return false;
-      }
+  while (!mbar_try_wait_sleep(b, parity, 20000u)) {
+    if (*abort_flag) return false;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) {
+      t0 = t;
+    } else if (t - t0 > limit_ns) {
+      *abort_flag = 1;
+      return false;
     }
   }
+  return true;
 }
 
 // ---------------------------------------------------------------- TMA
@@ -152,18 +151,19 @@ __device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t saddr) {
   return d;
 }
 
-// Shared-memory matrix descriptor for an operand whose rows run along K and whose 128-byte swizzled rows hold 64
-// consecutive M (or N) elements: 8-row atoms of 1024 bytes along K, `mn_stride` bytes between blocks of 64 elements.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
+// Shared-memory matrix descriptor of an operand in 128-byte swizzled atoms of eight 128-byte rows. K-major (a row
+// holds 64 consecutive K of one M or N index): `sbo` bytes between groups of eight rows. MN-major (a row holds 64
+// consecutive M or N of one K): `sbo` bytes between groups of eight K, `lbo` bytes between blocks of 64 elements.
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   uint64_t d = 0;
   d |= uint64_t((saddr & 0x3FFFFu) >> 4);
-  d |= uint64_t(mn_stride >> 4) << 16;
-  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(lbo >> 4) << 16;
+  d |= uint64_t(sbo >> 4) << 32;
   d |= uint64_t(1) << 46;
   d |= uint64_t(2) << 61;
   return d;
 }
-// bit of the instruction descriptor: B is laid out along N (sdesc_mn_sw128)
+// bit of the instruction descriptor: B is MN-major
 constexpr uint32_t kIdescBMajorMN = 1u << 16;
 
 // Instruction descriptor of kind::f16 with fp32 accumulation, both operands K-major.
@@ -224,7 +224,7 @@ __device__ __forceinline__ void tmem_ld16x2_nowait(uint32_t ta, uint32_t tb, uin
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// 32 columns of this warp's 32 lanes without waiting; the outputs are valid after tmem_ld_wait().
+// 32 (or 16) columns of this warp's 32 lanes without waiting; the outputs are valid after tmem_ld_wait().
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t ta, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -233,6 +233,14 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t ta, uint32_t* r) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t ta, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(ta)
       : "memory");
 }
