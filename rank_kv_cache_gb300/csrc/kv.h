@@ -115,7 +115,11 @@ struct KvAttendArgs {
   ErrWord* err;
 };
 constexpr int kKvFewRows = 16;           // query rows (token, head of the group) of a unit
-constexpr int kKvFewStep = 128;          // cached tokens the unit's warps take together
+constexpr int kKvFewTokens = 64;         // cached tokens of 128 elements that a CTA's warps take together
+constexpr int kKvFewCtas = 2;            // CTAs of an SM
+constexpr int kKvFewSplits = 512;        // most ranges of a unit (their weights are joined in shared memory)
+// once a handle, on its device: what the kernel's launches need set
+cudaError_t prepare_kv_attend_few(int head_dim, bool bf16);
 cudaError_t launch_kv_attend_few(const KvAttendArgs& a, cudaStream_t st);
 
 // Work list of the tensor-core kernel, in the workspace.
@@ -143,6 +147,7 @@ struct KvTcPlan {
   int slots;         // most pieces x key/value heads whose partials the workspace holds
   int sm_count;
 };
+cudaError_t prepare_kv_attend_tc(int head_dim, bool bf16);
 cudaError_t launch_kv_attend_tc(const KvAttendArgs& a, const KvTcPlan& t, cudaStream_t st);
 
 }  // namespace palu

@@ -8,9 +8,10 @@
 // the 128-row tcgen05 shapes would leave 7/8 of their rows empty here, and the rate needed, 16 rows
 // for every 4 d cached bytes, is a few per cent of what this instruction gives.
 //
-// A unit's cached tokens are cut into n_splits ranges, one CTA each; its four warps take 32 tokens in
-// turn, each with its own online softmax (fp32 maximum, sum and output) and its own three-stage ring of
-// cp.async copies, so no barrier stands between the warps until they are joined. Rows past the end are
+// A unit's cached tokens are cut into n_splits ranges, one CTA each, two CTAs an SM (so that one's start
+// and join hide behind the other's stream); a CTA's four warps take 16 tokens (d = 64: 32) in turn, each
+// with its own online softmax (fp32 maximum, sum and output) and its own three-stage ring of cp.async
+// copies, so no barrier stands between the warps until they are joined. Rows past the end are
 // written as zeros into shared memory and masked, never read. The last CTA of a unit to finish joins
 // the ranges in a fixed order. The weights p are rounded to the cache's type for the product with V, as
 // the matrix instruction takes it; the sum is of the unrounded p.
@@ -20,7 +21,6 @@ namespace palu {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTok = 32;       // tokens a warp takes at once
 constexpr int kStages = 3;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -52,10 +52,13 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 template <int DH> struct Sm {
+  static constexpr int kTok = kKvFewTokens / kWarps * 128 / DH;   // tokens a warp takes at once: 16, or 32 of d = 64
+  static constexpr int kStep = kWarps * kTok;
   static constexpr int kRow = DH * 2;                       // bytes of a token's head row
   static constexpr int kTile = kTok * kRow;                 // one warp's K (or V) stage
   static constexpr int kWarp = kStages * 2 * kTile;
   static constexpr int kBytes = kWarps * kWarp;
+  static_assert(kKvFewRows * kKvFewSplits * 4 <= kBytes && kWarps * kKvFewRows * DH * 4 <= kBytes, "joins");
 };
 
 // Rows are stored with their 16-byte chunks exchanged by the row's low three bits, so that the eight
@@ -65,8 +68,9 @@ template <int DH> __device__ __forceinline__ uint32_t swz(int row, int chunk) {
 }
 
 template <int DH, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvAttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvAttendArgs a) {
   using S = Sm<DH>;
+  constexpr int kTok = S::kTok, kNT = kTok / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 ml_s[kWarps][kKvFewRows];
   __shared__ float wgt[kWarps][kKvFewRows];
@@ -89,10 +93,56 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
   const int seen = max(0, min(L, L - n + i_last + 1));             // cached tokens it attends to
   // the row's own ranges: n_splits at most, whole steps of the CTA
   int per = (seen + a.n_splits - 1) / a.n_splits;
-  per = (per + kKvFewStep - 1) / kKvFewStep * kKvFewStep;
+  per = (per + S::kStep - 1) / S::kStep * S::kStep;
   const int ns = per > 0 ? (seen + per - 1) / per : 1;
   if (split >= ns) return;
   const int t0 = split * per, t1 = min(seen, t0 + per);
+
+  float o[DH / 8][4];
+#pragma unroll
+  for (int i = 0; i < DH / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  uint8_t* ring = smem + warp * S::kWarp;
+  const uint32_t ring_a = smem_u32(ring);
+  const int first = t0 + warp * kTok;
+  const int n_it = first < t1 ? (t1 - first + S::kStep - 1) / S::kStep : 0;
+  const uint16_t* kb = static_cast<const uint16_t*>(a.pages.k) + h * DH;
+  const uint16_t* vb = static_cast<const uint16_t*>(a.pages.v) + h * DH;
+  const int64_t tok_stride = (int64_t)a.n_kv * DH;
+
+  // slot of this lane's token of step `it` (-1: past the range, or a page outside the pool)
+  auto slot_of = [&](int it) -> int {
+    const int t = first + it * S::kStep + lane;
+    if (it >= n_it || lane >= kTok || t >= t1) return -1;
+    const int64_t s = kv_slot(R, a.pages, b, t);
+    if (s < 0) record_error(a.err, kCodeDevice, kErrPage, t, b);
+    return int(s);
+  };
+  auto load = [&](int it, int slot) {
+    if (it < n_it) {
+      const uint32_t st = ring_a + (it % kStages) * 2 * S::kTile;
+      constexpr int kCh = DH / 8;                                  // 16-byte chunks of a row
+#pragma unroll
+      for (int x = 0; x < kTok * kCh / 32; ++x) {
+        const int row = (x * 32 + lane) / kCh, ch = lane % kCh;
+        const int s = __shfl_sync(0xffffffffu, slot, row);
+        const int64_t off = s < 0 ? 0 : s * tok_stride + ch * 8;
+        const int bytes = s < 0 ? 0 : 16;
+        cp16(st + swz<DH>(row, ch), kb + off, bytes);
+        cp16(st + S::kTile + swz<DH>(row, ch), vb + off, bytes);
+      }
+    }
+    cp_commit();
+  };
+
+  int next = slot_of(0);
+#pragma unroll
+  for (int it = 0; it < kStages - 1; ++it) {
+    const int cur = next;
+    next = slot_of(it + 1);
+    load(it, cur);
+  }
 
   // query rows as the A operand: row = lane / 4 and + 8, column pairs by lane % 4
   const int r0 = lane >> 2, cp = lane & 3;
@@ -114,51 +164,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
   }
   const int vis_min = L - n + rt * kKvFewRows / a.g;               // every row sees slots up to here
 
-  float o[DH / 8][4];
-#pragma unroll
-  for (int i = 0; i < DH / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  uint8_t* ring = smem + warp * S::kWarp;
-  const uint32_t ring_a = smem_u32(ring);
-  const int first = t0 + warp * kTok;
-  const int n_it = first < t1 ? (t1 - first + kKvFewStep - 1) / kKvFewStep : 0;
-  const uint16_t* kb = static_cast<const uint16_t*>(a.pages.k) + h * DH;
-  const uint16_t* vb = static_cast<const uint16_t*>(a.pages.v) + h * DH;
-  const int64_t tok_stride = (int64_t)a.n_kv * DH;
-
-  // slot of this lane's token of step `it` (-1: past the range, or a page outside the pool)
-  auto slot_of = [&](int it) -> int {
-    const int t = first + it * kKvFewStep + lane;
-    if (it >= n_it || t >= t1) return -1;
-    const int64_t s = kv_slot(R, a.pages, b, t);
-    if (s < 0) record_error(a.err, kCodeDevice, kErrPage, t, b);
-    return int(s);
-  };
-  auto load = [&](int it, int slot) {
-    if (it < n_it) {
-      const uint32_t st = ring_a + (it % kStages) * 2 * S::kTile;
-      constexpr int kCh = DH / 8;                                  // 16-byte chunks of a row
-#pragma unroll
-      for (int x = 0; x < kCh; ++x) {
-        const int row = (x * 32 + lane) / kCh, ch = lane % kCh;
-        const int s = __shfl_sync(0xffffffffu, slot, row);
-        const int64_t off = s < 0 ? 0 : s * tok_stride + ch * 8;
-        const int bytes = s < 0 ? 0 : 16;
-        cp16(st + swz<DH>(row, ch), kb + off, bytes);
-        cp16(st + S::kTile + swz<DH>(row, ch), vb + off, bytes);
-      }
-    }
-    cp_commit();
-  };
-
-  int next = slot_of(0);
-#pragma unroll
-  for (int it = 0; it < kStages - 1; ++it) {
-    const int cur = next;
-    next = slot_of(it + 1);
-    load(it, cur);
-  }
   for (int it = 0; it < n_it; ++it) {
     {
       const int cur = next;
@@ -168,24 +173,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
     cp_wait<kStages - 1>();
     __syncwarp();
     const uint32_t ks = ring_a + (it % kStages) * 2 * S::kTile, vs = ks + S::kTile;
-    float s[4][4];
+    float s[kNT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+    for (int i = 0; i < kNT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
     const int tr = ((lane >> 4) & 1) * 8 + (lane & 7), kc = (lane >> 3) & 1;
 #pragma unroll
     for (int k = 0; k < DH / 16; ++k) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
+      for (int p = 0; p < kNT / 2; ++p) {
         uint32_t f[4];
         ldsm4(f, ks + swz<DH>(p * 16 + tr, k * 2 + kc));
         mma<BF16>(s[2 * p], qf[k], f[0], f[1]);
         mma<BF16>(s[2 * p + 1], qf[k], f[2], f[3]);
       }
     }
-    const int tb = first + it * kKvFewStep;
+    const int tb = first + it * S::kStep;
     if (tb + kTok > t1 || tb + kTok - 1 > vis_min) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kNT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int t = tb + i * 8 + cp * 2 + (e & 1);
@@ -195,8 +200,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
     float al[2], base[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      float mx = fmaxf(fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1])),
-                       fmaxf(fmaxf(s[2][2 * x], s[2][2 * x + 1]), fmaxf(s[3][2 * x], s[3][2 * x + 1])));
+      float mx = fmaxf(s[0][2 * x], s[0][2 * x + 1]);
+#pragma unroll
+      for (int i = 1; i < kNT; ++i) mx = fmaxf(mx, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float mn = fmaxf(m[x], mx * a.scale_log2);
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
       m[x] = mn;
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kNT; ++i) {
         s[i][2 * x] = ex2(fmaf(s[i][2 * x], a.scale_log2, -base[x]));
         s[i][2 * x + 1] = ex2(fmaf(s[i][2 * x + 1], a.scale_log2, -base[x]));
         sum += s[i][2 * x] + s[i][2 * x + 1];
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
     }
     const int vr = ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kNT / 2; ++k) {
       const uint32_t pf[4] = {pack2<BF16>(s[2 * k][0], s[2 * k][1]), pack2<BF16>(s[2 * k][2], s[2 * k][3]),
                               pack2<BF16>(s[2 * k + 1][0], s[2 * k + 1][1]),
                               pack2<BF16>(s[2 * k + 1][2], s[2 * k + 1][3])};
@@ -350,10 +356,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_few_kernel(const KvA
   if (threadIdx.x == 0) a.counters[unit] = 0u;
 }
 
+template <int DH, bool BF16> cudaError_t prepare_few() {
+  return cudaFuncSetAttribute(kv_attend_few_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Sm<DH>::kBytes);
+}
 template <int DH, bool BF16> cudaError_t launch_few(const KvAttendArgs& a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kv_attend_few_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Sm<DH>::kBytes);
-  if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)a.rows.max_new * a.g + kKvFewRows - 1) / kKvFewRows;
   const dim3 grid((unsigned)(tiles * a.n_kv * a.n_splits), (unsigned)a.rows.batch);
   kv_attend_few_kernel<DH, BF16><<<grid, kWarps * 32, Sm<DH>::kBytes, st>>>(a);
@@ -361,6 +368,11 @@ template <int DH, bool BF16> cudaError_t launch_few(const KvAttendArgs& a, cudaS
 }
 
 }  // namespace
+
+cudaError_t prepare_kv_attend_few(int head_dim, bool bf16) {
+  if (head_dim == 128) return bf16 ? prepare_few<128, true>() : prepare_few<128, false>();
+  return bf16 ? prepare_few<64, true>() : prepare_few<64, false>();
+}
 
 cudaError_t launch_kv_attend_few(const KvAttendArgs& a, cudaStream_t st) {
   if (a.head_dim == 128) return a.bf16 ? launch_few<128, true>(a, st) : launch_few<128, false>(a, st);

@@ -921,6 +921,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tc::tmem_dealloc(tmem, 512);
 }
 
+template <int DH, bool BF16> cudaError_t prepare_tc() {
+  return cudaFuncSetAttribute(kv_attend_tc_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Lay<DH>::kSmem);
+}
 template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const KvTcPlan& t, cudaStream_t st) {
   const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   TcParams P{};
@@ -957,10 +961,8 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
     if (!tma_encode(&tm_v, dt, 2, a.pages.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
   }
   auto kern = kv_attend_tc_kernel<DH, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DH>::kSmem);
-  if (e != cudaSuccess) return e;
   kv_plan_kernel<<<1, kPlanThreads, 0, st>>>(P);
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
   kern<<<(unsigned)(most < t.sm_count ? most : t.sm_count), kThreads, Lay<DH>::kSmem, st>>>(tm_q, tm_k, tm_v, tm_kb, tm_vb, P);
@@ -973,6 +975,11 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
 }
 
 }  // namespace
+
+cudaError_t prepare_kv_attend_tc(int head_dim, bool bf16) {
+  if (head_dim == 128) return bf16 ? prepare_tc<128, true>() : prepare_tc<128, false>();
+  return bf16 ? prepare_tc<64, true>() : prepare_tc<64, false>();
+}
 
 cudaError_t launch_kv_attend_tc(const KvAttendArgs& a, const KvTcPlan& t, cudaStream_t st) {
   if (!tma_available()) return cudaErrorNotSupported;

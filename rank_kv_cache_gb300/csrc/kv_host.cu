@@ -189,6 +189,14 @@ palu_status_t palu_kv_create(const palu_kv_desc* desc, void* workspace, size_t w
     const double v = ldexp(turns - floor(turns), 64);
     h->freq.turn[k] = v >= 18446744073709549568.0 ? ~0ull : (uint64_t)v;
   }
+  if (desc->dtype != PALU_F32) {
+    const bool bf16 = desc->dtype == PALU_BF16;
+    if (prepare_kv_attend_few(desc->head_dim, bf16) != cudaSuccess ||
+        prepare_kv_attend_tc(desc->head_dim, bf16) != cudaSuccess) {
+      delete h;
+      return PALU_ERR_CUDA;
+    }
+  }
   const size_t clear = desc->dtype == PALU_F32 ? 256 : L.part_ml;   // error word and counters
   if (cudaMemsetAsync(h->ws, 0, clear, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
     delete h;
@@ -345,13 +353,14 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
   // Ranges of a unit: enough CTAs to fill the GPU in whole waves, each range worth its start and join.
   const int64_t units = (((int64_t)a.rows.max_new * a.g + kKvFewRows - 1) / kKvFewRows) * a.n_kv * a.rows.batch;
   if (units >= (int64_t(1) << 31)) return PALU_ERR_UNSUPPORTED;
-  const int64_t steps = (a.rows.max_kv_len + kKvFewStep - 1) / kKvFewStep;
+  const int step = kKvFewTokens * 128 / d.head_dim;
+  const int64_t steps = (a.rows.max_kv_len + step - 1) / step, ctas = (int64_t)kKvFewCtas * h->sm_count;
   int64_t best = 1;
   double least = 1e300;
-  for (int64_t k = 1; k <= steps && k * units <= kPartSlots; ++k) {
+  for (int64_t k = 1; k <= steps && k <= kKvFewSplits && k * units <= kPartSlots; ++k) {
     const int64_t per = (steps + k - 1) / k;
     if ((steps + per - 1) / per != k) continue;
-    const double est = double((units * k + h->sm_count - 1) / h->sm_count) * double(per + 2);
+    const double est = double((units * k + ctas - 1) / ctas) * double(per + 2);
     if (est < least - 1e-9) {
       least = est;
       best = k;

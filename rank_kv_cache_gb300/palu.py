@@ -635,6 +635,7 @@ class PagedAttention:
         self.dtype, self.x_dtype = names[dtype], names[x_dtype]
         self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
+        self._current = torch._C._cuda_getCurrentRawStream
         base = int(self.workspace.data_ptr())
         st, self.handle = palu_kv_create(self.desc, base + (-base) % 256, nbytes, self._stream(stream))
         check(st, "palu_kv_create")
@@ -651,9 +652,8 @@ class PagedAttention:
             pass
 
     def _stream(self, stream) -> int:
-        if stream is None:
-            stream = _torch().cuda.current_stream(self.device)
-        return stream.cuda_stream
+        # the raw handle of the current stream: building torch's Stream object takes longer than the call
+        return self._current(self.device.index) if stream is None else stream.cuda_stream
 
     def _view(self, name, t, heads, dtype, n_tokens):
         """(pointer, token stride) of a [n_tokens][heads][head_dim] tensor whose tokens may lie apart."""
