@@ -108,19 +108,19 @@ struct KvAttendArgs {
   int head_dim;
   int bf16;
   float scale_log2;            // log2(e) / sqrt(d)
-  int n_splits;                // few rows: ranges a row's cached tokens are cut into, at most
   float* part_o;               // fp32 partial outputs, not yet divided by their sums
   float2* part_ml;             // their running maxima (log2 units) and sums
-  unsigned* counters;          // [unit], zero between calls
+  unsigned* counters;          // few rows: [piece of a cut unit], zero between calls
+  int ctas;                    // few rows: CTAs that the GPU holds at once
   ErrWord* err;
 };
 constexpr int kKvFewRows = 16;           // query rows (token, head of the group) of a unit
 constexpr int kKvFewTokens = 64;         // cached tokens of 128 elements that a CTA's warps take together
 constexpr int kKvFewCtas = 2;            // CTAs of an SM
-constexpr int kKvFewSplits = 512;        // most ranges of a unit (their weights are joined in shared memory)
+constexpr int kKvFewMostCtas = 512;      // most CTAs of a call; cut units have at most twice as many pieces
 // once a handle, on its device: what the kernel's launches need set
 cudaError_t prepare_kv_attend_few(int head_dim, bool bf16);
-cudaError_t launch_kv_attend_few(const KvAttendArgs& a, cudaStream_t st);
+cudaError_t launch_kv_attend_few(KvAttendArgs a, int sm_count, cudaStream_t st);   // max_new g <= 16
 
 // Work list of the tensor-core kernel, in the workspace.
 constexpr int kKvTcRows = 128;           // query rows of a tile

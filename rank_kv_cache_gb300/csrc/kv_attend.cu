@@ -2,19 +2,22 @@
 //
 //   o = softmax(q K^T / sqrt(d)) V over slots 0 .. L - n + i of the query's row,  lse = ln sum e^s.
 //
-// A unit is (row, key/value head, 16 query rows): query row r = i g + j is new token i under head j of
+// A unit is (row, key/value head): query row r = i g + j of its n g <= 16 is new token i under head j of
 // the g heads that share the key/value head. Bound: HBM, each cached row is read once for the whole
-// group. The g heads are the rows of 16-row matrix instructions (mma.sync m16n8k16, fp32 accumulation):
+// group. The query rows are those of 16-row matrix instructions (mma.sync m16n8k16, fp32 accumulation):
 // the 128-row tcgen05 shapes would leave 7/8 of their rows empty here, and the rate needed, 16 rows
 // for every 4 d cached bytes, is a few per cent of what this instruction gives.
 //
-// A unit's cached tokens are cut into n_splits ranges, one CTA each, two CTAs an SM (so that one's start
-// and join hide behind the other's stream); a CTA's four warps take 16 tokens (d = 64: 32) in turn, each
-// with its own online softmax (fp32 maximum, sum and output) and its own three-stage ring of cp.async
-// copies, so no barrier stands between the warps until they are joined. Rows past the end are
-// written as zeros into shared memory and masked, never read. The last CTA of a unit to finish joins
-// the ranges in a fixed order. The weights p are rounded to the cache's type for the product with V, as
-// the matrix instruction takes it; the sum is of the unrounded p.
+// The units' steps of 64 cached tokens (d = 64: 128) are cut into pieces of about one length, so many that
+// they fill the GPU in whole waves, two CTAs an SM (one's start and join hide behind the other's stream).
+// The lengths are read on the device: rows of unlike lengths give unlike numbers of pieces. The last CTA of
+// a cut unit to finish joins its pieces in their order.
+//
+// A CTA's four warps take 16 tokens (d = 64: 32) in turn, each with its own online softmax (fp32 maximum,
+// sum and output) and its own three-stage ring of cp.async copies, so no barrier stands between the warps
+// until they are joined. Rows past the end are written as zeros into shared memory and masked, never
+// read. The weights p are rounded to the cache's type for the product with V, as the matrix instruction
+// takes it; the sum is of the unrounded p.
 #include "kv.h"
 
 namespace palu {
@@ -58,13 +61,41 @@ template <int DH> struct Sm {
   static constexpr int kTile = kTok * kRow;                 // one warp's K (or V) stage
   static constexpr int kWarp = kStages * 2 * kTile;
   static constexpr int kBytes = kWarps * kWarp;
-  static_assert(kKvFewRows * kKvFewSplits * 4 <= kBytes && kWarps * kKvFewRows * DH * 4 <= kBytes, "joins");
+  static_assert(kKvFewRows * 2 * kKvFewMostCtas * 4 <= kBytes && kWarps * kKvFewRows * DH * 4 <= kBytes, "joins");
 };
 
 // Rows are stored with their 16-byte chunks exchanged by the row's low three bits, so that the eight
 // rows of an ldmatrix fall into different banks.
 template <int DH> __device__ __forceinline__ uint32_t swz(int row, int chunk) {
   return uint32_t(row * (DH * 2) + ((chunk ^ (row & 7)) << 4));
+}
+
+// How the rows' steps are cut: the pieces of each row (32 rows at a time, one a lane) and the numbers of the first
+// of them among all pieces, and among those of cut units. Every warp works it out for itself, alike.
+struct Cut {
+  int per;          // steps of a piece, at most
+  int pieces;       // of this lane's row, for each of its key/value heads
+  int start, cut;   // pieces (of one head) of the rows before it; those of cut units
+  int total, total_cut;
+};
+
+__device__ __forceinline__ void cut_rows(int steps, int per, Cut& c, int base, int base_cut) {
+  const int lane = threadIdx.x & 31;
+  c.per = per;
+  c.pieces = (steps + per - 1) / per;
+  int x = c.pieces, y = c.pieces > 1 ? c.pieces : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
+  }
+  c.start = base + x - c.pieces;
+  c.cut = base_cut + y - (c.pieces > 1 ? c.pieces : 0);
+  c.total = base + __shfl_sync(0xffffffffu, x, 31);
+  c.total_cut = base_cut + __shfl_sync(0xffffffffu, y, 31);
 }
 
 template <int DH, bool BF16>
@@ -76,294 +107,339 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
   __shared__ float wgt[kWarps][kKvFewRows];
   __shared__ float2 tot[kKvFewRows];
   __shared__ int last_cta;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x % a.n_splits;
-  const int uy = blockIdx.x / a.n_splits;
-  const int h = uy % a.n_kv, rt = uy / a.n_kv, b = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvRows& R = a.rows;
 
-  int q0, n, L;
-  unsigned bad;
-  const bool use = kv_row(R, b, q0, n, L, bad);
-  if (bad && split == 0 && uy == 0 && threadIdx.x == 0) record_error(a.err, kCodeDevice, bad, b, b);
-  if (!use) return;
-  const int rows = min(n * a.g - rt * kKvFewRows, kKvFewRows);
-  if (rows <= 0) return;
-  const int i_last = (rt * kKvFewRows + rows - 1) / a.g;           // the unit's last new token
-  const int seen = max(0, min(L, L - n + i_last + 1));             // cached tokens it attends to
-  // the row's own ranges: n_splits at most, whole steps of the CTA
-  int per = (seen + a.n_splits - 1) / a.n_splits;
-  per = (per + S::kStep - 1) / S::kStep * S::kStep;
-  const int ns = per > 0 ? (seen + per - 1) / per : 1;
-  if (split >= ns) return;
-  const int t0 = split * per, t1 = min(seen, t0 + per);
-
-  float o[DH / 8][4];
-#pragma unroll
-  for (int i = 0; i < DH / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  uint8_t* ring = smem + warp * S::kWarp;
-  const uint32_t ring_a = smem_u32(ring);
-  const int first = t0 + warp * kTok;
-  const int n_it = first < t1 ? (t1 - first + S::kStep - 1) / S::kStep : 0;
-  const uint16_t* kb = static_cast<const uint16_t*>(a.pages.k) + h * DH;
-  const uint16_t* vb = static_cast<const uint16_t*>(a.pages.v) + h * DH;
-  const int64_t tok_stride = (int64_t)a.n_kv * DH;
-
-  // slot of this lane's token of step `it` (-1: past the range, or a page outside the pool)
-  auto slot_of = [&](int it) -> int {
-    const int t = first + it * S::kStep + lane;
-    if (it >= n_it || lane >= kTok || t >= t1) return -1;
-    const int64_t s = kv_slot(R, a.pages, b, t);
-    if (s < 0) record_error(a.err, kCodeDevice, kErrPage, t, b);
-    return int(s);
+  // steps of a row (0: nothing to do); one without cached tokens takes a step too, for its empty outputs
+  auto row_steps = [&](int b, bool report) -> int {
+    if (b >= R.batch) return 0;
+    int q0, n, L;
+    unsigned bad;
+    const bool use = kv_row(R, b, q0, n, L, bad);
+    if (bad && report) record_error(a.err, kCodeDevice, bad, b, b);
+    return !use || n == 0 ? 0 : max(1, (L + S::kStep - 1) / S::kStep);
   };
-  auto load = [&](int it, int slot) {
-    if (it < n_it) {
-      const uint32_t st = ring_a + (it % kStages) * 2 * S::kTile;
-      constexpr int kCh = DH / 8;                                  // 16-byte chunks of a row
-#pragma unroll
-      for (int x = 0; x < kTok * kCh / 32; ++x) {
-        const int row = (x * 32 + lane) / kCh, ch = lane % kCh;
-        const int s = __shfl_sync(0xffffffffu, slot, row);
-        const int64_t off = s < 0 ? 0 : s * tok_stride + ch * 8;
-        const int bytes = s < 0 ? 0 : 16;
-        cp16(st + swz<DH>(row, ch), kb + off, bytes);
-        cp16(st + S::kTile + swz<DH>(row, ch), vb + off, bytes);
-      }
+  const int steps0 = row_steps(lane, blockIdx.x == 0 && warp == 0);
+  int64_t all = __reduce_add_sync(0xffffffffu, steps0);
+  for (int b0 = 32; b0 < R.batch; b0 += 32)
+    all += __reduce_add_sync(0xffffffffu, row_steps(b0 + lane, blockIdx.x == 0 && warp == 0));
+  if (all == 0) return;
+  // A piece's length: at least an equal share of all CTAs that the GPU holds. Up to 32 rows, each lane weighs one
+  // length, 1 to 3 times that share: the waves of CTAs times the length and what a CTA's start and end cost (eight
+  // steps), and the join of what is cut (four). More rows are cut a quarter longer than the share.
+  const int share = int(max((int64_t)1, (all * a.n_kv + a.ctas - 1) / a.ctas));
+  int per = share + share / 4;
+  if (R.batch <= 32) {
+    const int mine = share + share * lane / 16;
+    const float inv = 1.f / mine;
+    int count = 0, cuts = 0;
+    for (int b = 0; b < R.batch; ++b) {
+      const int p = int(ceilf(__shfl_sync(0xffffffffu, steps0, b) * inv));
+      count += p;
+      cuts |= p > 1;
     }
-    cp_commit();
-  };
-
-  int next = slot_of(0);
-#pragma unroll
-  for (int it = 0; it < kStages - 1; ++it) {
-    const int cur = next;
-    next = slot_of(it + 1);
-    load(it, cur);
+    const unsigned est = unsigned((count * a.n_kv + a.ctas - 1) / a.ctas) * unsigned(mine + 8) + (cuts ? 4u : 0u);
+    const unsigned least = __reduce_min_sync(0xffffffffu, est);
+    per = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, est == least)) - 1);
+  }
+  Cut cut0;
+  cut_rows(steps0, per, cut0, 0, 0);
+  int pieces_all = cut0.total;
+  if (R.batch > 32) {
+    Cut x = cut0;
+    for (int b0 = 32; b0 < R.batch; b0 += 32) cut_rows(row_steps(b0 + lane, false), per, x, x.total, x.total_cut);
+    pieces_all = x.total;
   }
 
-  // query rows as the A operand: row = lane / 4 and + 8, column pairs by lane % 4
-  const int r0 = lane >> 2, cp = lane & 3;
-  uint32_t qf[DH / 16][4];
-  int vis[2];                                                      // last slot the two query rows see
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int rr = rt * kKvFewRows + r0 + 8 * x;
-    const bool ok = r0 + 8 * x < rows;
-    const int i = rr / a.g, head = h * a.g + rr % a.g;
-    vis[x] = ok ? L - n + i : -1;
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
-                                                          (int64_t)(q0 + i) * a.q_stride + head * DH);
-#pragma unroll
-    for (int k = 0; k < DH / 16; ++k) {
-      qf[k][x] = ok ? p[k * 8 + cp] : 0u;
-      qf[k][2 + x] = ok ? p[k * 8 + 4 + cp] : 0u;
+  for (int64_t idx = blockIdx.x; idx < (int64_t)pieces_all * a.n_kv; idx += gridDim.x) {
+    // the piece's row b, head h and number among the unit's np, and its place among those of cut units
+    Cut x = cut0;
+    int b = 0;
+    unsigned at;
+    while (!(at = __ballot_sync(0xffffffffu, idx < (int64_t)(x.start + x.pieces) * a.n_kv))) {
+      b += 32;
+      cut_rows(row_steps(b + lane, false), per, x, x.total, x.total_cut);
     }
-  }
-  const int vis_min = L - n + rt * kKvFewRows / a.g;               // every row sees slots up to here
+    const int src = __ffs(at) - 1;
+    b += src;
+    const int np = __shfl_sync(0xffffffffu, x.pieces, src);
+    const int in_row = int(idx - (int64_t)__shfl_sync(0xffffffffu, x.start, src) * a.n_kv);
+    const int h = in_row / np, piece = in_row % np;
+    const int first_slot = __shfl_sync(0xffffffffu, x.cut, src) * a.n_kv + h * np;
+    int q0, n, L;
+    unsigned bad;
+    kv_row(R, b, q0, n, L, bad);
+    const int rows = n * a.g;
+    int len = (L + S::kStep - 1) / S::kStep;                       // the row's steps, cut evenly
+    len = (len + np - 1) / np * S::kStep;
+    const int t0 = min(L, piece * len), t1 = min(L, t0 + len);
 
-  for (int it = 0; it < n_it; ++it) {
-    {
-      const int cur = next;
-      next = slot_of(it + kStages);
-      load(it + kStages - 1, cur);
-    }
-    cp_wait<kStages - 1>();
-    __syncwarp();
-    const uint32_t ks = ring_a + (it % kStages) * 2 * S::kTile, vs = ks + S::kTile;
-    float s[kNT][4];
+    float o[DH / 8][4];
 #pragma unroll
-    for (int i = 0; i < kNT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-    const int tr = ((lane >> 4) & 1) * 8 + (lane & 7), kc = (lane >> 3) & 1;
+    for (int i = 0; i < DH / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    uint8_t* ring = smem + warp * S::kWarp;
+    const uint32_t ring_a = smem_u32(ring);
+    const int first = t0 + warp * kTok;
+    const int n_it = first < t1 ? (t1 - first + S::kStep - 1) / S::kStep : 0;
+    const uint16_t* kb = static_cast<const uint16_t*>(a.pages.k) + h * DH;
+    const uint16_t* vb = static_cast<const uint16_t*>(a.pages.v) + h * DH;
+    const int64_t tok_stride = (int64_t)a.n_kv * DH;
+
+    // slot of this lane's token of step `it` (-1: past the range, or a page outside the pool)
+    auto slot_of = [&](int it) -> int {
+      const int t = first + it * S::kStep + lane;
+      if (it >= n_it || lane >= kTok || t >= t1) return -1;
+      const int64_t s = kv_slot(R, a.pages, b, t);
+      if (s < 0) record_error(a.err, kCodeDevice, kErrPage, t, b);
+      return int(s);
+    };
+    auto load = [&](int it, int slot) {
+      if (it < n_it) {
+        const uint32_t st = ring_a + (it % kStages) * 2 * S::kTile;
+        constexpr int kCh = DH / 8;                                  // 16-byte chunks of a row
 #pragma unroll
-    for (int k = 0; k < DH / 16; ++k) {
-#pragma unroll
-      for (int p = 0; p < kNT / 2; ++p) {
-        uint32_t f[4];
-        ldsm4(f, ks + swz<DH>(p * 16 + tr, k * 2 + kc));
-        mma<BF16>(s[2 * p], qf[k], f[0], f[1]);
-        mma<BF16>(s[2 * p + 1], qf[k], f[2], f[3]);
-      }
-    }
-    const int tb = first + it * S::kStep;
-    if (tb + kTok > t1 || tb + kTok - 1 > vis_min) {
-#pragma unroll
-      for (int i = 0; i < kNT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = tb + i * 8 + cp * 2 + (e & 1);
-          if (t >= t1 || t > vis[e >> 1]) s[i][e] = -INFINITY;
+        for (int x = 0; x < kTok * kCh / 32; ++x) {
+          const int row = (x * 32 + lane) / kCh, ch = lane % kCh;
+          const int s = __shfl_sync(0xffffffffu, slot, row);
+          const int64_t off = s < 0 ? 0 : s * tok_stride + ch * 8;
+          const int bytes = s < 0 ? 0 : 16;
+          cp16(st + swz<DH>(row, ch), kb + off, bytes);
+          cp16(st + S::kTile + swz<DH>(row, ch), vb + off, bytes);
         }
+      }
+      cp_commit();
+    };
+
+    int next = slot_of(0);
+#pragma unroll
+    for (int it = 0; it < kStages - 1; ++it) {
+      const int cur = next;
+      next = slot_of(it + 1);
+      load(it, cur);
     }
-    float al[2], base[2];
+
+    // query rows as the A operand: row = lane / 4 and + 8, column pairs by lane % 4
+    const int r0 = lane >> 2, cp = lane & 3;
+    uint32_t qf[DH / 16][4];
+    int vis[2];                                                      // last slot the two query rows see
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      float mx = fmaxf(s[0][2 * x], s[0][2 * x + 1]);
+      const int rr = r0 + 8 * x;
+      const bool ok = rr < rows;
+      const int i = rr / a.g, head = h * a.g + rr % a.g;
+      vis[x] = ok ? L - n + i : -1;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
+                                                            (int64_t)(q0 + i) * a.q_stride + head * DH);
 #pragma unroll
-      for (int i = 1; i < kNT; ++i) mx = fmaxf(mx, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[x], mx * a.scale_log2);
-      base[x] = mn == -INFINITY ? 0.f : mn;                        // nothing seen yet: every p is 2^-inf = 0
-      al[x] = ex2(m[x] - base[x]);
-      m[x] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kNT; ++i) {
-        s[i][2 * x] = ex2(fmaf(s[i][2 * x], a.scale_log2, -base[x]));
-        s[i][2 * x + 1] = ex2(fmaf(s[i][2 * x + 1], a.scale_log2, -base[x]));
-        sum += s[i][2 * x] + s[i][2 * x + 1];
-      }
-      l[x] = fmaf(l[x], al[x], sum);
-    }
-    if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
-#pragma unroll
-      for (int i = 0; i < DH / 8; ++i) {
-        o[i][0] *= al[0];
-        o[i][1] *= al[0];
-        o[i][2] *= al[1];
-        o[i][3] *= al[1];
+      for (int k = 0; k < DH / 16; ++k) {
+        qf[k][x] = ok ? p[k * 8 + cp] : 0u;
+        qf[k][2 + x] = ok ? p[k * 8 + 4 + cp] : 0u;
       }
     }
-    const int vr = ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
-#pragma unroll
-    for (int k = 0; k < kNT / 2; ++k) {
-      const uint32_t pf[4] = {pack2<BF16>(s[2 * k][0], s[2 * k][1]), pack2<BF16>(s[2 * k][2], s[2 * k][3]),
-                              pack2<BF16>(s[2 * k + 1][0], s[2 * k + 1][1]),
-                              pack2<BF16>(s[2 * k + 1][2], s[2 * k + 1][3])};
-#pragma unroll
-      for (int i = 0; i < DH / 16; ++i) {
-        uint32_t f[4];
-        ldsm4t(f, vs + swz<DH>(k * 16 + vr, 2 * i + vc));
-        mma<BF16>(o[2 * i], pf, f[0], f[1]);
-        mma<BF16>(o[2 * i + 1], pf, f[2], f[3]);
-      }
-    }
-    __syncwarp();
-  }
-  cp_wait<0>();
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-  }
-  __syncthreads();
+    const int vis_min = L - n;                                       // every row sees slots up to here
 
-  // join the warps: each leaves its output rows in the (now free) ring
-  float* ob = reinterpret_cast<float*>(smem) + warp * kKvFewRows * DH;
-  if (cp == 0) {
-    ml_s[warp][r0] = make_float2(m[0], l[0]);
-    ml_s[warp][r0 + 8] = make_float2(m[1], l[1]);
-  }
+    for (int it = 0; it < n_it; ++it) {
+      {
+        const int cur = next;
+        next = slot_of(it + kStages);
+        load(it + kStages - 1, cur);
+      }
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t ks = ring_a + (it % kStages) * 2 * S::kTile, vs = ks + S::kTile;
+      float s[kNT][4];
 #pragma unroll
-  for (int i = 0; i < DH / 8; ++i) {
-    *reinterpret_cast<float2*>(ob + r0 * DH + i * 8 + cp * 2) = make_float2(o[i][0], o[i][1]);
-    *reinterpret_cast<float2*>(ob + (r0 + 8) * DH + i * 8 + cp * 2) = make_float2(o[i][2], o[i][3]);
-  }
-  __syncthreads();
-  if (threadIdx.x < kKvFewRows) {
-    const int r = threadIdx.x;
-    float M = -INFINITY, Lsum = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml_s[w][r].x);
-    for (int w = 0; w < kWarps; ++w) {
-      const float x = M == -INFINITY ? 0.f : ex2(ml_s[w][r].x - M);
-      wgt[w][r] = x;
-      Lsum = fmaf(ml_s[w][r].y, x, Lsum);
+      for (int i = 0; i < kNT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      const int tr = ((lane >> 4) & 1) * 8 + (lane & 7), kc = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < DH / 16; ++k) {
+#pragma unroll
+        for (int p = 0; p < kNT / 2; ++p) {
+          uint32_t f[4];
+          ldsm4(f, ks + swz<DH>(p * 16 + tr, k * 2 + kc));
+          mma<BF16>(s[2 * p], qf[k], f[0], f[1]);
+          mma<BF16>(s[2 * p + 1], qf[k], f[2], f[3]);
+        }
+      }
+      const int tb = first + it * S::kStep;
+      if (tb + kTok > t1 || tb + kTok - 1 > vis_min) {
+#pragma unroll
+        for (int i = 0; i < kNT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = tb + i * 8 + cp * 2 + (e & 1);
+            if (t >= t1 || t > vis[e >> 1]) s[i][e] = -INFINITY;
+          }
+      }
+      float al[2], base[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float mx = fmaxf(s[0][2 * x], s[0][2 * x + 1]);
+#pragma unroll
+        for (int i = 1; i < kNT; ++i) mx = fmaxf(mx, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[x], mx * a.scale_log2);
+        base[x] = mn == -INFINITY ? 0.f : mn;                        // nothing seen yet: every p is 2^-inf = 0
+        al[x] = ex2(m[x] - base[x]);
+        m[x] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) {
+          s[i][2 * x] = ex2(fmaf(s[i][2 * x], a.scale_log2, -base[x]));
+          s[i][2 * x + 1] = ex2(fmaf(s[i][2 * x + 1], a.scale_log2, -base[x]));
+          sum += s[i][2 * x] + s[i][2 * x + 1];
+        }
+        l[x] = fmaf(l[x], al[x], sum);
+      }
+      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i) {
+          o[i][0] *= al[0];
+          o[i][1] *= al[0];
+          o[i][2] *= al[1];
+          o[i][3] *= al[1];
+        }
+      }
+      const int vr = ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
+#pragma unroll
+      for (int k = 0; k < kNT / 2; ++k) {
+        const uint32_t pf[4] = {pack2<BF16>(s[2 * k][0], s[2 * k][1]), pack2<BF16>(s[2 * k][2], s[2 * k][3]),
+                                pack2<BF16>(s[2 * k + 1][0], s[2 * k + 1][1]),
+                                pack2<BF16>(s[2 * k + 1][2], s[2 * k + 1][3])};
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i) {
+          uint32_t f[4];
+          ldsm4t(f, vs + swz<DH>(k * 16 + vr, 2 * i + vc));
+          mma<BF16>(o[2 * i], pf, f[0], f[1]);
+          mma<BF16>(o[2 * i + 1], pf, f[2], f[3]);
+        }
+      }
+      __syncwarp();
     }
-    tot[r] = make_float2(M, Lsum);
-  }
-  __syncthreads();
+    cp_wait<0>();
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    }
+    __syncthreads();
 
-  const float* of = reinterpret_cast<const float*>(smem);
-  const int64_t unit = (int64_t)b * (gridDim.x / a.n_splits) + uy;
-  auto write_lse = [&](int r, float M, float Lsum) {
-    const int rr = rt * kKvFewRows + r;
-    if (a.lse)
-      a.lse[(int64_t)(q0 + rr / a.g) * a.n_heads + h * a.g + rr % a.g] =
-          Lsum == 0.f ? -INFINITY : (M + log2f(Lsum)) * 0.69314718055994531f;
-  };
-  auto out_at = [&](int r) -> int64_t {
-    const int rr = rt * kKvFewRows + r;
-    return ((int64_t)(q0 + rr / a.g) * a.n_heads + h * a.g + rr % a.g) * DH;
-  };
-  if (ns == 1) {
-    for (int x = threadIdx.x; x < rows * (DH / 2); x += kWarps * 32) {
-      const int r = x / (DH / 2), c = x % (DH / 2) * 2;
+    // join the warps: each leaves its output rows in the (now free) ring
+    float* ob = reinterpret_cast<float*>(smem) + warp * kKvFewRows * DH;
+    if (cp == 0) {
+      ml_s[warp][r0] = make_float2(m[0], l[0]);
+      ml_s[warp][r0 + 8] = make_float2(m[1], l[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < DH / 8; ++i) {
+      *reinterpret_cast<float2*>(ob + r0 * DH + i * 8 + cp * 2) = make_float2(o[i][0], o[i][1]);
+      *reinterpret_cast<float2*>(ob + (r0 + 8) * DH + i * 8 + cp * 2) = make_float2(o[i][2], o[i][3]);
+    }
+    __syncthreads();
+    if (threadIdx.x < kKvFewRows) {
+      const int r = threadIdx.x;
+      float M = -INFINITY, Lsum = 0.f;
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml_s[w][r].x);
+      for (int w = 0; w < kWarps; ++w) {
+        const float x = M == -INFINITY ? 0.f : ex2(ml_s[w][r].x - M);
+        wgt[w][r] = x;
+        Lsum = fmaf(ml_s[w][r].y, x, Lsum);
+      }
+      tot[r] = make_float2(M, Lsum);
+    }
+    __syncthreads();
+
+    const float* of = reinterpret_cast<const float*>(smem);
+    auto write_lse = [&](int r, float M, float Lsum) {
+      if (a.lse)
+        a.lse[(int64_t)(q0 + r / a.g) * a.n_heads + h * a.g + r % a.g] =
+            Lsum == 0.f ? -INFINITY : (M + log2f(Lsum)) * 0.69314718055994531f;
+    };
+    auto out_at = [&](int r) -> int64_t { return ((int64_t)(q0 + r / a.g) * a.n_heads + h * a.g + r % a.g) * DH; };
+    const bool whole = np == 1;
+    float* po = a.part_o + (int64_t)(first_slot + piece) * kKvFewRows * DH;
+    for (int x = tid; x < rows * (DH / 2); x += kWarps * 32) {
+      const int r = x / (DH / 2), cl = x % (DH / 2) * 2;
       float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 u = *reinterpret_cast<const float2*>(of + (w * kKvFewRows + r) * DH + c);
-        v.x = fmaf(u.x, wgt[w][r], v.x);
-        v.y = fmaf(u.y, wgt[w][r], v.y);
+      for (int y = 0; y < kWarps; ++y) {
+        const float2 u = *reinterpret_cast<const float2*>(of + (y * kKvFewRows + r) * DH + cl);
+        v.x = fmaf(u.x, wgt[y][r], v.x);
+        v.y = fmaf(u.y, wgt[y][r], v.y);
       }
-      const float Lsum = tot[r].y, inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out_at(r) + c) = pack2<BF16>(v.x * inv, v.y * inv);
-      if (c == 0) write_lse(r, tot[r].x, Lsum);
+      if (whole) {
+        const float Lsum = tot[r].y, inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out_at(r) + cl) = pack2<BF16>(v.x * inv, v.y * inv);
+        if (cl == 0) write_lse(r, tot[r].x, Lsum);
+      } else {
+        *reinterpret_cast<float2*>(po + r * DH + cl) = v;
+      }
     }
-    return;
-  }
-  float* po = a.part_o + (unit * a.n_splits + split) * kKvFewRows * DH;
-  for (int x = threadIdx.x; x < rows * (DH / 2); x += kWarps * 32) {
-    const int r = x / (DH / 2), c = x % (DH / 2) * 2;
-    float2 v = make_float2(0.f, 0.f);
+    if (!whole) {
+      if (tid < rows) a.part_ml[(int64_t)(first_slot + piece) * kKvFewRows + tid] = tot[tid];
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) last_cta = atomicAdd(&a.counters[first_slot], 1u) == unsigned(np - 1);
+      __syncthreads();
+      if (last_cta) {
+        __threadfence();
+        // join the pieces, in their order
+        float* wr = reinterpret_cast<float*>(smem);                  // [rows][np] weights
+        auto slot = [&](int k) { return (int64_t)(first_slot + k) * kKvFewRows; };
+        for (int r = warp; r < rows; r += kWarps) {
+          float M = -INFINITY, Lsum = 0.f;
+          for (int k = lane; k < np; k += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot(k) + r]).x);
+          M = warp_max(M);
+          for (int k = lane; k < np; k += 32) {
+            const float2 v = __ldcg(&a.part_ml[slot(k) + r]);
+            const float x = M == -INFINITY ? 0.f : ex2(v.x - M);
+            wr[r * np + k] = x;
+            Lsum = fmaf(v.y, x, Lsum);
+          }
+          Lsum = warp_sum(Lsum);
+          if (lane == 0) tot[r] = make_float2(M, Lsum);
+        }
+        __syncthreads();
+        for (int x = tid; x < rows * (DH / 4); x += kWarps * 32) {
+          const int r = x / (DH / 4), cl = x % (DH / 4) * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k0 = 0; k0 < np; k0 += 8) {                   // eight pieces' loads in flight
+            float4 u[8];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 u = *reinterpret_cast<const float2*>(of + (w * kKvFewRows + r) * DH + c);
-      v.x = fmaf(u.x, wgt[w][r], v.x);
-      v.y = fmaf(u.y, wgt[w][r], v.y);
+            for (int y = 0; y < 8; ++y)
+              if (k0 + y < np)
+                u[y] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(k0 + y) + r) * DH + cl));
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              if (k0 + y < np) {
+                const float f = wr[r * np + k0 + y];
+                v.x = fmaf(u[y].x, f, v.x);
+                v.y = fmaf(u[y].y, f, v.y);
+                v.z = fmaf(u[y].z, f, v.z);
+                v.w = fmaf(u[y].w, f, v.w);
+              }
+          }
+          const float Lsum = tot[r].y, inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_at(r) + cl) =
+              make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+          if (cl == 0) write_lse(r, tot[r].x, Lsum);
+        }
+        if (tid == 0) a.counters[first_slot] = 0u;
+      }
     }
-    *reinterpret_cast<float2*>(po + r * DH + c) = v;
+    __syncthreads();                                                 // the joins' space becomes the ring again
   }
-  if (threadIdx.x < rows) a.part_ml[(unit * a.n_splits + split) * kKvFewRows + threadIdx.x] = tot[threadIdx.x];
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last_cta = atomicAdd(&a.counters[unit], 1u) == unsigned(ns - 1);
-  __syncthreads();
-  if (!last_cta) return;
-  __threadfence();
-  // join the ranges, in their order
-  float* wr = reinterpret_cast<float*>(smem);                       // [rows][ns] weights
-  const float2* pm = a.part_ml + unit * a.n_splits * kKvFewRows;
-  for (int r = warp; r < rows; r += kWarps) {
-    float M = -INFINITY, Lsum = 0.f;
-    for (int k = lane; k < ns; k += 32) M = fmaxf(M, __ldcg(&pm[k * kKvFewRows + r]).x);
-    M = warp_max(M);
-    for (int k = lane; k < ns; k += 32) {
-      const float2 v = __ldcg(&pm[k * kKvFewRows + r]);
-      const float x = M == -INFINITY ? 0.f : ex2(v.x - M);
-      wr[r * ns + k] = x;
-      Lsum = fmaf(v.y, x, Lsum);
-    }
-    Lsum = warp_sum(Lsum);
-    if (lane == 0) tot[r] = make_float2(M, Lsum);
-  }
-  __syncthreads();
-  const float* pb = a.part_o + unit * a.n_splits * kKvFewRows * DH;
-  for (int x = threadIdx.x; x < rows * (DH / 2); x += kWarps * 32) {
-    const int r = x / (DH / 2), c = x % (DH / 2) * 2;
-    float2 v = make_float2(0.f, 0.f);
-    for (int k = 0; k < ns; ++k) {
-      const float2 u = __ldcg(reinterpret_cast<const float2*>(pb + ((int64_t)k * kKvFewRows + r) * DH + c));
-      v.x = fmaf(u.x, wr[r * ns + k], v.x);
-      v.y = fmaf(u.y, wr[r * ns + k], v.y);
-    }
-    const float Lsum = tot[r].y, inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out_at(r) + c) = pack2<BF16>(v.x * inv, v.y * inv);
-    if (c == 0) write_lse(r, tot[r].x, Lsum);
-  }
-  if (threadIdx.x == 0) a.counters[unit] = 0u;
 }
 
 template <int DH, bool BF16> cudaError_t prepare_few() {
   return cudaFuncSetAttribute(kv_attend_few_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Sm<DH>::kBytes);
 }
-template <int DH, bool BF16> cudaError_t launch_few(const KvAttendArgs& a, cudaStream_t st) {
-  const int64_t tiles = ((int64_t)a.rows.max_new * a.g + kKvFewRows - 1) / kKvFewRows;
-  const dim3 grid((unsigned)(tiles * a.n_kv * a.n_splits), (unsigned)a.rows.batch);
-  kv_attend_few_kernel<DH, BF16><<<grid, kWarps * 32, Sm<DH>::kBytes, st>>>(a);
+template <int DH, bool BF16> cudaError_t launch_few(const KvAttendArgs& a, int ctas, cudaStream_t st) {
+  kv_attend_few_kernel<DH, BF16><<<ctas, kWarps * 32, Sm<DH>::kBytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -374,9 +450,14 @@ cudaError_t prepare_kv_attend_few(int head_dim, bool bf16) {
   return bf16 ? prepare_few<64, true>() : prepare_few<64, false>();
 }
 
-cudaError_t launch_kv_attend_few(const KvAttendArgs& a, cudaStream_t st) {
-  if (a.head_dim == 128) return a.bf16 ? launch_few<128, true>(a, st) : launch_few<128, false>(a, st);
-  return a.bf16 ? launch_few<64, true>(a, st) : launch_few<64, false>(a, st);
+cudaError_t launch_kv_attend_few(KvAttendArgs a, int sm_count, cudaStream_t st) {
+  // the cut aims at the CTAs that the GPU holds; no more are launched than the rows' bounds give steps
+  a.ctas = kKvFewCtas * sm_count < kKvFewMostCtas ? kKvFewCtas * sm_count : kKvFewMostCtas;
+  const int step = kKvFewTokens * 128 / a.head_dim;
+  const int64_t steps = (((int64_t)a.rows.max_kv_len + step - 1) / step + 1) * a.rows.batch * a.n_kv;
+  const int grid = steps < a.ctas ? (int)steps : a.ctas;
+  if (a.head_dim == 128) return a.bf16 ? launch_few<128, true>(a, grid, st) : launch_few<128, false>(a, grid, st);
+  return a.bf16 ? launch_few<64, true>(a, grid, st) : launch_few<64, false>(a, grid, st);
 }
 
 }  // namespace palu

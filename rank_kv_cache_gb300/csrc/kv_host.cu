@@ -12,10 +12,9 @@ namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Split partials of a call: a unit that is cut into ranges takes one slot a range. Plans keep to these
-// numbers (a few waves of CTAs), so the workspace does not grow with the call. The two kernels' partials
-// share the space.
-constexpr int kPartSlots = 2048;   // few rows: ranges of 16 query rows
+// Partials of a call: work that is cut takes a slot for each piece. The cuts keep to these numbers, so the
+// workspace does not grow with the call. The two kernels' partials share the space.
+constexpr int kPartSlots = 2 * kKvFewMostCtas;   // few rows: pieces of 16 query rows
 constexpr int kTcSlots = 456;      // tensor-core kernel: pieces x key/value heads, of two 128-row tiles
 
 struct KvLayout {
@@ -335,10 +334,13 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
   a.counters = reinterpret_cast<unsigned*>(h->ws + h->L.counters);
   a.err = reinterpret_cast<ErrWord*>(h->ws + h->L.err);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // One 16-row tile holds every row's queries: the few-row kernel streams the cache once. More rows: the
-  // tensor-core kernel (see there for the sizes at which each was measured).
-  const int64_t cached_rows = a.pages.n_pages * a.pages.page_size * a.n_kv;
-  if ((int64_t)a.rows.max_new * a.g > kKvFewRows && cached_rows < (int64_t(1) << 31) - 1) {
+  cudaError_t e;
+  if ((int64_t)a.rows.max_new * a.g <= kKvFewRows) {
+    // 16 query rows hold every row's tokens: the few-row kernel streams the cache once
+    e = launch_kv_attend_few(a, h->sm_count, s);
+  } else {
+    // the gathers index cached head rows with 31 bits
+    if (pages->n_pages * pages->page_size * d.n_kv_heads >= (int64_t(1) << 31) - 1) return PALU_ERR_UNSUPPORTED;
     KvTcPlan t{};
     t.head = reinterpret_cast<KvPlanHead*>(h->ws + h->L.head);
     t.items = reinterpret_cast<KvItem*>(h->ws + h->L.items);
@@ -347,27 +349,9 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
     t.tile_cap = (int)tc_tile_cap(d, rows->n_tokens, rows->batch);
     t.slots = kTcSlots;
     t.sm_count = h->sm_count;
-    const cudaError_t e = launch_kv_attend_tc(a, t, s);
-    return e == cudaSuccess ? PALU_OK : e == cudaErrorNotSupported ? PALU_ERR_UNSUPPORTED : PALU_ERR_CUDA;
+    e = launch_kv_attend_tc(a, t, s);
+    if (e == cudaErrorNotSupported) return PALU_ERR_UNSUPPORTED;
   }
-  // Ranges of a unit: enough CTAs to fill the GPU in whole waves, each range worth its start and join.
-  const int64_t units = (((int64_t)a.rows.max_new * a.g + kKvFewRows - 1) / kKvFewRows) * a.n_kv * a.rows.batch;
-  if (units >= (int64_t(1) << 31)) return PALU_ERR_UNSUPPORTED;
-  const int step = kKvFewTokens * 128 / d.head_dim;
-  const int64_t steps = (a.rows.max_kv_len + step - 1) / step, ctas = (int64_t)kKvFewCtas * h->sm_count;
-  int64_t best = 1;
-  double least = 1e300;
-  for (int64_t k = 1; k <= steps && k <= kKvFewSplits && k * units <= kPartSlots; ++k) {
-    const int64_t per = (steps + k - 1) / k;
-    if ((steps + per - 1) / per != k) continue;
-    const double est = double((units * k + ctas - 1) / ctas) * double(per + 2);
-    if (est < least - 1e-9) {
-      least = est;
-      best = k;
-    }
-  }
-  a.n_splits = (int)best;
-  const cudaError_t e = launch_kv_attend_few(a, s);
   return e == cudaSuccess ? PALU_OK : PALU_ERR_CUDA;
 }
 
