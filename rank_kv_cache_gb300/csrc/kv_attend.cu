@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
   // A piece's length: at least an equal share of all CTAs that the GPU holds. Up to 32 rows, each lane weighs one
   // length, 1 to 3 times that share: the waves of CTAs times the length and what a CTA's start and end cost (eight
   // steps), and the join of what is cut (four). More rows are cut a quarter longer than the share.
-  const int share = int(max((int64_t)1, (all * a.n_kv + a.ctas - 1) / a.ctas));
+  const int64_t work = all * a.n_kv;
+  const int share = work < (1 << 30) ? (int(work) + a.ctas - 1) / a.ctas : int((work + a.ctas - 1) / a.ctas);
   int per = share + share / 4;
   if (R.batch <= 32) {
     const int mine = share + share * lane / 16;
@@ -151,19 +152,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
     pieces_all = x.total;
   }
 
-  for (int64_t idx = blockIdx.x; idx < (int64_t)pieces_all * a.n_kv; idx += gridDim.x) {
+  for (int idx = blockIdx.x; idx < pieces_all * a.n_kv; idx += gridDim.x) {
     // the piece's row b, head h and number among the unit's np, and its place among those of cut units
     Cut x = cut0;
     int b = 0;
     unsigned at;
-    while (!(at = __ballot_sync(0xffffffffu, idx < (int64_t)(x.start + x.pieces) * a.n_kv))) {
+    while (!(at = __ballot_sync(0xffffffffu, idx < (x.start + x.pieces) * a.n_kv))) {
       b += 32;
       cut_rows(row_steps(b + lane, false), per, x, x.total, x.total_cut);
     }
     const int src = __ffs(at) - 1;
     b += src;
     const int np = __shfl_sync(0xffffffffu, x.pieces, src);
-    const int in_row = int(idx - (int64_t)__shfl_sync(0xffffffffu, x.start, src) * a.n_kv);
+    const int in_row = idx - __shfl_sync(0xffffffffu, x.start, src) * a.n_kv;
     const int h = in_row / np, piece = in_row % np;
     const int first_slot = __shfl_sync(0xffffffffu, x.cut, src) * a.n_kv + h * np;
     int q0, n, L;

@@ -17,34 +17,34 @@
 namespace palu {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
-// eight consecutive elements as floats
+// eight consecutive elements: as they lie in memory, and as four packed pairs of fp32 values
 template <typename T> struct Vec8 {
-  static __device__ __forceinline__ void load(const void* base, int64_t i, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
-    const T* e = reinterpret_cast<const T*>(&u);
+  uint4 r[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = to_f32(e[j]);
+    for (int k = 0; k < int(sizeof(T) / 2); ++k) r[k] = p[k];
   }
-  static __device__ __forceinline__ void store(void* base, int64_t i, const float (&x)[8]) {
-    uint4 u;
-    T* e = reinterpret_cast<T*>(&u);
+  __device__ __forceinline__ void store(void* base, int64_t i) const {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(base) + i);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = from_f32<T>(x[j]);
-    *reinterpret_cast<uint4*>(static_cast<T*>(base) + i) = u;
+    for (int k = 0; k < int(sizeof(T) / 2); ++k) p[k] = r[k];
   }
-};
-template <> struct Vec8<float> {
-  static __device__ __forceinline__ void load(const void* base, int64_t i, float (&x)[8]) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  __device__ __forceinline__ void get(uint64_t (&x)[4]) const {
+    const T* e = reinterpret_cast<const T*>(r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = pair(to_f32(e[2 * j]), to_f32(e[2 * j + 1]));
   }
-  static __device__ __forceinline__ void store(void* base, int64_t i, const float (&x)[8]) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __device__ __forceinline__ void set(const uint64_t (&x)[4]) {
+    T* e = reinterpret_cast<T*>(r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = unpair(x[j]);
+      e[2 * j] = from_f32<T>(v.x);
+      e[2 * j + 1] = from_f32<T>(v.y);
+    }
   }
 };
 
@@ -67,11 +67,26 @@ template <typename TI, typename TO, int DH>
 __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a, const __grid_constant__ KvFreq f,
                                                            int parts, int chunks_per_part) {
   constexpr int kLanes = DH / 16;          // lanes of a head
-  constexpr int kHeads = 32 / kLanes;      // heads a warp takes at once
+  constexpr int kHeads = 32 / kLanes;      // heads a warp takes at once: a chunk
   const int lane = threadIdx.x & 31, j = lane % kLanes, hl = lane / kLanes;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int t = int(unit / parts), part = int(unit % parts);
+  const unsigned unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int t = int(unit / unsigned(parts)), part = int(unit % unsigned(parts));
   if (t >= a.n_tokens) return;
+  const int nq = a.heads[0], nk = a.heads[1], total = nq + nk + a.heads[2];
+  const int c0 = part * chunks_per_part, c1 = min(c0 + chunks_per_part, (total + kHeads - 1) / kHeads);
+
+  auto side_of = [&](int h) { return h < nq ? 0 : h < nq + nk ? 1 : 2; };
+  auto in_side = [&](int h, int side) { return h - (side == 0 ? 0 : side == 1 ? nq : nq + nk); };
+  Vec8<TI> lo, hi;                         // the chunk that comes next
+  auto load = [&](int c) {
+    const int h = c * kHeads + hl, side = side_of(h);
+    if (c < c1 && h < total) {
+      const int64_t at = (int64_t)t * a.src_stride[side] + in_side(h, side) * DH + j * 8;
+      lo.load(a.src[side], at);
+      hi.load(a.src[side], at + DH / 2);
+    }
+  };
+  load(c0);                                // under way while the token's place and angles are found
 
   // the token's position and, for the append, its slot in the pages
   int pos = 0;
@@ -86,72 +101,83 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a, c
     if (slot < 0 && part == 0 && lane == 0) record_error(a.err, kCodeDevice, kErrSlot, pos, b);
   }
   if (a.positions) pos = a.positions[t];
-
-  float cs[8], sn[8];
-  if (a.rotate) {
+  uint64_t cs[4], sn[4];
+  // values alone need no angles
+  if (a.rotate && c0 * kHeads < nq + nk) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t phase = (int64_t)(uint64_t((int64_t)pos) * f.turn[j * 8 + e]);   // turns * 2^64, in [-1/2, 1/2)
-      sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &sn[e], &cs[e]);     // half turns: * 2^-63
+    for (int e = 0; e < 4; ++e) {
+      float c[2], s[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // turns * 2^64, in [-1/2, 1/2); half turns: * 2^-63
+        const int64_t phase = (int64_t)(uint64_t((int64_t)pos) * f.turn[j * 8 + 2 * e + k]);
+        sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s[k], &c[k]);
+      }
+      cs[e] = pair(c[0], c[1]);
+      sn[e] = pair(s[0], s[1]);
     }
   }
 
-  const int nq = a.heads[0], nk = a.heads[1], total = nq + nk + a.heads[2];
-  const int c1 = min((part + 1) * chunks_per_part, (total + kHeads - 1) / kHeads);
-#pragma unroll 2
-  for (int c = part * chunks_per_part; c < c1; ++c) {
-    const int h = c * kHeads + hl;
-    const int side = h < nq ? 0 : h < nq + nk ? 1 : 2;
-    const int hs = h - (side == 0 ? 0 : side == 1 ? nq : nq + nk);   // head within its side
+  uint64_t gl[4], gu[4];                   // this lane's norm weights, of the side of the chunk before
+  int g_side = 2;
+  for (int c = c0; c < c1; ++c) {
+    const Vec8<TI> xl = lo, xh = hi;
+    load(c + 1);
+    const int h = c * kHeads + hl, side = side_of(h), hs = in_side(h, side);
     const bool live = h < total;
-    float lo[8], hi[8];
-    if (live) {
-      const int64_t at = (int64_t)t * a.src_stride[side] + (int64_t)hs * DH + j * 8;
-      Vec8<TI>::load(a.src[side], at, lo);
-      Vec8<TI>::load(a.src[side], at + DH / 2, hi);
-    } else {
+    uint64_t l[4], u[4];
+    xl.get(l);
+    xh.get(u);
+    if (a.w[0] || a.w[1]) {
+      uint64_t ss2 = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) lo[e] = hi[e] = 0.f;
-    }
-    float ss = 0.f;
+      for (int e = 0; e < 4; ++e) ss2 = fma2(l[e], l[e], fma2(u[e], u[e], ss2));
+      const float2 s = unpair(ss2);
+      float ss = s.x + s.y;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!live) continue;
-    if (side < 2) {
-      if (a.w[side]) {
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (live && side < 2 && a.w[side]) {
+        if (side != g_side) {
+          Vec8<TI> w;
+          w.load(a.w[side], j * 8);
+          w.get(gl);
+          w.load(a.w[side], j * 8 + DH / 2);
+          w.get(gu);
+          g_side = side;
+        }
         const float r = rsqrtf(ss * (1.f / DH) + a.eps);
-        float wl[8], wh[8];
-        Vec8<TI>::load(a.w[side], j * 8, wl);
-        Vec8<TI>::load(a.w[side], j * 8 + DH / 2, wh);
+        const uint64_t r2 = pair(r, r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo[e] *= r * wl[e];
-          hi[e] *= r * wh[e];
+        for (int e = 0; e < 4; ++e) {
+          l[e] = mul2(l[e], mul2(r2, gl[e]));
+          u[e] = mul2(u[e], mul2(r2, gu[e]));
         }
       }
-      if (a.rotate) {
+    }
+    if (!live) continue;
+    if (a.rotate && side < 2) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = lo[e], y = hi[e];
-          lo[e] = x * cs[e] - y * sn[e];
-          hi[e] = y * cs[e] + x * sn[e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t p = l[e], q = u[e];
+        l[e] = fma2(p, cs[e], mul2(q, sn[e]) ^ 0x8000000080000000ull);
+        u[e] = fma2(q, cs[e], mul2(p, sn[e]));
       }
     }
     void* dst;
     int64_t at;
     if (side == 0 || !a.append) {
       dst = a.dst[side];
-      at = (int64_t)t * a.dst_stride[side] + (int64_t)hs * DH + j * 8;
+      at = (int64_t)t * a.dst_stride[side] + hs * DH + j * 8;
     } else {
       if (slot < 0) continue;
       dst = side == 1 ? a.pages.k : a.pages.v;
       at = (slot * nk + hs) * DH + j * 8;
     }
-    Vec8<TO>::store(dst, at, lo);
-    Vec8<TO>::store(dst, at + DH / 2, hi);
+    Vec8<TO> y;
+    y.set(l);
+    y.store(dst, at);
+    y.set(u);
+    y.store(dst, at + DH / 2);
   }
 }
 
