@@ -260,82 +260,64 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P)
 }
 
 // ------------------------------------------------------------------------------------------- join
-// A block takes eight query rows of a cut tile: o = sum_k 2^(m_k - M) o_k / L over its pieces. The weights are
-// formed once, then a thread sums four columns of a row, eight pieces' loads in flight at a time (from L2: one
-// piece after the other took a microsecond each).
-constexpr int kJoinRows = 8;
-template <int DH, bool BF16>
-__global__ void __launch_bounds__(kJoinRows * DH / 4) kv_join_kernel(const TcParams P, int max_pieces) {
-  extern __shared__ float wgt[];                           // [pieces][8 rows]
-  __shared__ float inv_s[kJoinRows];
+// one 32-byte sector
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// A block takes 32 query rows of a cut tile, a lane one row, a warp 16 of its columns:
+// o = sum_k 2^(m_k - M) o_k / L over the pieces. Four pieces' loads are in flight at a time (they come from L2:
+// one piece after the other took a microsecond each), and no thread waits for another.
+constexpr int kJoinRows = 32;
+template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_kernel(const TcParams P) {
   const KvAttendArgs& a = P.a;
   const KvTcPlan& plan = P.plan;
-  const int r8 = threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kGroups = kTile / kJoinRows;
+  const int lane = threadIdx.x & 31, c0 = (threadIdx.x >> 5) * 4;
   const int heads = plan.head->n_joins * a.n_kv;
   // the row groups run slowest, so that the tiles' live rows spread over the blocks
-  for (int u = blockIdx.x; u < heads * 2 * kGroups; u += gridDim.x) {
+  for (int u = blockIdx.x; u < heads * 2 * (kTile / kJoinRows); u += gridDim.x) {
     const KvJoin J = plan.joins[u % heads / a.n_kv];
-    const int h = u % heads % a.n_kv, tile = u / heads % 2, row0 = u / heads / 2 * kJoinRows;
-    if (tile >= J.tiles || row0 >= P.per_tile * a.g || J.tok0 + tile * P.per_tile + row0 / a.g >= J.n) continue;
-    const int pieces = min(J.pieces, max_pieces);
-    const int64_t s0 = ((int64_t)J.slot * a.n_kv + h) * 2 + tile, step = 2 * a.n_kv;
-    auto query = [&](int r, int& i) {                      // the row's token; whether it is one
-      i = J.tok0 + tile * P.per_tile + r / a.g;
-      return r < P.per_tile * a.g && i < J.n;
-    };
-    for (int x = warp; x < kJoinRows; x += blockDim.x / 32) {
-      int i;
-      const int r = row0 + x;
-      if (!query(r, i)) continue;
-      const float2* ml = a.part_ml + s0 * kTile + r;
-      float M = -INFINITY, L = 0.f;
-      for (int k = lane; k < pieces; k += 32) M = fmaxf(M, ml[k * step * kTile].x);
-      M = warp_max(M);
-      const float base = M == -INFINITY ? 0.f : M;
-      for (int k = lane; k < pieces; k += 32) {
-        const float2 v = ml[k * step * kTile];
-        const float w = exp2f(v.x - base);
-        wgt[k * kJoinRows + x] = w;
-        L = fmaf(v.y, w, L);
-      }
-      L = warp_sum(L);
-      if (lane == 0) {
-        inv_s[x] = L == 0.f ? 0.f : 1.f / L;
-        if (a.lse)
-          a.lse[(int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g] =
-              L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994531f;
+    const int h = u % heads % a.n_kv, tile = u / heads % 2, r = u / heads / 2 * kJoinRows + lane;
+    const int i = J.tok0 + tile * P.per_tile + r / a.g;
+    if (tile >= J.tiles || r >= P.per_tile * a.g || i >= J.n) continue;
+    const int64_t s0 = ((int64_t)J.slot * a.n_kv + h) * 2 + tile;
+    const int64_t pitch = (int64_t)2 * a.n_kv * kTile;             // rows between two pieces' partials
+    const float2* ml = a.part_ml + s0 * kTile + r;
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < J.pieces; ++k) M = fmaxf(M, ml[k * pitch].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + c0) * kTile + r;
+    float L = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < J.pieces; ++k) {
+      const float2 v = ml[k * pitch];
+      const float w = exp2f(v.x - base);
+      L = fmaf(v.y, w, L);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = po[k * pitch * (DH / 4) + c * kTile];
+        acc[c].x = fmaf(x.x, w, acc[c].x);
+        acc[c].y = fmaf(x.y, w, acc[c].y);
+        acc[c].z = fmaf(x.z, w, acc[c].z);
+        acc[c].w = fmaf(x.w, w, acc[c].w);
       }
     }
-    __syncthreads();
-    int i;
-    const int r = row0 + r8;
-    if (query(r, i)) {
-      const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + c4) * kTile + r;
-      const int64_t pitch = step * (DH / 4) * kTile;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k0 = 0; k0 < pieces; k0 += 8) {
-        float4 v[8];
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g;
+    if (c0 == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994531f;
+    uint32_t w8[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (k0 + x < pieces) v[x] = po[(k0 + x) * pitch];
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (k0 + x < pieces) {
-            const float w = wgt[(k0 + x) * kJoinRows + r8];
-            acc.x = fmaf(v[x].x, w, acc.x);
-            acc.y = fmaf(v[x].y, w, acc.y);
-            acc.z = fmaf(v[x].z, w, acc.z);
-            acc.w = fmaf(v[x].w, w, acc.w);
-          }
-      }
-      const float inv = inv_s[r8];
-      const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * DH + c4 * 4) =
-          make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+    for (int c = 0; c < 4; ++c) {
+      w8[2 * c] = pack2<BF16>(acc[c].x * inv, acc[c].y * inv);
+      w8[2 * c + 1] = pack2<BF16>(acc[c].z * inv, acc[c].w * inv);
     }
-    __syncthreads();
+    store32(static_cast<uint16_t*>(a.out) + row * DH + c0 * 4, w8);
   }
 }
 
@@ -344,13 +326,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-// one 32-byte sector
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
 }
 
 // steps of unit u of an item (its cached tiles), and the tile of its step k
@@ -947,9 +922,7 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
   kern<<<(unsigned)(most < t.sm_count ? most : t.sm_count), kThreads, Lay<DH>::kSmem, st>>>(tm_q, tm_k, tm_v, tm_kb, tm_vb, P);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // a cut makes slots / n_kv pieces at most
-  const int max_pieces = t.slots / a.n_kv > 1 ? t.slots / a.n_kv : 1;
-  kv_join_kernel<DH, BF16><<<8 * t.sm_count, kJoinRows * DH / 4, max_pieces * kJoinRows * sizeof(float), st>>>(P, max_pieces);
+  kv_join_kernel<DH, BF16><<<8 * t.sm_count, 2 * DH, 0, st>>>(P);
   return cudaGetLastError();
 }
 
