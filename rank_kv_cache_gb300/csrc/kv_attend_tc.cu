@@ -267,57 +267,98 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// A block takes 32 query rows of a cut tile, a lane one row, a warp 16 of its columns:
-// o = sum_k 2^(m_k - M) o_k / L over the pieces. Four pieces' loads are in flight at a time (they come from L2:
-// one piece after the other took a microsecond each), and no thread waits for another.
-constexpr int kJoinRows = 32;
+// A block takes 32 query rows of a cut tile, a lane one row: o = sum_k 2^(m_k - M) o_k / L over the pieces. A warp
+// takes 16 of the columns, and four pieces' loads are in flight at a time (they come from L2: one piece after the
+// other took a microsecond each). Where few tiles are cut, into many pieces then, a block takes 16 columns and its
+// warps share the pieces.
+constexpr int kJoinRows = 32, kJoinFew = 32;
 template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_kernel(const TcParams P) {
+  constexpr int kWarps = DH / 16;
+  __shared__ float4 acc_s[kWarps][4][32];
+  __shared__ float2 ml_s[kWarps][32];
   const KvAttendArgs& a = P.a;
   const KvTcPlan& plan = P.plan;
-  const int lane = threadIdx.x & 31, c0 = (threadIdx.x >> 5) * 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = plan.head->n_joins * a.n_kv;
+  const bool few = heads <= kJoinFew;
+  const int parts = few ? kWarps : 1;
   // the row groups run slowest, so that the tiles' live rows spread over the blocks
-  for (int u = blockIdx.x; u < heads * 2 * (kTile / kJoinRows); u += gridDim.x) {
-    const KvJoin J = plan.joins[u % heads / a.n_kv];
-    const int h = u % heads % a.n_kv, tile = u / heads % 2, r = u / heads / 2 * kJoinRows + lane;
+  for (int u = blockIdx.x; u < heads * parts * 2 * (kTile / kJoinRows); u += gridDim.x) {
+    const int group = u / (heads * parts), in_group = u % (heads * parts);
+    const KvJoin J = plan.joins[in_group / parts / a.n_kv];
+    const int h = in_group / parts % a.n_kv, tile = group % 2, r0 = group / 2 * kJoinRows, r = r0 + lane;
+    const int c0 = (few ? in_group % parts : warp) * 4;
+    if (tile >= J.tiles || r0 >= P.per_tile * a.g || J.tok0 + tile * P.per_tile + r0 / a.g >= J.n) continue;
     const int i = J.tok0 + tile * P.per_tile + r / a.g;
-    if (tile >= J.tiles || r >= P.per_tile * a.g || i >= J.n) continue;
+    const bool live = r < P.per_tile * a.g && i < J.n;
     const int64_t s0 = ((int64_t)J.slot * a.n_kv + h) * 2 + tile;
     const int64_t pitch = (int64_t)2 * a.n_kv * kTile;             // rows between two pieces' partials
     const float2* ml = a.part_ml + s0 * kTile + r;
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < J.pieces; ++k) M = fmaxf(M, ml[k * pitch].x);
-    const float base = M == -INFINITY ? 0.f : M;
     const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + c0) * kTile + r;
-    float L = 0.f;
+    float M = -INFINITY, L = 0.f;
     float4 acc[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto sum = [&](int first, int step) {
+#pragma unroll 8
+      for (int k = first; k < J.pieces; k += step) M = fmaxf(M, ml[k * pitch].x);
+      const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-    for (int k = 0; k < J.pieces; ++k) {
-      const float2 v = ml[k * pitch];
-      const float w = exp2f(v.x - base);
-      L = fmaf(v.y, w, L);
+      for (int k = first; k < J.pieces; k += step) {
+        const float2 v = ml[k * pitch];
+        const float w = exp2f(v.x - base);
+        L = fmaf(v.y, w, L);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 x = po[k * pitch * (DH / 4) + c * kTile];
-        acc[c].x = fmaf(x.x, w, acc[c].x);
-        acc[c].y = fmaf(x.y, w, acc[c].y);
-        acc[c].z = fmaf(x.z, w, acc[c].z);
-        acc[c].w = fmaf(x.w, w, acc[c].w);
+        for (int c = 0; c < 4; ++c) {
+          const float4 x = po[k * pitch * (DH / 4) + c * kTile];
+          acc[c].x = fmaf(x.x, w, acc[c].x);
+          acc[c].y = fmaf(x.y, w, acc[c].y);
+          acc[c].z = fmaf(x.z, w, acc[c].z);
+          acc[c].w = fmaf(x.w, w, acc[c].w);
+        }
+      }
+    };
+    if (live && few) sum(warp, kWarps);
+    if (live && !few) sum(0, 1);
+    if (few) {
+      ml_s[warp][lane] = make_float2(M, L);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc_s[warp][c][lane] = acc[c];
+      __syncthreads();
+      if (warp == 0) {
+        for (int x = 1; x < kWarps; ++x) M = fmaxf(M, ml_s[x][lane].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < kWarps; ++x) {
+          const float2 v = ml_s[x][lane];
+          const float w = exp2f(v.x - base);
+          L = fmaf(v.y, w, L);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4 y = acc_s[x][c][lane];
+            acc[c].x = fmaf(y.x, w, acc[c].x);
+            acc[c].y = fmaf(y.y, w, acc[c].y);
+            acc[c].z = fmaf(y.z, w, acc[c].z);
+            acc[c].w = fmaf(y.w, w, acc[c].w);
+          }
+        }
       }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g;
-    if (c0 == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994531f;
-    uint32_t w8[8];
+    if (live && (!few || warp == 0)) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g;
+      if (c0 == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+      uint32_t w8[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      w8[2 * c] = pack2<BF16>(acc[c].x * inv, acc[c].y * inv);
-      w8[2 * c + 1] = pack2<BF16>(acc[c].z * inv, acc[c].w * inv);
+      for (int c = 0; c < 4; ++c) {
+        w8[2 * c] = pack2<BF16>(acc[c].x * inv, acc[c].y * inv);
+        w8[2 * c + 1] = pack2<BF16>(acc[c].z * inv, acc[c].w * inv);
+      }
+      store32(static_cast<uint16_t*>(a.out) + row * DH + c0 * 4, w8);
     }
-    store32(static_cast<uint16_t*>(a.out) + row * DH + c0 * 4, w8);
+    if (few) __syncthreads();
   }
 }
 
