@@ -45,6 +45,27 @@ __device__ __forceinline__ int64_t kv_slot(const KvRows& r, const KvPages& p, in
   return (int64_t)page * p.page_size + (t - pg * p.page_size);
 }
 
+// The kernels here are launched to start while the one ahead of them in the stream still runs: every thread first
+// waits for that one's end (grid_wait, before anything of it is read or its memory written), and says at once that the
+// next one may set itself up. A few microseconds of launch latency hide behind the work.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                         const Args&... args) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Row b's first packed token, new tokens and cached length, clamped to the call's bounds; false where the row
 // is skipped. `bad`: what to record (an ErrWhere), or 0.
 __device__ __forceinline__ bool kv_row(const KvRows& r, int b, int& q0, int& n, int& L, unsigned& bad) {

@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
   __shared__ int last_cta;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvRows& R = a.rows;
+  grid_wait();
+  grid_release();
 
   // steps of a row (0: nothing to do); one without cached tokens takes a step too, for its empty outputs
   auto row_steps = [&](int b, bool report) -> int {
@@ -440,8 +442,7 @@ template <int DH, bool BF16> cudaError_t prepare_few() {
                               Sm<DH>::kBytes);
 }
 template <int DH, bool BF16> cudaError_t launch_few(const KvAttendArgs& a, int ctas, cudaStream_t st) {
-  kv_attend_few_kernel<DH, BF16><<<ctas, kWarps * 32, Sm<DH>::kBytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(kv_attend_few_kernel<DH, BF16>, dim3(ctas), kWarps * 32, Sm<DH>::kBytes, st, a);
 }
 
 }  // namespace

@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P)
   __shared__ uint64_t sums[32];
   __shared__ int tops[32];
   __shared__ float est_s[32];
-  tc::grid_release();                // the attention may set itself up meanwhile
+  grid_wait();
+  grid_release();
   const KvAttendArgs& a = P.a;
   const KvRows& R = a.rows;
   const KvTcPlan& plan = P.plan;
@@ -280,7 +281,8 @@ template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_k
   const KvAttendArgs& a = P.a;
   const KvTcPlan& plan = P.plan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  tc::grid_wait();
+  grid_wait();
+  grid_release();
   const int heads = plan.head->n_joins * a.n_kv;
   const bool few = heads <= kJoinFew;
   const int parts = few ? kWarps : 1;
@@ -422,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = S.tmem;
-  tc::grid_wait();                             // for the plan
-  tc::grid_release();
+  grid_wait();                                 // for the plan
+  grid_release();
 
   if (warp >= 8) {
     tc::regs_shrink<kRegsOther>();
@@ -959,28 +961,14 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
     if (!tma_encode(&tm_k, dt, 2, a.pages.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     if (!tma_encode(&tm_v, dt, 2, a.pages.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
   }
-  auto kern = kv_attend_tc_kernel<DH, BF16>;
-  kv_plan_kernel<<<1, kPlanThreads, 0, st>>>(P);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(kv_plan_kernel, dim3(1), kPlanThreads, 0, st, P);
   if (e != cudaSuccess) return e;
   const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
-  // The attention and the join start while the kernel ahead of them runs, set themselves up and wait for it.
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)(most < t.sm_count ? most : t.sm_count));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Lay<DH>::kSmem;
-  e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, tm_kb, tm_vb, P);
+  const unsigned grid = (unsigned)(most < t.sm_count ? most : t.sm_count);
+  e = launch_early(kv_attend_tc_kernel<DH, BF16>, dim3(grid), kThreads, Lay<DH>::kSmem, st, tm_q, tm_k, tm_v, tm_kb, tm_vb,
+                   P);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(8 * t.sm_count);
-  cfg.blockDim = dim3(2 * DH);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<DH, BF16>, P);
+  return launch_early(kv_join_kernel<DH, BF16>, dim3(8 * t.sm_count), 2 * DH, 0, st, P);
 }
 
 }  // namespace

@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a, c
   constexpr int kLanes = DH / 16;          // lanes of a head
   constexpr int kHeads = 32 / kLanes;      // heads a warp takes at once: a chunk
   const int lane = threadIdx.x & 31, j = lane % kLanes, hl = lane / kLanes;
+  grid_wait();
+  grid_release();
   const unsigned unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int t = int(unit / unsigned(parts)), part = int(unit % unsigned(parts));
   if (t >= a.n_tokens) return;
@@ -193,11 +195,8 @@ cudaError_t launch_typed(const KvRopeArgs& a, const KvFreq& f, int sm_count, cud
   parts = (chunks + cpp - 1) / cpp;
   const int64_t units = (int64_t)a.n_tokens * parts;
   const unsigned grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32));
-  if (a.head_dim == 128)
-    kv_rope_kernel<TI, TO, 128><<<grid, kThreads, 0, st>>>(a, f, parts, cpp);
-  else
-    kv_rope_kernel<TI, TO, 64><<<grid, kThreads, 0, st>>>(a, f, parts, cpp);
-  return cudaGetLastError();
+  if (a.head_dim == 128) return launch_early(kv_rope_kernel<TI, TO, 128>, dim3(grid), kThreads, 0, st, a, f, parts, cpp);
+  return launch_early(kv_rope_kernel<TI, TO, 64>, dim3(grid), kThreads, 0, st, a, f, parts, cpp);
 }
 
 template <typename TI>

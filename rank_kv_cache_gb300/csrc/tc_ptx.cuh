@@ -109,11 +109,6 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t* b, uint32_t parity, vo
   return true;
 }
 
-// A kernel launched to start before the one ahead of it has ended: it waits here until that one's writes are
-// there; the one ahead lets it start early.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
