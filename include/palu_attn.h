@@ -430,6 +430,9 @@ palu_status_t palu_project_latents(palu_attn_t h, const void* W, palu_dtype_t w_
  * one handle share the workspace, so calls that may overlap on the GPU (two streams, two captured
  * graphs) need a handle each. No call but palu_kv_check synchronises; all can be captured into a
  * graph. The calls run on the workspace's device and leave the thread's current device as it was.
+ * The workspace holds the partials of work that is cut along the cached tokens (62 MB for
+ * head_dim 128) and a work list that grows with max_tokens and max_batch; one handle serves all
+ * layers of a shape that run one after the other.
  */
 typedef struct palu_kv_desc {
   int abi_version;        /* must be PALU_ABI_VERSION */
@@ -444,6 +447,8 @@ typedef struct palu_kv_desc {
   double norm_eps;        /* added to the mean square by the norm; >= 0 */
   int max_batch;          /* largest batch of a call, <= 65535 */
   int64_t max_tokens;     /* largest n_tokens of a call, < 2^31 */
+  uint32_t flags;         /* 0, or PALU_FLAG_TEST_STALL (test builds of callers only): the tensor-core kernel's value
+                             loader issues no loads, and its waits give up after 50 ms */
 } palu_kv_desc;
 
 typedef struct palu_kv* palu_kv_t;
@@ -467,7 +472,7 @@ typedef struct palu_kv_pages {
  * The new tokens of a batch, packed: row b's are row_start[b] .. row_start[b + 1] - 1 of the token
  * arrays (row_start does not decrease). kv_len[b] counts the row's cached tokens with the new ones,
  * which are the last: new token i of n_b has slot kv_len[b] - n_b + i. Rows without new tokens are
- * fine. Token array rows that belong to no batch row are neither read nor written.
+ * fine. Output rows of tokens that belong to no batch row are left as they were.
  */
 typedef struct palu_kv_rows {
   const int32_t* row_start;   /* device [batch + 1] */
@@ -502,7 +507,7 @@ palu_status_t palu_norm_rope(palu_kv_t h, const void* q, int64_t q_stride, const
  * Append the new tokens' keys, normed and rotated as by palu_norm_rope, and their values to the pages,
  * and norm and rotate their queries into q_out, in one launch. k, v (and q) as q, k above with
  * n_kv_heads heads; q and q_out (device [n_tokens][n_heads][head_dim] contiguous, dtype) may both be
- * NULL. Rotation positions are rows->positions, or the slots. A token whose slot is negative, lies past
+ * NULL. The inputs do not overlap the pages. Rotation positions are rows->positions, or the slots. A token whose slot is negative, lies past
  * the page table or in a page outside the pool is recorded in the error word and not stored. Two
  * tokens that fall on one slot (a page shared by two rows that both append to it) leave either's.
  */
@@ -524,7 +529,11 @@ palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
  * length outside [0, max_kv_len], a row with more than max_new new tokens (both clamped), a decreasing
  * row_start (the row is skipped) and a page outside the pool (read as zeros) are recorded in the
  * error word. The result does not depend on timing: the same call gives the same bits.
- * PALU_ERR_UNSUPPORTED for F32 handles.
+ * max_new * n_heads / n_kv_heads decides the kernel: up to 16 query rows of a key/value head run on
+ * the streaming kernel (one launch), more on the tensor-core kernel (three launches). Its cached
+ * tokens come by TMA; page sizes without a factor of eight are gathered row by row, at less than
+ * half the rate. PALU_ERR_UNSUPPORTED for F32 handles, and on the tensor-core kernel where
+ * n_pages * page_size * n_kv_heads >= 2^31 - 1.
  */
 palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu_kv_rows* rows, const void* q,
                              int64_t q_stride, void* out, float* lse, palu_stream_t stream);

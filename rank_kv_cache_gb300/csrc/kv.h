@@ -194,6 +194,8 @@ struct KvTcPlan {
   int tile_cap;      // most tiles the call's packed tokens can make
   int slots;         // most pieces x key/value heads whose partials the workspace holds
   int sm_count;
+  int test_stall;    // failure-detection test hook: the value loader issues nothing
+  uint64_t wait_ns;  // bound of the kernel's waits
 };
 cudaError_t prepare_kv_attend_tc(int head_dim, bool bf16);
 cudaError_t launch_kv_attend_tc(const KvAttendArgs& a, const KvTcPlan& t, cudaStream_t st);

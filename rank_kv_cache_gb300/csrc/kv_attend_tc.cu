@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto step = [&](bool k_tile, int j) {
           mine <<= 1;
           ++seq;
-          if (k_tile == keys) load(j);
+          if (k_tile == keys && !(P.plan.test_stall && !keys)) load(j);
           if (++st == Y::kStages) {
             st = 0;
             par ^= 1;
@@ -934,7 +934,7 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
   P.per_tile = kTile / a.g;
   const int64_t rows = a.pages.n_pages * a.pages.page_size * a.n_kv;
   P.oob_row = rows;
-  P.wait_ns = 1000000000ull;
+  P.wait_ns = t.wait_ns;
   CUtensorMap tm_q, tm_k, tm_v, tm_kb, tm_vb;
   {
     // queries [token][head][d]: boxes of 64 columns, one group's heads, a tile's tokens

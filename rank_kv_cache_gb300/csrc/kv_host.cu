@@ -62,7 +62,7 @@ palu_status_t check_kv_desc(const palu_kv_desc* d) {
     return PALU_ERR_INVALID_ARG;
   if (!(d->rope_theta >= 0.0) || !isfinite(d->rope_theta) || !(d->norm_eps >= 0.0) || !isfinite(d->norm_eps))
     return PALU_ERR_INVALID_ARG;
-  if (d->max_batch <= 0 || d->max_tokens <= 0) return PALU_ERR_INVALID_ARG;
+  if (d->max_batch <= 0 || d->max_tokens <= 0 || (d->flags & ~PALU_FLAG_TEST_STALL)) return PALU_ERR_INVALID_ARG;
   if (d->head_dim != 64 && d->head_dim != 128) return PALU_ERR_UNSUPPORTED;
   if (d->dtype == PALU_INT4 || d->x_dtype == PALU_INT4) return PALU_ERR_UNSUPPORTED;
   if (d->n_heads / d->n_kv_heads > 64 || d->n_heads > 4096) return PALU_ERR_UNSUPPORTED;
@@ -349,6 +349,8 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
     t.tile_cap = (int)tc_tile_cap(d, rows->n_tokens, rows->batch);
     t.slots = kTcSlots;
     t.sm_count = h->sm_count;
+    t.test_stall = (d.flags & PALU_FLAG_TEST_STALL) != 0;
+    t.wait_ns = t.test_stall ? 50000000ull : 1000000000ull;   // bound of every device wait
     e = launch_kv_attend_tc(a, t, s);
     if (e == cudaErrorNotSupported) return PALU_ERR_UNSUPPORTED;
   }

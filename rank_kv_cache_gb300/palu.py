@@ -70,7 +70,7 @@ class palu_kv_desc(ctypes.Structure):
     _fields_ = [("abi_version", ctypes.c_int), ("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("x_dtype", ctypes.c_int),
                 ("rope_theta", ctypes.c_double), ("norm_eps", ctypes.c_double), ("max_batch", ctypes.c_int),
-                ("max_tokens", ctypes.c_int64)]
+                ("max_tokens", ctypes.c_int64), ("flags", ctypes.c_uint32)]
 
 
 class palu_kv_pages(ctypes.Structure):
@@ -623,12 +623,12 @@ class PagedAttention:
     torch-allocated workspace; calls that may overlap on the GPU need an object each."""
 
     def __init__(self, *, n_heads, n_kv_heads, head_dim, dtype, x_dtype=None, rope_theta=10000.0, norm_eps=1e-6,
-                 max_batch=1, max_tokens=1, device="cuda", stream=None):
+                 max_batch=1, max_tokens=1, flags=0, device="cuda", stream=None):
         torch = _torch()
         names = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
         x_dtype = x_dtype or dtype
         self.desc = palu_kv_desc(PALU_ABI_VERSION, n_heads, n_kv_heads, head_dim, DTYPES[dtype], DTYPES[x_dtype],
-                                 float(rope_theta), float(norm_eps), max_batch, max_tokens)
+                                 float(rope_theta), float(norm_eps), max_batch, max_tokens, flags)
         st, nbytes = palu_kv_workspace_size(self.desc)
         check(st, "palu_kv_workspace_size")
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
@@ -654,6 +654,14 @@ class PagedAttention:
     def _stream(self, stream) -> int:
         # the raw handle of the current stream: building torch's Stream object takes longer than the call
         return self._current(self.device.index) if stream is None else stream.cuda_stream
+
+    def _empty(self, shape, dtype, stream):
+        """An output that belongs to the stream it is written on."""
+        torch = _torch()
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _view(self, name, t, heads, dtype, n_tokens):
         """(pointer, token stride) of a [n_tokens][heads][head_dim] tensor whose tokens may lie apart."""
@@ -686,9 +694,9 @@ class PagedAttention:
         torch = _torch()
         N = int(q.shape[0])
         if q_out is None:
-            q_out = torch.empty((N, self.n_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            q_out = self._empty((N, self.n_heads, self.head_dim), self.dtype, stream)
         if k is not None and k_out is None:
-            k_out = torch.empty((N, self.n_kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            k_out = self._empty((N, self.n_kv_heads, self.head_dim), self.dtype, stream)
         if positions is not None and (positions.dtype != torch.int32 or positions.shape != (N,) or
                                       positions.device != self.device or not positions.is_contiguous()):
             raise ValueError(f"positions must be a contiguous [{N}] int32 tensor on {self.device}")
@@ -715,7 +723,7 @@ class PagedAttention:
         qp, qs, qo = None, 0, None
         if q is not None:
             if q_out is None:
-                q_out = _torch().empty((N, self.n_heads, self.head_dim), dtype=self.dtype, device=self.device)
+                q_out = self._empty((N, self.n_heads, self.head_dim), self.dtype, stream)
             qp, qs = self._view("q", q, self.n_heads, self.x_dtype, N)
             qo, qos = self._view("q_out", q_out, self.n_heads, self.dtype, N)
             if qos != self.n_heads * self.head_dim:
@@ -735,7 +743,7 @@ class PagedAttention:
         N = rows.n_tokens
         qp, qs = self._view("q", q, self.n_heads, self.dtype, N)
         if out is None:
-            out = torch.empty((N, self.n_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            out = self._empty((N, self.n_heads, self.head_dim), self.dtype, stream)
         op, os_ = self._view("out", out, self.n_heads, self.dtype, N)
         if os_ != self.n_heads * self.head_dim:
             raise ValueError("out must be contiguous")

@@ -319,3 +319,109 @@ def test_appended_sinks_and_window_feed_the_hybrid_decode():
     # the stored keys' fp16 rounding moves a score by at most 2^-11 sum |q k| / sqrt(d), which the hybrid's bounds hold
     assert_close(out.cpu().double().numpy(), ref_l, lse.cpu().double().numpy(), ref_lse)
     assert_close(out_d.cpu().double().numpy(), ref_d)
+
+
+@pytest.mark.parametrize("batch,new", [(33, 1), (100, 3), (1100, 1), (40, 17), (1100, 18)])
+def test_many_rows(batch, new):
+    # more rows than a warp's lanes (few-row cut) and than the plan's block, lengths from nothing to a few tiles
+    rng = np.random.default_rng(batch)
+    news = [int(x) for x in rng.integers(0, new + 1, batch)]
+    news[0] = new
+    lens = [int(max(n, x)) for n, x in zip(news, rng.integers(0, 300, batch))]
+    Batch(n=2, m=2, d=64, dtype="f16", news=news, lens=lens, page=32, seed=batch, max_new=new).run_and_check()
+
+
+def test_more_tiles_than_the_plan_weighs():
+    # 4200 rows of 17 new tokens: a tile each, more than are weighed for cutting; spot checks
+    news, lens = [17] * 4200, [17 + i % 40 for i in range(4200)]
+    b = Batch(n=1, m=1, d=64, dtype="bf16", news=news, lens=lens, page=64, seed=21)
+    out, lse = b.attend()
+    b.layer.check_device()
+    b.check_sampled(out, lse, [0, 16, 17 * 2049 + 5, 17 * 4199, 17 * 4200 - 1], [0])
+
+
+@pytest.mark.parametrize("new,length", [(20, 9000), (200, 5000), (129, 700), (64, 30000)])
+@pytest.mark.parametrize("n,m", [(2, 2), (8, 1), (6, 2)])
+def test_long_rows_cut_into_many_pieces(new, length, n, m):
+    b = Batch(n=n, m=m, d=128, dtype="bf16", news=[new], lens=[length], page=64, seed=new, q_scale=2.0)
+    out, lse = b.attend()
+    b.layer.check_device()
+    b.check_sampled(out, lse, sorted({0, new // 3, new - 2, new - 1}), [0, n - 1])
+    o2, l2 = b.attend()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_rows_that_overlap_in_the_packed_arrays_are_reported():
+    from rank_kv_cache_gb300 import palu as P
+    b = Batch(n=1, m=1, d=64, dtype="f16", news=[2048, 0, 0, 0], lens=[2048, 0, 0, 0], page=64, seed=22)
+    b.rows.tensors[0].copy_(torch.tensor([0, 2048, 0, 2048, 0], dtype=torch.int32))   # rows 0 and 2 share the tokens
+    b.attend()
+    with pytest.raises(P.PaluError):
+        b.layer.check_device()
+    b.layer.check_device()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+def test_bounded_waits_give_up_and_report_a_timeout(dtype, d):
+    from rank_kv_cache_gb300 import palu as P
+    b = Batch(n=4, m=2, d=d, dtype=dtype, news=[200, 20], lens=[900, 3000], page=16, seed=23)
+    good = b.layer
+    b.layer = P.PagedAttention(n_heads=4, n_kv_heads=2, head_dim=d, dtype=dtype, max_batch=2, max_tokens=b.N,
+                               flags=P.PALU_FLAG_TEST_STALL)
+    b.attend()
+    with pytest.raises(P.PaluError) as e:
+        b.layer.check_device()
+    assert e.value.status == P.PALU_ERR_TIMEOUT
+    b.layer = good
+    b.run_and_check()
+
+
+def test_call_on_a_side_stream_allocates_there():
+    b = Batch(n=4, m=2, d=128, dtype="f16", news=[1, 30], lens=[400, 90], page=16, seed=24)
+    ref, _ = b.attend()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [b.layer.attend(b.pages, b.rows, b.qd, stream=s) for _ in range(4)]
+    s.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
+def test_every_layer_of_a_step_on_one_handle_in_a_graph():
+    """Append and attend of several layers, one handle and one set of rows, captured and replayed with new lengths."""
+    from rank_kv_cache_gb300 import palu as P
+    rng = np.random.default_rng(25)
+    n, m, d, layers, B = 8, 2, 128, 3, 3
+    dev = torch.device("cuda:0")
+    layer = P.PagedAttention(n_heads=n, n_kv_heads=m, head_dim=d, dtype="bf16", max_batch=B, max_tokens=B)
+    pages = [P.KVPages(*(rounded(rng, (B * 8, 16, m, d), "bf16").to(dev) for _ in range(2))) for _ in range(layers)]
+    table = torch.from_numpy(rng.permutation(B * 8).reshape(B, 8).astype(np.int32)).to(dev)
+    start, lens = torch.arange(B + 1, dtype=torch.int32, device=dev), torch.tensor([5, 60, 100], dtype=torch.int32, device=dev)
+    rows = P.KVRows(start, lens, n_tokens=B, max_new=1, max_kv_len=128, page_table=table)
+    x = [rounded(rng, (B, (n + 2 * m) * d), "bf16").to(dev) for _ in range(layers)]
+    q_out = [torch.empty(B, n, d, dtype=torch.bfloat16, device=dev) for _ in range(layers)]
+    out = [torch.empty(B, n, d, dtype=torch.bfloat16, device=dev) for _ in range(layers)]
+
+    def step():
+        for i in range(layers):
+            q, k, v = (x[i][:, a * d:e * d].unflatten(1, (e - a, d)) for a, e in ((0, n), (n, n + m), (n + m, n + 2 * m)))
+            layer.append(pages[i], rows, k, v, q=q, q_out=q_out[i])
+            layer.attend(pages[i], rows, q_out[i], out=out[i])
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for now in ([6, 61, 101], [128, 1, 17]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        for o in out:
+            o.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        for i in range(layers):
+            o, s, size, reach = KO.attend(q_out[i].double().cpu().numpy(), pages[i].k.double().cpu().numpy(),
+                                          pages[i].v.double().cpu().numpy(), [0, 1, 2, 3], now, table.cpu().numpy())
+            b = Batch(n=n, m=m, d=d, dtype="bf16", news=[1] * B, lens=now, page=16, seed=26)
+            b.pv = pages[i].v.cpu()
+            b.check(out[i], torch.from_numpy(s), (o, s, size, reach))
+    layer.check_device()

@@ -9,14 +9,15 @@ from rank_kv_cache_gb300 import palu as P
 
 def _desc(**kw):
     base = dict(n_heads=32, n_kv_heads=8, head_dim=128, dtype=P.PALU_BF16, x_dtype=P.PALU_BF16, rope_theta=1e4,
-                norm_eps=1e-6, max_batch=4, max_tokens=64)
+                norm_eps=1e-6, max_batch=4, max_tokens=64, flags=0)
     base.update(kw)
     return P.palu_kv_desc(P.PALU_ABI_VERSION, *[base[f] for f, _ in P.palu_kv_desc._fields_[1:]])
 
 
 @pytest.mark.parametrize("kw", [{}, dict(dtype=P.PALU_F16), dict(head_dim=64), dict(rope_theta=0.0),
                                 dict(n_kv_heads=32), dict(n_heads=64, n_kv_heads=1), dict(dtype=P.PALU_F32),
-                                dict(x_dtype=P.PALU_F32), dict(n_heads=7, n_kv_heads=7)])
+                                dict(x_dtype=P.PALU_F32), dict(n_heads=7, n_kv_heads=7),
+                                dict(flags=P.PALU_FLAG_TEST_STALL)])
 def test_descriptors_accepted(kw):
     st, n = P.palu_kv_workspace_size(_desc(**kw))
     assert st == P.PALU_OK and n > 0 and n % 256 == 0
@@ -40,6 +41,7 @@ def test_descriptors_accepted(kw):
     (dict(max_batch=65536), P.PALU_ERR_UNSUPPORTED),
     (dict(max_tokens=0), P.PALU_ERR_INVALID_ARG),
     (dict(max_tokens=1 << 31), P.PALU_ERR_UNSUPPORTED),
+    (dict(flags=P.PALU_FLAG_ALIBI), P.PALU_ERR_INVALID_ARG),
 ])
 def test_descriptors_refused(kw, status):
     assert P.palu_kv_workspace_size(_desc(**kw))[0] == status
