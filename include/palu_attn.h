@@ -430,9 +430,8 @@ palu_status_t palu_project_latents(palu_attn_t h, const void* W, palu_dtype_t w_
  * one handle share the workspace, so calls that may overlap on the GPU (two streams, two captured
  * graphs) need a handle each. No call but palu_kv_check synchronises; all can be captured into a
  * graph. The calls run on the workspace's device and leave the thread's current device as it was.
- * The workspace holds the partials of work that is cut along the cached tokens (62 MB for
- * head_dim 128) and a work list that grows with max_tokens and max_batch; one handle serves all
- * layers of a shape that run one after the other.
+ * The workspace holds the partials of work that is cut along the cached tokens (61 MB for
+ * head_dim 128); one handle serves all layers of a shape that run one after the other.
  */
 typedef struct palu_kv_desc {
   int abi_version;        /* must be PALU_ABI_VERSION */
@@ -530,7 +529,7 @@ palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
  * row_start (the row is skipped) and a page outside the pool (read as zeros) are recorded in the
  * error word. The result does not depend on timing: the same call gives the same bits.
  * max_new * n_heads / n_kv_heads decides the kernel: up to 16 query rows of a key/value head run on
- * the streaming kernel (one launch), more on the tensor-core kernel (three launches). Its cached
+ * the streaming kernel (one launch), more on the tensor-core kernel (one launch or two). Its cached
  * tokens come by TMA; page sizes without a factor of eight are gathered row by row, at less than
  * half the rate. PALU_ERR_UNSUPPORTED for F32 handles, and on the tensor-core kernel where
  * n_pages * page_size * n_kv_heads >= 2^31 - 1.

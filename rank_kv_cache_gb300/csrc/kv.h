@@ -170,28 +170,17 @@ constexpr int kKvFewMostCtas = 512;      // most CTAs of a call; cut units have 
 cudaError_t prepare_kv_attend_few(int head_dim, bool bf16);
 cudaError_t launch_kv_attend_few(KvAttendArgs a, int sm_count, cudaStream_t st);   // max_new g <= 16
 
-// Work list of the tensor-core kernel, in the workspace.
+// the tensor-core kernel
 constexpr int kKvTcRows = 128;           // query rows of a tile
-struct KvItem {      // one or two tiles of a row's query tokens over cached steps [kv0, kv1) of 128 tokens
-  int b, q0, n, L;   // row; its first packed token, new tokens, cached length
-  int tok0, tiles;   // first new token; tiles of per_tile tokens
-  int kv0, kv1;
-  int split;         // number of the item among those that were cut, or -1: it writes the output itself
-  int pad[3];
-};
-struct KvJoin {      // a cut item's pieces: numbers slot .. slot + pieces - 1
-  int q0, n, tok0, tiles, slot, pieces, pad[2];
-};
+constexpr int kKvTcWhole = 4;            // steps of 128 cached tokens up to which a tile is not cut
 struct KvPlanHead {
-  int n_items, n_joins;
-  unsigned next;     // the next item to take
+  unsigned next;     // the next item to take; zero between calls
+  unsigned done;     // CTAs that have ended; zero between calls
+  int target, joins; // the plan, for the join
 };
 struct KvTcPlan {
   KvPlanHead* head;
-  KvItem* items;     // [tile_cap + slots]
-  KvJoin* joins;     // [slots]
-  int* row_base;     // [batch + 1]: tiles before each row
-  int tile_cap;      // most tiles the call's packed tokens can make
+  int tile_cap;      // most tiles (or pairs of tiles) the call's packed tokens can make
   int slots;         // most pieces x key/value heads whose partials the workspace holds
   int sm_count;
   int test_stall;    // failure-detection test hook: the value loader issues nothing

@@ -7,11 +7,11 @@
 // under head j, floor(128 / g) tokens fill a 128-row tile, and K and V are read once for the group. A
 // work item is (row of the batch, key/value head, one or two tiles, a range of the cached tokens).
 //
-// Three launches. kv_plan_kernel lists the items from the lengths on the device: the longest first
-// within a row, and cut along the cached tokens where whole tiles would leave SMs idle (few rows, long
-// caches). kv_attend_tc_kernel is persistent, one CTA an SM, and takes items off the list by an atomic
-// counter (which item runs where does not change any sum). kv_join_kernel joins the ranges of items
-// that were cut, in their order.
+// Two launches. kv_attend_tc_kernel is persistent, one CTA an SM; each CTA works out the list of items from
+// the rows' lengths (the longest first within a row, cut along the cached tokens where whole tiles would
+// leave SMs idle) and takes items off it by an atomic counter (which item runs where does not change any
+// sum). kv_join_kernel joins the pieces of what was cut, in their order; it is left out where the call's
+// bounds allow no cut.
 //
 // One CTA: two softmax warpgroups, two loader warps and an MMA warp.
 //   * The loaders bring 128 cached tokens at a time by TMA into a ring of K and V tiles (128-byte
@@ -43,8 +43,7 @@ namespace {
 
 constexpr int kTile = 128;               // query rows of a tile, cached tokens of a step
 constexpr int kThreads = 384;            // two softmax warpgroups; two loader warps, MMA and an idle warp
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanTiles = 4096;         // tiles the plan weighs for cutting; longer lists are not cut
+constexpr int kWhole = kKvTcWhole;       // tiles of so few steps are not cut: the join would cost more
 // Registers: launched with 168 a thread (65536 / 384, in eights); 2 * 128 * 200 + 128 * 104 = 384 * 168.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr float kRaise = 8.f;            // log2 by which a score may exceed the running maximum
@@ -87,177 +86,129 @@ struct TcParams {
 };
 
 // ------------------------------------------------------------------------------------------- plan
-// exclusive sums over the block of values packed into one 64-bit word; kPlanThreads
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, uint64_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t x = v;
+// The list of items, which every CTA works out for itself from the rows, 32 at a time, one a lane. A row of n new
+// tokens makes `tiles` tiles (or pairs of tiles), the last tokens' first, as they see most; all of a row's tiles are
+// cut along the cached tokens into the same number of pieces, so that none is longer than the target.
+struct Rows32 {
+  int q0, n, L;                           // this lane's row
+  int tiles, pieces;
+  int item0, slot0, join0;                // items (of one head), pieces of cut tiles and cut tiles before the row
+  int items, slots, joins;                // the same behind the 32 rows, for the whole warp
+  int row0;
+};
+
+__device__ __forceinline__ int steps_of(int tokens) { return (max(tokens, 0) + kTile - 1) / kTile; }
+
+// loads the rows row0 .. row0 + 31; cuts them by the target and counts on from `items`, `slots` and `joins`
+__device__ __forceinline__ unsigned rows_load(Rows32& x, const KvRows& R, int row0, int per) {
+  const int b = row0 + (threadIdx.x & 31);
+  unsigned bad = 0;
+  x.row0 = row0;
+  x.q0 = x.n = x.L = 0;
+  if (b < R.batch) kv_row(R, b, x.q0, x.n, x.L, bad);
+  x.tiles = ((x.n + per - 1) / per + 1) / 2;
+  return bad;
+}
+__device__ __forceinline__ void rows_cut(Rows32& x, int target) {
+  const int lane = threadIdx.x & 31;
+  x.pieces = max(1, (steps_of(x.L) + target - 1) / target);
+  // three running sums in one word: items (28 bits), pieces of cut tiles (18), cut tiles (18)
+  const bool cut = x.pieces > 1;
+  const uint64_t v = uint64_t(x.tiles * x.pieces) | uint64_t(cut ? x.tiles * x.pieces : 0) << 28 |
+                     uint64_t(cut ? x.tiles : 0) << 46;
+  uint64_t y = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const uint64_t z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
   }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  uint64_t s = warp_sums[lane];      // every warp sums the warps for itself
-  const uint64_t own = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
-  }
-  total = __shfl_sync(0xffffffffu, s, 31);
-  const uint64_t before = __shfl_sync(0xffffffffu, s - own, warp);
-  __syncthreads();                   // warp_sums may be written again
-  return x - v + before;
+  const uint64_t before = y - v, all = __shfl_sync(0xffffffffu, y, 31);
+  x.item0 = x.items + int(before & 0xfffffff);
+  x.slot0 = x.slots + int(before >> 28 & 0x3ffff);
+  x.join0 = x.joins + int(before >> 46);
+  x.items += int(all & 0xfffffff);
+  x.slots += int(all >> 28 & 0x3ffff);
+  x.joins += int(all >> 46);
 }
 
-// cut a tile of c steps into pieces of at most `target`: their number, and their length
-__device__ __forceinline__ int cut(int c, int target, int* len) {
-  if (c <= target) {
-    *len = c;
-    return 1;
-  }
-  const int p = (c + target - 1) / target;
-  *len = (c + p - 1) / p;
-  return (c + *len - 1) / *len;
-}
+struct Plan {
+  int target;                             // longest piece, in steps of 128 cached tokens
+  int items, joins;                       // of one head; cut tiles
+};
 
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const TcParams P) {
-  __shared__ int cost[kPlanTiles];
-  __shared__ int row_base_s[kPlanThreads + 1];
-  __shared__ uint64_t sums[32];
-  __shared__ int tops[32];
-  __shared__ float est_s[32];
-  grid_wait();
-  grid_release();
-  const KvAttendArgs& a = P.a;
-  const KvRows& R = a.rows;
-  const KvTcPlan& plan = P.plan;
-  // tiles before each row: in shared memory where the batch fits
-  int* base = R.batch <= kPlanThreads ? row_base_s : plan.row_base;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = P.per_tile, tile_cap = plan.tile_cap, slots = plan.slots, sms = plan.sm_count;
-
-  // tiles (or pairs) of each row, and their running number
-  int T = 0;
-  for (int b0 = 0; b0 < R.batch; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int w = 0;
-    if (b < R.batch) {
-      int q0, n, L;
-      unsigned bad;
-      if (kv_row(R, b, q0, n, L, bad)) w = ((n + per - 1) / per + 1) / 2;
-      if (bad) record_error(a.err, kCodeDevice, bad, b, b);
-    }
-    uint64_t total;
-    const int at = int(block_scan(uint64_t(w), sums, total));
-    if (b < R.batch) base[b] = T + at;
-    T += int(total);
-  }
-  if (tid == 0) base[R.batch] = T;
-  if (T > tile_cap) {   // rows that overlap in the packed arrays: more tiles than tokens
-    if (tid == 0) record_error(a.err, kCodeDevice, kErrRows, T, 0);
-    T = tile_cap;
-  }
-  __syncthreads();
-
-  auto tile_of = [&](int i, KvItem& it) -> int {   // fills the item of tile i, uncut; its steps
-    int lo = 0, hi = R.batch;                      // the last row with base[row] <= i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (base[mid] <= i) lo = mid; else hi = mid;
-    }
-    unsigned bad;
-    kv_row(R, lo, it.q0, it.n, it.L, bad);
-    it.b = lo;
-    it.tok0 = (base[lo + 1] - 1 - i) * 2 * per;    // the last tokens, which see most, first
-    it.tiles = it.n - it.tok0 > per ? 2 : 1;
-    const int last = min(it.n, it.tok0 + it.tiles * per) - 1;
-    const int seen = max(0, min(it.L, it.L - it.n + last + 1));
-    return (seen + kTile - 1) / kTile;
+// The plan: the same for every warp that asks. `first` gets the first 32 rows, cut.
+__device__ __forceinline__ Plan plan_rows(const TcParams& P, Rows32& first, bool report) {
+  const KvRows& R = P.a.rows;
+  const int lane = threadIdx.x & 31, n_kv = P.a.n_kv, sms = P.plan.sm_count;
+  // this lane's rows: the longest, and the steps of all their tiles (from the first tile's and the last's)
+  auto load = [&](Rows32& x, int row0, int& top, float& sum) {
+    const unsigned bad = rows_load(x, R, row0, P.per_tile);
+    if (bad && report) record_error(P.a.err, kCodeDevice, bad, row0 + lane, row0 + lane);
+    const int c1 = steps_of(x.L), c0 = steps_of(min(x.L, x.L - x.n + min(x.n, 2 * P.per_tile)));
+    top = x.tiles ? c1 : 0;
+    sum = 0.5f * float(c0 + c1) * x.tiles;
   };
+  int top, tiles_all;
+  float sum;
+  load(first, 0, top, sum);
+  tiles_all = first.tiles;
+  int longest = top;
+  float all = sum;
+  for (int row0 = 32; row0 < R.batch; row0 += 32) {
+    Rows32 x;
+    int t;
+    float s;
+    load(x, row0, t, s);
+    longest = max(longest, t);
+    all += s;
+    tiles_all += x.tiles;
+  }
+  longest = max(1, __reduce_max_sync(0xffffffffu, longest));
+  tiles_all = __reduce_add_sync(0xffffffffu, tiles_all);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  if (report && lane == 0 && tiles_all > P.plan.tile_cap) record_error(P.a.err, kCodeDevice, kErrRows, tiles_all, 0);
 
-  KvItem mine{};                                   // tile `tid`, kept for the list
-  int mine_c = 0, top = 0, sum = 0;
-  for (int i = tid; i < T; i += kPlanThreads) {
-    KvItem it{};
-    const int c = tile_of(i, it);
-    if (i < kPlanTiles) cost[i] = c;
-    if (i == tid) {
-      mine = it;
-      mine_c = c;
+  int target = longest;
+  if (longest > kWhole) {
+    if (R.batch <= 32) {
+      // Each lane weighs one way to cut: the longest row into s pieces, the others into pieces as long. The time is
+      // estimated as the waves of items times their mean length and start-up, at least the longest item, and the join
+      // of what was cut (in steps).
+      const int s = lane < 16 ? lane + 1 : lane < 24 ? 16 + (lane - 15) * 4 : 48 + (lane - 23) * 13;
+      const int mine = (longest + s - 1) / s;
+      const float inv = 1.f / mine;
+      int items = 0, cuts = 0;
+      for (int b = 0; b < R.batch; ++b) {
+        const int w = __shfl_sync(0xffffffffu, first.tiles, b);
+        const int p = max(1, int(ceilf(__shfl_sync(0xffffffffu, top, b) * inv - 1e-4f)));
+        items += w * p;
+        if (p > 1) cuts += w * p;
+      }
+      const float waves = ceilf(float(items) * n_kv / sms);
+      float est = fmaxf(waves * (all / max(items, 1) + 2.f), mine + 2.f) + (cuts ? 4.f : 0.f);
+      if (float(cuts) * n_kv > float(P.plan.slots)) est = INFINITY;
+      // the best way, the fewest pieces among equals; estimates are not negative, so their bits order them
+      const unsigned e = __float_as_uint(est);
+      const int best = __ffs(__ballot_sync(0xffffffffu, e == __reduce_min_sync(0xffffffffu, e))) - 1;
+      target = __shfl_sync(0xffffffffu, mine, best);
+    } else {
+      // many rows: only what is twice an SM's share, or longer, is cut, into shares
+      const int share = max(kWhole, int(ceilf(all * n_kv / sms)));
+      if (longest >= 2 * share) target = share;
     }
-    top = max(top, c);
-    sum += c;
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) {
-    tops[warp] = top;
-    sums[warp] = uint64_t(sum);
-  }
-  __syncthreads();
-  top = max(1, __reduce_max_sync(0xffffffffu, tops[lane]));
-  const int all_c = __reduce_add_sync(0xffffffffu, int(sums[lane]));
-
-  // Each warp weighs one way to cut: the longest tile into s pieces, the others into pieces as long. The
-  // time is estimated as the waves of items times their mean length and start-up, at least the longest
-  // item, and the join of what was cut (in steps of 128 tokens).
-  const int s_way = warp < 16 ? warp + 1 : warp < 24 ? 16 + (warp - 15) * 4 : 48 + (warp - 23) * 13;
-  if (T <= kPlanTiles) {
-    const int target = max(1, (top + s_way - 1) / s_way);
-    int items = 0, cut_items = 0;
-    for (int i = lane; i < T; i += 32) {
-      int len;
-      const int p = cut(cost[i], target, &len);
-      items += p;
-      if (p > 1) cut_items += p;
+  for (;;) {
+    first.items = first.slots = first.joins = 0;
+    rows_cut(first, target);
+    Rows32 x = first;
+    for (int row0 = 32; row0 < R.batch; row0 += 32) {
+      rows_load(x, R, row0, P.per_tile);
+      rows_cut(x, target);
     }
-    items = __reduce_add_sync(0xffffffffu, items);
-    cut_items = __reduce_add_sync(0xffffffffu, cut_items);
-    const float waves = ceilf(float(items) * a.n_kv / sms);
-    float est = fmaxf(waves * (float(all_c) / max(items, 1) + 2.f), target + 2.f) + (cut_items ? 4.f : 0.f);
-    if ((int64_t)cut_items * a.n_kv > slots) est = INFINITY;
-    if (lane == 0) est_s[warp] = est;
-  } else if (lane == 0) {
-    est_s[warp] = warp == 0 ? 0.f : INFINITY;
-  }
-  __syncthreads();
-  // the best way, the fewest pieces among equals; estimates are not negative, so their bits order them
-  const unsigned e = __float_as_uint(est_s[lane]);
-  const int best = __ffs(__ballot_sync(0xffffffffu, e == __reduce_min_sync(0xffffffffu, e))) - 1;
-  const int s_best = best < 16 ? best + 1 : best < 24 ? 16 + (best - 15) * 4 : 48 + (best - 23) * 13;
-  const int target = max(1, (top + s_best - 1) / s_best);
-
-  int n_items = 0, n_cut = 0, n_joins = 0;
-  for (int i0 = 0; i0 < T; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    KvItem it = mine;
-    int p = 0, len = 0, c = mine_c;
-    if (i < T) {
-      if (i0 > 0) c = tile_of(i, it);
-      p = cut(c, target, &len);
-    }
-    // items (28 bits), cut items (18) and joins (18) in one scan; slots bounds the last two
-    uint64_t tot;
-    const uint64_t sc = block_scan(uint64_t(p) | uint64_t(p > 1 ? p : 0) << 28 | uint64_t(p > 1) << 46, sums, tot);
-    const int at = n_items + int(sc & 0xfffffff), slot = n_cut + int(sc >> 28 & 0x3ffff);
-    const int join = n_joins + int(sc >> 46);
-    for (int k = 0; k < p; ++k) {
-      it.kv0 = k * len;
-      it.kv1 = min(c, it.kv0 + len);
-      it.split = p > 1 ? slot + k : -1;
-      plan.items[at + k] = it;
-    }
-    if (p > 1) plan.joins[join] = KvJoin{it.q0, it.n, it.tok0, it.tiles, slot, p, {0, 0}};
-    n_items += int(tot & 0xfffffff);
-    n_cut += int(tot >> 28 & 0x3ffff);
-    n_joins += int(tot >> 46);
-  }
-  if (tid == 0) {
-    plan.head->n_items = n_items;
-    plan.head->n_joins = n_joins;
-    plan.head->next = 0;
+    // the estimates leave no cut that the workspace does not hold; if one does, nothing is cut
+    if (x.slots == 0 || (int64_t)x.slots * n_kv <= P.plan.slots) return Plan{target, x.items, x.joins};
+    target = longest;
   }
 }
 
@@ -279,17 +230,37 @@ template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_k
   __shared__ float4 acc_s[kWarps][4][32];
   __shared__ float2 ml_s[kWarps][32];
   const KvAttendArgs& a = P.a;
-  const KvTcPlan& plan = P.plan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_wait();
   grid_release();
-  const int heads = plan.head->n_joins * a.n_kv;
+  const int target = P.plan.head->target, heads = P.plan.head->joins * a.n_kv;
+  if (heads == 0) return;
+  Rows32 rows;
+  rows_load(rows, a.rows, 0, P.per_tile);
+  rows.items = rows.slots = rows.joins = 0;
+  rows_cut(rows, target);
   const bool few = heads <= kJoinFew;
   const int parts = few ? kWarps : 1;
   // the row groups run slowest, so that the tiles' live rows spread over the blocks
   for (int u = blockIdx.x; u < heads * parts * 2 * (kTile / kJoinRows); u += gridDim.x) {
     const int group = u / (heads * parts), in_group = u % (heads * parts);
-    const KvJoin J = plan.joins[in_group / parts / a.n_kv];
+    const int join = in_group / parts / a.n_kv;
+    Rows32 x = rows;                                               // the row of the cut tile
+    unsigned at;
+    while (!(at = __ballot_sync(0xffffffffu, x.pieces > 1 && join >= x.join0 && join < x.join0 + x.tiles))) {
+      rows_load(x, a.rows, x.row0 + 32, P.per_tile);
+      rows_cut(x, target);
+    }
+    const int src = __ffs(at) - 1, in_row = join - __shfl_sync(0xffffffffu, x.join0, src);
+    struct {
+      int q0, n, tok0, tiles, slot, pieces;
+    } J;
+    J.q0 = __shfl_sync(0xffffffffu, x.q0, src);
+    J.n = __shfl_sync(0xffffffffu, x.n, src);
+    J.pieces = __shfl_sync(0xffffffffu, x.pieces, src);
+    J.slot = __shfl_sync(0xffffffffu, x.slot0, src) + in_row * J.pieces;
+    J.tok0 = (__shfl_sync(0xffffffffu, x.tiles, src) - 1 - in_row) * 2 * P.per_tile;
+    J.tiles = J.n - J.tok0 > P.per_tile ? 2 : 1;
     const int h = in_group / parts % a.n_kv, tile = group % 2, r0 = group / 2 * kJoinRows, r = r0 + lane;
     const int c0 = (few ? in_group % parts : warp) * 4;
     if (tile >= J.tiles || r0 >= P.per_tile * a.g || J.tok0 + tile * P.per_tile + r0 / a.g >= J.n) continue;
@@ -437,7 +408,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool keys = warp == 8;
       const CUtensorMap* rows_map = keys ? &tm_k : &tm_v;
       const CUtensorMap* box_map = keys ? &tm_kb : &tm_vb;
-      const int total = P.plan.head->n_items * a.n_kv;
+      Rows32 rows;
+      Plan plan{};
+      if (keys) {
+        plan = plan_rows(P, rows, blockIdx.x == 0);
+        if (blockIdx.x == 0 && lane == 0) {
+          P.plan.head->target = plan.target;
+          P.plan.head->joins = plan.joins;
+        }
+      }
+      const int total = plan.items * a.n_kv;
       const int oob = int(P.oob_row), box = P.box, n_box = box ? kTile / box : 0;
       const int ps = a.pages.page_size, tile_pages = kTile / ps, tile_rest = kTile % ps;
       const int table_pages = int(a.rows.table_pages), n_pages = int(a.pages.n_pages);
@@ -462,8 +442,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) idx = (int)atomicAdd(&P.plan.head->next, 1u);
           idx = __shfl_sync(0xffffffffu, idx, 0);
           if (idx < total) {
-            const KvItem e = P.plan.items[idx / a.n_kv];
-            it = Item{e.q0, e.n, e.L, e.tok0, e.tiles, e.kv0, e.kv1, e.split, idx % a.n_kv, e.b};
+            const int e = idx / a.n_kv;    // never less than the one before
+            while (e >= rows.items) {
+              rows_load(rows, a.rows, rows.row0 + 32, P.per_tile);
+              rows_cut(rows, plan.target);
+            }
+            const int src = __ffs(__ballot_sync(0xffffffffu, e < rows.item0 + rows.tiles * rows.pieces)) - 1;
+            const int in_row = e - __shfl_sync(0xffffffffu, rows.item0, src);
+            const int pieces = __shfl_sync(0xffffffffu, rows.pieces, src), tile = in_row / pieces;
+            it.b = rows.row0 + src;
+            it.h = idx % a.n_kv;
+            it.q0 = __shfl_sync(0xffffffffu, rows.q0, src);
+            it.n = __shfl_sync(0xffffffffu, rows.n, src);
+            it.L = __shfl_sync(0xffffffffu, rows.L, src);
+            it.tok0 = (__shfl_sync(0xffffffffu, rows.tiles, src) - 1 - tile) * 2 * P.per_tile;
+            it.tiles = it.n - it.tok0 > P.per_tile ? 2 : 1;
+            const int last = min(it.n, it.tok0 + it.tiles * P.per_tile) - 1;
+            const int steps = steps_of(min(it.L, it.L - it.n + last + 1)), len = (steps + pieces - 1) / pieces;
+            it.kv0 = min(steps, in_row % pieces * len);
+            it.kv1 = min(steps, it.kv0 + len);
+            it.split = pieces > 1 ? __shfl_sync(0xffffffffu, rows.slot0, src) + in_row : -1;
           }
           if (lane == 0) {
             S.item[i & 1] = it;
@@ -918,7 +916,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (threadIdx.x == 0 && *abort_flag) record_error(a.err, kCodeTimeout, kErrWait, blockIdx.x, 0);
+  if (threadIdx.x == 0) {
+    if (*abort_flag) record_error(a.err, kCodeTimeout, kErrWait, blockIdx.x, 0);
+    // the last CTA to end sets the counter back for the next call; `done` wraps to zero by itself
+    __threadfence();
+    if (atomicInc(&P.plan.head->done, gridDim.x - 1) == gridDim.x - 1) P.plan.head->next = 0;
+  }
   if (warp == 9) tc::tmem_dealloc(tmem, 512);
 }
 
@@ -961,14 +964,12 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
     if (!tma_encode(&tm_k, dt, 2, a.pages.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     if (!tma_encode(&tm_v, dt, 2, a.pages.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
   }
-  cudaError_t e = launch_early(kv_plan_kernel, dim3(1), kPlanThreads, 0, st, P);
-  if (e != cudaSuccess) return e;
   const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
   const unsigned grid = (unsigned)(most < t.sm_count ? most : t.sm_count);
-  e = launch_early(kv_attend_tc_kernel<DH, BF16>, dim3(grid), kThreads, Lay<DH>::kSmem, st, tm_q, tm_k, tm_v, tm_kb, tm_vb,
-                   P);
-  if (e != cudaSuccess) return e;
-  return launch_early(kv_join_kernel<DH, BF16>, dim3(8 * t.sm_count), 2 * DH, 0, st, P);
+  const cudaError_t e = launch_early(kv_attend_tc_kernel<DH, BF16>, dim3(grid), kThreads, Lay<DH>::kSmem, st, tm_q, tm_k,
+                                     tm_v, tm_kb, tm_vb, P);
+  if (e != cudaSuccess || (a.rows.max_kv_len + kTile - 1) / kTile <= kWhole) return e;   // nothing is cut
+  return launch_early(kv_join_kernel<DH, BF16>, dim3(4 * t.sm_count), 2 * DH, 0, st, P);
 }
 
 }  // namespace

@@ -18,7 +18,7 @@ constexpr int kPartSlots = 2 * kKvFewMostCtas;   // few rows: pieces of 16 query
 constexpr int kTcSlots = 456;      // tensor-core kernel: pieces x key/value heads, of two 128-row tiles
 
 struct KvLayout {
-  size_t err, counters, part_ml, part_o, head, items, joins, row_base, total;
+  size_t err, head, counters, part_ml, part_o, total;
 };
 
 // tiles (or pairs of tiles) that n_tokens packed new tokens of `batch` rows make at most
@@ -35,21 +35,14 @@ KvLayout kv_layout(const palu_kv_desc& d) {
   if (d.dtype != PALU_F32) {
     const size_t few = (size_t)kPartSlots * kKvFewRows, tc = (size_t)kTcSlots * 2 * kKvTcRows;
     const size_t rows = few > tc ? few : tc;
-    const size_t cap = (size_t)tc_tile_cap(d, d.max_tokens, d.max_batch);
+    L.head = off;
+    off = align256(off + sizeof(KvPlanHead));
     L.counters = off;
     off = align256(off + kPartSlots * sizeof(unsigned));
     L.part_ml = off;
     off = align256(off + rows * sizeof(float2));
     L.part_o = off;
     off = align256(off + rows * d.head_dim * sizeof(float));
-    L.head = off;
-    off = align256(off + sizeof(KvPlanHead));
-    L.items = off;
-    off = align256(off + (cap + kTcSlots) * sizeof(KvItem));
-    L.joins = off;
-    off = align256(off + kTcSlots * sizeof(KvJoin));
-    L.row_base = off;
-    off = align256(off + ((size_t)d.max_batch + 1) * sizeof(int));
   }
   L.total = off;
   return L;
@@ -196,7 +189,7 @@ palu_status_t palu_kv_create(const palu_kv_desc* desc, void* workspace, size_t w
       return PALU_ERR_CUDA;
     }
   }
-  const size_t clear = desc->dtype == PALU_F32 ? 256 : L.part_ml;   // error word and counters
+  const size_t clear = desc->dtype == PALU_F32 ? 256 : L.part_ml;   // error word, list head and counters
   if (cudaMemsetAsync(h->ws, 0, clear, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
     delete h;
     return PALU_ERR_CUDA;
@@ -343,9 +336,6 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
     if (pages->n_pages * pages->page_size * d.n_kv_heads >= (int64_t(1) << 31) - 1) return PALU_ERR_UNSUPPORTED;
     KvTcPlan t{};
     t.head = reinterpret_cast<KvPlanHead*>(h->ws + h->L.head);
-    t.items = reinterpret_cast<KvItem*>(h->ws + h->L.items);
-    t.joins = reinterpret_cast<KvJoin*>(h->ws + h->L.joins);
-    t.row_base = reinterpret_cast<int*>(h->ws + h->L.row_base);
     t.tile_cap = (int)tc_tile_cap(d, rows->n_tokens, rows->batch);
     t.slots = kTcSlots;
     t.sm_count = h->sm_count;
