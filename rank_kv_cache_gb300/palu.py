@@ -581,7 +581,7 @@ class KVPages:
             raise ValueError("k and v must be [n_pages][page_size][n_kv_heads][head_dim] of one dtype and device")
         self.k, self.v = k, v
         self.n_pages, self.page_size = int(k.shape[0]), int(k.shape[1])
-        self.heads, self.dtype = tuple(k.shape[2:]), k.dtype
+        self.heads, self.dtype, self.index = tuple(k.shape[2:]), k.dtype, k.get_device()
         self._c = palu_kv_pages(_ptr(k), _ptr(v), self.n_pages, self.page_size)
 
     def c_struct(self) -> palu_kv_pages:
@@ -608,7 +608,7 @@ class KVRows:
             raise ValueError("page_table must be [batch][pages]")
         if positions is not None and positions.shape != (n_tokens,):
             raise ValueError("positions must hold n_tokens entries")
-        self.tensors, self.device = (row_start, kv_len, page_table, positions), row_start.device
+        self.tensors, self.index = (row_start, kv_len, page_table, positions), row_start.get_device()
         self.batch, self.n_tokens = batch, int(n_tokens)
         self._c = palu_kv_rows(_ptr(row_start), _ptr(kv_len), _ptr(page_table),
                                0 if page_table is None else int(page_table.shape[1]), _ptr(positions), batch,
@@ -635,6 +635,7 @@ class PagedAttention:
         self.dtype, self.x_dtype = names[dtype], names[x_dtype]
         self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
+        self._index = self.device.index
         self._current = torch._C._cuda_getCurrentRawStream
         base = int(self.workspace.data_ptr())
         st, self.handle = palu_kv_create(self.desc, base + (-base) % 256, nbytes, self._stream(stream))
@@ -653,7 +654,7 @@ class PagedAttention:
 
     def _stream(self, stream) -> int:
         # the raw handle of the current stream: building torch's Stream object takes longer than the call
-        return self._current(self.device.index) if stream is None else stream.cuda_stream
+        return self._current(self._index) if stream is None else stream.cuda_stream
 
     def _empty(self, shape, dtype, stream):
         """An output that belongs to the stream it is written on."""
@@ -665,7 +666,7 @@ class PagedAttention:
 
     def _view(self, name, t, heads, dtype, n_tokens):
         """(pointer, token stride) of a [n_tokens][heads][head_dim] tensor whose tokens may lie apart."""
-        if t.dtype != dtype or t.device != self.device:
+        if t.dtype is not dtype or t.get_device() != self._index:
             raise ValueError(f"{name} must be a {dtype} tensor on {self.device}")
         if t.shape != (n_tokens, heads, self.head_dim):
             raise ValueError(f"{name} must be [{n_tokens}][{heads}][{self.head_dim}]")
@@ -684,7 +685,7 @@ class PagedAttention:
     def _batch(self, pages, rows):
         if pages.heads != (self.n_kv_heads, self.head_dim) or pages.dtype != self.dtype:
             raise ValueError(f"pages must hold {self.n_kv_heads} heads of {self.head_dim} {self.dtype} values")
-        if pages.k.device != self.device or rows.device != self.device:
+        if pages.index != self._index or rows.index != self._index:
             raise ValueError(f"pages and rows must be on {self.device}")
 
     def norm_rope(self, q, k=None, positions=None, *, q_weight=None, k_weight=None, q_out=None, k_out=None,
