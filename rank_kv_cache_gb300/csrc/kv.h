@@ -172,7 +172,7 @@ cudaError_t launch_kv_attend_few(KvAttendArgs a, int sm_count, cudaStream_t st);
 
 // the tensor-core kernel
 constexpr int kKvTcRows = 128;           // query rows of a tile
-constexpr int kKvTcWhole = 4;            // steps of 128 cached tokens up to which a tile is not cut
+constexpr int kKvTcWhole = 12;           // steps of 128 cached tokens up to which a tile is not cut
 struct KvPlanHead {
   unsigned next;     // the next item to take; zero between calls
   unsigned done;     // CTAs that have ended; zero between calls

@@ -186,7 +186,7 @@ __device__ __forceinline__ Plan plan_rows(const TcParams& P, Rows32& first, bool
         if (p > 1) cuts += w * p;
       }
       const float waves = ceilf(float(items) * n_kv / sms);
-      float est = fmaxf(waves * (all / max(items, 1) + 2.f), mine + 2.f) + (cuts ? 4.f : 0.f);
+      float est = fmaxf(waves * (all / max(items, 1) + 2.f), mine + 2.f) + (cuts ? 6.f : 0.f);
       if (float(cuts) * n_kv > float(P.plan.slots)) est = INFINITY;
       // the best way, the fewest pieces among equals; estimates are not negative, so their bits order them
       const unsigned e = __float_as_uint(est);
@@ -222,9 +222,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 
 // A block takes 32 query rows of a cut tile, a lane one row: o = sum_k 2^(m_k - M) o_k / L over the pieces. A warp
 // takes 16 of the columns, and four pieces' loads are in flight at a time (they come from L2: one piece after the
-// other took a microsecond each). Where few tiles are cut, into many pieces then, a block takes 16 columns and its
-// warps share the pieces.
-constexpr int kJoinRows = 32, kJoinFew = 32;
+// other took a microsecond each). Tiles of as many pieces as a block has warps, so few that there is a block for each
+// 16 columns, are joined with the warps sharing the pieces of 16 columns.
+constexpr int kJoinRows = 32;
 template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_kernel(const TcParams P) {
   constexpr int kWarps = DH / 16;
   __shared__ float4 acc_s[kWarps][4][32];
@@ -233,13 +233,14 @@ template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_k
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_wait();
   grid_release();
+  Rows32 rows;
+  rows_load(rows, a.rows, 0, P.per_tile);      // under way with the plan
   const int target = P.plan.head->target, heads = P.plan.head->joins * a.n_kv;
   if (heads == 0) return;
-  Rows32 rows;
-  rows_load(rows, a.rows, 0, P.per_tile);
   rows.items = rows.slots = rows.joins = 0;
   rows_cut(rows, target);
-  const bool few = heads <= kJoinFew;
+  const int groups = (min(2 * P.per_tile, a.rows.max_new) * a.g + kJoinRows - 1) / kJoinRows;
+  const bool few = rows.slots >= kWarps * rows.joins && (int64_t)heads * groups * kWarps <= gridDim.x;
   const int parts = few ? kWarps : 1;
   // the row groups run slowest, so that the tiles' live rows spread over the blocks
   for (int u = blockIdx.x; u < heads * parts * 2 * (kTile / kJoinRows); u += gridDim.x) {
