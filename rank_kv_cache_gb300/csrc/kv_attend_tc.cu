@@ -7,11 +7,10 @@
 // under head j, floor(128 / g) tokens fill a 128-row tile, and K and V are read once for the group. A
 // work item is (row of the batch, key/value head, one or two tiles, a range of the cached tokens).
 //
-// Two launches. kv_attend_tc_kernel is persistent, one CTA an SM; each CTA works out the list of items from
-// the rows' lengths (the longest first within a row, cut along the cached tokens where whole tiles would
-// leave SMs idle) and takes items off it by an atomic counter (which item runs where does not change any
-// sum). kv_join_kernel joins the pieces of what was cut, in their order; it is left out where the call's
-// bounds allow no cut.
+// One launch, persistent, one CTA an SM. Each CTA works out the list of items from the rows' lengths (the longest
+// first within a row, cut along the cached tokens where whole tiles would leave SMs idle) and takes items off it
+// by an atomic counter (which item runs where does not change any sum). When the list is empty, the CTAs wait for
+// the pieces of what was cut, and join them in their order.
 //
 // One CTA: two softmax warpgroups, two loader warps and an MMA warp.
 //   * The loaders bring 128 cached tokens at a time by TMA into a ring of K and V tiles (128-byte
@@ -64,12 +63,19 @@ struct Item {
   int q0, n, L, tok0, tiles, kv0, kv1, split, h, b;
 };
 
+struct Plan {
+  int target;                             // longest piece, in steps of 128 cached tokens
+  int items, joins, slots;                // of one head: items, cut tiles, pieces of cut tiles
+};
+
 struct Shared {
   uint64_t full[10], empty[10];
   uint64_t q_full, q_empty, x_full, drained;
   uint64_t s_full[2], o_full[2], p_full[2][2];
   uint64_t item_full[2], item_empty[2];
   Item item[2];
+  Plan plan;
+  unsigned cut;                           // pieces of cut tiles that this CTA has taken
   uint32_t tmem;
   int abort_flag;
   float2 ml[kTile];
@@ -130,11 +136,6 @@ __device__ __forceinline__ void rows_cut(Rows32& x, int target) {
   x.slots += int(all >> 28 & 0x3ffff);
   x.joins += int(all >> 46);
 }
-
-struct Plan {
-  int target;                             // longest piece, in steps of 128 cached tokens
-  int items, joins;                       // of one head; cut tiles
-};
 
 // The plan: the same for every warp that asks. `first` gets the first 32 rows, cut.
 __device__ __forceinline__ Plan plan_rows(const TcParams& P, Rows32& first, bool report) {
@@ -207,7 +208,7 @@ __device__ __forceinline__ Plan plan_rows(const TcParams& P, Rows32& first, bool
       rows_cut(x, target);
     }
     // the estimates leave no cut that the workspace does not hold; if one does, nothing is cut
-    if (x.slots == 0 || (int64_t)x.slots * n_kv <= P.plan.slots) return Plan{target, x.items, x.joins};
+    if (x.slots == 0 || (int64_t)x.slots * n_kv <= P.plan.slots) return Plan{target, x.items, x.joins, x.slots};
     target = longest;
   }
 }
@@ -220,54 +221,63 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// A block takes 32 query rows of a cut tile, a lane one row: o = sum_k 2^(m_k - M) o_k / L over the pieces. A warp
-// takes 16 of the columns, and four pieces' loads are in flight at a time (they come from L2: one piece after the
-// other took a microsecond each). Tiles of as many pieces as a block has warps, so few that there is a block for each
-// 16 columns, are joined with the warps sharing the pieces of 16 columns.
-constexpr int kJoinRows = 32;
-template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_kernel(const TcParams P) {
-  constexpr int kWarps = DH / 16;
-  __shared__ float4 acc_s[kWarps][4][32];
-  __shared__ float2 ml_s[kWarps][32];
+// The join, by the softmax warps of all CTAs once every piece is stored: o = sum_k 2^(m_k - M) o_k / L over a tile's
+// pieces, in their order. A warp takes 32 query rows, a lane one, and 16 columns; four pieces' loads are in flight at a
+// time (they come from L2: one piece after the other took a microsecond each; eight at a time took longer, with fewer
+// registers left). Where such units are no more than the CTAs and have two pieces a warp or more, a CTA takes a unit
+// and its warps share the pieces: 8 new tokens at 65536 (19 pieces) 63.8 against 70.6 us, of two sequences (9 pieces)
+// 92.0 against 89.3, so not there. As a kernel of its own behind this one the join took 2 to 7 us more.
+constexpr int kJoinRows = 32, kJoinWarps = 8, kJoinLoads = 4;
+// waits, at most `limit_ns`, until `pieces` are stored
+__device__ __forceinline__ bool pieces_wait(const unsigned* stored, unsigned pieces, uint64_t limit_ns) {
+  const uint64_t t0 = tc::globaltimer();
+  for (;;) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(stored) : "memory");
+    if (v == pieces) return true;
+    if (tc::globaltimer() - t0 > limit_ns) return false;
+    __nanosleep(50);
+  }
+}
+
+struct JoinShared {
+  float4 acc[kJoinWarps][4][32];
+  float2 ml[kJoinWarps][32];
+};
+static_assert(sizeof(JoinShared) <= 2 * Lay<64>::kTileB, "in the queries' space");
+
+template <int DH, bool BF16>
+__device__ __forceinline__ void join_pieces(const TcParams& P, const Plan& plan, Rows32& rows, JoinShared& X) {
   const KvAttendArgs& a = P.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  grid_wait();
-  grid_release();
-  Rows32 rows;
-  rows_load(rows, a.rows, 0, P.per_tile);      // under way with the plan
-  const int target = P.plan.head->target, heads = P.plan.head->joins * a.n_kv;
-  if (heads == 0) return;
   rows.items = rows.slots = rows.joins = 0;
-  rows_cut(rows, target);
-  const int groups = (min(2 * P.per_tile, a.rows.max_new) * a.g + kJoinRows - 1) / kJoinRows;
-  const bool few = rows.slots >= kWarps * rows.joins && (int64_t)heads * groups * kWarps <= gridDim.x;
-  const int parts = few ? kWarps : 1;
-  // the row groups run slowest, so that the tiles' live rows spread over the blocks
-  for (int u = blockIdx.x; u < heads * parts * 2 * (kTile / kJoinRows); u += gridDim.x) {
-    const int group = u / (heads * parts), in_group = u % (heads * parts);
-    const int join = in_group / parts / a.n_kv;
+  rows_cut(rows, plan.target);
+  // unit: columns fastest, then heads, tiles, and last the row groups of which a tile may have none
+  constexpr int kParts = DH / 16;
+  const int inner = plan.joins * a.n_kv * kParts;
+  const int live = (min(2 * P.per_tile, a.rows.max_new) * a.g + kJoinRows - 1) / kJoinRows;
+  const bool share = plan.slots >= 2 * kJoinWarps * plan.joins && (int64_t)inner * live <= gridDim.x;
+  const int first = share ? blockIdx.x : blockIdx.x + gridDim.x * warp, step = gridDim.x * (share ? 1 : kJoinWarps);
+  for (int un = first; un < inner * 2 * (kTile / kJoinRows); un += step) {
+    const int group = un / inner, in_group = un % inner, join = in_group / kParts / a.n_kv;
     Rows32 x = rows;                                               // the row of the cut tile
     unsigned at;
     while (!(at = __ballot_sync(0xffffffffu, x.pieces > 1 && join >= x.join0 && join < x.join0 + x.tiles))) {
       rows_load(x, a.rows, x.row0 + 32, P.per_tile);
-      rows_cut(x, target);
+      rows_cut(x, plan.target);
     }
     const int src = __ffs(at) - 1, in_row = join - __shfl_sync(0xffffffffu, x.join0, src);
-    struct {
-      int q0, n, tok0, tiles, slot, pieces;
-    } J;
-    J.q0 = __shfl_sync(0xffffffffu, x.q0, src);
-    J.n = __shfl_sync(0xffffffffu, x.n, src);
-    J.pieces = __shfl_sync(0xffffffffu, x.pieces, src);
-    J.slot = __shfl_sync(0xffffffffu, x.slot0, src) + in_row * J.pieces;
-    J.tok0 = (__shfl_sync(0xffffffffu, x.tiles, src) - 1 - in_row) * 2 * P.per_tile;
-    J.tiles = J.n - J.tok0 > P.per_tile ? 2 : 1;
-    const int h = in_group / parts % a.n_kv, tile = group % 2, r0 = group / 2 * kJoinRows, r = r0 + lane;
-    const int c0 = (few ? in_group % parts : warp) * 4;
-    if (tile >= J.tiles || r0 >= P.per_tile * a.g || J.tok0 + tile * P.per_tile + r0 / a.g >= J.n) continue;
-    const int i = J.tok0 + tile * P.per_tile + r / a.g;
-    const bool live = r < P.per_tile * a.g && i < J.n;
-    const int64_t s0 = ((int64_t)J.slot * a.n_kv + h) * 2 + tile;
+    const int q0 = __shfl_sync(0xffffffffu, x.q0, src), n = __shfl_sync(0xffffffffu, x.n, src);
+    const int pieces = __shfl_sync(0xffffffffu, x.pieces, src);
+    const int slot = __shfl_sync(0xffffffffu, x.slot0, src) + in_row * pieces;
+    const int tok0 = (__shfl_sync(0xffffffffu, x.tiles, src) - 1 - in_row) * 2 * P.per_tile;
+    const int tiles = n - tok0 > P.per_tile ? 2 : 1;
+    const int h = in_group / kParts % a.n_kv, tile = group % 2, r0 = group / 2 * kJoinRows, r = r0 + lane;
+    const int c0 = in_group % kParts * 4;
+    if (tile >= tiles || r0 >= P.per_tile * a.g || tok0 + tile * P.per_tile + r0 / a.g >= n) continue;
+    const int i = tok0 + tile * P.per_tile + r / a.g;
+    const bool live_row = r < P.per_tile * a.g && i < n;
+    const int64_t s0 = ((int64_t)slot * a.n_kv + h) * 2 + tile;
     const int64_t pitch = (int64_t)2 * a.n_kv * kTile;             // rows between two pieces' partials
     const float2* ml = a.part_ml + s0 * kTile + r;
     const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + c0) * kTile + r;
@@ -275,56 +285,72 @@ template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_k
     float4 acc[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto sum = [&](int first, int step) {
-#pragma unroll 8
-      for (int k = first; k < J.pieces; k += step) M = fmaxf(M, ml[k * pitch].x);
-      const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-      for (int k = first; k < J.pieces; k += step) {
-        const float2 v = ml[k * pitch];
-        const float w = exp2f(v.x - base);
-        L = fmaf(v.y, w, L);
+    auto add = [&](const float4 (&v)[4], float w) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 x = po[k * pitch * (DH / 4) + c * kTile];
-          acc[c].x = fmaf(x.x, w, acc[c].x);
-          acc[c].y = fmaf(x.y, w, acc[c].y);
-          acc[c].z = fmaf(x.z, w, acc[c].z);
-          acc[c].w = fmaf(x.w, w, acc[c].w);
-        }
+      for (int c = 0; c < 4; ++c) {
+        acc[c].x = fmaf(v[c].x, w, acc[c].x);
+        acc[c].y = fmaf(v[c].y, w, acc[c].y);
+        acc[c].z = fmaf(v[c].z, w, acc[c].z);
+        acc[c].w = fmaf(v[c].w, w, acc[c].w);
       }
     };
-    if (live && few) sum(warp, kWarps);
-    if (live && !few) sum(0, 1);
-    if (few) {
-      ml_s[warp][lane] = make_float2(M, L);
+    if (live_row) {
+      const int dk = share ? kJoinWarps : 1;
+#pragma unroll 1
+      for (int k0 = share ? warp : 0; k0 < pieces; k0 += kJoinLoads * dk) {
+        float2 v[kJoinLoads];
+        float4 y[kJoinLoads][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc_s[warp][c][lane] = acc[c];
-      __syncthreads();
+        for (int e = 0; e < kJoinLoads; ++e) {
+          const int k = k0 + e * dk;
+          v[e] = make_float2(-INFINITY, 0.f);
+          if (k >= pieces) continue;
+          v[e] = __ldcg(&ml[k * pitch]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[e][c] = __ldcg(&po[k * pitch * (DH / 4) + c * kTile]);
+        }
+        float top = M;
+#pragma unroll
+        for (int e = 0; e < kJoinLoads; ++e) top = fmaxf(top, v[e].x);
+        const float base = top == -INFINITY ? 0.f : top, f = exp2f(M - base);
+        M = top;
+        L *= f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = make_float4(acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f);
+#pragma unroll
+        for (int e = 0; e < kJoinLoads; ++e) {
+          if (k0 + e * dk >= pieces) continue;
+          const float w = exp2f(v[e].x - base);
+          L = fmaf(v[e].y, w, L);
+          add(y[e], w);
+        }
+      }
+    }
+    if (share) {
+      X.ml[warp][lane] = make_float2(M, L);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) X.acc[warp][c][lane] = acc[c];
+      tc::named_bar(1, kJoinWarps * 32);
       if (warp == 0) {
-        for (int x = 1; x < kWarps; ++x) M = fmaxf(M, ml_s[x][lane].x);
+        for (int k = 1; k < kJoinWarps; ++k) M = fmaxf(M, X.ml[k][lane].x);
         const float base = M == -INFINITY ? 0.f : M;
         L = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = 0; x < kWarps; ++x) {
-          const float2 v = ml_s[x][lane];
+        for (int k = 0; k < kJoinWarps; ++k) {
+          const float2 v = X.ml[k][lane];
+          float4 y[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[c] = X.acc[k][c][lane];
           const float w = exp2f(v.x - base);
           L = fmaf(v.y, w, L);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 y = acc_s[x][c][lane];
-            acc[c].x = fmaf(y.x, w, acc[c].x);
-            acc[c].y = fmaf(y.y, w, acc[c].y);
-            acc[c].z = fmaf(y.z, w, acc[c].z);
-            acc[c].w = fmaf(y.w, w, acc[c].w);
-          }
+          add(y, w);
         }
       }
     }
-    if (live && (!few || warp == 0)) {
+    if (live_row && (!share || warp == 0)) {
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      const int64_t row = (int64_t)(J.q0 + i) * a.n_heads + h * a.g + r % a.g;
+      const int64_t row = (int64_t)(q0 + i) * a.n_heads + h * a.g + r % a.g;
       if (c0 == 0 && a.lse) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
       uint32_t w8[8];
 #pragma unroll
@@ -334,7 +360,7 @@ template <int DH, bool BF16> __global__ void __launch_bounds__(2 * DH) kv_join_k
       }
       store32(static_cast<uint16_t*>(a.out) + row * DH + c0 * 4, w8);
     }
-    if (few) __syncthreads();
+    if (share) tc::named_bar(1, kJoinWarps * 32);
   }
 }
 
@@ -386,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&S.item_empty[u], 10);     // eight softmax warps, the MMA warp, the value loader
     }
     S.abort_flag = 0;
+    S.cut = 0;
     tc::fence_barrier_init();
   }
   if (warp == 9) {
@@ -413,10 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Plan plan{};
       if (keys) {
         plan = plan_rows(P, rows, blockIdx.x == 0);
-        if (blockIdx.x == 0 && lane == 0) {
-          P.plan.head->target = plan.target;
-          P.plan.head->joins = plan.joins;
-        }
+        if (lane == 0) S.plan = plan;        // the first item's arrival publishes it
       }
       const int total = plan.items * a.n_kv;
       const int oob = int(P.oob_row), box = P.box, n_box = box ? kTile / box : 0;
@@ -732,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&S.item_empty[i & 1]);
       if (it.tiles == 0) break;
+      if (threadIdx.x == 0 && it.split >= 0) ++S.cut;
       const int tile = it.tiles == 2 ? u : 0;
       const int first_tok = it.tok0 + tile * P.per_tile;
       const int tok = first_tok + r / a.g;
@@ -912,6 +937,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&S.q_empty);
       }
     }
+    // The join. Every item has been taken when a CTA comes here, by CTAs that run and wait for none: the wait for
+    // their pieces ends whichever CTAs the GPU holds. All warps meet first, also after a wait that gave up.
+    const auto any = [](bool bad) { return tc::named_bar_or(1, kJoinWarps * 32, bad); };
+    if (!any(!ok) && S.plan.joins > 0) {
+      Rows32 rows;
+      rows_load(rows, a.rows, 0, P.per_tile);
+      if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(&P.plan.head->pieces, S.cut);
+        ok = pieces_wait(&P.plan.head->pieces, unsigned(S.plan.slots * a.n_kv), P.wait_ns);
+        if (!ok) *abort_flag = 1;
+      }
+      // the queries' space is free: nothing is in flight behind the last item
+      if (!any(!ok)) join_pieces<DH, BF16>(P, S.plan, rows, *reinterpret_cast<JoinShared*>(smem));
+    }
   }
 
   tc::tc_fence_before();
@@ -919,9 +959,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_after();
   if (threadIdx.x == 0) {
     if (*abort_flag) record_error(a.err, kCodeTimeout, kErrWait, blockIdx.x, 0);
-    // the last CTA to end sets the counter back for the next call; `done` wraps to zero by itself
+    // the last CTA to end sets the counters back for the next call; `done` wraps to zero by itself
     __threadfence();
-    if (atomicInc(&P.plan.head->done, gridDim.x - 1) == gridDim.x - 1) P.plan.head->next = 0;
+    if (atomicInc(&P.plan.head->done, gridDim.x - 1) == gridDim.x - 1) P.plan.head->next = P.plan.head->pieces = 0;
   }
   if (warp == 9) tc::tmem_dealloc(tmem, 512);
 }
@@ -967,10 +1007,8 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
   }
   const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
   const unsigned grid = (unsigned)(most < t.sm_count ? most : t.sm_count);
-  const cudaError_t e = launch_early(kv_attend_tc_kernel<DH, BF16>, dim3(grid), kThreads, Lay<DH>::kSmem, st, tm_q, tm_k,
-                                     tm_v, tm_kb, tm_vb, P);
-  if (e != cudaSuccess || (a.rows.max_kv_len + kTile - 1) / kTile <= kWhole) return e;   // nothing is cut
-  return launch_early(kv_join_kernel<DH, BF16>, dim3(4 * t.sm_count), 2 * DH, 0, st, P);
+  return launch_early(kv_attend_tc_kernel<DH, BF16>, dim3(grid), kThreads, Lay<DH>::kSmem, st, tm_q, tm_k, tm_v, tm_kb,
+                      tm_vb, P);
 }
 
 }  // namespace

@@ -425,3 +425,42 @@ def test_every_layer_of_a_step_on_one_handle_in_a_graph():
             b.pv = pages[i].v.cpu()
             b.check(out[i], torch.from_numpy(s), (o, s, size, reach))
     layer.check_device()
+
+
+@pytest.mark.parametrize("n,m", [(8, 1), (6, 3)])
+def test_cut_rows_behind_the_first_32(n, m):
+    # the join finds its rows 32 at a time: long ones first, in the second 32 and last
+    news, lens = [3] * 70, [40 + i for i in range(70)]
+    for b in (1, 37, 69):
+        news[b], lens[b] = 40, 9000 + b
+    b = Batch(n=n, m=m, d=128, dtype="bf16", news=news, lens=lens, page=64, seed=26)
+    out, lse = b.attend()
+    b.layer.check_device()
+    at = np.concatenate([[0], np.cumsum(news)])
+    b.check_sampled(out, lse, [int(at[x]) + y for x in (1, 37, 69) for y in (0, 39)] + [int(at[36])], [0, n - 1])
+    o2, l2 = b.attend()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_cut_calls_side_by_side():
+    """Two handles' calls whose pieces both wait for the join, on two streams at once."""
+    a = Batch(n=8, m=2, d=128, dtype="bf16", news=[64], lens=[20000], page=64, seed=27)
+    b = Batch(n=8, m=8, d=64, dtype="f16", news=[300, 20], lens=[6000, 9000], page=16, seed=28)
+    ra, rb = a.attend(), b.attend()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(20):
+        oa, ob = torch.empty_like(ra[0]), torch.empty_like(rb[0])
+        la, lb = torch.empty_like(ra[1]), torch.empty_like(rb[1])
+        torch.cuda.synchronize()
+        for _ in range(5):
+            a.layer.attend(a.pages, a.rows, a.qd, out=oa, lse=la, stream=sa)
+            b.layer.attend(b.pages, b.rows, b.qd, out=ob, lse=lb, stream=sb)
+        outs.append((oa, la, ob, lb))
+    torch.cuda.synchronize()
+    a.layer.check_device()
+    b.layer.check_device()
+    for oa, la, ob, lb in outs:
+        assert torch.equal(oa, ra[0]) and torch.equal(la, ra[1])
+        assert torch.equal(ob, rb[0]) and torch.equal(lb, rb[1])
