@@ -31,6 +31,13 @@
 // Sums, maxima, S and O are fp32; the weights p are rounded to the cache's type, as the product takes
 // them; l is the sum of the unrounded p.
 //
+// Bound: the tensor cores while the softmax of one unit hides behind the other's products; in long calls the power
+// limit, at which library matrix products of this type settle near the same rate (1680 TFLOP/s).
+// Measured on a GB300, 32 / 8 heads of 128, bf16: 2048 new tokens at 65536 1436 us (1510 TFLOP/s); a chunk of 512
+// among 15 sequences that decode, at 16384, 208 us; up to five drafted tokens of eight ragged sequences up to 16384
+// 82 us, 4800 GB/s. Four prompts of 4096, 32 / 32 heads, fp16: 405 us (1360). At d = 64 the products halve and the
+// softmax does not, and bounds it: 1024 new tokens of two sequences at 16384 316 us, 840 TFLOP/s.
+//
 // Every wait is bounded; one that gives up records PALU_ERR_TIMEOUT, and all roles wait for their own
 // copies and products in flight before tensor memory is freed.
 #include "kv.h"
@@ -70,7 +77,7 @@ struct Plan {
 
 struct Shared {
   uint64_t full[10], empty[10];
-  uint64_t q_full, q_empty, x_full, drained;
+  uint64_t q_full, q_empty, x_full, x_empty, drained;
   uint64_t s_full[2], o_full[2], p_full[2][2];
   uint64_t item_full[2], item_empty[2];
   Item item[2];
@@ -401,8 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&S.empty[i], 1);
     }
     tc::mbar_init(&S.q_full, 1);
-    tc::mbar_init(&S.q_empty, 5);              // the products that read the queries; warpgroup 0's warps
+    tc::mbar_init(&S.q_empty, 1);              // the products that read the queries
     tc::mbar_init(&S.x_full, 4);
+    tc::mbar_init(&S.x_empty, 4);
     tc::mbar_init(&S.drained, 1);
     for (int u = 0; u < 2; ++u) {
       tc::mbar_init(&S.s_full[u], 1);
@@ -448,6 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int table_pages = int(a.rows.table_pages), n_pages = int(a.pages.n_pages);
       const int oob_slot = n_pages * ps;
       int st = 0, loads_q = 0, seq = 0;    // the ring's next stage; stages counted
+      int n_x = 0;                         // exchanges of the units, and whether the last is still to be waited for
+      bool exchanged = false;
       uint32_t par = 1, mine = 0;          // what `empty` is waited for; which of the last stages this warp filled
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -505,7 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kv1 == kv0) continue;
         const int32_t* table = a.rows.page_table ? a.rows.page_table + (int64_t)b * table_pages : nullptr;
         if (keys) {
+          // the queries' space: read by the last item's products and, where its units met there, by warpgroup 0
           if (!wait(&S.q_empty, (loads_q & 1) ^ 1)) break;
+          if (exchanged && !wait(&S.x_empty, n_x++ & 1)) break;
+          exchanged = tiles == 1 && kv1 - kv0 > 1;
           if (lane == 0) {
             tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(tiles) * P.per_tile * a.g * DH * 2);
             for (int t = 0; t < tiles; ++t)
@@ -764,10 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vis = it.L - it.n + tok;                         // last slot this row sees
       const int vis_min = it.L - it.n + first_tok;               // every row of the tile sees slots up to here
       const int steps = unit_steps(it, u, P.per_tile);
-      const bool any = it.kv1 > it.kv0;
-      // queries are free for the next item once warpgroup 0 needs nothing of their space either
       const bool exchange = it.tiles == 1 && it.kv1 - it.kv0 > 1;
-      if (any && !exchange && u == 0 && lane == 0) tc::mbar_arrive(&S.q_empty);
 
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < steps; ++k) {
@@ -934,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (exchange) {                                            // the queries' space is read: TMA may fill it again
         tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.q_empty);
+        if (lane == 0) tc::mbar_arrive(&S.x_empty);
       }
     }
     // The join. Every item has been taken when a CTA comes here, by CTAs that run and wait for none: the wait for
@@ -994,7 +1004,8 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
     const cuuint32_t box[2] = {64, 1};
     const cuuint64_t bdims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)(a.pages.n_pages * a.pages.page_size)};
     const cuuint64_t bstrides[2] = {DH * 2, (cuuint64_t)a.n_kv * DH * 2};
-    // a box must lie in one page: without a table a row is one page, else the largest power of two that divides it
+    // A box must lie in one page: without a table a row is one page, else the largest power of two that divides it.
+    // 512 new tokens at 8192: 76 us from pages of 64 and more, 84 of 16, 92 of 8, and 157 gathered from pages of 100.
     int box_tokens = a.rows.page_table ? a.pages.page_size & -a.pages.page_size : kTile;
     box_tokens = box_tokens > kTile ? kTile : box_tokens;
     P.box = box_tokens >= 8 ? box_tokens : 0;

@@ -464,3 +464,34 @@ def test_cut_calls_side_by_side():
     for oa, la, ob, lb in outs:
         assert torch.equal(oa, ra[0]) and torch.equal(la, ra[1])
         assert torch.equal(ob, rb[0]) and torch.equal(lb, rb[1])
+
+
+@pytest.mark.parametrize("n,m,d,batch,new,extra", [(32, 32, 128, 11, 400, 0), (24, 8, 128, 9, 700, 900), (8, 8, 64, 27, 830, 0),
+                                                   (28, 4, 64, 17, 600, 1), (32, 8, 128, 12, 40, 2000)])
+def test_many_items_a_cta_give_the_same_bits_every_time(n, m, d, batch, new, extra):
+    """Items follow each other on a CTA while a unit of the one before still runs: repeated calls agree bit for bit, and
+    with float64 on a sample."""
+    news = [new - i % 5 for i in range(batch)]
+    b = Batch(n=n, m=m, d=d, dtype="bf16", news=news, lens=[x + extra for x in news], page=32, seed=29)
+    ref, ref_lse = b.attend()
+    at = np.concatenate([[0], np.cumsum(news)])
+    b.check_sampled(ref, ref_lse, [int(at[x]) for x in (0, batch // 2)] + [int(at[batch]) - 1], [0, n - 1])
+    diff = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        out, lse = b.attend()
+        diff += (out != ref).sum() + (lse != ref_lse).sum()
+    b.layer.check_device()
+    assert int(diff) == 0
+
+
+def test_a_handle_made_on_a_side_stream():
+    from rank_kv_cache_gb300 import palu as P
+    b = Batch(n=4, m=2, d=128, dtype="f16", news=[1, 30], lens=[400, 2000], page=16, seed=30)
+    ref, _ = b.attend()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    layer = P.PagedAttention(n_heads=4, n_kv_heads=2, head_dim=128, dtype="f16", max_batch=2, max_tokens=b.N, stream=s)
+    out = layer.attend(b.pages, b.rows, b.qd, stream=s)
+    s.synchronize()
+    assert torch.equal(out, ref)
+    layer.check_device(s)
