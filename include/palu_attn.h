@@ -506,9 +506,10 @@ palu_status_t palu_norm_rope(palu_kv_t h, const void* q, int64_t q_stride, const
  * Append the new tokens' keys, normed and rotated as by palu_norm_rope, and their values to the pages,
  * and norm and rotate their queries into q_out, in one launch. k, v (and q) as q, k above with
  * n_kv_heads heads; q and q_out (device [n_tokens][n_heads][head_dim] contiguous, dtype) may both be
- * NULL. The inputs do not overlap the pages. Rotation positions are rows->positions, or the slots. A token whose slot is negative, lies past
- * the page table or in a page outside the pool is recorded in the error word and not stored. Two
- * tokens that fall on one slot (a page shared by two rows that both append to it) leave either's.
+ * NULL. The inputs do not overlap the pages. Rotation positions are rows->positions, or the slots. A token
+ * whose slot is negative, lies past the page table or in a page outside the pool is recorded in the error
+ * word and not stored. Two tokens that fall on one slot (a page shared by two rows that both append to it)
+ * leave a mixture of the two, in 16-byte pieces.
  */
 palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu_kv_rows* rows, const void* q,
                              int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -520,7 +521,7 @@ palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
  * 1/sqrt(head_dim).
  *   q    device [n_tokens][n_heads][head_dim] in dtype, rotated, 16-byte aligned, tokens q_stride elements apart
  *        (a multiple of 8)
- *   out  device [n_tokens][n_heads][head_dim] in dtype, contiguous, 16-byte aligned
+ *   out  device [n_tokens][n_heads][head_dim] in dtype, contiguous, 16-byte aligned; overlaps no input
  *   lse  device [n_tokens][n_heads] float32 natural log-sum-exp of the scaled scores, or NULL
  * A token that sees no slot (kv_len[b] < n_b) yields 0 and lse = -inf. Slots at or past kv_len[b] are
  * not read and may hold anything; the slots below it must be finite. fp32 scores, softmax statistics

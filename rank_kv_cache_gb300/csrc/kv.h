@@ -162,9 +162,12 @@ struct KvAttendArgs {
   int ctas;                    // few rows: CTAs that the GPU holds at once
   ErrWord* err;
 };
-constexpr int kKvFewRows = 16;           // query rows (token, head of the group) of a unit
+// Query rows (token, head of the group) of a unit: what one matrix instruction takes, and the most that run here.
+// 16 rows took 169 us here against 179 on the tensor-core kernel (64 sequences at 4096), 64 against 66 (one at
+// 65536) and 12.0 against 11.3 (16 at 256); 20 rows, in two passes, 120 against 82 (eight ragged up to 16384).
+constexpr int kKvFewRows = 16;
 constexpr int kKvFewTokens = 64;         // cached tokens of 128 elements that a CTA's warps take together
-constexpr int kKvFewCtas = 2;            // CTAs of an SM
+constexpr int kKvFewCtas = 2;            // CTAs of an SM; one takes 237 us where two take 160 (four at 65536)
 constexpr int kKvFewMostCtas = 512;      // most CTAs of a call; cut units have at most twice as many pieces
 // once a handle, on its device: what the kernel's launches need set
 cudaError_t prepare_kv_attend_few(int head_dim, bool bf16);

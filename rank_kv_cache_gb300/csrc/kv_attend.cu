@@ -18,6 +18,10 @@
 // until they are joined. Rows past the end are written as zeros into shared memory and masked, never
 // read. The weights p are rounded to the cache's type for the product with V, as the matrix instruction
 // takes it; the sum is of the unrounded p.
+//
+// Measured on a GB300, 32 / 8 heads of 128, bf16: one token of four sequences at 65536 (1.07 GB) 160 us, 6700
+// GB/s; of 64 sequences at 4096 163 us. 32 / 32 heads, one sequence at 4096 (67 MB): 20 us, 17 with the cache in
+// L2, of which the start and the join are half. 8 / 8 heads of 64, one at 512: 8 us.
 #include "kv.h"
 
 namespace palu {
@@ -128,7 +132,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
   if (all == 0) return;
   // A piece's length: at least an equal share of all CTAs that the GPU holds. Up to 32 rows, each lane weighs one
   // length, 1 to 3 times that share: the waves of CTAs times the length and what a CTA's start and end cost (eight
-  // steps), and the join of what is cut (four). More rows are cut a quarter longer than the share.
+  // steps), and the join of what is cut (four). More rows are cut a quarter longer than the share. The quarter alone
+  // took 169 us against 136 for 32 ragged rows up to 8192 and 137 against 119 for 20 of 7000, and up to 1 us less
+  // for few equal rows (48.4 against 50.3, one of 65536).
   const int64_t work = all * a.n_kv;
   const int share = work < (1 << 30) ? (int(work) + a.ctas - 1) / a.ctas : int((work + a.ctas - 1) / a.ctas);
   int per = share + share / 4;

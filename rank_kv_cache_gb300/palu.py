@@ -633,7 +633,8 @@ class PagedAttention:
         check(st, "palu_kv_workspace_size")
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
         self.dtype, self.x_dtype = names[dtype], names[x_dtype]
-        self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        self.device = torch.device(device)
+        self.workspace = self._empty((nbytes + 256,), torch.uint8, stream)
         self.device = self.workspace.device
         self._index = self.device.index
         self._current = torch._C._cuda_getCurrentRawStream
