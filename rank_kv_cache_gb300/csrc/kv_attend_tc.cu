@@ -31,12 +31,12 @@
 // Sums, maxima, S and O are fp32; the weights p are rounded to the cache's type, as the product takes
 // them; l is the sum of the unrounded p.
 //
-// Bound: the tensor cores while the softmax of one unit hides behind the other's products; in long calls the power
-// limit, at which library matrix products of this type settle near the same rate (1680 TFLOP/s).
+// Bound: the round of a unit, S to weights to its products, of which two in turn keep the tensor cores 61% busy at
+// 1.9 GHz (exponentials 36%, issue 42%); in long calls the clock falls besides, with the power limit.
 // Measured on a GB300, 32 / 8 heads of 128, bf16: 2048 new tokens at 65536 1436 us (1510 TFLOP/s); a chunk of 512
 // among 15 sequences that decode, at 16384, 208 us; up to five drafted tokens of eight ragged sequences up to 16384
 // 82 us, 4800 GB/s. Four prompts of 4096, 32 / 32 heads, fp16: 405 us (1360). At d = 64 the products halve and the
-// softmax does not, and bounds it: 1024 new tokens of two sequences at 16384 316 us, 840 TFLOP/s.
+// softmax does not: 1024 new tokens of two sequences at 16384 316 us, 840 TFLOP/s.
 //
 // Every wait is bounded; one that gives up records PALU_ERR_TIMEOUT, and all roles wait for their own
 // copies and products in flight before tensor memory is freed.
