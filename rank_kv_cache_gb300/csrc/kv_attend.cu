@@ -131,15 +131,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
     all += __reduce_add_sync(0xffffffffu, row_steps(b0 + lane, blockIdx.x == 0 && warp == 0));
   if (all == 0) return;
   // A piece's length: at least an equal share of all CTAs that the GPU holds. Up to 32 rows, each lane weighs one
-  // length, 1 to 3 times that share: the waves of CTAs times the length and what a CTA's start and end cost (eight
-  // steps), and the join of what is cut (four). More rows are cut a quarter longer than the share. The quarter alone
+  // length, from that share to three times it or 31 steps more: the waves of CTAs times the length and what a CTA's
+  // start and end cost (eight steps), and the join of what is cut (four; with eight, 8 sequences at 1000 took 12.3 us
+  // against 9.6; with lengths up to twice a share of one step only, 300 tokens of two sequences 7.6 against 6.5). More rows are cut a quarter longer than the share. The quarter alone
   // took 169 us against 136 for 32 ragged rows up to 8192 and 137 against 119 for 20 of 7000, and up to 1 us less
   // for few equal rows (48.4 against 50.3, one of 65536).
   const int64_t work = all * a.n_kv;
   const int share = work < (1 << 30) ? (int(work) + a.ctas - 1) / a.ctas : int((work + a.ctas - 1) / a.ctas);
   int per = share + share / 4;
   if (R.batch <= 32) {
-    const int mine = share + share * lane / 16;
+    const int mine = share + lane * max(1, share / 16);
     const float inv = 1.f / mine;
     int count = 0, cuts = 0;
     for (int b = 0; b < R.batch; ++b) {
