@@ -25,8 +25,6 @@ enum ErrWhere : unsigned {
   kErrSlot = 3,       // an append slot outside the cache
   kErrQueryPos = 4,   // q_pos outside the RoPE table
   kErrWait = 5,       // a bounded mbarrier wait gave up
-  kErrPage = 6,       // a page table entry outside the page pool
-  kErrRows = 7,       // row_start decreases, or a row has more new tokens than the call's bound
 };
 constexpr unsigned kCodeDevice = 4;   // PALU_ERR_DEVICE
 constexpr unsigned kCodeTimeout = 5;  // PALU_ERR_TIMEOUT

@@ -9,6 +9,10 @@
 
 namespace palu {
 
+// what this cache's operators record beside ErrWhere's
+constexpr unsigned kErrPage = 6;   // a page table entry outside the page pool
+constexpr unsigned kErrRows = 7;   // row_start decreases, or a row has more new tokens than the call's bound
+
 constexpr int kKvMaxHalf = 64;   // pairs of a head: head_dim / 2
 
 // Rotation frequencies: F_k = frac(theta^(-2k/d) / 2 pi) as a 64-bit fraction of a turn, so that

@@ -42,7 +42,7 @@
 // copies and products in flight before tensor memory is freed.
 #include "kv.h"
 #include "internal.h"
-#include "tc_ptx.cuh"
+#include "kv_tc_ptx.cuh"
 
 namespace palu {
 namespace {
