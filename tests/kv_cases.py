@@ -54,7 +54,7 @@ class Batch:
     """Rows of new tokens over paged caches, with every slot that no row may read set to NaN."""
 
     def __init__(self, *, n, m, d, dtype, news, lens, page, table=True, seed=0, q_scale=1.0, slack=2, extra_tokens=0,
-                 max_new=None, max_kv=None, big=False):
+                 max_new=None, max_kv=None):
         from rank_kv_cache_gb300 import palu as P
         rng = np.random.default_rng(seed)
         self.n, self.m, self.d, self.dtype, self.news, self.lens, self.page = n, m, d, dtype, news, lens, page

@@ -495,3 +495,40 @@ def test_a_handle_made_on_a_side_stream():
     s.synchronize()
     assert torch.equal(out, ref)
     layer.check_device(s)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("table", [True, False])
+def test_pools_past_32_bit_offsets(new, table):
+    """Pages at both ends of a pool of over 2^32 elements: the same bits, written and read, as from a small pool."""
+    from rank_kv_cache_gb300 import palu as P
+    rng, dev = np.random.default_rng(31), torch.device("cuda:0")
+    n, m, d, B, L = 16, 8, 128, 2, 300
+    page, small = (64, 12) if table else (L + 20, B)
+    far = 2 ** 32 // (m * d * 64) + 40 if table else B
+    wide = 64 if table else 2 ** 32 // (m * d) + 64                     # without a table row 1 is page 1
+    ids = torch.tensor([far - 1 - i if i % 2 else i for i in range(small)]) if table else torch.arange(B)
+    pools = []
+    for pages, size in ((small, page), (far, wide)):
+        pools.append(P.KVPages(*(torch.empty(pages, size, m, d, dtype=torch.bfloat16, device=dev) for _ in range(2))))
+    for name in ("k", "v"):
+        x = rounded(rng, (small, page, m, d), "bf16").to(dev)
+        getattr(pools[0], name).copy_(x)
+        getattr(pools[1], name)[ids.to(dev), :page] = x
+    layer = P.PagedAttention(n_heads=n, n_kv_heads=m, head_dim=d, dtype="bf16", max_batch=B, max_tokens=B * new)
+    start = torch.arange(0, B * new + 1, new, dtype=torch.int32, device=dev)
+    lens = torch.tensor([L, L - 7], dtype=torch.int32, device=dev)
+    order = torch.from_numpy(rng.permutation(small)[:B * 5].reshape(B, 5)) if table else None
+    q, k, v = (rounded(rng, (B * new, h, d), "bf16").to(dev) for h in (n, m, m))
+    got = []
+    for pool, where in zip(pools, (None, ids)):
+        t = None if order is None else (order if where is None else where[order]).int().to(dev)
+        rows = P.KVRows(start, lens, n_tokens=B * new, max_new=new, max_kv_len=L, page_table=t)
+        lse = torch.empty(B * new, n, dtype=torch.float32, device=dev)
+        q_rot = layer.append(pool, rows, k, v, q=q)
+        got.append((q_rot, layer.attend(pool, rows, q_rot, lse=lse), lse))
+    layer.check_device()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    for name in ("k", "v"):
+        assert torch.equal(getattr(pools[0], name), getattr(pools[1], name)[ids.to(dev), :page])
