@@ -95,6 +95,7 @@ struct TcParams {
   int per_tile;        // tokens of a 128-row tile: floor(128 / g)
   int box;             // cached tokens a TMA box takes: 8 .. 128, a power of two; 0: rows are gathered
   int64_t oob_row;     // a row index outside the gather maps
+  int out_sectors;     // the output is 32-byte aligned, and with it each 16 columns of a head; else 16-byte aligned
   uint64_t wait_ns;
 };
 
@@ -225,8 +226,13 @@ __device__ __forceinline__ Plan plan_rows(const TcParams& P, Rows32& first, bool
 }
 
 // ------------------------------------------------------------------------------------------- join
-// one 32-byte sector
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+// 32 bytes of output; `sector`: p is 32-byte aligned, as one store of that size needs
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], int sector) {
+  if (!sector) {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    return;
+  }
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
@@ -369,7 +375,7 @@ __device__ __forceinline__ void join_pieces(const TcParams& P, const Plan& plan,
         w8[2 * c] = pack2<BF16>(acc[c].x * inv, acc[c].y * inv);
         w8[2 * c + 1] = pack2<BF16>(acc[c].z * inv, acc[c].w * inv);
       }
-      store32(static_cast<uint16_t*>(a.out) + row * DH + c0 * 4, w8);
+      store32(static_cast<uint16_t*>(a.out) + row * DH + c0 * 4, w8, P.out_sectors);
     }
     if (share) tc::named_bar(1, kJoinWarps * 32);
   }
@@ -940,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[8];
 #pragma unroll
             for (int z = 0; z < 8; ++z) w[z] = pack2<BF16>(o[16 * y + 2 * z], o[16 * y + 2 * z + 1]);
-            store32(out + 16 * y, w);
+            store32(out + 16 * y, w, P.out_sectors);
           }
         }
       }
@@ -992,6 +998,7 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
   P.per_tile = kTile / a.g;
   const int64_t rows = a.pages.n_pages * a.pages.page_size * a.n_kv;
   P.oob_row = rows;
+  P.out_sectors = (uintptr_t)a.out % 32 == 0;
   P.wait_ns = t.wait_ns;
   CUtensorMap tm_q, tm_k, tm_v, tm_kb, tm_vb;
   {
