@@ -525,7 +525,8 @@ palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
  *   lse  device [n_tokens][n_heads] float32 natural log-sum-exp of the scaled scores, or NULL
  * A token that sees no slot (kv_len[b] < n_b) yields 0 and lse = -inf. Slots at or past kv_len[b] are
  * not read and may hold anything; the slots below it must be finite. fp32 scores, softmax statistics
- * and accumulation; the softmax weights are rounded to dtype for the product with the values. A
+ * and accumulation; the softmax weights are rounded to dtype for the product with the values (F16: at
+ * least in steps of 2^-31 of the row's largest, as long as scores stay below 2^20 log2 units). A
  * length outside [0, max_kv_len], a row with more than max_new new tokens (both clamped), a decreasing
  * row_start (the row is skipped) and a page outside the pool (read as zeros) are recorded in the
  * error word. The result does not depend on timing: the same call gives the same bits.

@@ -117,6 +117,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// What the exponents of a softmax's weights are taken from, for a largest score `top` (log2 units): p = 2^(s - base).
+// The weights are rounded to the cache's type for the product with V, while their sum is not. In fp16 a weight below
+// 2^-25 would vanish from the product alone: behind a score 17.4 (natural) above the others, as attention sinks have,
+// 65536 tokens would lose 2^-9 of that score's weight, and all of their own. So fp16 weights are lifted to use the
+// type's range, the largest 2^lift; a shift of the base changes neither o / l nor m + log2 l. Scores past 2^20, whose
+// fp32 steps could carry the largest weight out of range, are not lifted. bf16 has the range of fp32.
+template <bool BF16> __device__ __forceinline__ float softmax_base(float top, float lift) {
+  if constexpr (BF16) return top;
+  return fabsf(top) < 1048576.f ? top - lift : top;
+}
+
 template <bool BF16> __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (BF16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);

@@ -17,7 +17,7 @@
 // sum and output) and its own three-stage ring of cp.async copies, so no barrier stands between the warps
 // until they are joined. Rows past the end are written as zeros into shared memory and masked, never
 // read. The weights p are rounded to the cache's type for the product with V, as the matrix instruction
-// takes it; the sum is of the unrounded p.
+// takes it (fp16: up to 2^15, see softmax_base); the sum is of the unrounded p.
 //
 // Measured on a GB300, 32 / 8 heads of 128, bf16: one token of four sequences at 65536 (1.07 GB) 160 us, 6700
 // GB/s; of 64 sequences at 4096 163 us. 32 / 32 heads, one sequence at 4096 (67 MB): 20 us, 17 with the cache in
@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
+constexpr float kLift = 15.f;            // log2 of the largest fp16 weight
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
         for (int i = 1; i < kNT; ++i) mx = fmaxf(mx, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[x], mx * a.scale_log2);
+        const float mn = fmaxf(m[x], softmax_base<BF16>(mx * a.scale_log2, kLift));
         base[x] = mn == -INFINITY ? 0.f : mn;                        // nothing seen yet: every p is 2^-inf = 0
         al[x] = ex2(m[x] - base[x]);
         m[x] = mn;

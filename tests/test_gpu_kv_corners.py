@@ -40,3 +40,78 @@ def test_outputs_and_queries_at_16_modulo_32(dtype, d, n, m, news, lens):
     b.layer.check_device()
     # the address changes how the output is stored, not what is computed
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("d,dtype", [(128, "f16"), (64, "f16"), (128, "bf16")])
+def test_long_tails_behind_attention_sinks_keep_their_weight(new, d, dtype):
+    """Seven sinks with a score of 18 above 65529 tokens of score 0, which hold all the values: each of those weighs
+    2^-26 of a sink, together 1.4e-4 of the output. The sinks stand where every warp, unit and tile of the kernels' first
+    steps has one, and the rows are as many as leave them whole.
+
+    Bound: the score 18 is a sum of d products accumulated in fp32 (2^-16 of it), the exponential 2^-20, both of them in
+    the sinks' weights and the others'; a weight's rounding u, or half an fp16 step (2^-25) of weights that are lifted so
+    that a sink's is 2^7 at least: 2^-32 of it for each of the others; the sums 2^-20; the output u and half its smallest
+    step."""
+    from rank_kv_cache_gb300 import palu as P
+    B, m, L, page = 38, 8, 65536, 256
+    dev, t = torch.device("cuda:0"), TYPES[dtype]
+    sinks = torch.tensor([0, 16, 32, 48, 64, 96, 128], device=dev)
+    k, v = torch.zeros(L // page, page, m, d, dtype=t, device=dev), torch.full((L // page, page, m, d), 64.0, dtype=t, device=dev)
+    each = torch.tensor(18.0 * d ** 0.5 / d).to(t)
+    k.view(L, m, d)[sinks] = each.to(dev)
+    v.view(L, m, d)[sinks] = 0
+    score = float(each) * d / d ** 0.5
+    table = torch.arange(L // page, dtype=torch.int32, device=dev).expand(B, -1).contiguous()   # all rows read the same
+    rows = P.KVRows(torch.arange(0, B * new + 1, new, dtype=torch.int32, device=dev),
+                    torch.full((B,), L, dtype=torch.int32, device=dev), n_tokens=B * new, max_new=new, max_kv_len=L,
+                    page_table=table)
+    layer = P.PagedAttention(n_heads=m, n_kv_heads=m, head_dim=d, dtype=dtype, max_batch=B, max_tokens=B * new)
+    q = torch.ones(B * new, m, d, dtype=t, device=dev)
+    lse = torch.empty(B * new, m, dtype=torch.float32, device=dev)
+    out = layer.attend(P.KVPages(k, v), rows, q, lse=lse)
+    layer.check_device()
+    others = L - new + 1 + np.arange(new, dtype=np.float64) - 7      # of new token i
+    total = others + 7 * np.exp(score)
+    ref = np.tile(64 * others / total, B)[:, None, None]
+    ref_lse = np.tile(np.log(total), B)[:, None]
+    f = torch.finfo(t)
+    e = 2.0 ** -16 * score + 2.0 ** -20
+    steps = 2.0 ** -32 * 64 * L / 7 if dtype == "f16" else 0.0
+    tol = (f.eps + 2 * e + 2.0 ** -20) * ref + steps + f.smallest_normal * f.eps / 2
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3f} of the bound"
+    assert np.all(np.abs(lse.double().cpu().numpy() - ref_lse) <= e + 2.0 ** -20 * (1 + ref_lse))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_scores_past_the_lifted_range_stay_finite(new):
+    # every score is 4.5e6 or more (log2 units 6.5e6), and the first of all by 2^-3 of that: one-hot rows
+    from rank_kv_cache_gb300 import palu as P
+    dev, d, L = torch.device("cuda:0"), 128, 700
+    k = torch.full((1, L, 1, d), 1000.0, dtype=torch.float16, device=dev)
+    k[0, 0] = 1125.0
+    v = torch.randn(1, L, 1, d, generator=torch.Generator(dev).manual_seed(41), device=dev).half()
+    q = torch.full((new, 2, d), 400.0, dtype=torch.float16, device=dev)
+    rows = P.KVRows(torch.tensor([0, new], dtype=torch.int32, device=dev), torch.tensor([L], dtype=torch.int32, device=dev),
+                    n_tokens=new, max_new=new, max_kv_len=L)
+    layer = P.PagedAttention(n_heads=2, n_kv_heads=1, head_dim=d, dtype="f16", max_tokens=new)
+    lse = torch.empty(new, 2, dtype=torch.float32, device=dev)
+    out = layer.attend(P.KVPages(k, v), rows, q, lse=lse)
+    layer.check_device()
+    # the base is a multiple of 1/2 at this size, so the one weight left is 2^x, |x| <= 1/4, not 1: it is rounded to fp16
+    # (u) for the product and not for the sum, and the quotient is rounded once more (u)
+    ref, u = v[0, 0, 0].double(), 2.0 ** -11
+    assert torch.all((out.double() - ref).abs() <= (2 * u + 2.0 ** -20) * ref.abs() + 2.0 ** -25)
+    s = 400.0 * 1125 * d / d ** 0.5
+    assert torch.all((lse.double() - s).abs() <= 2.0 ** -16 * s)
+
+
+@pytest.mark.parametrize("new,q_scale", [(1, 12.0), (50, 2.0), (200, 12.0)])
+def test_fp16_rows_whose_maximum_rises(new, q_scale):
+    # scores that rise and fall by more and by less than the threshold, over cut and whole tiles
+    b = Batch(n=4, m=2, d=128, dtype="f16", news=[new, new], lens=[1500, 400], page=16, seed=42, q_scale=q_scale)
+    wave = 1 + torch.sin(torch.arange(b.pk.shape[0] * 16) / 200).reshape(-1, 16, 1, 1)
+    b.pk = (b.pk.float() * wave).half()
+    b.pages.k.copy_(b.pk)
+    b.run_and_check()
