@@ -495,7 +495,8 @@ typedef struct palu_kv_rows {
  *   positions       device [n_tokens], any int32; may be NULL when the handle rotates nothing
  *   q_out, k_out    device, dtype, same layout and rules; may be q and k themselves where dtype = x_dtype and
  *                   the strides agree. Other overlaps are not allowed
- * fp32 arithmetic, one rounding to dtype at the end; angles are reduced exactly at any position.
+ * fp32 arithmetic, one rounding to dtype at the end; before the fp32 sine and cosine an angle is right to
+ * 2^-34 turns at any position (rope_theta >= 1).
  */
 palu_status_t palu_norm_rope(palu_kv_t h, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                              const void* q_norm, const void* k_norm, const int32_t* positions, int64_t n_tokens,

@@ -15,8 +15,9 @@ constexpr unsigned kErrRows = 7;   // row_start decreases, or a row has more new
 
 constexpr int kKvMaxHalf = 64;   // pairs of a head: head_dim / 2
 
-// Rotation frequencies: F_k = frac(theta^(-2k/d) / 2 pi) as a 64-bit fraction of a turn, so that
-// pos * F_k mod 2^64 is the phase of position pos, range-reduced exactly for every int32 position.
+// Rotation frequencies: F_k = frac(theta^(-2k/d) / 2 pi) as a 64-bit fraction of a turn, rounded to nearest.
+// pos * F_k mod 2^64 is then the phase of position pos: of the product nothing is lost, and the rounding of
+// F_k moves it by at most 2^-34 turns for any int32 position.
 struct KvFreq {
   uint64_t turn[kKvMaxHalf];
 };

@@ -84,6 +84,43 @@ struct DeviceGuard {
   }
 };
 
+// An unevaluated sum of two doubles, the second at most half an ulp of the first: 106 bits (Dekker 1971). The leading
+// product is kept from being fused with what follows.
+struct Dd {
+  double hi, lo;
+};
+Dd dd_sum(double a, double b) {            // |a| >= |b|
+  volatile double s = a + b;
+  return {s, b - (s - a)};
+}
+Dd dd_mul(Dd a, Dd b) {
+  volatile double p = a.hi * b.hi;
+  return dd_sum(p, fma(a.hi, b.hi, -p) + fma(a.hi, b.lo, a.lo * b.hi));
+}
+Dd dd_sqrt(Dd a) {                         // one Newton step from the double's root
+  const double s = sqrt(a.hi);
+  return dd_sum(s, (fma(-s, s, a.hi) + a.lo) / (2 * s));
+}
+Dd dd_inverse(Dd a) {
+  const double q = 1 / a.hi;
+  return dd_sum(q, q * fma(-q, a.lo, fma(-q, a.hi, 1.0)));
+}
+
+// turn[k] = theta^(-2k/d) / 2 pi in units of 2^-64 turns, rounded to a whole one (bases below 1 reach whole turns, which
+// fall away). In doubles the 53 bits of a frequency are off by up to 3e-7 rad at the far end of the positions; here the
+// root theta^(2/d) takes five or six square roots and each frequency one product, with 2^-96 of error.
+void rope_turns(double theta, int half, uint64_t* turn) {
+  Dd root{theta, 0.0};
+  for (int n = half; n > 1; n /= 2) root = dd_sqrt(root);
+  const Dd step = dd_inverse(root);
+  Dd w{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};       // 1 / (2 pi)
+  for (int k = 0; k < half; ++k, w = dd_mul(w, step)) {
+    const double t = ldexp(w.hi - floor(w.hi), 64), whole = floor(t);
+    const double rest = (t - whole) + ldexp(w.lo - floor(w.lo + 0.5), 64);
+    turn[k] = isfinite(t) && fabs(rest) < 0x1p63 ? (whole < 0x1p64 ? (uint64_t)whole : 0) + (uint64_t)llrint(rest) : 0;
+  }
+}
+
 }  // namespace
 
 struct palu_kv {
@@ -175,12 +212,7 @@ palu_status_t palu_kv_create(const palu_kv_desc* desc, void* workspace, size_t w
   h->L = L;
   h->device = attr.device;
   h->sm_count = sms;
-  const int half = desc->head_dim / 2;
-  for (int k = 0; k < half && desc->rope_theta > 0.0; ++k) {
-    const double turns = pow(desc->rope_theta, -2.0 * k / desc->head_dim) / 6.283185307179586476925286766559;
-    const double v = ldexp(turns - floor(turns), 64);
-    h->freq.turn[k] = v >= 18446744073709549568.0 ? ~0ull : (uint64_t)v;
-  }
+  if (desc->rope_theta > 0.0) rope_turns(desc->rope_theta, desc->head_dim / 2, h->freq.turn);
   if (desc->dtype != PALU_F32) {
     const bool bf16 = desc->dtype == PALU_BF16;
     if (prepare_kv_attend_few(desc->head_dim, bf16) != cudaSuccess ||

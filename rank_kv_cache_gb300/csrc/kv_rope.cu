@@ -12,7 +12,7 @@
 // lanes make a head, and a warp takes 4 (d = 128) or 8 heads at once. The angles of a token are the
 // same for all of its heads: a warp computes its lanes' eight sines and cosines once and walks over
 // the token's heads with them, the next heads' loads under way (the first ones' while it looks up the
-// token's place). Phases are 64-bit fractions of a turn, so far positions lose nothing. The arithmetic
+// token's place). Phases are 64-bit fractions of a turn, so far positions keep theirs. The arithmetic
 // is packed two fp32 to an instruction: unpacked it was bound by issue.
 //
 // Measured on a GB300: 16384 tokens of 32 + 8 heads of 128, bf16, normed: 57.7 us, 5820 GB/s, as a

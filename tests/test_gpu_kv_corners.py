@@ -115,3 +115,51 @@ def test_fp16_rows_whose_maximum_rises(new, q_scale):
     b.pk = (b.pk.float() * wave).half()
     b.pages.k.copy_(b.pk)
     b.run_and_check()
+
+
+def _turns(theta, d, k, digits=60):
+    """theta^(-2k/d) / 2 pi, as a Decimal."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = digits
+
+    def arctan_inverse(n):
+        term, total, i = Decimal(1) / n, Decimal(1) / n, 1
+        while abs(term) > Decimal(10) ** -digits:
+            term, i = -term / (n * n), i + 2
+            total += term / i
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))           # Machin
+    return (Decimal(theta).ln() * (Decimal(-2 * k) / d)).exp() / (2 * pi)
+
+
+@pytest.mark.parametrize("theta", [1e4, 1e5])
+@pytest.mark.parametrize("d,sign", [(128, 1), (64, 1), (64, -1)])
+def test_far_positions_against_sixty_digits(theta, d, sign):
+    """Of the 2^20 farthest positions, each pair's whose angle comes nearest to whole turns: there fp32 holds the sine to
+    2^-24 of itself, and an error of the frequency shows. Bound: half of 2^-64 turns, times the position, in radians; four
+    roundings of the sine."""
+    from decimal import Decimal
+    from rank_kv_cache_gb300 import palu as P
+    half, dev = d // 2, torch.device("cuda:0")
+    pos = sign * (np.int64(2 ** 31 - 1) - np.arange(2 ** 20))
+    exact = [_turns(theta, d, k) for k in range(half)]
+    at, sines = [], []
+    for f in exact:
+        turn = np.uint64(int((f % 1) * 2 ** 64))                     # to find the positions; the angles are exact
+        with np.errstate(over="ignore"):
+            phase = (pos.astype(np.uint64) * turn).view(np.int64)
+        i = int(np.argmin(np.abs(phase.astype(np.float64))))
+        x = (f * int(pos[i])) % 1
+        x = float(x - 1 if x > Decimal("0.5") else x + 1 if x < Decimal("-0.5") else x)
+        at.append(int(pos[i]))
+        sines.append(np.sin(2 * np.pi * x))
+    x = torch.zeros(half, 1, d, device=dev)
+    x[:, :, :half] = 1.0                                             # pairs (1, 0) turn into (cos, sin)
+    layer = P.PagedAttention(n_heads=1, n_kv_heads=1, head_dim=d, dtype="f32", rope_theta=theta, max_tokens=half)
+    y, _ = layer.norm_rope(x, positions=torch.tensor(at, dtype=torch.int32, device=dev))
+    got = y[:, 0].diagonal(half).double().cpu().numpy()              # token k's sine of pair k
+    sines = np.array(sines)
+    assert np.abs(sines).max() < 2.0 ** -9
+    tol = 2.0 ** -65 * 2.0 ** 31 * 2 * np.pi + 2.0 ** -22 * np.abs(sines)
+    assert np.all(np.abs(got - sines) <= tol), np.max(np.abs(got - sines) / tol)
