@@ -507,9 +507,11 @@ palu_status_t palu_norm_rope(palu_kv_t h, const void* q, int64_t q_stride, const
  * Append the new tokens' keys, normed and rotated as by palu_norm_rope, and their values to the pages,
  * and norm and rotate their queries into q_out, in one launch. k, v (and q) as q, k above with
  * n_kv_heads heads; q and q_out (device [n_tokens][n_heads][head_dim] contiguous, dtype) may both be
- * NULL. The inputs do not overlap the pages. Rotation positions are rows->positions, or the slots. A token
- * whose slot is negative, lies past the page table or in a page outside the pool is recorded in the error
- * word and not stored. Two tokens that fall on one slot (a page shared by two rows that both append to it)
+ * NULL; q_out may be q itself where dtype = x_dtype and q is contiguous. The inputs do not overlap the
+ * pages. Rotation positions are rows->positions, or the slots. A token whose slot is negative, lies past the
+ * page table or in a page outside the pool is recorded in the error word and not stored; a length outside
+ * [0, max_kv_len], a row with more than max_new new tokens and a decreasing row_start are recorded as by
+ * palu_attend_kv (the tokens that have a row and a slot are stored). Two tokens that fall on one slot (a page shared by two rows that both append to it)
  * leave a mixture of the two, in 16-byte pieces.
  */
 palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu_kv_rows* rows, const void* q,

@@ -54,19 +54,27 @@ template <typename T> struct Vec8 {
   }
 };
 
-// Row of packed token t: the number of rows that end at or before it (row_start does not decrease).
-// Warp-wide: 32 row ends a step.
+// Row of packed token t: the first that ends behind it (batch: none does), so that a row out of order behind it changes
+// nothing. Warp-wide: 32 row ends a step.
 __device__ __forceinline__ int row_of_token(const KvRows& r, int t) {
   const int lane = threadIdx.x & 31;
-  int b = 0;
   for (int base = 0; base < r.batch; base += 32) {
     const int i = base + lane;
-    const bool past = i < r.batch && r.row_start[i + 1] <= t;
-    const unsigned m = __ballot_sync(0xffffffffu, past);
-    b += __popc(m);
-    if (m != 0xffffffffu) break;
+    const unsigned m = __ballot_sync(0xffffffffu, i < r.batch && r.row_start[i + 1] > t);
+    if (m) return base + __ffs(m) - 1;
   }
-  return b;
+  return r.batch;
+}
+
+// Records what the attention would of the rows: bounds that do not hold, a row_start that decreases. A warp of its own
+// does it, beside those of the tokens.
+__device__ __noinline__ void check_rows(const KvRopeArgs& a) {
+  for (int b = threadIdx.x & 31; b < a.rows.batch; b += 32) {
+    int q0, n, L;
+    unsigned bad;
+    kv_row(a.rows, b, q0, n, L, bad);
+    if (bad) record_error(a.err, kCodeDevice, bad, b, b);
+  }
 }
 
 template <typename TI, typename TO, int DH>
@@ -80,7 +88,10 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a, c
   // the same for the warp, and told so
   const unsigned unit = __shfl_sync(0xffffffffu, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), 0);
   const int t = int(unit / unsigned(parts)), part = int(unit % unsigned(parts));
-  if (t >= a.n_tokens) return;
+  if (t >= a.n_tokens) {
+    if (a.append && unit == unsigned(a.n_tokens) * unsigned(parts)) check_rows(a);
+    return;
+  }
   const int nq = (a.heads[0] + kHeads - 1) / kHeads, nk = (a.heads[1] + kHeads - 1) / kHeads;   // chunks
   const int c0 = part * chunks_per_part, c1 = min(c0 + chunks_per_part, nq + nk + (a.heads[2] + kHeads - 1) / kHeads);
 
@@ -197,7 +208,7 @@ cudaError_t launch_typed(const KvRopeArgs& a, const KvFreq& f, int sm_count, cud
   while (parts > 1 && (int64_t)a.n_tokens * parts > (int64_t)sm_count * 64) parts = (parts + 1) / 2;
   const int cpp = (chunks + parts - 1) / parts;
   parts = (chunks + cpp - 1) / cpp;
-  const int64_t units = (int64_t)a.n_tokens * parts;
+  const int64_t units = (int64_t)a.n_tokens * parts + (a.append ? 1 : 0);   // one to check the rows
   const unsigned grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32));
   if (a.head_dim == 128) return launch_early(kv_rope_kernel<TI, TO, 128>, dim3(grid), kThreads, 0, st, a, f, parts, cpp);
   return launch_early(kv_rope_kernel<TI, TO, 64>, dim3(grid), kThreads, 0, st, a, f, parts, cpp);

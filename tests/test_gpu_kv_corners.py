@@ -163,3 +163,38 @@ def test_far_positions_against_sixty_digits(theta, d, sign):
     assert np.abs(sines).max() < 2.0 ** -9
     tol = 2.0 ** -65 * 2.0 ** 31 * 2 * np.pi + 2.0 ** -22 * np.abs(sines)
     assert np.all(np.abs(got - sines) <= tol), np.max(np.abs(got - sines) / tol)
+
+
+@pytest.mark.parametrize("what,row_start,lens,max_new,max_kv", [
+    ("a length past the bound, with pages for it", [0, 2, 4], [9, 5], 2, 8),
+    ("a negative length of a row without new tokens", [0, 4, 4], [9, -1], 4, 12),
+    ("more new tokens than the bound", [0, 3, 4], [9, 5], 2, 12),
+    ("a bound of no new tokens", [0, 3, 4], [9, 5], 0, 12),
+    ("a row that starts before the one ahead of it", [0, 3, 1], [9, 5], 4, 12),
+    ("a row that ends behind the tokens", [0, 3, 5], [9, 5], 4, 12),
+    ("the last of many rows", [0, 2, 4] + [4] * 40, [9, 5] + [4] * 39 + [13], 2, 12),
+])
+def test_append_reports_rows_that_break_their_bounds(what, row_start, lens, max_new, max_kv):
+    """What attend reports of the rows, append does too: not every cache that is filled here is read by attend."""
+    from rank_kv_cache_gb300 import palu as P
+    rng, dev, batch = np.random.default_rng(43), torch.device("cuda:0"), len(lens)
+    k, v = rounded(rng, (4, 1, 64), "f16").to(dev), rounded(rng, (4, 1, 64), "f16").to(dev)
+    layer = P.PagedAttention(n_heads=1, n_kv_heads=1, head_dim=64, dtype="f16", max_batch=batch, max_tokens=4)
+    table = torch.arange(batch * 4, dtype=torch.int32, device=dev).view(batch, 4)
+
+    def run(row_start, lens, max_new, max_kv):
+        pages = P.KVPages(*(torch.zeros(batch * 4, 4, 1, 64, dtype=torch.float16, device=dev) for _ in range(2)))
+        rows = P.KVRows(torch.tensor(row_start, dtype=torch.int32, device=dev), torch.tensor(lens, dtype=torch.int32, device=dev),
+                        n_tokens=4, max_new=max_new, max_kv_len=max_kv, page_table=table)
+        layer.append(pages, rows, k, v)
+        return pages
+
+    run([0, 2, 4] + [4] * (batch - 2), [9, 5] + [4] * (batch - 2), 2, 12)
+    layer.check_device()                                             # rows that keep their bounds
+    pages = run(row_start, lens, max_new, max_kv)
+    with pytest.raises(P.PaluError):
+        layer.check_device()
+    layer.check_device()                                             # reported once
+    # tokens 0 and 1 have a row and a slot in every case: they are stored
+    n = row_start[1]
+    assert torch.equal(pages.v.view(batch, 16, 64)[0, 9 - n:11 - n], v[:2, 0])
