@@ -336,7 +336,7 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
   if (st != PALU_OK) return st;
   const palu_kv_desc& d = h->d;
   if (d.dtype == PALU_F32) return PALU_ERR_UNSUPPORTED;
-  if (rows->batch == 0 || rows->n_tokens == 0 || rows->max_new == 0) return PALU_OK;
+  if (rows->batch == 0 || rows->n_tokens == 0) return PALU_OK;
   if (bad_view(q, q_stride, d.n_heads, d.head_dim, d.dtype)) return PALU_ERR_INVALID_ARG;
   if (!out || (uintptr_t)out % 16 || (uintptr_t)lse % 4) return PALU_ERR_INVALID_ARG;
   DeviceGuard dev(h->device);

@@ -198,3 +198,15 @@ def test_append_reports_rows_that_break_their_bounds(what, row_start, lens, max_
     # tokens 0 and 1 have a row and a slot in every case: they are stored
     n = row_start[1]
     assert torch.equal(pages.v.view(batch, 16, 64)[0, 9 - n:11 - n], v[:2, 0])
+
+
+def test_attend_reports_new_tokens_past_a_bound_of_none():
+    from rank_kv_cache_gb300 import palu as P
+    b = Batch(n=4, m=2, d=64, dtype="f16", news=[2, 0], lens=[20, 30], page=16, seed=44, max_new=0)
+    out, lse = b.attend()
+    with pytest.raises(P.PaluError):
+        b.layer.check_device()
+    assert torch.all(out == 7.0) and torch.all(lse == 7.0)           # clamped to no new tokens
+    b.rows.tensors[0].zero_()                                        # rows that keep the bound
+    b.attend()
+    b.layer.check_device()
