@@ -206,10 +206,10 @@ __device__ __forceinline__ Plan plan_rows(const TcParams& P, Rows32& first, bool
       const int best = __ffs(__ballot_sync(0xffffffffu, e == __reduce_min_sync(0xffffffffu, e))) - 1;
       target = __shfl_sync(0xffffffffu, mine, best);
     } else {
-      // many rows: only what is longer than twice an SM's share is cut, into shares. Cut from one share on, 48 rows of
-      // up to 128 new tokens up to 2048 on one key/value head took 54 us against 41; uncut, 33 of 16 up to 12000 90
-      // against 54, and 40 decodes with a chunk of 512 at 8192 102 against 55; from two on, 100 rows of up to 16 up to
-      // 1500 (12 steps, a share of six) 41 against 27.
+      // many rows: where one is longer than twice an SM's share, all are cut into shares (those longer than one have
+      // pieces). Cut wherever one is longer than a share, 48 rows of up to 128 new tokens up to 2048 on one key/value head
+      // took 54 us against 41; uncut, 33 of 16 up to 12000 90 against 54, and 40 decodes with a chunk of 512 at 8192 102
+      // against 55; cut from two on, 100 rows of up to 16 up to 1500 (12 steps, a share of six) 41 against 27.
       const int share = max(kWhole, int(ceilf(all * n_kv / sms)));
       if (longest > 2 * share) target = share;
     }
@@ -222,9 +222,11 @@ __device__ __forceinline__ Plan plan_rows(const TcParams& P, Rows32& first, bool
       rows_load(x, R, row0, P.per_tile);
       rows_cut(x, target);
     }
-    // the estimates leave no cut that the workspace does not hold; if one does, nothing is cut
+    // A cut that the workspace does not hold is made coarser until it fits: the first branch weighs with rounded quotients,
+    // the second not at all (a row of two shares whose first new tokens see little has as many pieces as one whose all see
+    // much). Left whole instead, a decode at 57000 beside a prompt of 7400 and 31 short rows took 441 us against 129.
     if (x.slots == 0 || (int64_t)x.slots * n_kv <= P.plan.slots) return Plan{target, x.items, x.joins, x.slots};
-    target = longest;
+    target = min(longest, target + (target + 3) / 4);
   }
 }
 

@@ -210,3 +210,105 @@ def test_attend_reports_new_tokens_past_a_bound_of_none():
     b.rows.tensors[0].zero_()                                        # rows that keep the bound
     b.attend()
     b.layer.check_device()
+
+
+class Rows:
+    """A ragged batch made on the GPU, its rows' pages scattered over one pool; float64 references of single tokens."""
+
+    def __init__(self, *, n, m, d, dtype, news, lens, page, seed):
+        from rank_kv_cache_gb300 import palu as P
+        g = torch.Generator("cuda:0").manual_seed(seed)
+        dev, t = torch.device("cuda:0"), TYPES[dtype]
+        self.n, self.m, self.d, self.dtype, self.news, self.lens, self.page = n, m, d, dtype, news, lens, page
+        per = [-(-x // page) for x in lens]
+        order = torch.randperm(sum(per), generator=g, device=dev).int()
+        self.table = torch.full((len(lens), max(per)), -1, dtype=torch.int32, device=dev)    # past a row's end: no page
+        at = 0
+        for b, x in enumerate(per):
+            self.table[b, :x] = order[at:at + x]
+            at += x
+        self.start = np.concatenate([[0], np.cumsum(news)])
+        N = int(self.start[-1])
+        self.k, self.v = (torch.randn(sum(per), page, m, d, generator=g, device=dev).to(t) for _ in range(2))
+        self.q = torch.randn(N, n, d, generator=g, device=dev).to(t)
+        self.layer = P.PagedAttention(n_heads=n, n_kv_heads=m, head_dim=d, dtype=dtype, max_batch=len(lens), max_tokens=N)
+        self.pages = P.KVPages(self.k, self.v)
+        self.rows = P.KVRows(torch.from_numpy(self.start).int().to(dev), torch.tensor(lens, dtype=torch.int32, device=dev),
+                             page_table=self.table, n_tokens=N, max_new=max(news), max_kv_len=max(lens))
+        self.out = torch.empty(N, n, d, dtype=t, device=dev)
+        self.lse = torch.empty(N, n, dtype=torch.float32, device=dev)
+
+    def attend(self):
+        self.layer.attend(self.pages, self.rows, self.q, out=self.out, lse=self.lse)
+
+    def check(self, tokens, heads):
+        """(row, new token) pairs against float64; the bounds of Batch.check."""
+        g, u = self.n // self.m, torch.finfo(TYPES[self.dtype]).eps / 2
+        for b, i in tokens:
+            L, n = self.lens[b], self.news[b]
+            t = torch.arange(L - n + i + 1, device=self.k.device)
+            at = self.table[b, t // self.page].long() * self.page + t % self.page
+            tok = int(self.start[b]) + i
+            for h in heads:
+                K, V = (x.flatten(0, 1)[at, h // g].double() for x in (self.k, self.v))
+                q = self.q[tok, h].double()
+                s = K @ q / self.d ** 0.5
+                p = torch.softmax(s, 0)
+                e = 2.0 ** -16 * float((K.abs() @ q.abs()).max()) / self.d ** 0.5 + 2.0 ** -20
+                o = p @ V
+                tol = u * o.abs() + (u + 2 * e + 2.0 ** -20) * (p @ V.abs())
+                if self.dtype == "f16":
+                    tol = tol + 2.0 ** -25 * L * 8 + 2.0 ** -25
+                assert bool(((self.out[tok, h].double() - o).abs() <= tol).all()), (b, i, h)
+                lse = torch.logsumexp(s, 0)
+                assert abs(float(self.lse[tok, h].double() - lse)) <= e + 2.0 ** -20 * (1 + abs(float(lse)))
+
+    def time(self, passes=15):
+        """Median of several passes, in microseconds."""
+        for _ in range(3):
+            self.attend()
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2 * passes)]
+        torch.cuda.synchronize()
+        for i in range(passes):
+            ev[2 * i].record()
+            self.attend()
+            ev[2 * i + 1].record()
+        torch.cuda.synchronize()
+        return float(np.median([1e3 * ev[2 * i].elapsed_time(ev[2 * i + 1]) for i in range(passes)]))
+
+
+def test_more_pieces_than_the_workspace_holds_are_cut_coarser():
+    """33 rows on one key/value head: a prompt of 7400, a decode at 57000 and 31 at 1000. An SM's share is 50 steps of
+    128 tokens; in shares the prompt's 232 pairs of tiles and the decode make 473 pieces, the workspace holds 456. With 32
+    rows the pieces are weighed instead. The 33rd row adds 8 steps to 7600, and a cut a quarter coarser lets the last wave
+    last a quarter longer: 1.6 times the 32 rows' time leaves room for both. Whole, the decode's 446 steps alone are nine
+    shares."""
+    news, lens = [7400, 1] + [1] * 31, [7400, 57000] + [1000] * 31
+    shape = dict(n=8, m=1, d=128, dtype="bf16", page=64, seed=45)
+    many, few = Rows(news=news, lens=lens, **shape), Rows(news=news[:-1], lens=lens[:-1], **shape)
+    for x in (many, few):
+        x.attend()
+        x.layer.check_device()
+        x.check([(0, 0), (0, 3700), (0, 7399), (1, 0), (2, 0), (len(x.lens) - 1, 0)], [0, 7])
+    a, b = many.time(), few.time()
+    print(f"33 rows {a:.1f} us, 32 rows {b:.1f} us")
+    assert a <= 1.6 * b, f"{a:.1f} us against {b:.1f}"
+
+
+@pytest.mark.parametrize("n,m,news,lens", [
+    (4, 4, [2560] * 6 + [1] + [0] * 26, [2560] * 6 + [5120] + [9] * 26),         # 492 pieces of one-share prompts
+    (2, 2, [40] * 30 + [300] * 30, [40 + 977 * i % 9000 for i in range(60)]),
+    (1, 1, [17] * 4190 + [500] * 10, [17 + i % 40 for i in range(4190)] + [500 + 3000 * i for i in range(10)]),
+])
+def test_many_rows_with_cut_ones(n, m, news, lens):
+    lens = [max(a, b) for a, b in zip(news, lens)]
+    x = Rows(n=n, m=m, d=128, dtype="f16", news=news, lens=lens, page=32, seed=46)
+    x.attend()
+    x.layer.check_device()
+    longest = int(np.argmax(lens))
+    live = [b for b in range(len(news)) if news[b]]
+    x.check([(b, i) for b in {live[0], live[len(live) // 2], longest, live[-1]} for i in (0, news[b] - 1)], [0, n - 1])
+    first = x.out.clone(), x.lse.clone()
+    for _ in range(5):
+        x.attend()
+        assert torch.equal(x.out, first[0]) and torch.equal(x.lse, first[1])
