@@ -162,17 +162,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
     pieces_all = x.total;
   }
 
+  // the 32 rows of the piece: a CTA's pieces only go on, so they are looked for from the last one's. (From the first row
+  // each time 4096 rows of 16 tokens and 8 heads took 2437 us against 432.)
+  Cut x = cut0;
+  int row0 = 0;
   for (int idx = blockIdx.x; idx < pieces_all * a.n_kv; idx += gridDim.x) {
     // the piece's row b, head h and number among the unit's np, and its place among those of cut units
-    Cut x = cut0;
-    int b = 0;
     unsigned at;
     while (!(at = __ballot_sync(0xffffffffu, idx < (x.start + x.pieces) * a.n_kv))) {
-      b += 32;
-      cut_rows(row_steps(b + lane, false), per, x, x.total, x.total_cut);
+      row0 += 32;
+      cut_rows(row_steps(row0 + lane, false), per, x, x.total, x.total_cut);
     }
-    const int src = __ffs(at) - 1;
-    b += src;
+    const int src = __ffs(at) - 1, b = row0 + src;
     const int np = __shfl_sync(0xffffffffu, x.pieces, src);
     const int in_row = idx - __shfl_sync(0xffffffffu, x.start, src) * a.n_kv;
     const int h = in_row / np, piece = in_row % np;

@@ -312,3 +312,30 @@ def test_many_rows_with_cut_ones(n, m, news, lens):
     for _ in range(5):
         x.attend()
         assert torch.equal(x.out, first[0]) and torch.equal(x.lse, first[1])
+
+
+def test_the_time_of_many_short_rows_grows_with_their_number():
+    """Decode of rows of 16 tokens, 8 heads: four times the rows are four times the pieces, and each CTA walks the rows'
+    lengths a fixed number of times. 6.5 times the time leaves room for that; a search from the first row for each piece
+    is 16 times as long."""
+    shape = dict(n=8, m=8, d=64, dtype="f16", page=16, seed=47)
+    a, b = (Rows(news=[1] * B, lens=[16] * B, **shape) for B in (2048, 8192))
+    for x in (a, b):
+        x.attend()
+        x.layer.check_device()
+        last = len(x.lens) - 1
+        x.check([(0, 0), (31, 0), (32, 0), (last // 2, 0), (last, 0)], [0, 7])
+    ta, tb = a.time(), b.time()
+    print(f"2048 rows {ta:.1f} us, 8192 rows {tb:.1f} us")
+    assert tb <= 6.5 * ta, f"{tb:.1f} us against {ta:.1f}"
+
+
+@pytest.mark.parametrize("batch,top", [(33, 4000), (100, 700), (1100, 90)])
+def test_many_ragged_rows_of_one_token(batch, top):
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in np.exp(rng.uniform(0, np.log(top), batch))]
+    lens[batch // 2] = top * 20                                       # one that is cut
+    x = Rows(n=8, m=4, d=128, dtype="bf16", news=[1] * batch, lens=lens, page=16, seed=48)
+    x.attend()
+    x.layer.check_device()
+    x.check([(b, 0) for b in sorted({0, 1, 31, 32, batch // 2 - 1, batch // 2, batch // 2 + 1, batch - 1})], [0, 7])
