@@ -511,8 +511,12 @@ palu_status_t palu_norm_rope(palu_kv_t h, const void* q, int64_t q_stride, const
  * pages. Rotation positions are rows->positions, or the slots. A token whose slot is negative, lies past the
  * page table or in a page outside the pool is recorded in the error word and not stored; a length outside
  * [0, max_kv_len], a row with more than max_new new tokens and a decreasing row_start are recorded as by
- * palu_attend_kv (the tokens that have a row and a slot are stored). Two tokens that fall on one slot (a page shared by two rows that both append to it)
- * leave a mixture of the two, in 16-byte pieces.
+ * palu_attend_kv (the tokens that have a row and a slot are stored). Two tokens that
+ * fall on one slot (a page shared by two rows that both append to it) leave a mixture of the two, in 16-byte
+ * pieces.
+ *
+ * A window that rolls (palu_decode_hybrid): one new token in a row with kv_len = slot + 1 and its own position in
+ * `positions` overwrites that slot; the order of a dense segment's tokens does not matter.
  */
 palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu_kv_rows* rows, const void* q,
                              int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,

@@ -339,3 +339,153 @@ def test_many_ragged_rows_of_one_token(batch, top):
     x.attend()
     x.layer.check_device()
     x.check([(b, 0) for b in sorted({0, 1, 31, 32, batch // 2 - 1, batch // 2, batch // 2 + 1, batch - 1})], [0, 7])
+
+
+@pytest.mark.parametrize("capacity,new", [(20, 20), (3, 3), (20, 2), (130, 40)])
+def test_contiguous_caches_smaller_than_a_tile(capacity, new):
+    Batch(n=24, m=1, d=64, dtype="f16", news=[new], lens=[capacity], page=capacity, table=False, seed=49).run_and_check()
+    Batch(n=24, m=3, d=128, dtype="bf16", news=[1, new, new], lens=[1, new, capacity], page=capacity, table=False,
+          seed=50).run_and_check()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_empty_caches_with_a_bound_of_no_length(new):
+    b = Batch(n=4, m=2, d=128, dtype="bf16", news=[new, 0], lens=[0, 0], page=16, seed=51, max_kv=0)
+    out, lse = b.run_and_check()
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+@pytest.mark.parametrize("news,lens", [([1, 3], [40, 2000]), ([60, 5], [300, 9000])])
+def test_a_query_that_is_not_a_number_stays_by_itself(news, lens):
+    b = Batch(n=4, m=2, d=128, dtype="f16", news=news, lens=lens, page=16, seed=52)
+    ref, ref_lse = b.attend()
+    b.qd[0, 1, 5] = float("nan")
+    b.qd[news[0], 2] = float("inf")
+    out, lse = b.attend()
+    bad = torch.zeros(b.N, 4, dtype=torch.bool, device=b.dev)
+    bad[0, 1] = bad[news[0], 2] = True
+    assert torch.all(torch.isnan(out[bad])) and torch.all(torch.isnan(lse[bad]))
+    assert torch.all(torch.isfinite(out[~bad])) and torch.all(torch.isfinite(lse[~bad]))
+    # rows of a warp are rescaled together, by factors of one: their neighbours' bits stay
+    assert torch.equal(out[~bad], ref[~bad]) and torch.equal(lse[~bad], ref_lse[~bad])
+
+
+@pytest.mark.parametrize("news,lens", [([1], [30000]), ([40], [30000]), ([5, 1], [64, 9])])
+def test_outputs_without_the_log_sum(news, lens):
+    b = Batch(n=4, m=2, d=64, dtype="bf16", news=news, lens=lens, page=64, seed=53)
+    ref, _ = b.attend()
+    assert torch.equal(b.layer.attend(b.pages, b.rows, b.qd), ref)
+
+
+def test_queries_rotated_in_place_by_the_append():
+    from rank_kv_cache_gb300 import palu as P
+    rng, dev = np.random.default_rng(54), torch.device("cuda:0")
+    q, k, v = (rounded(rng, (5, h, 64), "bf16").to(dev) for h in (8, 2, 2))
+    w = rounded(rng, (64,), "bf16").to(dev)
+    rows = P.KVRows(torch.tensor([0, 2, 5], dtype=torch.int32, device=dev), torch.tensor([20, 7], dtype=torch.int32, device=dev),
+                    n_tokens=5, max_new=3, max_kv_len=32)
+    layer = P.PagedAttention(n_heads=8, n_kv_heads=2, head_dim=64, dtype="bf16", max_batch=2, max_tokens=5)
+    got = []
+    for out in (None, q.clone()):
+        pages = P.KVPages(*(torch.zeros(2, 32, 2, 64, dtype=torch.bfloat16, device=dev) for _ in range(2)))
+        given = q if out is None else out
+        got.append((layer.append(pages, rows, k, v, q=given, q_weight=w, k_weight=w, q_out=out), pages.k, pages.v))
+    layer.check_device()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_graphs_of_one_handle_replayed_in_turn():
+    """A step's graph and a prompt's share the handle's workspace; they follow each other on a stream, any way round."""
+    a = Batch(n=8, m=2, d=128, dtype="bf16", news=[1, 1], lens=[9000, 700], page=16, seed=55)
+    b = Batch(n=8, m=2, d=128, dtype="bf16", news=[150, 40], lens=[5000, 9000], page=16, seed=56)
+    b.layer.close()
+    a.layer.close()
+    from rank_kv_cache_gb300 import palu as P
+    a.layer = b.layer = P.PagedAttention(n_heads=8, n_kv_heads=2, head_dim=128, dtype="bf16", max_batch=2, max_tokens=190)
+    refs, graphs, outs = [], [], []
+    for x in (a, b):
+        refs.append(x.attend())
+        x.check_sampled(*refs[-1], [0, x.news[0] - 1, x.N - 1], [0, 7])
+        outs.append((torch.empty_like(refs[-1][0]), torch.empty_like(refs[-1][1])))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.layer.attend(x.pages, x.rows, x.qd, out=outs[-1][0], lse=outs[-1][1])
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1), (1, 0, 1, 0, 1)):
+        for o, s in outs:
+            o.fill_(7.0)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert torch.equal(outs[i][0], refs[i][0]) and torch.equal(outs[i][1], refs[i][1])
+    a.layer.check_device()
+
+
+def test_two_handles_side_by_side_against_float64():
+    a = Batch(n=8, m=2, d=128, dtype="f16", news=[1, 1], lens=[9000, 800], page=16, seed=57)
+    b = Batch(n=8, m=2, d=128, dtype="f16", news=[150, 3], lens=[5000, 700], page=16, seed=58)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, s, o in zip((a, b), streams, outs):
+            lse = torch.empty(x.N, 8, dtype=torch.float32, device=x.dev)
+            o.append((x.layer.attend(x.pages, x.rows, x.qd, lse=lse, stream=s), lse))
+    torch.cuda.synchronize()
+    for x, s, o in zip((a, b), streams, outs):
+        x.layer.check_device(s)
+        x.check_sampled(*o[0], [0, x.news[0] // 2, x.news[0], x.N - 1], [0, 3, 7])
+        assert all(torch.equal(y[0], o[0][0]) and torch.equal(y[1], o[0][1]) for y in o)
+
+
+def test_a_hybrid_window_that_rolls():
+    """The window of a hybrid decode over several steps: each new token takes the oldest window slot (one new token with
+    kv_len = slot + 1, at its own position), the token that leaves moves to the latent middle. Against the oracle."""
+    from oracle import kv_oracle as KO
+    from oracle import palu_oracle as O
+    from rank_kv_cache_gb300 import palu as P
+    from synthetic import gen
+    from tests.gpu_cases import Case, assert_close
+    sinks, window, T, steps, B = 4, 8, 300, 11, 2
+    D = sinks + window
+    cfg = gen.ROPE_FP16.with_(T=T, batch=B)
+    latent_pos = np.stack([sinks + np.arange(T)] * B).astype(np.int32)
+    c = Case(cfg, positions=latent_pos, q_pos=[0] * B, max_position=T + D + steps)
+    n, d, dev = cfg.n_heads, cfg.head_dim, c.dev
+    rng = np.random.default_rng(59)
+    pages = P.KVPages(*(torch.full((B, D, n, d), float("nan"), dtype=torch.float16, device=dev) for _ in range(2)))
+    layer = P.PagedAttention(n_heads=n, n_kv_heads=n, head_dim=d, dtype="f16", x_dtype="f32", rope_theta=cfg.theta,
+                             max_batch=B, max_tokens=B * D)
+    full = torch.full((B,), D, dtype=torch.int32, device=dev)
+    middle = T - steps                                                # latent tokens when the decode begins
+    dense_pos = np.concatenate([np.arange(sinks), sinks + middle + np.arange(window)])
+    k, v = rounded(rng, (B * D, n, d), "f32", 0.25), rounded(rng, (B * D, n, d), "f32")
+    rows = P.KVRows(torch.tensor([0, D, 2 * D], dtype=torch.int32, device=dev), full, n_tokens=B * D, max_new=D,
+                    max_kv_len=D, positions=torch.from_numpy(np.tile(dense_pos, B).astype(np.int32)).to(dev))
+    layer.append(pages, rows, k.to(dev), v.to(dev))
+    rk = KO.norm_rope(k.double().numpy(), None, np.tile(dense_pos, B), cfg.theta, 0.0).reshape(B, D, n, d)
+    rv = v.double().numpy().reshape(B, D, n, d).copy()
+    start = torch.arange(B + 1, dtype=torch.int32, device=dev)
+    posd = torch.from_numpy(latent_pos).to(dev)
+    for step in range(steps):
+        slot, now = sinks + step % window, sinks + middle + window + step
+        k1, v1 = rounded(rng, (B, n, d), "f32", 0.25), rounded(rng, (B, n, d), "f32")
+        rows = P.KVRows(start, torch.full((B,), slot + 1, dtype=torch.int32, device=dev), n_tokens=B, max_new=1, max_kv_len=D,
+                        positions=torch.full((B,), now, dtype=torch.int32, device=dev))
+        layer.append(pages, rows, k1.to(dev), v1.to(dev))
+        rk[:, slot] = KO.norm_rope(k1.double().numpy(), None, [now] * B, cfg.theta, 0.0)
+        rv[:, slot] = v1.double().numpy()
+        if step not in (0, 1, window - 1, window, steps - 1):
+            continue
+        seen = middle + step + 1                                      # the token that left the window is latent now
+        out, out_d, lse = c.attn.decode_hybrid(c.q_t.to(dev), c.cache, torch.full((B,), seen, dtype=torch.int32, device=dev),
+                                               pages.k, pages.v, full, max_seq_len=T, positions=posd,
+                                               q_pos=torch.full((B,), now, dtype=torch.int32, device=dev))
+        torch.cuda.synchronize()
+        ref_l, ref_d, ref_lse = O.decode_hybrid(c.q64, c.hk64, c.hv64, c.bk64, [seen] * B, cfg.group_size, rk, rv, [D] * B,
+                                               theta=cfg.theta, positions=latent_pos, q_pos=[now] * B)
+        assert_close(out.cpu().double().numpy(), ref_l, lse.cpu().double().numpy(), ref_lse)
+        assert_close(out_d.cpu().double().numpy(), ref_d)
+    c.attn.check_device()
+    layer.check_device()
