@@ -539,7 +539,7 @@ palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
  * error word. The result does not depend on timing: the same call gives the same bits.
  * max_new * n_heads / n_kv_heads decides the kernel: up to 16 query rows of a key/value head run on
  * the streaming kernel (one launch), more on the tensor-core kernel (one launch). Its cached
- * tokens come by TMA; page sizes without a factor of eight are gathered row by row, at less than
+ * tokens come by TMA; page sizes without a factor of eight are gathered row by row, at about
  * half the rate. PALU_ERR_UNSUPPORTED for F32 handles, and on the tensor-core kernel where
  * n_pages * page_size * n_kv_heads >= 2^31 - 1.
  */

@@ -19,9 +19,10 @@
 // read. The weights p are rounded to the cache's type for the product with V, as the matrix instruction
 // takes it (fp16: up to 2^15, see softmax_base); the sum is of the unrounded p.
 //
-// Measured on a GB300, 32 / 8 heads of 128, bf16: one token of four sequences at 65536 (1.07 GB) 160 us, 6700
-// GB/s; of 64 sequences at 4096 163 us. 32 / 32 heads, one sequence at 4096 (67 MB): 20 us, 17 with the cache in
-// L2, of which the start and the join are half. 8 / 8 heads of 64, one at 512: 8 us.
+// Measured on a GB300 with states in turn, 32 / 8 heads of 128, bf16: one token of four sequences at 65536 (1.07 GB)
+// 162 to 166 us, 6450 to 6600 GB/s; of 64 sequences at 4096 165 us from pages of 64, 174 of 16; of 256 at 1024 186.
+// 32 / 32 heads, one sequence at 4096 (67 MB): 20 us, 16.5 with the cache in L2, of which the start and the join are
+// half. 8 / 8 heads of 64, one at 512: 8 us.
 #include "kv.h"
 
 namespace palu {
@@ -134,9 +135,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
   // A piece's length: at least an equal share of all CTAs that the GPU holds. Up to 32 rows, each lane weighs one
   // length, from that share to three times it or 31 steps more: the waves of CTAs times the length and what a CTA's
   // start and end cost (eight steps), and the join of what is cut (four; with eight, 8 sequences at 1000 took 12.3 us
-  // against 9.6; with lengths up to twice a share of one step only, 300 tokens of two sequences 7.6 against 6.5). More rows are cut a quarter longer than the share. The quarter alone
-  // took 169 us against 136 for 32 ragged rows up to 8192 and 137 against 119 for 20 of 7000, and up to 1 us less
-  // for few equal rows (48.4 against 50.3, one of 65536).
+  // against 9.6; with lengths up to twice a share of one step only, 300 tokens of two sequences 7.6 against 6.5). More
+  // rows are cut a quarter longer than the share. The quarter alone took 169 us against 136 for 32 ragged rows up to
+  // 8192 and 137 against 119 for 20 of 7000, and up to 1 us less for few equal rows (48.4 against 50.3, one of 65536).
   const int64_t work = all * a.n_kv;
   const int share = work < (1 << 30) ? (int(work) + a.ctas - 1) / a.ctas : int((work + a.ctas - 1) / a.ctas);
   int per = share + share / 4;

@@ -33,10 +33,11 @@
 //
 // Bound: the round of a unit, S to weights to its products, of which two in turn keep the tensor cores 61% busy at
 // 1.9 GHz (exponentials 36%, issue 42%); in long calls the clock falls besides, with the power limit.
-// Measured on a GB300, 32 / 8 heads of 128, bf16: 2048 new tokens at 65536 1436 us (1510 TFLOP/s); a chunk of 512
-// among 15 sequences that decode, at 16384, 208 us; up to five drafted tokens of eight ragged sequences up to 16384
-// 82 us, 4800 GB/s. Four prompts of 4096, 32 / 32 heads, fp16: 405 us (1360). At d = 64 the products halve and the
-// softmax does not: 1024 new tokens of two sequences at 16384 316 us, 840 TFLOP/s.
+// Measured on a GB300 with states in turn, 32 / 8 heads of 128, bf16: 2048 new tokens at 65536 1500 to 1530 us (1410 to
+// 1440 TFLOP/s); a chunk of 512 among 15 sequences that decode, at 16384, 209 us; up to five drafted tokens of eight
+// ragged sequences up to 16384 82 us, 4800 GB/s. Four prompts of 4096, 32 / 32 heads, fp16: 440 us (1250). Where one
+// state's calls follow each other in a graph, the first take 1470 us (1470 TFLOP/s) and the last 399 (1380). At d = 64 the
+// products halve and the softmax does not: 1024 new tokens of two sequences at 16384 319 us, 835 TFLOP/s.
 //
 // Every wait is bounded; one that gives up records PALU_ERR_TIMEOUT, and all roles wait for their own
 // copies and products in flight before tensor memory is freed.
@@ -1021,7 +1022,7 @@ template <int DH, bool BF16> cudaError_t launch_tc(const KvAttendArgs& a, const 
     const cuuint64_t bdims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)(a.pages.n_pages * a.pages.page_size)};
     const cuuint64_t bstrides[2] = {DH * 2, (cuuint64_t)a.n_kv * DH * 2};
     // A box must lie in one page: without a table a row is one page, else the largest power of two that divides it.
-    // 512 new tokens at 8192: 76 us from pages of 64 and more, 84 of 16, 92 of 8, and 157 gathered from pages of 100.
+    // 512 new tokens at 8192: 77 us from pages of 64 and more, 80 of 16, 94 of 8, and 158 gathered from pages of 100 or 1.
     int box_tokens = a.rows.page_table ? a.pages.page_size & -a.pages.page_size : kTile;
     box_tokens = box_tokens > kTile ? kTile : box_tokens;
     P.box = box_tokens >= 8 ? box_tokens : 0;

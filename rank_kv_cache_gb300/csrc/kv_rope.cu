@@ -15,9 +15,10 @@
 // token's place). Phases are 64-bit fractions of a turn, so far positions keep theirs. The arithmetic
 // is packed two fp32 to an instruction: unpacked it was bound by issue.
 //
-// Measured on a GB300: 16384 tokens of 32 + 8 heads of 128, bf16, normed: 57.7 us, 5820 GB/s, as a
-// plain copy of the same bytes (57.3 us). Four prompts of 12831 tokens appended, with the queries:
-// 58.3 us, 5410 GB/s. Eight tokens of 32 + 32 heads: 2.6 us, one launch.
+// Measured on a GB300: 16384 tokens of 32 + 8 heads of 128, bf16, normed: 58 us, 5800 GB/s, as a
+// plain copy of the same bytes (57.3 us); 4096 19.4 us, 4350 GB/s; 512 8 us. Four prompts of 12831 tokens
+// appended, with the queries: 59 us, 5360 GB/s; 4096 tokens 23.7. 8192 tokens in fp32: 55 us, 6090 GB/s.
+// Eight tokens of 32 + 32 heads: 2.6 us, one launch.
 #include "kv.h"
 
 namespace palu {
