@@ -546,6 +546,127 @@ palu_status_t palu_append_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
 palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu_kv_rows* rows, const void* q,
                              int64_t q_stride, void* out, float* lse, palu_stream_t stream);
 
+/*
+ * Paged KV cache held in 8 bits, and the steps around its attention: rows and pages planned on the device, and the
+ * verification of drafted tokens. All take a handle of palu_kv_create, with its rules: no call synchronises, all can be
+ * captured, what goes wrong on the device is recorded in the handle's error word. The pages give no 8-bit dense cache;
+ * the layout and its rules are this library's.
+ *
+ *   k, v              [n_pages][page_size][n_kv_heads][head_dim] e4m3 codes (one byte each), 16-byte aligned
+ *   k_scale, v_scale  [n_pages][page_size / 16][n_kv_heads] float32
+ *
+ * A value is its code times the scale of its head and its block of 16 slots. page_size is a multiple of 16 (with a
+ * page table or without); n_pages * page_size < 2^31.
+ */
+#define PALU_KV8_BLOCK 16
+typedef struct palu_kv8_pages {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages;
+  int page_size;
+} palu_kv8_pages;
+
+/*
+ * palu_append_kv with pages of 8 bits. The new tokens' keys (normed, rotated) and values of a block and head share a
+ * scale: the least power of two, from 2^-64 to 2^64, that brings their largest magnitude to 448 or below. Where older
+ * tokens stand in the block (its first slot is none of the row's new ones) the scale is at least theirs; when it grows,
+ * their codes are restated under it, which by a power of two moves the codes' exponents and loses only what falls
+ * below the least subnormal. A block that begins with a new token begins anew. Codes are rounded to nearest (even), so
+ * a value of at least 2^-6 scales is off by at most 2^-4 of itself. NaN is stored as NaN; values past 448 * 2^64
+ * (infinities among them) as the largest code.
+ * Each row appends to blocks of its own: two rows do not append to one block of 16 slots, and a dense window
+ * does not roll in place, as what lies behind a row's new tokens in their last block keeps its codes while the scale
+ * may change. PALU_ERR_UNSUPPORTED for F32 handles.
+ */
+palu_status_t palu_append_kv8(palu_kv_t h, const palu_kv8_pages* pages, const palu_kv_rows* rows, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const void* q_norm, const void* k_norm, void* q_out, palu_stream_t stream);
+
+/*
+ * palu_attend_kv over pages of 8 bits. Slots at or past kv_len[b] may hold anything and change nothing (their page is
+ * theirs to read, up to the end of a 128-token tile); codes and scales below it must be finite, and the scales
+ * within 2^-64 .. 2^64 (any such number; one that is not positive counts as 1). fp32 scores, softmax statistics
+ * and accumulation. Codes enter the products exactly, as fp16; BF16 queries are lifted by a power of two of their row's
+ * own to fp16, which loses what lies 2^-38 and more below the row's largest; the softmax weights, with their values'
+ * scales, are rounded to fp16 relative to the row's largest (steps of 2^-31 of it, or finer).
+ * Kernels, determinism and limits as palu_attend_kv.
+ */
+palu_status_t palu_attend_kv8(palu_kv_t h, const palu_kv8_pages* pages, const palu_kv_rows* rows, const void* q,
+                              int64_t q_stride, void* out, float* lse, palu_stream_t stream);
+
+/*
+ * Pages of a batch's requests, kept on the device. Row b holds the pages page_table[b][0 .. held[b]), which cover its
+ * cached tokens. Free pages stand in a ring of n_pages entries: free_state[0] is the place of the first, free_state[1]
+ * their number.
+ */
+typedef struct palu_kv_pool {
+  int32_t* page_table;        /* device [batch][table_pages] */
+  int64_t table_pages;
+  int32_t* held;              /* device [batch] */
+  int32_t* free_pages;        /* device [n_pages] */
+  int32_t* free_state;        /* device [2] */
+  int64_t n_pages;
+  int page_size;
+} palu_kv_pool;
+
+/*
+ * The plan of a step: from each row's new tokens and cached length to the arrays of palu_kv_rows.
+ *   new_tokens  device [batch]: tokens that row b brings (0: none), or a negative number: the request has ended
+ *   kv_len      device [batch]: cached tokens before the step
+ * Rows are admitted in order as long as the free pages and the n_tokens packed places last: the first row for which
+ * one of the two does not, and every row with new tokens behind it, gets no tokens and no pages. An admitted row takes
+ * the pages that its length with the new tokens needs beyond those it holds, from the front of the ring. An ended
+ * row's pages go behind the ring's end and can be taken from the next call on; it holds none then, and its
+ * length is 0.
+ *   row_start   device [batch + 1], written: the packed tokens of the admitted rows
+ *   kv_len_out  device [batch], written: the lengths with the new tokens; may be kv_len
+ *   held_out, state_out   device [batch] and [2], written: what held and free_state are behind the step; NULL, or
+ *               held and free_state themselves: in place. Elsewhere, the call can be repeated on the same pool
+ *   positions   device [n_tokens] or NULL, written: each packed token's place in its row (0 behind the last)
+ *   slots       device [n_tokens] or NULL, written: its page * page_size + offset (-1 behind the last)
+ * Page table entries are written in place. A row whose length is negative or not covered by its pages, that holds
+ * more pages than the table, or that brings more than max_new tokens or past max_kv_len, is recorded in the error word
+ * and left as it is, without new tokens (ended rows: freed all the same, if `held` is right); so is a ring whose number
+ * is not within 0 .. n_pages, or would be past it with the pages given back, and a page outside the pool (slot -1).
+ * The outputs overlap no input but as said. batch 0: nothing is done.
+ */
+palu_status_t palu_plan_kv_rows(palu_kv_t h, const palu_kv_pool* pool, const int32_t* new_tokens, const int32_t* kv_len,
+                                int batch, int64_t n_tokens, int max_new, int64_t max_kv_len, int32_t* row_start,
+                                int32_t* kv_len_out, int32_t* held_out, int32_t* state_out, int32_t* positions,
+                                int32_t* slots, palu_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities. Row b of the batch has the target rows
+ * row_start[b] .. row_start[b + 1] - 1: n_b of them, for n_b - 1 drafts (0 rows: nothing is done for it). Draft i,
+ * the token x_i, is accepted while every one before it was and
+ *   u_i q_i(x_i) < p_i(x_i),
+ * p_i being target row i of b and q_i the draft's. Behind the last accepted one a token is drawn: from max(p - q, 0) of
+ * the first rejected draft (from p where that is zero throughout), or from p of the last target row where all are
+ * accepted: the lowest index whose running sum exceeds u times the whole sum.
+ *   target        device [n_tokens][vocab] in p_dtype (F32, F16 or BF16), rows target_stride elements apart
+ *   draft         device [batch][max_draft][vocab] in p_dtype, rows draft_stride elements apart, or NULL: each draft
+ *                 was certain (q_i is 1 at x_i and 0 elsewhere)
+ *   draft_tokens  device [batch][max_draft]
+ *   uniforms      device [batch][max_draft + 1] in [0, 1): u_i of draft i, and last that of the drawn token
+ *   tokens        device [batch][max_draft + 1], written: the accepted drafts, the drawn token, and -1 behind it
+ *   accepted      device [batch], written: how many drafts were accepted
+ *   kv_len, kv_len_out   device [batch], both NULL or both given (they may be one): lengths with all new tokens in, and
+ *                 without the rejected ones out
+ * Probabilities are finite; they need not sum to 1, and negative ones and NaN count as 0. Products and differences
+ * are exact, sums are carried in twice the bits of fp32 and joined in fp64. Uniforms outside [0, 1) are brought to its
+ * ends. A draft outside the vocabulary is rejected, and recorded in the error word; so are a row with more than
+ * max_draft drafts (its first max_draft are taken), a decreasing row_start (nothing is done) and a distribution that is
+ * zero throughout (the token is -1). vocab <= 2^20. Rows of any alignment; those whose addresses are multiples of
+ * 16 bytes are read fastest.
+ */
+palu_status_t palu_verify_drafts(palu_kv_t h, const void* target, int64_t target_stride, const void* draft,
+                                 int64_t draft_stride, palu_dtype_t p_dtype, int64_t vocab, const int32_t* row_start,
+                                 int batch, int64_t n_tokens, const int32_t* draft_tokens, int max_draft,
+                                 const float* uniforms, int32_t* tokens, int32_t* accepted, const int32_t* kv_len,
+                                 int32_t* kv_len_out, palu_stream_t stream);
+
 /* Free the host handle. Does not synchronise: no work on it may be in flight. NULL is fine. */
 palu_status_t palu_destroy(palu_attn_t h);
 

@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(PKG, "_lib")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libpalu_attn.so"
 SOURCES = ["palu_host.cu", "prep.cu", "decode_simt.cu", "decode_tc.cu", "decode_abs.cu", "noalloc.cu", "oproj.cu", "prefill.cu", "hybrid.cu", "paged.cu",
-           "kv_host.cu", "kv_rope.cu", "kv_attend.cu", "kv_attend_tc.cu"]
+           "kv_host.cu", "kv_rope.cu", "kv_attend.cu", "kv_attend_tc.cu",
+           "kv8_host.cu", "kv8_append.cu", "kv8_attend.cu", "kv8_attend_tc.cu", "kv_plan.cu", "kv_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,307 @@
+// Norm and rotation of queries and keys, and the append of keys and values into a paged cache held in 8 bits, in one pass.
+//
+// As kv_rope.cu for the arithmetic up to the rotated key; then, for each head and each block of 16 slots,
+//   s = 2^ceil(log2(max |y| / 448)) over the call's new tokens of the block, at least the scale of older tokens in it,
+//   code = e4m3(y / s).
+// s is a power of two, so y / s is exact (but for what falls under the least subnormal) and codes, being floating
+// point, lose nothing against a scale of full precision: their steps follow each value's own exponent. It also keeps
+// older codes whole when a block's scale grows under them: only their exponents move.
+//
+// A group is a row's new tokens of one block. A CTA takes the groups that begin among 16 packed tokens: one or two of a
+// prompt, 16 of a decode step. It computes the sines and cosines of their tokens (31 at most) once, in shared memory;
+// then a warp takes one group and head at a time: the 16 tokens' halves of a head stay in registers (16 elements of a
+// token a lane, as in kv_rope.cu) from the loads over norm, rotation and the maximum to the codes. Old codes are read
+// only where a scale grows.
+//
+// Bound: HBM; each input is read once and each output written once.
+#include "kv8.h"
+#include "kv_vec.cuh"
+
+namespace palu {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kChunk = kKv8Block;          // packed tokens whose groups a CTA takes
+
+struct Group {
+  int t0, n;        // packed tokens
+  int pos0;         // slot of the first in its row; the block begins at pos0 & ~15
+  int slot0;        // its slot in the pages, or -1
+};
+
+template <int DH> struct Sm {
+  static constexpr int kHalf = DH / 2, kTokens = 2 * kChunk - 1;
+  float cs[kTokens][kHalf], sn[kTokens][kHalf];   // pairs 8 j + e of a token at (e / 4) (kHalf / 2) + 4 j + e % 4
+  Group group[kChunk];
+  int groups, t0, n;                              // the groups' tokens: t0 .. t0 + n - 1
+};
+
+// The first row that ends behind packed token t (batch: none does): of row ends that ascend. Warp-wide, 32 at a time.
+__device__ __forceinline__ int find_row(const KvRows& r, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = r.batch;                        // among rows lo .. lo + n - 1, or lo + n
+  while (n > 0) {
+    const int step = (n + 31) / 32;               // each lane looks at the last row of its share
+    const int i = min(lane * step + step, n) - 1;
+    const unsigned m = __ballot_sync(0xffffffffu, r.row_start[lo + i + 1] > t);
+    if (!m) return lo + n;
+    const int k = __ffs(m) - 1;
+    const int first = k * step, last = min(first + step, n) - 1;
+    lo += first;
+    n = last - first;                             // row lo + n ends behind t
+  }
+  return lo;
+}
+
+// the least k, from -64 to 64, with top <= 448 * 2^k; top = 1.f * 2^e and 448 = 1.75 * 2^8
+__device__ __forceinline__ int scale_exponent(float top) {
+  const uint32_t bits = __float_as_uint(top);
+  const int k = int(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+  return min(64, max(-64, k));
+}
+
+// Records what the attention would of the rows: bounds that do not hold, a row_start that decreases.
+__device__ __noinline__ void check_rows(const KvRopeArgs& a) {
+  for (int b = threadIdx.x; b < a.rows.batch; b += kThreads) {
+    int q0, n, L;
+    unsigned bad;
+    kv_row(a.rows, b, q0, n, L, bad);
+    if (bad) record_error(a.err, kCodeDevice, bad, b, b);
+  }
+}
+
+template <typename TI, typename TO, int DH>
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvRopeArgs a, const Kv8Pages P,
+                                                              const __grid_constant__ KvFreq f) {
+  constexpr int kLanes = DH / 16;          // lanes of a token's head
+  constexpr int kTok = 32 / kLanes;        // tokens that a warp takes at once
+  constexpr int kPass = kKv8Block / kTok;
+  constexpr int kQuarter = DH / 4;
+  __shared__ __align__(16) Sm<DH> S;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane % kLanes, tl = lane / kLanes;
+  const KvRows& R = a.rows;
+  grid_wait();
+  grid_release();
+  const int parts = gridDim.y, part = blockIdx.y, heads = a.heads[0] + a.heads[1] + a.heads[2];
+  if ((int64_t)blockIdx.x * kChunk >= a.n_tokens) {
+    if (part == 0) check_rows(a);
+    return;
+  }
+
+  // the groups that begin here
+  if (warp == 0) {
+    const int c0 = blockIdx.x * kChunk, t = c0 + lane;
+    int base = find_row(R, c0), row = R.batch;
+    int e = base + lane < R.batch ? R.row_start[base + lane + 1] : INT_MAX;
+    for (int i = 0; i < kChunk; ++i) {
+      unsigned m;
+      while (!(m = __ballot_sync(0xffffffffu, e > c0 + i))) {       // a lane past the last row ends the search
+        base += 32;
+        e = base + lane < R.batch ? R.row_start[base + lane + 1] : INT_MAX;
+      }
+      if (lane == i) row = min(base + __ffs(m) - 1, R.batch);
+    }
+    bool first = false;
+    Group g{t, 0, 0, -1};
+    if (lane < kChunk && row < R.batch && t < a.n_tokens) {
+      const int start = R.row_start[row], end = min(R.row_start[row + 1], a.n_tokens);
+      if (t >= start) {
+        g.pos0 = R.kv_len[row] - R.row_start[row + 1] + t;
+        first = t == start || (g.pos0 & (kKv8Block - 1)) == 0;
+        if (first) {
+          g.n = min(end - t, kKv8Block - (g.pos0 & (kKv8Block - 1)));
+          if (g.pos0 >= 0) g.slot0 = (int)kv_slot(R, P.codes, row, g.pos0);
+          if (g.slot0 < 0 && part == 0) record_error(a.err, kCodeDevice, kErrSlot, g.pos0, row);
+        }
+      }
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, first);
+    if (first) S.group[__popc(m & ((1u << lane) - 1))] = g;
+    const int lead = m ? __ffs(m) - 1 : 0, last = m ? 31 - __clz(m) : 0;
+    const int end = __shfl_sync(0xffffffffu, t + g.n, last);
+    if (lane == 0) {
+      S.groups = __popc(m);
+      S.t0 = c0 + lead;
+      S.n = m ? end - c0 - lead : 0;
+    }
+  }
+  __syncthreads();
+  const int groups = S.groups, t0 = S.t0;
+
+  if (a.rotate) {
+    const int n = S.n;
+    for (int i = tid; i < n * (DH / 2); i += kThreads) {
+      const int tok = i / (DH / 2), k = i % (DH / 2);
+      int pos;
+      if (a.positions) {
+        pos = a.positions[t0 + tok];
+      } else {
+        int g = 0;                                 // the group that holds the token: they are in order
+        while (g + 1 < groups && S.group[g + 1].t0 <= t0 + tok) ++g;
+        pos = S.group[g].pos0 + t0 + tok - S.group[g].t0;
+      }
+      // turns * 2^64, in [-1/2, 1/2); half turns: * 2^-63
+      const int64_t phase = (int64_t)(uint64_t((int64_t)pos) * f.turn[k]);
+      const int at = (k & 4) / 4 * kQuarter + k / 8 * 4 + (k & 3);
+      sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &S.sn[tok][at], &S.cs[tok][at]);
+    }
+    __syncthreads();
+  }
+
+  for (int task = part * kWarps + warp; task < groups * heads; task += parts * kWarps) {
+    const Group g = S.group[task / heads];
+    int h = task % heads;
+    const int side = h < a.heads[0] ? 0 : h < a.heads[0] + a.heads[1] ? 1 : 2;
+    h -= side == 0 ? 0 : side == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
+    const TI* x = static_cast<const TI*>(a.src[side]) + (int64_t)g.t0 * a.src_stride[side] + (h * DH + j * 8);
+    Vec8<TI> lo[kPass], hi[kPass];
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      const int tok = p * kTok + tl;
+      if (tok < g.n) {
+        lo[p].load(x + (int64_t)tok * a.src_stride[side], 0);
+        hi[p].load(x + (int64_t)tok * a.src_stride[side], DH / 2);
+      }
+    }
+    const int64_t block = g.slot0 < 0 ? 0 : g.slot0 / kKv8Block;
+    const int older = g.pos0 & (kKv8Block - 1);    // older tokens of the block
+    float* scale = side == 0 ? nullptr : P.scale[side - 1] + block * a.heads[1] + h;
+    float was = 0.f;
+    if (side != 0 && g.slot0 >= 0 && older > 0) was = *scale;
+    uint64_t gl[4], gu[4];                         // this lane's norm weights
+    const void* w = side < 2 ? a.w[side] : nullptr;
+    if (w) {
+      Vec8<TI> v;
+      v.load(w, j * 8);
+      v.get(gl);
+      v.load(w, j * 8 + DH / 2);
+      v.get(gu);
+    }
+    uint64_t l[kPass][4], u[kPass][4];
+    float top = 0.f;
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      const int tok = p * kTok + tl;
+      if (p * kTok >= g.n) break;
+      lo[p].get(l[p]);
+      hi[p].get(u[p]);
+      if (w) {
+        uint64_t ss2 = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ss2 = fma2(l[p][e], l[p][e], fma2(u[p][e], u[p][e], ss2));
+        const float2 s = unpair(ss2);
+        float ss = s.x + s.y;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.f / DH) + a.eps);
+        const uint64_t r2 = pair(r, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          l[p][e] = mul2(mul2(l[p][e], r2), gl[e]);
+          u[p][e] = mul2(mul2(u[p][e], r2), gu[e]);
+        }
+      }
+      if (a.rotate && side < 2) {
+        const int at = min(g.t0 - t0 + tok, S.n - 1);
+        const uint64_t* cp = reinterpret_cast<const uint64_t*>(S.cs[at]);
+        const uint64_t* sp = reinterpret_cast<const uint64_t*>(S.sn[at]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = e / 2 * (kQuarter / 2) + j * 2 + e % 2;
+          const uint64_t p0 = l[p][e], p1 = u[p][e], cs = cp[i], sn = sp[i];
+          l[p][e] = fma2(p0, cs, mul2(p1, sn) ^ 0x8000000080000000ull);
+          u[p][e] = fma2(p1, cs, mul2(p0, sn));
+        }
+      }
+      if (side == 0) {
+        if (tok < g.n) {
+          TO* dst = static_cast<TO*>(a.dst[0]) + (int64_t)(g.t0 + tok) * a.dst_stride[0];
+          Vec8<TO> y;
+          y.set(l[p]);
+          y.store(dst, h * DH + j * 8);
+          y.set(u[p]);
+          y.store(dst, h * DH + j * 8 + DH / 2);
+        }
+      } else if (tok < g.n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = unpair(l[p][e]), z = unpair(u[p][e]);
+          top = fmaxf(fmaxf(fmaxf(top, fabsf(y.x)), fabsf(y.y)), fmaxf(fabsf(z.x), fabsf(z.y)));
+        }
+      }
+    }
+    if (side == 0 || g.slot0 < 0) continue;
+
+    top = warp_max(top);
+    float s = __uint_as_float(uint32_t(scale_exponent(top) + 127) << 23);
+    uint8_t* codes = static_cast<uint8_t*>(side == 1 ? P.codes.k : P.codes.v);
+    const int64_t pitch = (int64_t)a.heads[1] * DH;                    // bytes between slots
+    if (older > 0) {
+      was = was >= kKv8ScaleMin ? fminf(was, kKv8ScaleMax) : kKv8ScaleMin;
+      if (s > was) {                                                   // the older codes under the larger scale
+        const float r = was / s;
+        uint8_t* c = codes + block * kKv8Block * pitch + h * DH;
+        for (int i = lane; i < older * (DH / 16); i += 32) {
+          uint4* at = reinterpret_cast<uint4*>(c + i / (DH / 16) * pitch + i % (DH / 16) * 16);
+          uint4 v = *at;
+          uint16_t* e = reinterpret_cast<uint16_t*>(&v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t y = f16_of_codes(e[k]);
+            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&y));
+            e[k] = codes_of(z.x * r, z.y * r);
+          }
+          *at = v;
+        }
+      }
+      s = fmaxf(s, was);
+    }
+    const float inv = 1.f / s;                                         // exact where s is a power of two
+    uint8_t* c = codes + (int64_t)g.slot0 * pitch + h * DH + j * 8;
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      const int tok = p * kTok + tl;
+      if (tok >= g.n) continue;
+      uint16_t y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = unpair(l[p][e]), z = unpair(u[p][e]);
+        y[e] = codes_of(v.x * inv, v.y * inv);
+        y[4 + e] = codes_of(z.x * inv, z.y * inv);
+      }
+      *reinterpret_cast<uint2*>(c + tok * pitch) = make_uint2(y[0] | uint32_t(y[1]) << 16, y[2] | uint32_t(y[3]) << 16);
+      *reinterpret_cast<uint2*>(c + tok * pitch + DH / 2) =
+          make_uint2(y[4] | uint32_t(y[5]) << 16, y[6] | uint32_t(y[7]) << 16);
+    }
+    if (lane == 0) *scale = s;
+  }
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_typed(const KvRopeArgs& a, const Kv8Pages& p, const KvFreq& f, int sm_count, cudaStream_t st) {
+  const int heads = a.heads[0] + a.heads[1] + a.heads[2];
+  const int chunks = (int)(((int64_t)a.n_tokens + kChunk - 1) / kChunk);
+  // Few chunks: one head of one group a warp, so that the call takes one load's latency (a chunk of a decode step has up to
+  // 16 groups). Many: a CTA keeps its angles for more heads.
+  const int most = (min(kChunk, a.n_tokens) * heads + kWarps - 1) / kWarps;
+  const int parts = (int)min((int64_t)most, max((int64_t)1, (int64_t)sm_count * 8 / chunks));
+  const dim3 grid((unsigned)chunks + 1, (unsigned)parts);              // one to check the rows
+  if (a.head_dim == 128) return launch_early(kv8_append_kernel<TI, TO, 128>, grid, kThreads, 0, st, a, p, f);
+  return launch_early(kv8_append_kernel<TI, TO, 64>, grid, kThreads, 0, st, a, p, f);
+}
+
+template <typename TI>
+cudaError_t launch_from(const KvRopeArgs& a, const Kv8Pages& p, const KvFreq& f, int sm_count, cudaStream_t st) {
+  if (a.dtype == kF16) return launch_typed<TI, __half>(a, p, f, sm_count, st);
+  return launch_typed<TI, __nv_bfloat16>(a, p, f, sm_count, st);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const KvRopeArgs& a, const Kv8Pages& p, const KvFreq& f, int sm_count, cudaStream_t st) {
+  if (a.x_dtype == kF32) return launch_from<float>(a, p, f, sm_count, st);
+  if (a.x_dtype == kF16) return launch_from<__half>(a, p, f, sm_count, st);
+  return launch_from<__nv_bfloat16>(a, p, f, sm_count, st);
+}
+
+}  // namespace palu

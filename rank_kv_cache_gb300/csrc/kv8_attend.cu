@@ -1,0 +1,364 @@
+// Attention of few new tokens over a paged KV cache held in 8 bits: decode steps, drafted tokens.
+//
+//   x_t = log2(e) / sqrt(d) s_k(t) q . c_k(t),   o = sum_t 2^x_t s_v(t) c_v(t) / sum_t 2^x_t,   lse = ln sum_t 2^x_t,
+//
+// c the e4m3 codes of slot t, s_k and s_v the scales of its block of 16 slots. The work is cut as for 16-bit caches
+// (kv_attend.cu: units of up to 16 query rows of a key/value head, pieces over all CTAs, four warps with a ring of cp.async
+// copies each); what differs lies between shared memory and the matrix instructions.
+//   * Codes become fp16 in registers, exactly, two an instruction. The order of a product's inner index is free, so a
+//     lane reads 16 consecutive codes of a key in one access and the queries' registers are loaded to match; of values,
+//     pairs of codes are transposed as if they were 16-bit elements, and each pair parted by one byte permutation.
+//   * bf16 queries become fp16, lifted by a power of two of their row so that the largest lies in [2^14, 2^15).
+//   * s_k multiplies 16 scores at once. s_v belongs into the weights of the product with c_v, not into their sum: with
+//     y_t = x_t + log2 s_v(t) and a running maximum M of y, weights are w_t = 2^(y_t - M), o = sum w c_v and
+//     l = sum over blocks of (sum w) / s_v, so that one exponential serves both and the fp16 weights are relative to the
+//     largest weight that enters the product, whatever the scales (up to 2^15 of it, see softmax_base).
+//
+// Bound: HBM; half the bytes of a 16-bit cache in as many copies.
+#include "kv8.h"
+#include "kv_few.cuh"
+
+namespace palu {
+namespace {
+
+constexpr int kWarps = kFewWarps;
+constexpr int kStages = 3;
+constexpr float kLift = 15.f;            // log2 of the largest weight
+
+template <int DH> struct Sm {
+  static constexpr int kTok = 4096 / DH;                    // tokens a warp takes at once: 32, or 64 of d = 64
+  static constexpr int kBlocks = kTok / kKv8Block;
+  static constexpr int kStep = kWarps * kTok;
+  static constexpr int kTile = kTok * DH;                   // one warp's K (or V) stage
+  static constexpr int kWarp = kStages * 2 * kTile;
+  static constexpr int kBytes = kWarps * kWarp;
+  static_assert(kKvFewRows * 2 * kKvFewMostCtas * 4 <= kBytes && kWarps * kKvFewRows * DH * 4 <= kBytes, "joins");
+};
+
+// Places of 16-byte chunks in a tile. Keys are read as 16 bytes of two tokens by eight lanes, four chunks each; values as
+// eight rows of one chunk. Both then fall into different banks. Rows are 8 (d = 128) or 4 chunks long.
+template <int DH> __device__ __forceinline__ uint32_t key_at(int row, int chunk) {
+  return uint32_t(row * DH + ((DH == 128 ? chunk ^ (row & 1) << 2 : chunk) << 4));
+}
+template <int DH> __device__ __forceinline__ uint32_t value_at(int row, int chunk) {
+  return uint32_t(row * DH + ((chunk ^ (DH == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// 4 bytes global -> shared; bytes = 0 writes zeros and reads nothing
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <int DH, bool BF16>
+__global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv8AttendArgs A) {
+  using S = Sm<DH>;
+  constexpr int kTok = S::kTok, kNT = kTok / 8, kBlocks = S::kBlocks;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ FewJoin X;
+  __shared__ float scales[kWarps][kStages][2][kBlocks];
+  const KvAttendArgs& a = A.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const KvRows& R = a.rows;
+  grid_wait();
+  grid_release();
+
+  // steps of a row (0: nothing to do); one without cached tokens takes a step too, for its empty outputs
+  auto row_steps = [&](int b, bool report) -> int {
+    if (b >= R.batch) return 0;
+    int q0, n, L;
+    unsigned bad;
+    const bool use = kv_row(R, b, q0, n, L, bad);
+    if (bad && report) record_error(a.err, kCodeDevice, bad, b, b);
+    return !use || n == 0 ? 0 : max(1, (L + S::kStep - 1) / S::kStep);
+  };
+  const int steps0 = row_steps(lane, blockIdx.x == 0 && warp == 0);
+  int64_t all = __reduce_add_sync(0xffffffffu, steps0);
+  for (int b0 = 32; b0 < R.batch; b0 += 32)
+    all += __reduce_add_sync(0xffffffffu, row_steps(b0 + lane, blockIdx.x == 0 && warp == 0));
+  if (all == 0) return;
+  const int per = piece_length(steps0, all, R.batch, a.n_kv, a.ctas);
+  Cut cut0;
+  cut_rows(steps0, per, cut0, 0, 0);
+  int pieces_all = cut0.total;
+  if (R.batch > 32) {
+    Cut x = cut0;
+    for (int b0 = 32; b0 < R.batch; b0 += 32) cut_rows(row_steps(b0 + lane, false), per, x, x.total, x.total_cut);
+    pieces_all = x.total;
+  }
+
+  // the 32 rows of the piece: a CTA's pieces only go on, so they are looked for from the last one's
+  Cut x = cut0;
+  int row0 = 0;
+  for (int idx = blockIdx.x; idx < pieces_all * a.n_kv; idx += gridDim.x) {
+    // the piece's row b, head h and number among the unit's np, and its place among those of cut units
+    unsigned at;
+    while (!(at = __ballot_sync(0xffffffffu, idx < (x.start + x.pieces) * a.n_kv))) {
+      row0 += 32;
+      cut_rows(row_steps(row0 + lane, false), per, x, x.total, x.total_cut);
+    }
+    const int src = __ffs(at) - 1, b = row0 + src;
+    const int np = __shfl_sync(0xffffffffu, x.pieces, src);
+    const int in_row = idx - __shfl_sync(0xffffffffu, x.start, src) * a.n_kv;
+    const int h = in_row / np, piece = in_row % np;
+    const int first_slot = __shfl_sync(0xffffffffu, x.cut, src) * a.n_kv + h * np;
+    int q0, n, L;
+    unsigned bad;
+    kv_row(R, b, q0, n, L, bad);
+    const int rows = n * a.g;
+    int len = (L + S::kStep - 1) / S::kStep;                       // the row's steps, cut evenly
+    len = (len + np - 1) / np * S::kStep;
+    const int t0 = min(L, piece * len), t1 = min(L, t0 + len);
+
+    float o[DH / 16][2][4];
+#pragma unroll
+    for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][0][e] = o[i][1][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    uint8_t* ring = smem + warp * S::kWarp;
+    const uint32_t ring_a = smem_u32(ring);
+    const int first = t0 + warp * kTok;
+    const int n_it = first < t1 ? (t1 - first + S::kStep - 1) / S::kStep : 0;
+    const uint8_t* kb = static_cast<const uint8_t*>(a.pages.k) + h * DH;
+    const uint8_t* vb = static_cast<const uint8_t*>(a.pages.v) + h * DH;
+    const int64_t tok_stride = (int64_t)a.n_kv * DH;
+
+    // slot of this lane's block of step `it` (-1: past the range, or a page outside the pool)
+    auto slot_of = [&](int it) -> int {
+      const int t = first + it * S::kStep + lane * kKv8Block;
+      if (it >= n_it || lane >= kBlocks || t >= t1) return -1;
+      const int64_t s = kv_slot(R, a.pages, b, t);
+      if (s < 0) record_error(a.err, kCodeDevice, kErrPage, t, b);
+      return int(s);
+    };
+    auto load = [&](int it, int slot) {
+      if (it < n_it) {
+        const uint32_t st = ring_a + (it % kStages) * 2 * S::kTile;
+        const int rest = t1 - first - it * S::kStep;                 // tokens of the step that are there
+        constexpr int kCh = DH / 16;                                 // 16-byte chunks of a row
+#pragma unroll
+        for (int x = 0; x < kTok * kCh / 32; ++x) {
+          const int row = (x * 32 + lane) / kCh, ch = lane % kCh;
+          const int s = __shfl_sync(0xffffffffu, slot, row / kKv8Block);
+          const bool in = s >= 0 && row < rest;
+          const int64_t off = in ? (s + row % kKv8Block) * tok_stride + ch * 16 : 0;
+          cp16(st + key_at<DH>(row, ch), kb + off, in ? 16 : 0);
+          cp16(st + S::kTile + value_at<DH>(row, ch), vb + off, in ? 16 : 0);
+        }
+        if (lane < kBlocks) {
+          const int64_t off = slot < 0 ? 0 : (int64_t)(slot / kKv8Block) * a.n_kv + h;
+          cp4(smem_u32(&scales[warp][it % kStages][0][lane]), A.k_scale + off, slot < 0 ? 0 : 4);
+          cp4(smem_u32(&scales[warp][it % kStages][1][lane]), A.v_scale + off, slot < 0 ? 0 : 4);
+        }
+      }
+      cp_commit();
+    };
+
+    int next = slot_of(0);
+#pragma unroll
+    for (int it = 0; it < kStages - 1; ++it) {
+      const int cur = next;
+      next = slot_of(it + 1);
+      load(it, cur);
+    }
+
+    // Query rows as the A operand: row = lane / 4 and + 8; inner index: lane % 4 has the elements [16 c + 4 w, + 4) of
+    // every 64 in the product w of the four that they take, as a key's chunk gives them.
+    const int r0 = lane >> 2, cp = lane & 3;
+    uint32_t qf[DH / 16][4];
+    int vis[2];                                                      // last slot the two query rows see
+    float scale[2];                                                  // log2(e) / sqrt(d), without the row's lift
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int rr = r0 + 8 * x;
+      const bool ok = rr < rows;
+      const int i = rr / a.g, head = h * a.g + rr % a.g;
+      vis[x] = ok ? L - n + i : -1;
+      scale[x] = a.scale_log2;
+      const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
+                                                      (int64_t)(q0 + i) * a.q_stride + head * DH + cp * 16);
+#pragma unroll
+      for (int k = 0; k < DH / 16; ++k) {
+        const uint2 v = ok ? p[k / 4 * 16 + k % 4] : make_uint2(0u, 0u);
+        qf[k][x] = v.x;
+        qf[k][2 + x] = v.y;
+      }
+      if constexpr (BF16) {
+        __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int k = 0; k < DH / 16; ++k) {
+          top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][x])));
+          top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][2 + x])));
+        }
+        float big = fmaxf(__low2float(top), __high2float(top));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const float lift = lift_of(big);
+        scale[x] *= 1.f / lift;                                      // powers of two
+#pragma unroll
+        for (int k = 0; k < DH / 16; ++k) {
+          qf[k][x] = lifted(qf[k][x], lift);
+          qf[k][2 + x] = lifted(qf[k][2 + x], lift);
+        }
+      }
+    }
+    const int vis_min = L - n;                                       // every row sees slots up to here
+
+    for (int it = 0; it < n_it; ++it) {
+      {
+        const int cur = next;
+        next = slot_of(it + kStages);
+        load(it + kStages - 1, cur);
+      }
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t ks = ring_a + (it % kStages) * 2 * S::kTile, vs = ks + S::kTile;
+      float s[kNT][4];
+#pragma unroll
+      for (int i = 0; i < kNT; ++i) {
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DH / 64; ++c) {
+          const uint4 v = lds16(ks + key_at<DH>(i * 8 + r0, c * 4 + cp));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma<false>(s[i], qf[c * 4 + k], f16_of_codes(uint16_t(w[k])), f16_of_codes(uint16_t(w[k] >> 16)));
+        }
+      }
+      const int tb = first + it * S::kStep;
+      if (tb + kTok > t1 || tb + kTok - 1 > vis_min) {
+#pragma unroll
+        for (int i = 0; i < kNT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = tb + i * 8 + cp * 2 + (e & 1);
+            if (t >= t1 || t > vis[e >> 1]) s[i][e] = -INFINITY;
+          }
+      }
+      float k_s[kBlocks], v_log[kBlocks], v_inv[kBlocks];
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        k_s[i] = scale_or_one(scales[warp][it % kStages][0][i]);
+        const float z = scale_or_one(scales[warp][it % kStages][1][i]);
+        v_log[i] = lg2(z);
+        v_inv[i] = rcp(z);
+      }
+      float al[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const float y = fmaxf(fmaxf(s[2 * i][2 * x], s[2 * i][2 * x + 1]), fmaxf(s[2 * i + 1][2 * x], s[2 * i + 1][2 * x + 1]));
+          mx = fmaxf(mx, fmaf(y, scale[x] * k_s[i], v_log[i]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[x], softmax_base<false>(mx, kLift));
+        const float base = mn == -INFINITY ? 0.f : mn;               // nothing seen yet: every weight is 2^-inf = 0
+        al[x] = ex2(m[x] - base);
+        m[x] = mn;
+        l[x] *= al[x];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const float c = scale[x] * k_s[i], d = v_log[i] - base;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[2 * i + e][2 * x] = ex2(fmaf(s[2 * i + e][2 * x], c, d));
+            s[2 * i + e][2 * x + 1] = ex2(fmaf(s[2 * i + e][2 * x + 1], c, d));
+            sum += s[2 * i + e][2 * x] + s[2 * i + e][2 * x + 1];
+          }
+          l[x] = fmaf(sum, v_inv[i], l[x]);
+        }
+      }
+      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            o[i][e][0] *= al[0];
+            o[i][e][1] *= al[0];
+            o[i][e][2] *= al[1];
+            o[i][e][3] *= al[1];
+          }
+      }
+      const int vr = ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
+#pragma unroll
+      for (int k = 0; k < kBlocks; ++k) {
+        const uint32_t pf[4] = {pack2<false>(s[2 * k][0], s[2 * k][1]), pack2<false>(s[2 * k][2], s[2 * k][3]),
+                                pack2<false>(s[2 * k + 1][0], s[2 * k + 1][1]),
+                                pack2<false>(s[2 * k + 1][2], s[2 * k + 1][3])};
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) {
+          uint32_t f[4];                                             // tokens 0 - 7 and 8 - 15 of two chunks
+          ldsm4t(f, vs + value_at<DH>(k * 16 + vr, 2 * i + vc));
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            // two tokens of an even and an odd column: parted, the even columns are one product, the odd ones another
+            const uint32_t b0 = __byte_perm(f[2 * z], 0u, 0x3120), b1 = __byte_perm(f[2 * z + 1], 0u, 0x3120);
+            mma<false>(o[2 * i + z][0], pf, f16_of_codes(uint16_t(b0)), f16_of_codes(uint16_t(b1)));
+            mma<false>(o[2 * i + z][1], pf, f16_of_codes(uint16_t(b0 >> 16)), f16_of_codes(uint16_t(b1 >> 16)));
+          }
+        }
+      }
+      __syncwarp();
+    }
+    cp_wait<0>();
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    }
+    __syncthreads();
+
+    // join the warps: each leaves its output rows in the (now free) ring
+    float* ob = reinterpret_cast<float*>(smem) + warp * kKvFewRows * DH;
+    if (cp == 0) {
+      X.ml[warp][r0] = make_float2(m[0], l[0]);
+      X.ml[warp][r0 + 8] = make_float2(m[1], l[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        *reinterpret_cast<float4*>(ob + (r0 + 8 * x) * DH + i * 16 + cp * 4) =
+            make_float4(o[i][0][2 * x], o[i][1][2 * x], o[i][0][2 * x + 1], o[i][1][2 * x + 1]);
+    __syncthreads();
+    finish_piece<DH, BF16>(a, X, smem, q0, rows, h, np, piece, first_slot);
+    __syncthreads();                                                 // the joins' space becomes the ring again
+  }
+}
+
+template <int DH, bool BF16> cudaError_t prepare_few() {
+  return cudaFuncSetAttribute(kv8_attend_few_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm<DH>::kBytes);
+}
+template <int DH, bool BF16> cudaError_t launch_few(const Kv8AttendArgs& a, int ctas, cudaStream_t st) {
+  return launch_early(kv8_attend_few_kernel<DH, BF16>, dim3(ctas), kWarps * 32, Sm<DH>::kBytes, st, a);
+}
+
+}  // namespace
+
+cudaError_t prepare_kv8_attend_few(int head_dim, bool bf16) {
+  if (head_dim == 128) return bf16 ? prepare_few<128, true>() : prepare_few<128, false>();
+  return bf16 ? prepare_few<64, true>() : prepare_few<64, false>();
+}
+
+cudaError_t launch_kv8_attend_few(Kv8AttendArgs A, int sm_count, cudaStream_t st) {
+  KvAttendArgs& a = A.a;
+  // the cut aims at the CTAs that the GPU holds; no more are launched than the rows' bounds give steps
+  a.ctas = kKvFewCtas * sm_count < kKvFewMostCtas ? kKvFewCtas * sm_count : kKvFewMostCtas;
+  const int step = a.head_dim == 128 ? Sm<128>::kStep : Sm<64>::kStep;
+  const int64_t steps = (((int64_t)a.rows.max_kv_len + step - 1) / step + 1) * a.rows.batch * a.n_kv;
+  const int grid = steps < a.ctas ? (int)steps : a.ctas;
+  if (a.head_dim == 128) return a.bf16 ? launch_few<128, true>(A, grid, st) : launch_few<128, false>(A, grid, st);
+  return a.bf16 ? launch_few<64, true>(A, grid, st) : launch_few<64, false>(A, grid, st);
+}
+
+}  // namespace palu

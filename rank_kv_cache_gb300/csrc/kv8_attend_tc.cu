@@ -1,0 +1,851 @@
+// Attention of many new tokens over a paged KV cache held in 8 bits on the tcgen05 tensor cores: prompts, chunks of
+// prompts, and batches that mix them with decode steps.
+//
+//   x_t = log2(e) / sqrt(d) s_k(t) q . c_k(t),   o = sum_t 2^x_t s_v(t) c_v(t) / sum_t 2^x_t,   lse = ln sum_t 2^x_t,
+//
+// c the e4m3 codes of slot t, s_k and s_v the scales of its block of 16 slots. Tiles, items, their cut along the cached
+// tokens and the join are those of 16-bit caches (kv_attend_tc.cu); what comes between the cache and the products:
+//   * The loaders bring 128 cached tokens' codes by TMA (boxes of a page's tokens) and, with the keys', the tile's 16
+//     scales by cp.async, into a ring of code tiles. What lies behind a row's length comes too: it changes nothing, as
+//     its scores are masked and its values' codes are replaced by zeros.
+//   * A third warpgroup turns code tiles into fp16 tiles, exactly, in the layout that the products read (128-byte
+//     swizzle). All products are fp16: bf16 queries are lifted to it in place by the softmax warps when they
+//     arrive, each row by a power of two of its own.
+//   * s_k multiplies 16 scores of a thread's row at once. With y_t = x_t + log2 s_v(t) and a running maximum of y, the
+//     weights 2^(y_t - M) are what c_v is multiplied by, and the sum takes them divided by s_v: one exponential
+//     serves both, and the fp16 weights are relative to the largest that enters the product, whatever the scales.
+// A product straight on the codes (kind::f8f6f4) would want the queries and weights in 8 bits too, in two or three terms
+// each to keep their precision: as many products as in fp16, and the weights' terms in the softmax, which bounds the
+// kernel already.
+//
+// Every wait is bounded; one that gives up records PALU_ERR_TIMEOUT, and all roles wait for their own
+// copies and products in flight before tensor memory is freed.
+#include "kv8.h"
+#include "kv_tc_items.cuh"
+
+namespace palu {
+namespace {
+
+constexpr int kThreads = 512;            // two softmax warpgroups; two loader warps, MMA and an idle warp; converters
+// Registers: launched with 128 a thread; 256 * 192 + 128 * 80 + 128 * 48 = 512 * 128.
+constexpr int kRegsSoftmax = 192, kRegsOther = 80, kRegsConvert = 48;
+constexpr int kBlocks = kTile / kKv8Block;
+
+template <int DH> struct Lay {
+  // fp16 tiles: 64 elements (128 bytes) of all rows, then the next 64. Code tiles: rows of DH bytes.
+  static constexpr int kHalf = kTile * 128;             // 64 elements of 128 rows
+  static constexpr int kTileB = kHalf * (DH / 64);
+  static constexpr int kCodeB = kTile * DH;
+  static constexpr int kStages = DH == 128 ? 3 : 5;     // fp16 tiles
+  static constexpr int kCodes = DH == 128 ? 4 : 8;      // code tiles
+  // Scales of key tiles in use. A tile's are written when its place in the ring of kStages tiles is free, and all
+  // tiles whose values' products had not ended then count: of the kStages - 1 places before it, and of the values up to
+  // three places behind their keys, at most kStages / 2 + 2.
+  static constexpr int kScales = DH == 128 ? 4 : 8;
+  static constexpr int kOffKv = 2 * kTileB;             // behind two query tiles
+  static constexpr int kOffCode = kOffKv + kStages * kTileB;
+  static constexpr int kOffBar = kOffCode + kCodes * kCodeB;
+  static constexpr int kShared = DH == 128 ? 2048 : 3072;   // barriers, items, scales, the units' exchange
+  static constexpr int kSmem = kOffBar + kShared + 1024;    // and alignment
+  static constexpr uint32_t kColO = 2 * kTile;          // tensor memory: S (and P) of the units, then O
+  static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
+};
+
+// a code tile, for the converters: its tokens that are below the row's length, and what it is
+struct Info {
+  int valid, kind;                        // kind: kKeys, kValues or kEnd
+};
+constexpr int kKeys = 0, kValues = 1, kEnd = 2;
+constexpr int kScaleLanes = 2 * kBlocks;  // lanes that load a key tile's scales
+
+template <int DH> struct Shared {
+  using Y = Lay<DH>;
+  uint64_t full[Y::kStages], empty[Y::kStages], code_full[Y::kCodes], code_empty[Y::kCodes], scale_full[Y::kScales];
+  uint64_t q_full, q_ready, q_empty, x_full, x_empty, drained;
+  uint64_t s_full[2], o_full[2], p_full[2][2];
+  uint64_t item_full[2], item_empty[2];
+  Item item[2];
+  Plan plan;
+  Info info[Y::kCodes];
+  unsigned cut;                           // pieces of cut tiles that this CTA has taken
+  uint32_t tmem;
+  int abort_flag;
+  float raw[Y::kCodes][2][kBlocks];       // scales of keys and values, as they arrive
+  float2 scale[Y::kScales][kBlocks];      // s_k and log2 s_v
+  union {
+    float2 ml[kTile];                     // of the units' exchange, at an item's end
+    float lift[kTile];                    // of the queries' rows where both units share a tile, at its beginning
+  };
+};
+static_assert(sizeof(Shared<128>) <= Lay<128>::kShared && sizeof(Shared<64>) <= Lay<64>::kShared, "shared block");
+static_assert(sizeof(JoinShared) <= 2 * Lay<64>::kTileB, "in the queries' space");
+
+struct Tc8Params {
+  TcParams P;
+  const float* k_scale;
+  const float* v_scale;
+};
+
+// 4 bytes global -> shared; bytes = 0 writes zeros and reads nothing
+__device__ __forceinline__ void cp4(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+// this thread's copies so far arrive at the barrier when they have landed
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_addr(bar)), "r"(n) : "memory");
+}
+
+// Lifts a row of bf16 queries, as TMA left it (two halves of 64 elements, 128-byte swizzle), to fp16 in place.
+template <int DH> __device__ __forceinline__ float lift_row(uint8_t* tile, int r) {
+  auto at = [&](int c) -> uint4* {
+    return reinterpret_cast<uint4*>(tile + c / 8 * Lay<DH>::kHalf + r * 128 + ((c % 8 ^ (r & 7)) << 4));
+  };
+  __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+  for (int c = 0; c < DH / 8; ++c) {
+    const uint4 v = *at(c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+  }
+  const float lift = lift_of(fmaxf(__low2float(top), __high2float(top)));
+#pragma unroll
+  for (int c = 0; c < DH / 8; ++c) {
+    const uint4 v = *at(c);
+    *at(c) = make_uint4(lifted(v.x, lift), lifted(v.y, lift), lifted(v.z, lift), lifted(v.w, lift));
+  }
+  return lift;
+}
+
+// ------------------------------------------------------------------------------------------- attend
+template <int DH, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const Tc8Params P8) {
+  using Y = Lay<DH>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared<DH>& S = *reinterpret_cast<Shared<DH>*>(smem + Y::kOffBar);
+  volatile int* abort_flag = &S.abort_flag;
+  const TcParams& P = P8.P;
+  const KvAttendArgs& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Y::kStages; ++i) {
+      tc::mbar_init(&S.full[i], 4);            // the converters
+      tc::mbar_init(&S.empty[i], 1);
+    }
+    for (int i = 0; i < Y::kCodes; ++i) {
+      tc::mbar_init(&S.code_full[i], 1 + kScaleLanes);
+      tc::mbar_init(&S.code_empty[i], 4);
+    }
+    for (int i = 0; i < Y::kScales; ++i) tc::mbar_init(&S.scale_full[i], 1);
+    tc::mbar_init(&S.q_full, 1);
+    tc::mbar_init(&S.q_ready, 8);              // bf16 queries, lifted by the softmax warps
+    tc::mbar_init(&S.q_empty, 1);              // the products that read the queries
+    tc::mbar_init(&S.x_full, 4);
+    tc::mbar_init(&S.x_empty, 4);
+    tc::mbar_init(&S.drained, 1);
+    for (int u = 0; u < 2; ++u) {
+      tc::mbar_init(&S.s_full[u], 1);
+      tc::mbar_init(&S.o_full[u], 1);
+      for (int k = 0; k < 2; ++k) tc::mbar_init(&S.p_full[u][k], 4);
+      tc::mbar_init(&S.item_full[u], 1);
+      tc::mbar_init(&S.item_empty[u], 10);     // eight softmax warps, the MMA warp, the value loader
+    }
+    S.abort_flag = 0;
+    S.cut = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&S.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  grid_wait();                                 // for the plan
+  grid_release();
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------------ converters
+    // 16 codes a lane and step: a warp reads 512 bytes in a row and writes its fp16 rows' two 16-byte halves, those of
+    // the upper 64 elements in the other order, so that eight lanes' writes fall into different banks.
+    tc::regs_shrink<kRegsConvert>();
+    constexpr int kCh = DH / 16, kEach = kTile * kCh / 128;      // 16-byte chunks of a row; of a thread
+    const int t = threadIdx.x - 384;
+    int sc = 0, st = 0, n_k = 0;
+    uint32_t par_c = 0, par = 1;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, tc::mbar_wait_short(bar, phase, abort_flag, P.wait_ns));
+    };
+    for (;;) {
+      if (!wait(&S.code_full[sc], par_c)) break;
+      const Info info = S.info[sc];
+      if (info.kind == kEnd) break;
+      if (!wait(&S.empty[st], par)) break;
+      if (info.kind == kKeys) {
+        if (warp == 12) {
+          if (lane < kBlocks)
+            S.scale[n_k % Y::kScales][lane] = make_float2(scale_or_one(S.raw[sc][0][lane]), lg2(scale_or_one(S.raw[sc][1][lane])));
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&S.scale_full[n_k % Y::kScales]);
+        }
+        ++n_k;
+      }
+      const uint8_t* src = smem + Y::kOffCode + sc * Y::kCodeB + t * 16;
+      uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB;
+      const int ch = t % kCh, upper = ch / 4, c0 = ch * 2 % 8;
+#pragma unroll
+      for (int x0 = 0; x0 < kEach; x0 += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = *reinterpret_cast<const uint4*>(src + (x0 + x) * 2048);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = (x0 + x) * (128 / kCh) + t / kCh;
+          if (row >= info.valid) v[x] = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = f16_of_codes(uint16_t(w[e]));
+            f[2 * e + 1] = f16_of_codes(uint16_t(w[e] >> 16));
+          }
+          uint8_t* at = dst + upper * Y::kHalf + row * 128;
+          const int lo = ((c0 ^ (row & 7)) << 4), hi = (((c0 + 1) ^ (row & 7)) << 4);
+          const uint4 f0 = make_uint4(f[0], f[1], f[2], f[3]), f1 = make_uint4(f[4], f[5], f[6], f[7]);
+          *reinterpret_cast<uint4*>(at + (upper ? hi : lo)) = upper ? f1 : f0;
+          *reinterpret_cast<uint4*>(at + (upper ? lo : hi)) = upper ? f0 : f1;
+        }
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&S.code_empty[sc]);
+        tc::mbar_arrive(&S.full[st]);
+      }
+      if (++sc == Y::kCodes) {
+        sc = 0;
+        par_c ^= 1;
+      }
+      if (++st == Y::kStages) {
+        st = 0;
+        par ^= 1;
+      }
+    }
+  } else if (warp >= 8) {
+    tc::regs_shrink<kRegsOther>();
+    if (warp == 8 || warp == 10) {
+      // ------------------------------------------------------------------ loaders
+      // Warp 8 takes the items and loads Q and K, warp 10 V. Both count every stage of the ring, in the order
+      // in which the products take them: K runs one tile ahead of V, two where the units alternate. Copies are
+      // issued by one lane with uniform operands.
+      const bool keys = warp == 8;
+      const CUtensorMap* map = keys ? &tm_k : &tm_v;
+      Rows32 rows;
+      Plan plan{};
+      if (keys) {
+        plan = plan_rows(P, rows, blockIdx.x == 0);
+        if (lane == 0) S.plan = plan;        // the first item's arrival publishes it
+      }
+      const int total = plan.items * a.n_kv;
+      const int box = P.box, n_box = kTile / box;
+      const int ps = a.pages.page_size, tile_pages = kTile / ps, tile_rest = kTile % ps;
+      const int table_pages = int(a.rows.table_pages), n_pages = int(a.pages.n_pages);
+      const int oob_slot = n_pages * ps;
+      int st = 0, loads_q = 0, seq = 0;    // the ring's next stage; stages counted
+      int n_x = 0;                         // exchanges of the units, and whether the last is still to be waited for
+      bool exchanged = false;
+      uint32_t par = 1, mine = 0;          // what `code_empty` is waited for; which of the last stages this warp filled
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, phase, abort_flag, P.wait_ns));
+        return ok;
+      };
+      if (lane == 0) {
+        if (keys) tc::tma_prefetch(&tm_q);
+        tc::tma_prefetch(map);
+      }
+      for (int i = 0; ok; ++i) {
+        Item it{};
+        if (keys) {
+          if (!wait(&S.item_empty[i & 1], ((i >> 1) & 1) ^ 1)) break;
+          int idx = 0;
+          if (lane == 0) idx = (int)atomicAdd(&P.plan.head->next, 1u);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
+          if (idx < total) {
+            const int e = idx / a.n_kv;    // never less than the one before
+            while (e >= rows.items) {
+              rows_load(rows, a.rows, rows.row0 + 32, P.per_tile);
+              rows_cut(rows, plan.target);
+            }
+            const int src = __ffs(__ballot_sync(0xffffffffu, e < rows.item0 + rows.tiles * rows.pieces)) - 1;
+            const int in_row = e - __shfl_sync(0xffffffffu, rows.item0, src);
+            const int pieces = __shfl_sync(0xffffffffu, rows.pieces, src), tile = in_row / pieces;
+            it.b = rows.row0 + src;
+            it.h = idx % a.n_kv;
+            it.q0 = __shfl_sync(0xffffffffu, rows.q0, src);
+            it.n = __shfl_sync(0xffffffffu, rows.n, src);
+            it.L = __shfl_sync(0xffffffffu, rows.L, src);
+            it.tok0 = (__shfl_sync(0xffffffffu, rows.tiles, src) - 1 - tile) * 2 * P.per_tile;
+            it.tiles = it.n - it.tok0 > P.per_tile ? 2 : 1;
+            const int last = min(it.n, it.tok0 + it.tiles * P.per_tile) - 1;
+            const int steps = steps_of(min(it.L, it.L - it.n + last + 1)), len = (steps + pieces - 1) / pieces;
+            it.kv0 = min(steps, in_row % pieces * len);
+            it.kv1 = min(steps, it.kv0 + len);
+            it.split = pieces > 1 ? __shfl_sync(0xffffffffu, rows.slot0, src) + in_row : -1;
+          }
+          if (lane == 0) {
+            S.item[i & 1] = it;
+            tc::mbar_arrive(&S.item_full[i & 1]);
+          }
+        } else {
+          if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
+          it = S.item[i & 1];
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&S.item_empty[i & 1]);
+        }
+        const int b = __shfl_sync(0xffffffffu, it.b, 0), L = __shfl_sync(0xffffffffu, it.L, 0);
+        const int h = __shfl_sync(0xffffffffu, it.h, 0), tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+        const int kv0 = __shfl_sync(0xffffffffu, it.kv0, 0), kv1 = __shfl_sync(0xffffffffu, it.kv1, 0);
+        if (tiles == 0) break;
+        if (kv1 == kv0) continue;
+        const int32_t* table = a.rows.page_table ? a.rows.page_table + (int64_t)b * table_pages : nullptr;
+        if (keys) {
+          // the queries' space: read by the last item's products and, where its units met there, by warpgroup 0
+          if (!wait(&S.q_empty, (loads_q & 1) ^ 1)) break;
+          if (exchanged && !wait(&S.x_empty, n_x++ & 1)) break;
+          exchanged = tiles == 1 && kv1 - kv0 > 1;
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(tiles) * P.per_tile * a.g * DH * 2);
+            for (int t = 0; t < tiles; ++t)
+              for (int c = 0; c < DH / 64; ++c)
+                tc::tma_load_3d(smem + t * Y::kTileB + c * Y::kHalf, &tm_q, &S.q_full, c * 64, h * a.g,
+                                it.q0 + it.tok0 + t * P.per_tile);
+          }
+          ++loads_q;
+          __syncwarp();
+        }
+        // One tile of 128 cached tokens in boxes of `box` tokens of a page. A lane looks up the slot of its box one tile
+        // ahead: the next tile's is 128 tokens on.
+        int tb = kv0 * kTile + lane * box;
+        int pg = tb / ps, off = tb - pg * ps;   // without a table ps is not exceeded: pg is 0
+        int next_page = -1, next_off = 0, next_t = 0;
+        auto look = [&]() {
+          next_page = table ? -1 : b;
+          if (lane < n_box && tb < L && table && pg < table_pages) next_page = table[pg];
+          next_off = off;
+          next_t = tb;
+          tb += kTile;
+          pg += tile_pages;
+          off += tile_rest;
+          if (off >= ps) {
+            off -= ps;
+            ++pg;
+          }
+        };
+        look();
+        auto load = [&](int j) {
+          int slot = oob_slot;                   // of this lane's box; outside the pool: zeros
+          if (lane < n_box && next_t < L) {
+            if (next_page >= 0 && next_page < n_pages) slot = next_page * ps + next_off;
+            else record_error(a.err, kCodeDevice, kErrPage, next_t, b);
+          }
+          // a lane's block of 16 of the tile, the first 8 lanes for the keys' scales, the next 8 for the values'
+          const int t16 = lane % kBlocks * kKv8Block;
+          const int slot16 = __shfl_sync(0xffffffffu, slot, t16 / box) + t16 % box;
+          if (!wait(&S.code_empty[st], par)) return;
+          if (lane == 0) {
+            S.info[st].valid = min(kTile, L - j * kTile);
+            S.info[st].kind = keys ? kKeys : kValues;
+          }
+          if (keys && lane < kScaleLanes) {
+            const bool in = j * kTile + t16 < L && slot16 < oob_slot;
+            const int64_t at = in ? (int64_t)(slot16 / kKv8Block) * a.n_kv + h : 0;
+            cp4(&S.raw[st][lane / kBlocks][lane % kBlocks], (lane < kBlocks ? P8.k_scale : P8.v_scale) + at, in ? 4 : 0);
+            cp_arrive(&S.code_full[st]);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (!keys) mbar_arrive_n(&S.code_full[st], kScaleLanes);
+            tc::mbar_arrive_expect_tx(&S.code_full[st], Y::kCodeB);
+          }
+          __syncwarp();
+          uint8_t* dst = smem + Y::kOffCode + st * Y::kCodeB;
+          for (int x = 0; x < n_box; ++x) {
+            const int sx = __shfl_sync(0xffffffffu, slot, x);
+            if (tc::elect_one()) tc::tma_load_3d(dst + x * box * DH, map, &S.code_full[st], 0, h, sx);
+            __syncwarp();
+          }
+          mine |= 1u;
+          look();
+        };
+        auto step = [&](bool k_tile, int j) {
+          mine <<= 1;
+          ++seq;
+          if (k_tile == keys && !(P.plan.test_stall && !keys)) load(j);
+          if (++st == Y::kCodes) {
+            st = 0;
+            par ^= 1;
+          }
+        };
+        const int lead = min(tiles == 1 ? 2 : 1, kv1 - kv0);
+        for (int j = kv0; ok && j < kv0 + lead; ++j) step(true, j);
+        for (int j = kv0; ok && j < kv1; ++j) {
+          step(false, j);
+          if (ok && j + lead < kv1) step(true, j + lead);
+        }
+      }
+      if (ok && keys && wait(&S.code_empty[st], par) && lane == 0) {   // the converters' end
+        S.info[st].kind = kEnd;
+        mbar_arrive_n(&S.code_full[st], 1 + kScaleLanes);
+      }
+      if (!ok) {   // copies still in flight must land before the CTA exits
+        volatile int quiet = 0;
+        for (int d = 0; d < Y::kCodes && d < seq; ++d) {
+          const int p = seq - 1 - d;
+          if (mine >> d & 1u)
+            tc::mbar_wait_bounded(&S.code_full[p % Y::kCodes], (p / Y::kCodes) & 1, &quiet, P.wait_ns / 10);
+        }
+        if (loads_q) tc::mbar_wait_bounded(&S.q_full, (loads_q - 1) & 1, &quiet, P.wait_ns / 10);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------------ MMA
+      // The whole warp walks the loop, so that stages and descriptors stay in uniform registers, and one lane
+      // issues: from a branch of one thread each product took 80 cycles to issue, longer than it runs. One warp
+      // issues for both units, in turn: with a warp each, the units fell into step and waited together.
+      const uint32_t id_qk = tc::idesc_f16(kTile, kTile, false);
+      const uint32_t id_pv = tc::idesc_f16(kTile, DH, false) | tc::kIdescBMajorMN;
+      const uint32_t base = tc::smem_addr(smem);
+      const uint64_t dq = tc::sdesc_sw128(base, 16, 1024), dk = tc::sdesc_sw128(base + Y::kOffKv, 16, 1024);
+      const uint64_t dv = tc::sdesc_sw128(base + Y::kOffKv, Y::kHalf, 1024);
+      int st = 0, loads_q = 0;           // the ring's stage that comes next
+      uint32_t par = 0, np[2] = {0, 0};  // its phase; the weights' phases of the units
+      // A wait that gives up only raises the abort flag, at which every later wait gives up at once; the loop
+      // looks at the flag once a tile, so that a wait that need not wait costs little more than its test.
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        if (!tc::mbar_try_wait(bar, phase)) tc::mbar_wait_short(bar, phase, abort_flag, P.wait_ns);
+      };
+      auto stage = [&]() -> int {        // waits for the next stage of the ring and takes it
+        const int s = st;
+        wait(&S.full[s], par);
+        if (++st == Y::kStages) {
+          st = 0;
+          par ^= 1;
+        }
+        return s;
+      };
+      // S_u = Q K^T of key stage s; `last`: the item's last product that reads the queries
+      auto qk = [&](int u, uint64_t q, int s, bool free, bool last) {
+        const uint64_t kd = dk + uint64_t(s) * (Y::kTileB >> 4);
+        __syncwarp();
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint64_t off = ((k / 4) * Y::kHalf + (k % 4) * 32) >> 4;
+            tc::umma_f16(tmem + u * kTile, q + off, kd + off, id_qk, k != 0);
+          }
+          tc::umma_commit(&S.s_full[u]);
+          if (free) tc::umma_commit(&S.empty[s]);
+          if (last) tc::umma_commit(&S.q_empty);
+        }
+      };
+      // O_u += P_u V of value stage s, the first half's weights first; `last`: the item's last for the unit
+      auto pv = [&](int u, int s, bool first, bool free, bool last) {
+        const uint64_t vd = dv + uint64_t(s) * (Y::kTileB >> 4);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          wait(&S.p_full[u][half], np[u]);
+          __syncwarp();
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int k = half * 4; k < half * 4 + 4; ++k)
+              tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, vd + ((k * 2048) >> 4), id_pv,
+                              !first || k != 0);
+            if (half == 1 && free) tc::umma_commit(&S.empty[s]);
+            if (half == 1 && last) tc::umma_commit(&S.o_full[u]);
+          }
+        }
+        np[u] ^= 1;
+      };
+      auto dead = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
+      for (int i = 0;; ++i) {
+        wait(&S.item_full[i & 1], (i >> 1) & 1);
+        if (dead()) break;
+        Item it = S.item[i & 1];
+        it.L = __shfl_sync(0xffffffffu, it.L, 0);
+        it.n = __shfl_sync(0xffffffffu, it.n, 0);
+        it.tok0 = __shfl_sync(0xffffffffu, it.tok0, 0);
+        it.tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+        it.kv0 = __shfl_sync(0xffffffffu, it.kv0, 0);
+        it.kv1 = __shfl_sync(0xffffffffu, it.kv1, 0);
+        if (lane == 0) tc::mbar_arrive(&S.item_empty[i & 1]);
+        if (it.tiles == 0) break;
+        const int n = it.kv1 - it.kv0;
+        if (n == 0) continue;
+        wait(BF16 ? &S.q_ready : &S.q_full, loads_q & 1);
+        ++loads_q;
+        if (it.tiles == 2) {
+          // both units over each tile; unit 0 may see fewer (it stops first)
+          const int n0 = unit_steps(it, 0, P.per_tile);
+          const uint64_t dq1 = dq + (Y::kTileB >> 4);
+          int sk = stage();
+          if (n0 > 0) qk(0, dq, sk, false, false);
+          qk(1, dq1, sk, true, n == 1);
+          for (int k = 0; k < n; ++k) {
+            if (dead()) break;
+            const int sv = stage();
+            if (k < n0) pv(0, sv, k == 0, false, k + 1 == n0);
+            if (k + 1 < n) {
+              sk = stage();
+              if (k + 1 < n0) qk(0, dq, sk, false, false);
+            }
+            pv(1, sv, k == 0, true, k + 1 == n);
+            if (k + 1 < n) qk(1, dq1, sk, true, k + 2 == n);
+          }
+        } else {
+          // the units take the tiles in turn
+          for (int k = 0; k < min(n, 2); ++k) {
+            const int s = stage();
+            qk(k, dq, s, true, k + 1 == n);
+          }
+          for (int k = 0; k < n; ++k) {
+            if (dead()) break;
+            const int sv = stage();
+            pv(k & 1, sv, k < 2, true, k + 2 >= n);
+            if (k + 2 < n) {
+              const int sk = stage();
+              qk(k & 1, dq, sk, true, k + 3 == n);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      __syncwarp();
+      // every product issued has completed once this commit lands
+      volatile int quiet = 0;
+      if (tc::elect_one()) tc::umma_commit(&S.drained);
+      __syncwarp();
+      tc::mbar_wait_bounded(&S.drained, 0, &quiet, P.wait_ns);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    tc::regs_grow<kRegsSoftmax>();
+    const int u = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;                        // query row of the tile = lane of tensor memory
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + u * kTile, t_o = tmem + lanes + Y::kColO + u * DH;
+    int n_s = 0, n_o = 0, n_o0 = 0, n_x = 0, n_q = 0, n_k = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t par) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, par, abort_flag, P.wait_ns));
+      tc::tc_fence_after();
+      return ok;
+    };
+    for (int i = 0; ok; ++i) {
+      if (!wait(&S.item_full[i & 1], (i >> 1) & 1)) break;
+      const Item it = S.item[i & 1];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&S.item_empty[i & 1]);
+      if (it.tiles == 0) break;
+      if (threadIdx.x == 0 && it.split >= 0) ++S.cut;
+      const int tile = it.tiles == 2 ? u : 0;
+      const int first_tok = it.tok0 + tile * P.per_tile;
+      const int tok = first_tok + r / a.g;
+      const bool live = r < P.per_tile * a.g && tok < it.n;
+      const int vis = it.L - it.n + tok;                         // last slot this row sees
+      const int vis_min = it.L - it.n + first_tok;               // every row of the tile sees slots up to here
+      const int steps = unit_steps(it, u, P.per_tile);
+      const bool exchange = it.tiles == 1 && it.kv1 - it.kv0 > 1;
+
+      float c = a.scale_log2;                                    // of this row's scores: without its lift
+      if (BF16 && it.kv1 > it.kv0) {
+        float lift = 1.f;
+        if (!wait(&S.q_full, n_q & 1)) break;                    // both units: neither arrives for an item to come
+        if (it.tiles == 2 || u == 0) {
+          if (r < P.per_tile * a.g) lift = lift_row<DH>(smem + tile * Y::kTileB, r);
+          if (it.tiles == 1) S.lift[r] = lift;
+          tc::fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.q_ready);
+        if (it.tiles == 1 && u == 1 && steps > 0) {
+          if (!wait(&S.q_ready, n_q & 1)) break;
+          lift = S.lift[r];
+        }
+        ++n_q;
+        c *= 1.f / lift;                                         // powers of two
+      }
+
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < steps; ++k) {
+        const int tk = unit_tile(it, u, k), kk = n_k + tk - it.kv0;
+        if (!wait(&S.scale_full[kk % Y::kScales], (kk / Y::kScales) & 1)) break;
+        if (!wait(&S.s_full[u], n_s & 1)) break;
+        ++n_s;
+        const float2* sc = S.scale[kk % Y::kScales];
+        const int t0 = tk * kTile;
+        if (t0 + kTile - 1 > vis_min) {
+          // tokens that a row does not see: masked in tensor memory, so that the common tile's code stays short
+          const int lim = vis - t0;
+#pragma unroll 1
+          for (int x = 0; x < kTile; x += 32) {
+            uint32_t w[32];
+            tc::tmem_ld32_nowait(t_s + x, w);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) w[y] = x + y > lim ? 0xff800000u : w[y];
+            tc::tmem_st32(t_s + x, w);
+          }
+          tc::tmem_st_wait();
+        }
+        float s[kTile];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tc::tmem_ld32_nowait(t_s + x * 32, reinterpret_cast<uint32_t*>(s) + x * 32);
+        tc::tmem_ld_wait();
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          float y0 = fmaxf(s[b * 16], s[b * 16 + 1]), y1 = fmaxf(s[b * 16 + 2], s[b * 16 + 3]);
+#pragma unroll
+          for (int y = 4; y < 16; y += 4) {
+            y0 = max3(y0, s[b * 16 + y], s[b * 16 + y + 1]);
+            y1 = max3(y1, s[b * 16 + y + 2], s[b * 16 + y + 3]);
+          }
+          const float2 z = sc[b];
+          mx[b & 1] = fmaxf(mx[b & 1], fmaf(fmaxf(y0, y1), z.x * c, z.y));
+        }
+        const float top = softmax_base<false>(fmaxf(mx[0], mx[1]), kLift);
+        const bool raise = top > m + kRaise;                     // true on the first finite score
+        if (__any_sync(0xffffffffu, raise)) {
+          const float mn = raise ? top : m;
+          const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - mn);
+          m = mn;
+          l *= f;
+          if (k > 0) {   // s_full also says that the product before it, into O, has completed
+#pragma unroll 1
+            for (int x = 0; x < DH; x += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16_nowait(t_o + x, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tc::tmem_st16(t_o + x, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;             // nothing seen yet: every p is 2^-inf = 0
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t p[16];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float2 z = sc[x * 2 + b];
+            const uint64_t c2 = pair(z.x * c, z.x * c), n2 = pair(z.y + neg, z.y + neg);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const float2 e = unpair(fma2(pair(s[x * 32 + b * 16 + 2 * y], s[x * 32 + b * 16 + 2 * y + 1]), c2, n2));
+              const float p0 = ex2(e.x), p1 = ex2(e.y);
+              sum2[y & 1] = add2(sum2[y & 1], pair(p0, p1));
+              p[b * 8 + y] = pack2<false>(p0, p1);
+            }
+            const float2 w = unpair(add2(sum2[0], sum2[1]));
+            l = fmaf(w.x + w.y, ex2(-z.y), l);                   // without the values' scale
+          }
+          tc::tmem_st16(t_s + x * 16, p);
+          if (x & 1) {                                           // 64 tokens' weights: the product may begin
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&S.p_full[u][x >> 1]);
+          }
+        }
+      }
+      if (!ok) break;
+      n_k += it.kv1 - it.kv0;
+
+      // the unit's row: O / l, or its partial
+      if (steps > 0) {
+        if (!wait(&S.o_full[u], n_o & 1)) break;
+        ++n_o;
+      }
+      float* xs = reinterpret_cast<float*>(smem);                // [d / 4][128 rows][4] in the queries' space
+      if (u == 1 && unit_steps(it, 0, P.per_tile) > 0) ++n_o0;
+      if (exchange && u == 1) {
+        if (!wait(&S.o_full[0], (n_o0 - 1) & 1)) break;          // unit 0's products read the queries too
+#pragma unroll 1
+        for (int x = 0; x < DH / 32; ++x) {
+          uint32_t o[32];
+          tc::tmem_ld32_nowait(t_o + x * 32, o);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            *reinterpret_cast<uint4*>(xs + ((x * 8 + y) * kTile + r) * 4) =
+                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
+        S.ml[r] = make_float2(m, l);
+        tc::fence_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.x_full);
+        continue;
+      }
+      if (it.tiles == 1 && u == 1) continue;                     // a single step: unit 0 has all of it
+      float f0 = 1.f, f1 = 0.f;
+      if (exchange) {
+        if (!wait(&S.x_full, n_x & 1)) break;
+        ++n_x;
+        const float2 o1 = S.ml[r];
+        const float mn = fmaxf(m, o1.x), b0 = mn == -INFINITY ? 0.f : mn;
+        f0 = exp2f(m - b0);
+        f1 = exp2f(o1.x - b0);
+        l = fmaf(l, f0, o1.y * f1);
+        m = mn;
+      }
+      const int64_t row = (int64_t)(it.q0 + tok) * a.n_heads + it.h * a.g + r % a.g;
+      const int64_t slot = ((int64_t)it.split * a.n_kv + it.h) * 2 + tile;
+      if (it.split < 0) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        f0 *= inv;
+        f1 *= inv;
+        if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      } else {
+        if (live) a.part_ml[slot * kTile + r] = make_float2(m, l);
+      }
+#pragma unroll 1
+      for (int x = 0; x < DH / 32; ++x) {
+        float o[32];
+        if (steps > 0) {
+          tc::tmem_ld32_nowait(t_o + x * 32, reinterpret_cast<uint32_t*>(o));
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] *= f0;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0.f;
+        }
+        if (exchange) {
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const float4 v = *reinterpret_cast<const float4*>(xs + ((x * 8 + y) * kTile + r) * 4);
+            o[4 * y] = fmaf(v.x, f1, o[4 * y]);
+            o[4 * y + 1] = fmaf(v.y, f1, o[4 * y + 1]);
+            o[4 * y + 2] = fmaf(v.z, f1, o[4 * y + 2]);
+            o[4 * y + 3] = fmaf(v.w, f1, o[4 * y + 3]);
+          }
+        }
+        if (it.split >= 0 && live) {
+          float4* po = reinterpret_cast<float4*>(a.part_o) + (slot * (DH / 4) + x * 8) * kTile + r;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) po[y * kTile] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        } else if (it.split < 0 && live) {
+          uint16_t* out = static_cast<uint16_t*>(a.out) + row * DH + x * 32;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            uint32_t w[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) w[z] = pack2<BF16>(o[16 * y + 2 * z], o[16 * y + 2 * z + 1]);
+            store32(out + 16 * y, w, P.out_sectors);
+          }
+        }
+      }
+      tc::tc_fence_before();
+      if (exchange) {                                            // the queries' space is read: TMA may fill it again
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.x_empty);
+      }
+    }
+    // The join. Every item has been taken when a CTA comes here, by CTAs that run and wait for none: the wait for
+    // their pieces ends whichever CTAs the GPU holds. All warps meet first, also after a wait that gave up.
+    const auto any = [](bool bad) { return tc::named_bar_or(1, kJoinWarps * 32, bad); };
+    if (!any(!ok) && S.plan.joins > 0) {
+      Rows32 rows;
+      rows_load(rows, a.rows, 0, P.per_tile);
+      if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(&P.plan.head->pieces, S.cut);
+        ok = pieces_wait(&P.plan.head->pieces, unsigned(S.plan.slots * a.n_kv), P.wait_ns);
+        if (!ok) *abort_flag = 1;
+      }
+      // the queries' space is free: nothing is in flight behind the last item
+      if (!any(!ok)) join_pieces<DH, BF16>(P, S.plan, rows, *reinterpret_cast<JoinShared*>(smem));
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (threadIdx.x == 0) {
+    if (*abort_flag) record_error(a.err, kCodeTimeout, kErrWait, blockIdx.x, 0);
+    // the last CTA to end sets the counters back for the next call; `done` wraps to zero by itself
+    __threadfence();
+    if (atomicInc(&P.plan.head->done, gridDim.x - 1) == gridDim.x - 1) P.plan.head->next = P.plan.head->pieces = 0;
+  }
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int DH, bool BF16> cudaError_t prepare_tc() {
+  return cudaFuncSetAttribute(kv8_attend_tc_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Lay<DH>::kSmem);
+}
+template <int DH, bool BF16> cudaError_t launch_tc(const Kv8AttendArgs& A, const KvTcPlan& t, cudaStream_t st) {
+  const KvAttendArgs& a = A.a;
+  Tc8Params P8{};
+  P8.k_scale = A.k_scale;
+  P8.v_scale = A.v_scale;
+  TcParams& P = P8.P;
+  P.a = a;
+  P.plan = t;
+  P.per_tile = kTile / a.g;
+  P.out_sectors = (uintptr_t)a.out % 32 == 0;
+  P.wait_ns = t.wait_ns;
+  CUtensorMap tm_q, tm_k, tm_v;
+  {
+    // queries [token][head][d]: boxes of 64 columns, one group's heads, a tile's tokens
+    const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[3] = {DH, (cuuint64_t)a.n_heads, (cuuint64_t)a.rows.n_tokens};
+    const cuuint64_t strides[2] = {DH * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)P.per_tile};
+    if (!tma_encode(&tm_q, dt, 3, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  }
+  {
+    // codes [slot][kv head][d]. A box lies in one page: the largest power of two (16 and more) that divides a page, and
+    // without a table, where a row's tokens lie in a row, a whole tile.
+    P.box = a.rows.page_table ? a.pages.page_size & -a.pages.page_size : kTile;
+    P.box = P.box > kTile ? kTile : P.box;
+    const cuuint64_t dims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)(a.pages.n_pages * a.pages.page_size)};
+    const cuuint64_t strides[2] = {DH, (cuuint64_t)a.n_kv * DH};
+    const cuuint32_t box[3] = {DH, 1, (cuuint32_t)P.box};
+    if (!tma_encode(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !tma_encode(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  }
+  const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
+  const unsigned grid = (unsigned)(most < t.sm_count ? most : t.sm_count);
+  return launch_early(kv8_attend_tc_kernel<DH, BF16>, dim3(grid), kThreads, Lay<DH>::kSmem, st, tm_q, tm_k, tm_v, P8);
+}
+
+}  // namespace
+
+cudaError_t prepare_kv8_attend_tc(int head_dim, bool bf16) {
+  if (head_dim == 128) return bf16 ? prepare_tc<128, true>() : prepare_tc<128, false>();
+  return bf16 ? prepare_tc<64, true>() : prepare_tc<64, false>();
+}
+
+cudaError_t launch_kv8_attend_tc(const Kv8AttendArgs& a, const KvTcPlan& t, cudaStream_t st) {
+  if (!tma_available()) return cudaErrorNotSupported;
+  if (a.a.head_dim == 128) return a.a.bf16 ? launch_tc<128, true>(a, t, st) : launch_tc<128, false>(a, t, st);
+  return a.a.bf16 ? launch_tc<64, true>(a, t, st) : launch_tc<64, false>(a, t, st);
+}
+
+}  // namespace palu

@@ -1,6 +1,8 @@
 // The handle of the paged KV cache's operators, and what its host files share.
 #pragma once
 
+#include <math.h>
+
 #include "palu_attn.h"
 #include "kv.h"
 
@@ -97,6 +99,38 @@ inline void rope_args(const palu_kv* h, KvRopeArgs& a) {
   a.rotate = h->d.rope_theta > 0.0;
   a.eps = (float)h->d.norm_eps;
   a.err = reinterpret_cast<ErrWord*>(h->ws + h->L.err);
+}
+
+// everything but the pages
+inline void attend_args(const palu_kv* h, const palu_kv_rows& rows, const void* q, int64_t q_stride, void* out, float* lse,
+                        KvAttendArgs& a) {
+  const palu_kv_desc& d = h->d;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.lse = lse;
+  a.rows = rows_of(rows);
+  a.n_heads = d.n_heads;
+  a.n_kv = d.n_kv_heads;
+  a.g = d.n_heads / d.n_kv_heads;
+  a.head_dim = d.head_dim;
+  a.bf16 = d.dtype == PALU_BF16;
+  a.scale_log2 = float(1.4426950408889634 / sqrt((double)d.head_dim));
+  a.part_o = reinterpret_cast<float*>(h->ws + h->L.part_o);
+  a.part_ml = reinterpret_cast<float2*>(h->ws + h->L.part_ml);
+  a.counters = reinterpret_cast<unsigned*>(h->ws + h->L.counters);
+  a.err = reinterpret_cast<ErrWord*>(h->ws + h->L.err);
+}
+
+inline KvTcPlan tc_plan(const palu_kv* h, const palu_kv_rows& rows) {
+  KvTcPlan t{};
+  t.head = reinterpret_cast<KvPlanHead*>(h->ws + h->L.head);
+  t.tile_cap = (int)tc_tile_cap(h->d, rows.n_tokens, rows.batch);
+  t.slots = kTcSlots;
+  t.sm_count = h->sm_count;
+  t.test_stall = (h->d.flags & PALU_FLAG_TEST_STALL) != 0;
+  t.wait_ns = t.test_stall ? 50000000ull : 1000000000ull;   // bound of every device wait
+  return t;
 }
 
 }  // namespace palu

@@ -3,6 +3,7 @@
 
 #include <new>
 
+#include "kv8.h"
 #include "kv_handle.h"
 
 using namespace palu;
@@ -126,7 +127,9 @@ palu_status_t palu_kv_create(const palu_kv_desc* desc, void* workspace, size_t w
   if (desc->dtype != PALU_F32) {
     const bool bf16 = desc->dtype == PALU_BF16;
     if (prepare_kv_attend_few(desc->head_dim, bf16) != cudaSuccess ||
-        prepare_kv_attend_tc(desc->head_dim, bf16) != cudaSuccess) {
+        prepare_kv_attend_tc(desc->head_dim, bf16) != cudaSuccess ||
+        prepare_kv8_attend_few(desc->head_dim, bf16) != cudaSuccess ||
+        prepare_kv8_attend_tc(desc->head_dim, bf16) != cudaSuccess) {
       delete h;
       return PALU_ERR_CUDA;
     }
@@ -252,22 +255,8 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
   DeviceGuard dev(h->device);
   if (!dev.ok) return PALU_ERR_CUDA;
   KvAttendArgs a{};
-  a.q = q;
-  a.q_stride = q_stride;
-  a.out = out;
-  a.lse = lse;
-  a.rows = rows_of(*rows);
+  attend_args(h, *rows, q, q_stride, out, lse, a);
   a.pages = pages_of(*pages);
-  a.n_heads = d.n_heads;
-  a.n_kv = d.n_kv_heads;
-  a.g = d.n_heads / d.n_kv_heads;
-  a.head_dim = d.head_dim;
-  a.bf16 = d.dtype == PALU_BF16;
-  a.scale_log2 = float(1.4426950408889634 / sqrt((double)d.head_dim));
-  a.part_o = reinterpret_cast<float*>(h->ws + h->L.part_o);
-  a.part_ml = reinterpret_cast<float2*>(h->ws + h->L.part_ml);
-  a.counters = reinterpret_cast<unsigned*>(h->ws + h->L.counters);
-  a.err = reinterpret_cast<ErrWord*>(h->ws + h->L.err);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if ((int64_t)a.rows.max_new * a.g <= kKvFewRows) {
@@ -276,14 +265,7 @@ palu_status_t palu_attend_kv(palu_kv_t h, const palu_kv_pages* pages, const palu
   } else {
     // the gathers index cached head rows with 31 bits
     if (pages->n_pages * pages->page_size * d.n_kv_heads >= (int64_t(1) << 31) - 1) return PALU_ERR_UNSUPPORTED;
-    KvTcPlan t{};
-    t.head = reinterpret_cast<KvPlanHead*>(h->ws + h->L.head);
-    t.tile_cap = (int)tc_tile_cap(d, rows->n_tokens, rows->batch);
-    t.slots = kTcSlots;
-    t.sm_count = h->sm_count;
-    t.test_stall = (d.flags & PALU_FLAG_TEST_STALL) != 0;
-    t.wait_ns = t.test_stall ? 50000000ull : 1000000000ull;   // bound of every device wait
-    e = launch_kv_attend_tc(a, t, s);
+    e = launch_kv_attend_tc(a, tc_plan(h, *rows), s);
     if (e == cudaErrorNotSupported) return PALU_ERR_UNSUPPORTED;
   }
   return e == cudaSuccess ? PALU_OK : PALU_ERR_CUDA;

@@ -1,0 +1,260 @@
+// The plan of a step's rows and pages: admission, packed rows, page table entries from a ring of free pages, and the place
+// and slot of every packed token.
+//
+//   pages(b) = max(0, ceil((L_b + n_b) / page) - held_b),  row_start = running sum of the admitted n_b,
+//   admitted: the running sums of pages and tokens, over all rows up to b, stay within what is free.
+//
+// Bound: latency (a step of 64 rows moves a few KB). One launch, one cluster of 1 to 8 CTAs: every CTA loads the rows, 4
+// a thread, and works out the three running sums (pages taken, tokens, pages given back) for itself in shared memory;
+// then the CTAs share the writes, each finding its rows by bisection of those sums. Nothing is read that
+// another CTA writes: pages are read from the ring's front and written behind its end, table entries are read below
+// `held` and written from there on, and what is replaced in place (lengths, held, the ring's state) is written behind a
+// barrier of the cluster.
+#include <cooperative_groups.h>
+
+#include "kv8.h"
+
+namespace palu {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kPer = 4, kRows = kThreads * kPer;   // rows of a chunk
+constexpr int kMostCtas = 8;
+// Tokens and pages that a CTA writes alone: past it the work goes to a cluster.
+constexpr int kWritesPerCta = 4096;
+
+struct Sums {
+  int64_t pages, tokens, back;
+};
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return Sums{a.pages + b.pages, a.tokens + b.tokens, a.back + b.back};
+}
+
+// the last of the `n` ascending numbers x[0 .. n) that is <= v (x[0] is)
+__device__ __forceinline__ int last_at_most(const int* x, int n, int v) {
+  int lo = 0;
+  for (int hi = n; hi - lo > 1;) {
+    const int mid = (lo + hi) >> 1;
+    if (x[mid] <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct Shared {
+  Sums warp[kThreads / 32];
+  // of the chunk's rows: running sums before the row (one more: behind the last), relative to the chunk's beginning
+  int tokens[kRows + 1], pages[kRows + 1], back[kRows + 1];
+  int len[kRows], held[kRows];
+};
+
+__global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& S = *reinterpret_cast<Shared*>(smem);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  grid_wait();
+  grid_release();
+  const int head0 = a.state[0], count0 = a.state[1];
+  const bool ring_ok = head0 >= 0 && head0 < a.n_pages && count0 >= 0 && count0 <= a.n_pages;
+  if (!ring_ok && rank == 0 && tid == 0) record_error(a.err, kCodeDevice, kErrPool, count0, head0);
+  const int head = ring_ok ? head0 : 0, count = ring_ok ? count0 : 0;
+  auto ring_at = [&](int64_t i) {
+    int64_t x = head + i;
+    while (x >= a.n_pages) x -= a.n_pages;   // twice at most where the counts add up
+    return (int)x;
+  };
+
+  Sums wanted{0, 0, 0};                // of all rows before the chunk, admitted or not
+  int64_t taken = 0, tokens = 0;       // of the admitted ones
+  if (rank == 0 && tid == 0) a.row_start[0] = 0;
+  for (int row0 = 0; row0 < a.batch; row0 += kRows) {
+    const int rows = min(kRows, a.batch - row0);
+    int n[kPer], L[kPer], held[kPer];
+    Sums w[kPer], run{0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int r = tid * kPer + e, b = row0 + r;
+      n[e] = L[e] = held[e] = 0;
+      w[e] = Sums{0, 0, 0};
+      if (r < rows) {
+        n[e] = a.fresh[b];
+        L[e] = a.kv_len[b];
+        held[e] = a.held[b];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int r = tid * kPer + e, b = row0 + r;
+      const bool held_ok = held[e] >= 0 && held[e] <= a.table_pages;
+      bool bad = !held_ok;
+      if (n[e] < 0) {
+        if (held_ok) w[e].back = held[e];
+      } else {
+        const int64_t end = (int64_t)L[e] + n[e];
+        bad = bad || L[e] < 0 || n[e] > a.max_new || end > a.max_kv_len || L[e] > (int64_t)held[e] * a.page_size;
+        if (bad) n[e] = 0;
+        if (n[e] > 0) {
+          w[e].tokens = n[e];
+          w[e].pages = max(0, (int)((end + a.page_size - 1) / a.page_size) - held[e]);
+        }
+      }
+      if (bad && rank == 0) record_error(a.err, kCodeDevice, kErrRows, b, b);
+      run = run + w[e];
+    }
+    // the running sums over the CTA
+    Sums scan = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums y{__shfl_up_sync(0xffffffffu, scan.pages, o), __shfl_up_sync(0xffffffffu, scan.tokens, o),
+                   __shfl_up_sync(0xffffffffu, scan.back, o)};
+      if (lane >= o) scan = scan + y;
+    }
+    if (lane == 31) S.warp[warp] = scan;
+    __syncthreads();
+    Sums before{0, 0, 0}, all{0, 0, 0};
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before = before + S.warp[i];
+      all = all + S.warp[i];
+    }
+    const bool back_ok = all.back <= a.n_pages;   // else the counts do not add up, and the chunk gives nothing back
+    if (!back_ok) {
+      if (rank == 0 && tid == 0) record_error(a.err, kCodeDevice, kErrPool, a.n_pages, row0);
+      all.back = 0;
+    }
+    before = Sums{before.pages + scan.pages - run.pages, before.tokens + scan.tokens - run.tokens,
+                  before.back + scan.back - run.back};
+    // Admission falls off once: from the first row that does not fit on. Sums of rows behind it are those of the last one
+    // that fits, so that admitted tokens and pages count on from 0.
+    Sums at = before;
+    int most_tokens = 0, most_pages = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const Sums to = at + w[e];
+      if (wanted.pages + to.pages <= count && wanted.tokens + to.tokens <= a.n_tokens) {
+        most_tokens = (int)to.tokens;
+        most_pages = (int)to.pages;
+      } else {
+        n[e] = min(n[e], 0);
+      }
+      at = to;
+    }
+    // what the chunk admits in all: the sums ascend, so the largest that fits is the last
+    most_tokens = __reduce_max_sync(0xffffffffu, most_tokens);
+    most_pages = __reduce_max_sync(0xffffffffu, most_pages);
+    __syncthreads();
+    if (lane == 0) S.warp[warp] = Sums{most_pages, most_tokens, 0};
+    __syncthreads();
+    for (int i = 0; i < kThreads / 32; ++i) {
+      most_tokens = max(most_tokens, (int)S.warp[i].tokens);
+      most_pages = max(most_pages, (int)S.warp[i].pages);
+    }
+    at = before;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int r = tid * kPer + e;
+      if (r < rows) {
+        S.tokens[r] = (int)min(at.tokens, (int64_t)most_tokens);
+        S.pages[r] = (int)min(at.pages, (int64_t)most_pages);
+        S.back[r] = back_ok ? (int)at.back : 0;
+        S.len[r] = L[e];
+        S.held[r] = held[e];
+      }
+      at = at + w[e];
+    }
+    if (tid == 0) {
+      S.tokens[rows] = most_tokens;
+      S.pages[rows] = most_pages;
+      S.back[rows] = (int)all.back;
+    }
+    // every CTA has read the chunk's rows: they may be replaced
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+
+    const int step = ctas * kThreads, me = rank * kThreads + tid;
+    if (rank == 0) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int r = tid * kPer + e, b = row0 + r;
+        if (r >= rows) continue;
+        const bool ended = n[e] < 0;
+        a.row_start[b + 1] = (int)tokens + S.tokens[r + 1];
+        a.kv_len_out[b] = ended ? 0 : L[e] + n[e];
+        a.held_out[b] = ended ? 0 : held[e] + S.pages[r + 1] - S.pages[r];
+      }
+    }
+    // pages taken: from the ring into the table
+    for (int j = me; j < most_pages; j += step) {
+      const int r = last_at_most(S.pages, rows + 1, j);
+      const int page = a.ring[ring_at(taken + j)];
+      a.table[(int64_t)(row0 + r) * a.table_pages + S.held[r] + j - S.pages[r]] = page;
+      if (page < 0 || page >= a.n_pages) record_error(a.err, kCodeDevice, kErrPage, page, row0 + r);
+    }
+    // pages given back: from the table into the ring
+    for (int j = me; j < (int)all.back; j += step) {
+      const int r = last_at_most(S.back, rows + 1, j);
+      a.ring[ring_at(count + wanted.back + j)] = a.table[(int64_t)(row0 + r) * a.table_pages + j - S.back[r]];
+    }
+    // the tokens' places, four at a time
+    if (a.positions || a.slots) {
+      for (int j0 = me * 4; j0 < most_tokens; j0 += step * 4) {
+        int r = last_at_most(S.tokens, rows + 1, j0);
+        for (int j = j0; j < min(j0 + 4, most_tokens); ++j) {
+          while (S.tokens[r + 1] <= j) ++r;
+          const int pos = S.len[r] + j - S.tokens[r];
+          if (a.positions) a.positions[tokens + j] = pos;
+          if (a.slots) {
+            const int pg = pos / a.page_size, more = pg - S.held[r];
+            const int page = more < 0 ? a.table[(int64_t)(row0 + r) * a.table_pages + pg]
+                                      : a.ring[ring_at(taken + S.pages[r] + more)];
+            const bool ok = page >= 0 && page < a.n_pages;
+            a.slots[tokens + j] = ok ? page * a.page_size + (pos - pg * a.page_size) : -1;
+            if (!ok) record_error(a.err, kCodeDevice, kErrPage, page, row0 + r);
+          }
+        }
+      }
+    }
+    tokens += most_tokens;
+    taken += most_pages;
+    wanted = wanted + all;
+    __syncthreads();                   // the sums' space is written anew
+  }
+  for (int64_t t = tokens + rank * kThreads + tid; t < a.n_tokens; t += (int64_t)ctas * kThreads) {
+    if (a.positions) a.positions[t] = 0;
+    if (a.slots) a.slots[t] = -1;
+  }
+  // The state is written when every CTA has read it: they have met since.
+  if (rank == 0 && tid == 0) {
+    const int64_t left = count - taken + wanted.back;
+    if (count + wanted.back > a.n_pages) record_error(a.err, kCodeDevice, kErrPool, (int)min(left, (int64_t)INT32_MAX), 0);
+    a.state_out[0] = ring_ok ? ring_at(taken) : head0;
+    a.state_out[1] = ring_ok ? (int)min(left, (int64_t)a.n_pages) : count0;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
+  // CTAs by what there may be to write: tokens, and the pages they can take
+  const int64_t writes = (int64_t)a.n_tokens + a.n_tokens / a.page_size + a.batch;
+  unsigned ctas = 1;
+  while (ctas < kMostCtas && writes > (int64_t)ctas * kWritesPerCta) ctas *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kv_plan_kernel, a);
+}
+
+}  // namespace palu

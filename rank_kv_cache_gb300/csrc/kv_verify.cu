@@ -1,0 +1,316 @@
+// Verification of drafted tokens against the target's probabilities, from given random numbers.
+//
+//   a = the first draft i with u_i q_i(x_i) >= p_i(x_i) (or all of them);  w = max(p_a - q_a, 0), or p_a where every draft
+//   was accepted, or where that is zero;  token = min { v : sum_{j <= v} w_j > u sum_j w_j }.
+//
+// The comparison of a draft is exact (two fp32 numbers' product in fp64). A token is drawn from sums of up to 2^20
+// numbers, of which fp32 would misplace about vocab 2^-24 of the draws: a difference p - q with its rounding error
+// (exact for p >= q >= 0) is added to a sum of two fp32 numbers (Knuth's two-sum), 512 values at a time; those
+// segments' sums are joined in fp64. fp64 throughout would be bound by that unit, at 2 lanes of an SM a cycle.
+//
+// Bound: HBM, one target and one draft row of each batch row. A cluster of 1 to 8 CTAs takes a row; a warp a segment of
+// 512 values, a lane 16 of them in four loads. The CTAs exchange their sums through distributed shared memory; the one
+// that holds the draw finds the segment by its running sums, and one warp reads that segment again (from L2) for the token.
+#include <cooperative_groups.h>
+
+#include "kv8.h"
+
+namespace palu {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSeg = 512, kVec = 4, kSteps = kSeg / (32 * kVec);   // values of a segment, of a lane's load; loads
+constexpr int kMostCtas = 8;
+
+// the cluster's CTAs have all started: before that their shared memory is not written
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+struct TwoSum {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x, float rest) {
+    const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)), rest));
+    hi = s;
+  }
+  __device__ __forceinline__ double value() const { return double(hi) + double(lo); }
+};
+
+// four probabilities at v of a row of `vocab`, those outside as 0; `wide`: the row's loads are aligned
+template <typename T> __device__ __forceinline__ void load4(float (&x)[kVec], const T* row, int v, int vocab, bool wide) {
+  if (wide && v + kVec <= vocab) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(row + v);
+      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+    } else {
+      const uint2 f = *reinterpret_cast<const uint2*>(row + v);
+      const T* e = reinterpret_cast<const T*>(&f);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = to_f32(e[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) x[i] = v + i < vocab ? to_f32(row[v + i]) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) x[i] = fmaxf(x[i], 0.f);   // NaN: 0
+}
+
+// What the token is drawn from: max(p - q, 0) as a difference and its rounding error.
+struct Weights {
+  float d[kVec], e[kVec];
+};
+template <typename T> struct Source {
+  const T* p;
+  const T* q;        // nullptr: none
+  int certain;       // a draft that was certain: its weight is 0 (or -1)
+  int vocab;
+  bool wide_p, wide_q;
+  __device__ __forceinline__ void load(Weights& w, int v) const {
+    load4(w.d, p, v, vocab, wide_p);
+    if (q) load4(w.e, q, v, vocab, wide_q);
+  }
+  __device__ __forceinline__ void finish(Weights& w, int v) const {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float x = w.d[i], y = q ? w.e[i] : 0.f;
+      const bool more = x > y && v + i != certain;
+      const float d = __fsub_rn(x, y);
+      w.d[i] = more ? d : 0.f;
+      w.e[i] = more ? __fsub_rn(__fsub_rn(x, d), y) : 0.f;
+    }
+  }
+};
+
+template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kernel(const KvVerifyArgs a) {
+  extern __shared__ __align__(16) double seg[];        // sums of the CTA's segments
+  __shared__ double part[kMostCtas];                    // sums of the cluster's CTAs
+  __shared__ int taken_s;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int b = blockIdx.x / ctas;
+  cluster_arrive();
+  grid_wait();
+  grid_release();
+
+  // the row's drafts
+  const int start = a.row_start[b], end = a.row_start[b + 1];
+  const bool row_ok = start >= 0 && end >= start && end <= a.n_tokens;
+  int n = row_ok ? end - start : 0;
+  if (rank == 0 && tid == 0 && (!row_ok || n - 1 > a.max_draft)) record_error(a.err, kCodeDevice, kErrRows, b, b);
+  n = min(n, a.max_draft + 1);
+  int32_t* out = a.tokens + (int64_t)b * (a.max_draft + 1);
+  const float* u = a.uniforms + (int64_t)b * (a.max_draft + 1);
+  const int32_t* drafts = a.draft_tokens + (int64_t)b * a.max_draft;
+  const T* target = static_cast<const T*>(a.target) + (int64_t)start * a.target_stride;
+  const T* draft = a.draft ? static_cast<const T*>(a.draft) + (int64_t)b * a.max_draft * a.draft_stride : nullptr;
+  if (n == 0) {                                         // the whole cluster
+    cluster_wait();
+    if (rank == 0) {
+      for (int i = tid; i <= a.max_draft; i += kThreads) out[i] = -1;
+      if (tid == 0) {
+        a.accepted[b] = 0;
+        if (a.kv_len_out) a.kv_len_out[b] = a.kv_len[b];
+      }
+    }
+    return;
+  }
+  if (warp == 0) {
+    int taken = n - 1;
+    for (int i0 = 0; i0 < n - 1; i0 += 32) {
+      const int i = i0 + lane;
+      bool no = false;
+      if (i < n - 1) {
+        const int x = drafts[i];
+        no = x < 0 || x >= a.vocab;
+        if (no) {
+          if (rank == 0) record_error(a.err, kCodeDevice, kErrToken, x, b);
+        } else {
+          const float p = fmaxf(to_f32(target[(int64_t)i * a.target_stride + x]), 0.f);
+          const float q = draft ? fmaxf(to_f32(draft[(int64_t)i * a.draft_stride + x]), 0.f) : 1.f;
+          no = !(double(fmaxf(u[i], 0.f)) * double(q) < double(p));
+        }
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, no);
+      if (m) {
+        taken = i0 + __ffs(m) - 1;
+        break;
+      }
+    }
+    if (lane == 0) taken_s = taken;
+  }
+  __syncthreads();
+  cluster_wait();
+  const int taken = taken_s;
+  const bool rejected = taken < n - 1;
+  if (rank == 0) {
+    for (int i = tid; i <= a.max_draft; i += kThreads)
+      if (i != taken) out[i] = i < taken ? drafts[i] : -1;
+    if (tid == 0) {
+      a.accepted[b] = taken;
+      if (a.kv_len_out) a.kv_len_out[b] = a.kv_len[b] - (n - 1 - taken);
+    }
+  }
+
+  Source<T> src;
+  src.p = target + (int64_t)taken * a.target_stride;
+  src.q = rejected && draft ? draft + (int64_t)taken * a.draft_stride : nullptr;
+  src.certain = rejected && !draft ? drafts[taken] : -1;
+  src.vocab = a.vocab;
+  src.wide_p = (uintptr_t)src.p % (kVec * sizeof(T)) == 0;
+  src.wide_q = (uintptr_t)src.q % (kVec * sizeof(T)) == 0;
+  const int segs = (a.vocab + kSeg - 1) / kSeg, per = (segs + ctas - 1) / ctas;
+  const int s0 = min(segs, rank * per), mine = min(segs, s0 + per) - s0;
+
+  double total, below, own;
+  for (;;) {
+    for (int s = warp; s < mine; s += kWarps) {
+      const int v0 = (s0 + s) * kSeg + lane * kVec;
+      Weights w[kSteps];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) src.load(w[k], v0 + k * 32 * kVec);
+      TwoSum sum;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        src.finish(w[k], v0 + k * 32 * kVec);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sum.add(w[k].d[i], w[k].e[i]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, o), lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
+        sum.add(hi, lo);
+      }
+      if (lane == 0) seg[s] = sum.value();
+    }
+    __syncthreads();
+    own = 0.0;
+    if (warp == 0) {                                    // in the segments' order by lanes, then over the lanes
+      for (int s = lane; s < mine; s += 32) own += seg[s];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+      if (lane < ctas) *cluster.map_shared_rank(&part[rank], lane) = own;
+    }
+    cluster.sync();
+    total = below = 0.0;
+    for (int c = 0; c < ctas; ++c) {
+      if (c < rank) below += part[c];
+      total += part[c];
+    }
+    if (total > 0.0 || (!src.q && src.certain < 0)) break;
+    src.q = nullptr;                                    // nothing is left of p - q: from p
+    src.certain = -1;
+    cluster.sync();                                     // every CTA has read the sums
+  }
+  if (!(total > 0.0)) {
+    if (rank == 0 && tid == 0) {
+      out[taken] = -1;
+      record_error(a.err, kCodeDevice, kErrToken, -1, b);
+    }
+    return;
+  }
+  // The draw falls to the first CTA whose running sum exceeds it; those are the same numbers in every CTA.
+  float u1 = u[a.max_draft];
+  u1 = u1 < 1.f ? fmaxf(u1, 0.f) : 0.99999994f;        // 1 - 2^-24; NaN too
+  const double t = double(u1) * total;
+  if (below + part[rank] <= t || below > t || warp != 0 || mine == 0) return;
+  // the segment: the first whose running sum exceeds it, or by another order of rounding the last that holds anything
+  double run = below, from = below;
+  int at = -1;
+  for (int i0 = 0; i0 < mine; i0 += 32) {
+    const double x = i0 + lane < mine ? seg[i0 + lane] : 0.0;
+    double y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    y += run;
+    const unsigned holds = __ballot_sync(0xffffffffu, x > 0.0), over = __ballot_sync(0xffffffffu, x > 0.0 && y > t);
+    const int pick = over ? __ffs(over) - 1 : 31 - __clz(holds);
+    if (holds) {
+      at = i0 + pick;
+      from = __shfl_sync(0xffffffffu, y - x, pick);
+    }
+    if (over) break;
+    run = __shfl_sync(0xffffffffu, y, 31);
+  }
+  // the token within it, alike
+  const int v0 = (s0 + at) * kSeg + lane * kVec;
+  Weights w[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) src.load(w[k], v0 + k * 32 * kVec);
+  run = from;
+  int token = -1;
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    src.finish(w[k], v0 + k * 32 * kVec);
+    double x[kVec], sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      sum += double(w[k].d[i]) + double(w[k].e[i]);
+      x[i] = sum;
+    }
+    double y = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    const double before = run + (y - sum);
+    int first = -1, last = -1;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      if (w[k].d[i] > 0.f) {
+        last = i;
+        if (first < 0 && before + x[i] > t) first = i;
+      }
+    }
+    const unsigned over = __ballot_sync(0xffffffffu, first >= 0), holds = __ballot_sync(0xffffffffu, last >= 0);
+    if (over) {
+      const int l = __ffs(over) - 1;
+      token = (s0 + at) * kSeg + k * 32 * kVec + l * kVec + __shfl_sync(0xffffffffu, first, l);
+      break;
+    }
+    if (holds) {
+      const int l = 31 - __clz(holds);
+      token = (s0 + at) * kSeg + k * 32 * kVec + l * kVec + __shfl_sync(0xffffffffu, last, l);
+    }
+    run = __shfl_sync(0xffffffffu, run + y, 31);
+  }
+  if (lane == 0) out[taken] = token;
+}
+
+template <typename T> cudaError_t launch_typed(const KvVerifyArgs& a, int sm_count, cudaStream_t st) {
+  // The row's segments are shared by as many CTAs as the GPU holds at once for all rows, four an SM.
+  unsigned ctas = kMostCtas;
+  while (ctas > 1 && (int64_t)a.batch * ctas > (int64_t)sm_count * 4) ctas /= 2;
+  const int segs = (a.vocab + kSeg - 1) / kSeg;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.batch * ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(double) * ((segs + ctas - 1) / ctas);   // at most 16 KB
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kv_verify_kernel<T>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_verify(const KvVerifyArgs& a, int sm_count, cudaStream_t st) {
+  if (a.dtype == kF32) return launch_typed<float>(a, sm_count, st);
+  if (a.dtype == kF16) return launch_typed<__half>(a, sm_count, st);
+  return launch_typed<__nv_bfloat16>(a, sm_count, st);
+}
+
+}  // namespace palu

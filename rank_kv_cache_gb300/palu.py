@@ -7,8 +7,8 @@ there is no CPU fallback.
 
 Low-level functions carry the C names and take raw integers (device pointers,
 stream handles); ``PaluAttention`` and ``LatentCache`` wrap them for torch
-tensors, and ``PagedAttention``, ``KVPages`` and ``KVRows`` those of the paged
-dense KV cache.
+tensors, and ``PagedAttention``, ``KVPages``, ``KVPages8``, ``KVRows`` and
+``KVPool`` those of the paged dense KV cache.
 """
 from __future__ import annotations
 
@@ -38,8 +38,10 @@ EXPORTS = ("palu_attn_workspace_size", "palu_attn_create", "palu_append_latents"
            "palu_fuse_value_output", "palu_output_proj_workspace_size", "palu_output_proj",
            "palu_down_proj_size", "palu_prepare_down_proj", "palu_project_latents", "palu_decode_hybrid",
            "palu_decode_paged", "palu_kv_workspace_size", "palu_kv_create", "palu_kv_destroy", "palu_kv_check",
-           "palu_norm_rope", "palu_append_kv", "palu_attend_kv")
+           "palu_norm_rope", "palu_append_kv", "palu_attend_kv", "palu_append_kv8", "palu_attend_kv8",
+           "palu_plan_kv_rows", "palu_verify_drafts")
 PALU_TRACE_CAPACITY = 4096
+PALU_KV8_BLOCK = 16
 
 
 class palu_attn_desc(ctypes.Structure):
@@ -82,6 +84,17 @@ class palu_kv_rows(ctypes.Structure):
     _fields_ = [("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("table_pages", ctypes.c_int64), ("positions", ctypes.c_void_p), ("batch", ctypes.c_int),
                 ("n_tokens", ctypes.c_int64), ("max_new", ctypes.c_int), ("max_kv_len", ctypes.c_int64)]
+
+
+class palu_kv8_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int)]
+
+
+class palu_kv_pool(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_pages", ctypes.c_int64), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_state", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int)]
 
 
 class PaluError(RuntimeError):
@@ -130,6 +143,11 @@ def _load():
         "palu_append_kv": (I, [P, ctypes.POINTER(palu_kv_pages), ctypes.POINTER(palu_kv_rows), P, I64, P, I64, P, I64,
                                P, P, P, P]),
         "palu_attend_kv": (I, [P, ctypes.POINTER(palu_kv_pages), ctypes.POINTER(palu_kv_rows), P, I64, P, P, P]),
+        "palu_append_kv8": (I, [P, ctypes.POINTER(palu_kv8_pages), ctypes.POINTER(palu_kv_rows), P, I64, P, I64, P, I64,
+                                P, P, P, P]),
+        "palu_attend_kv8": (I, [P, ctypes.POINTER(palu_kv8_pages), ctypes.POINTER(palu_kv_rows), P, I64, P, P, P]),
+        "palu_plan_kv_rows": (I, [P, ctypes.POINTER(palu_kv_pool), P, P, I, I64, I, I64, P, P, P, P, P, P, P]),
+        "palu_verify_drafts": (I, [P, P, I64, P, I64, I, I64, P, I, I64, P, I, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -308,6 +326,32 @@ def palu_append_kv(h, pages: palu_kv_pages, rows: palu_kv_rows, q, q_stride: int
 def palu_attend_kv(h, pages: palu_kv_pages, rows: palu_kv_rows, q: int, q_stride: int, out: int, lse,
                    stream: int) -> int:
     return _lib.palu_attend_kv(h, ctypes.byref(pages), ctypes.byref(rows), q, q_stride, out, lse, stream)
+
+
+def palu_append_kv8(h, pages: palu_kv8_pages, rows: palu_kv_rows, q, q_stride: int, k: int, k_stride: int, v: int,
+                    v_stride: int, q_norm, k_norm, q_out, stream: int) -> int:
+    return _lib.palu_append_kv8(h, ctypes.byref(pages), ctypes.byref(rows), q, q_stride, k, k_stride, v, v_stride,
+                                q_norm, k_norm, q_out, stream)
+
+
+def palu_attend_kv8(h, pages: palu_kv8_pages, rows: palu_kv_rows, q: int, q_stride: int, out: int, lse,
+                    stream: int) -> int:
+    return _lib.palu_attend_kv8(h, ctypes.byref(pages), ctypes.byref(rows), q, q_stride, out, lse, stream)
+
+
+def palu_plan_kv_rows(h, pool: palu_kv_pool, new_tokens: int, kv_len: int, batch: int, n_tokens: int, max_new: int,
+                      max_kv_len: int, row_start: int, kv_len_out: int, held_out, state_out, positions, slots,
+                      stream: int) -> int:
+    return _lib.palu_plan_kv_rows(h, ctypes.byref(pool), new_tokens, kv_len, batch, n_tokens, max_new, max_kv_len,
+                                  row_start, kv_len_out, held_out, state_out, positions, slots, stream)
+
+
+def palu_verify_drafts(h, target: int, target_stride: int, draft, draft_stride: int, p_dtype: int, vocab: int,
+                       row_start: int, batch: int, n_tokens: int, draft_tokens: int, max_draft: int, uniforms: int,
+                       tokens: int, accepted: int, kv_len, kv_len_out, stream: int) -> int:
+    return _lib.palu_verify_drafts(h, target, target_stride, draft, draft_stride, p_dtype, vocab, row_start, batch,
+                                   n_tokens, draft_tokens, max_draft, uniforms, tokens, accepted, kv_len, kv_len_out,
+                                   stream)
 
 
 def check(status: int, what: str = "palu") -> None:
@@ -588,6 +632,75 @@ class KVPages:
         return self._c
 
 
+class KVPages8:
+    """The pages of a KV cache held in 8 bits: e4m3 codes k and v [n_pages][page_size][n_kv_heads][head_dim] (float8_e4m3fn
+    or uint8) and float32 scales [n_pages][page_size / 16][n_kv_heads]; a value is its code times the scale of its
+    head and its 16 slots. page_size is a multiple of 16."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        _require_contiguous(k=k, v=v, k_scale=k_scale, v_scale=v_scale)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError("k and v must be [n_pages][page_size][n_kv_heads][head_dim] of float8_e4m3fn or uint8")
+        if k.shape[1] % PALU_KV8_BLOCK:
+            raise ValueError(f"the page size must be a multiple of {PALU_KV8_BLOCK}")
+        shape = (k.shape[0], k.shape[1] // PALU_KV8_BLOCK, k.shape[2])
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32 or tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be a float32 tensor [{shape[0]}][{shape[1]}][{shape[2]}]")
+        if any(t.device != k.device for t in (v, k_scale, v_scale)):
+            raise ValueError("codes and scales must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size = int(k.shape[0]), int(k.shape[1])
+        self.heads, self.index = tuple(k.shape[2:]), k.get_device()
+        self._c = palu_kv8_pages(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.n_pages, self.page_size)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, n_kv_heads, head_dim, device="cuda"):
+        """Pages of zeros."""
+        torch = _torch()
+        if page_size % PALU_KV8_BLOCK:
+            raise ValueError(f"the page size must be a multiple of {PALU_KV8_BLOCK}")
+        codes = [torch.zeros((n_pages, page_size, n_kv_heads, head_dim), dtype=torch.uint8, device=device)
+                 .view(torch.float8_e4m3fn) for _ in range(2)]
+        return cls(*codes, *(torch.ones((n_pages, page_size // PALU_KV8_BLOCK, n_kv_heads), device=device)
+                             for _ in range(2)))
+
+    def c_struct(self) -> palu_kv8_pages:
+        return self._c
+
+
+class KVPool:
+    """The pages that a batch's requests hold, and the free ones: device int32 tensors page_table [batch][pages] (row b
+    holds its first held[b] entries), held [batch], free_pages [n_pages], a ring, and state [2]: the place of the first free
+    page in it and how many there are. Made by `empty`, it holds nothing and all pages are free."""
+
+    def __init__(self, page_table, held, free_pages, state, *, page_size):
+        torch = _torch()
+        given = {"page_table": page_table, "held": held, "free_pages": free_pages, "state": state}
+        _require_contiguous(**given)
+        for name, t in given.items():
+            if t.dtype != torch.int32 or t.device != page_table.device:
+                raise ValueError(f"{name} must be an int32 tensor on page_table's device")
+        if page_table.dim() != 2 or held.shape != (page_table.shape[0],) or free_pages.dim() != 1 or state.shape != (2,):
+            raise ValueError("page_table must be [batch][pages], held [batch], free_pages [n_pages] and state [2]")
+        self.page_table, self.held, self.free_pages, self.state = page_table, held, free_pages, state
+        self.batch, self.page_size, self.index = int(held.shape[0]), int(page_size), page_table.get_device()
+        self._c = palu_kv_pool(_ptr(page_table), int(page_table.shape[1]), _ptr(held), _ptr(free_pages), _ptr(state),
+                               int(free_pages.shape[0]), self.page_size)
+
+    @classmethod
+    def empty(cls, batch, table_pages, n_pages, page_size, device="cuda"):
+        torch = _torch()
+        return cls(torch.zeros((batch, table_pages), dtype=torch.int32, device=device),
+                   torch.zeros(batch, dtype=torch.int32, device=device),
+                   torch.arange(n_pages, dtype=torch.int32, device=device),
+                   torch.tensor([0, n_pages], dtype=torch.int32, device=device), page_size=page_size)
+
+    def c_struct(self) -> palu_kv_pool:
+        return self._c
+
+
 class KVRows:
     """The new tokens of a batch and its rows' caches, as palu_kv_rows describes them: device int32 tensors
     row_start [batch + 1], kv_len [batch], page_table [batch][pages] (or None: row b is page b) and positions
@@ -609,18 +722,19 @@ class KVRows:
         if positions is not None and positions.shape != (n_tokens,):
             raise ValueError("positions must hold n_tokens entries")
         self.tensors, self.index = (row_start, kv_len, page_table, positions), row_start.get_device()
-        self.batch, self.n_tokens = batch, int(n_tokens)
+        self.batch, self.n_tokens, self.max_new, self.max_kv_len = batch, int(n_tokens), int(max_new), int(max_kv_len)
         self._c = palu_kv_rows(_ptr(row_start), _ptr(kv_len), _ptr(page_table),
                                0 if page_table is None else int(page_table.shape[1]), _ptr(positions), batch,
-                               self.n_tokens, int(max_new), int(max_kv_len))
+                               self.n_tokens, self.max_new, self.max_kv_len)
 
     def c_struct(self) -> palu_kv_rows:
         return self._c
 
 
 class PagedAttention:
-    """One layer's paged dense KV cache operators: norm_rope, append and attend. Owns one handle and its
-    torch-allocated workspace; calls that may overlap on the GPU need an object each."""
+    """One layer's paged dense KV cache operators: norm_rope, append and attend, over pages of dtype (KVPages) or of 8 bits
+    (KVPages8), and those around a step: plan and verify. Owns one handle and its torch-allocated workspace; calls
+    that may overlap on the GPU need an object each."""
 
     def __init__(self, *, n_heads, n_kv_heads, head_dim, dtype, x_dtype=None, rope_theta=10000.0, norm_eps=1e-6,
                  max_batch=1, max_tokens=1, flags=0, device="cuda", stream=None):
@@ -684,8 +798,8 @@ class PagedAttention:
         return t.data_ptr()
 
     def _batch(self, pages, rows):
-        if pages.heads != (self.n_kv_heads, self.head_dim) or pages.dtype != self.dtype:
-            raise ValueError(f"pages must hold {self.n_kv_heads} heads of {self.head_dim} {self.dtype} values")
+        if pages.heads != (self.n_kv_heads, self.head_dim) or not (type(pages) is KVPages8 or pages.dtype == self.dtype):
+            raise ValueError(f"pages must hold {self.n_kv_heads} heads of {self.head_dim} {self.dtype} values, or of codes")
         if pages.index != self._index or rows.index != self._index:
             raise ValueError(f"pages and rows must be on {self.device}")
 
@@ -713,11 +827,12 @@ class PagedAttention:
                                   self._stream(stream)), "palu_norm_rope")
         return q_out, k_out
 
-    def append(self, pages: KVPages, rows: KVRows, k, v, *, q=None, q_weight=None, k_weight=None, q_out=None,
+    def append(self, pages: KVPages | KVPages8, rows: KVRows, k, v, *, q=None, q_weight=None, k_weight=None, q_out=None,
                stream=None):
         """Writes the new tokens' keys (normed where k_weight is given, rotated at rows' positions or their slots)
         and values [n_tokens][n_kv_heads][head_dim] into the pages, and norms and rotates q into q_out in the same
-        launch. Returns q_out, or None without q."""
+        launch. Pages of 8 bits: the codes of each head's 16 slots get the least scale, a power of two, that holds their new
+        and older tokens; rows append to 16 slots of their own. Returns q_out, or None without q."""
         self._batch(pages, rows)
         N = rows.n_tokens
         kp, ks = self._view("k", k, self.n_kv_heads, self.x_dtype, N)
@@ -732,12 +847,12 @@ class PagedAttention:
                 raise ValueError("q_out must be contiguous")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        check(_lib.palu_append_kv(self.handle, pages._c, rows._c, qp, qs, kp, ks, vp, vs,
-                                  self._weight("q_weight", q_weight), self._weight("k_weight", k_weight), qo,
-                                  self._stream(stream)), "palu_append_kv")
+        call = _lib.palu_append_kv8 if type(pages) is KVPages8 else _lib.palu_append_kv
+        check(call(self.handle, pages._c, rows._c, qp, qs, kp, ks, vp, vs, self._weight("q_weight", q_weight),
+                   self._weight("k_weight", k_weight), qo, self._stream(stream)), call.__name__)
         return q_out
 
-    def attend(self, pages: KVPages, rows: KVRows, q, *, out=None, lse=None, stream=None):
+    def attend(self, pages: KVPages | KVPages8, rows: KVRows, q, *, out=None, lse=None, stream=None):
         """Causal attention of the new tokens' rotated queries q [n_tokens][n_heads][head_dim] over the pages.
         Returns out, of q's shape; lse, when given, is [n_tokens][n_heads] float32."""
         torch = _torch()
@@ -752,9 +867,77 @@ class PagedAttention:
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != (N, self.n_heads) or
                                 lse.device != self.device or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous [{N}][{self.n_heads}] float32 tensor on {self.device}")
-        check(_lib.palu_attend_kv(self.handle, pages._c, rows._c, qp, qs, op, _ptr(lse), self._stream(stream)),
-              "palu_attend_kv")
+        call = _lib.palu_attend_kv8 if type(pages) is KVPages8 else _lib.palu_attend_kv
+        check(call(self.handle, pages._c, rows._c, qp, qs, op, _ptr(lse), self._stream(stream)), call.__name__)
         return out
+
+    def _ints(self, name, t, shape):
+        if t.dtype is not _torch().int32 or t.get_device() != self._index or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def plan(self, pool: KVPool, new, kv_len, rows: KVRows, *, slots=None, held_out=None, state_out=None, stream=None):
+        """Plans a step's rows and pages on the GPU. new [batch] tokens that each row brings (negative: its request has
+        ended, and its pages are free from the next plan on) and kv_len [batch] cached tokens so far; rows, over
+        pool.page_table: its row_start, kv_len (which may be `kv_len`) and, where it has them, positions are written, and
+        slots [n_tokens], the packed tokens' places in the pages. Rows are admitted in order while pages and
+        rows.n_tokens last. held_out and state_out take what pool.held and pool.state become (None: in place)."""
+        row_start, kv_out, table, positions = rows.tensors
+        if table is None or table.data_ptr() != pool.page_table.data_ptr() or table.shape != pool.page_table.shape:
+            raise ValueError("rows must stand over the pool's page table")
+        if pool.index != self._index or rows.index != self._index:
+            raise ValueError(f"pool and rows must be on {self.device}")
+        B = rows.batch
+        check(_lib.palu_plan_kv_rows(
+            self.handle, pool._c, self._ints("new", new, (B,)), self._ints("kv_len", kv_len, (B,)), B, rows.n_tokens,
+            rows.max_new, rows.max_kv_len, row_start.data_ptr(), kv_out.data_ptr(),
+            None if held_out is None else self._ints("held_out", held_out, (B,)),
+            None if state_out is None else self._ints("state_out", state_out, (2,)), _ptr(positions),
+            None if slots is None else self._ints("slots", slots, (rows.n_tokens,)), self._stream(stream)),
+            "palu_plan_kv_rows")
+        return rows
+
+    def verify(self, target, draft_tokens, uniforms, row_start, *, draft=None, kv_len=None, tokens=None, accepted=None,
+               kv_len_out=None, stream=None):
+        """Verifies drafted tokens against the target's probabilities. target [n_tokens][vocab], the rows
+        row_start[b] .. row_start[b + 1] - 1 being request b's, one more than it has drafts; draft_tokens [batch][K],
+        draft [batch][K][vocab] their probabilities in target's dtype (None: the drafts were certain), uniforms
+        [batch][K + 1] in [0, 1). Returns (tokens [batch][K + 1]: accepted drafts, one drawn token, -1; accepted [batch]).
+        kv_len [batch] loses the rejected tokens, into kv_len_out (None: in place)."""
+        torch = _torch()
+        names = {torch.float32: PALU_F32, torch.float16: PALU_F16, torch.bfloat16: PALU_BF16}
+        if target.dim() != 2 or target.dtype not in names or target.get_device() != self._index or \
+                (target.shape[1] > 1 and target.stride(1) != 1):
+            raise ValueError(f"target must be [n_tokens][vocab] of float32, float16 or bfloat16 on {self.device}")
+        N, V = target.shape
+        if draft_tokens.dim() != 2:
+            raise ValueError("draft_tokens must be [batch][K]")
+        B, K = draft_tokens.shape
+        draft_stride = 0
+        if draft is not None:
+            if draft.dtype != target.dtype or draft.get_device() != self._index or draft.shape != (B, K, V):
+                raise ValueError(f"draft must be [{B}][{K}][{V}] {target.dtype} on {self.device}")
+            draft_stride = draft.stride(1) if K > 1 else draft.stride(0) if B > 1 else V
+            if (V > 1 and draft.stride(2) != 1) or (K > 1 and B > 1 and draft.stride(0) != K * draft_stride):
+                raise ValueError("draft: the rows of probabilities must lie evenly apart")
+        if uniforms.dtype != torch.float32 or uniforms.shape != (B, K + 1) or uniforms.get_device() != self._index or \
+                not uniforms.is_contiguous():
+            raise ValueError(f"uniforms must be a contiguous [{B}][{K + 1}] float32 tensor on {self.device}")
+        if tokens is None:
+            tokens = self._empty((B, K + 1), torch.int32, stream)
+        if accepted is None:
+            accepted = self._empty((B,), torch.int32, stream)
+        if kv_len is None and kv_len_out is not None:
+            raise ValueError("kv_len_out without kv_len")
+        lens = None if kv_len is None else self._ints("kv_len", kv_len, (B,))
+        lens_out = lens if kv_len_out is None else self._ints("kv_len_out", kv_len_out, (B,))
+        check(_lib.palu_verify_drafts(
+            self.handle, target.data_ptr(), target.stride(0) if N > 1 else V, _ptr(draft), draft_stride,
+            names[target.dtype], V, self._ints("row_start", row_start, (B + 1,)), B, N,
+            self._ints("draft_tokens", draft_tokens, (B, K)), K, uniforms.data_ptr(),
+            self._ints("tokens", tokens, (B, K + 1)), self._ints("accepted", accepted, (B,)), lens, lens_out,
+            self._stream(stream)), "palu_verify_drafts")
+        return tokens, accepted
 
     def check_device(self, stream=None):
         check(palu_kv_check(self.handle, self._stream(stream)), "palu_kv_check")
