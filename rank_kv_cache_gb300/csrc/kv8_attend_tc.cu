@@ -32,7 +32,7 @@ constexpr int kRegsSoftmax = 192, kRegsOther = 80, kRegsConvert = 48;
 constexpr int kBlocks = kTile / kKv8Block;
 
 template <int DH> struct Lay {
-  // fp16 tiles: 64 elements (128 bytes) of all rows, then the next 64. Code tiles: rows of DH bytes.
+  // fp16 tiles: 64 elements (128 bytes) of all rows, then the next 64. Code tiles: rows of DH bytes, those of 128 swizzled.
   static constexpr int kHalf = kTile * 128;             // 64 elements of 128 rows
   static constexpr int kTileB = kHalf * (DH / 64);
   static constexpr int kCodeB = kTile * DH;
@@ -174,11 +174,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 12) {
     // ------------------------------------------------------------------ converters
-    // 16 codes a lane and step: a warp reads 512 bytes in a row and writes its fp16 rows' two 16-byte halves, those of
-    // the upper 64 elements in the other order, so that eight lanes' writes fall into different banks.
+    // 16 codes a lane and step; a warp takes a group of eight rows and 64 of their columns: eight lanes at a time rows a
+    // and a ^ 5, whose 16-byte chunks lie in different banks both as codes (128-byte swizzle; rows of 64 bytes lie
+    // so without one) and as fp16. All places are a thread's base and constants.
     tc::regs_shrink<kRegsConvert>();
-    constexpr int kCh = DH / 16, kEach = kTile * kCh / 128;      // 16-byte chunks of a row; of a thread
-    const int t = threadIdx.x - 384;
+    constexpr int kHalves = DH / 64, kEach = kTile / 8 * kHalves / 4;   // steps of a warp
+    const int c = lane & 3, a7 = (lane >> 3) ^ (lane & 4 ? 5 : 0);       // a7: row of its group of eight
+    const uint32_t from = DH == 128 ? uint32_t(a7 * 128 + ((c ^ a7) << 4)) : uint32_t(a7 * 64 + (c << 4));
+    const uint32_t to = uint32_t(a7 * 128 + ((2 * c ^ a7) << 4));
+    const int group0 = (warp - 12) * (kEach / kHalves);
     int sc = 0, st = 0, n_k = 0;
     uint32_t par_c = 0, par = 1;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -198,18 +202,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_k;
       }
-      const uint8_t* src = smem + Y::kOffCode + sc * Y::kCodeB + t * 16;
-      uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB;
-      const int ch = t % kCh, upper = ch / 4, c0 = ch * 2 % 8;
+      const uint8_t* src = smem + Y::kOffCode + sc * Y::kCodeB + group0 * 8 * DH;
+      uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB + group0 * 1024;
+      const int valid = info.valid - group0 * 8 - a7;                  // of this thread's rows, those 8 x below it
+      const bool whole = info.valid == kTile;
 #pragma unroll
       for (int x0 = 0; x0 < kEach; x0 += 4) {
         uint4 v[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = *reinterpret_cast<const uint4*>(src + (x0 + x) * 2048);
+        for (int x = 0; x < 4; ++x)
+          v[x] = *reinterpret_cast<const uint4*>(src + (x0 + x) / kHalves * 8 * DH + (from ^ ((x0 + x) % kHalves * 64)));
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if ((x0 + x) / kHalves * 8 >= valid) v[x] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int row = (x0 + x) * (128 / kCh) + t / kCh;
-          if (row >= info.valid) v[x] = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
           uint32_t f[8];
 #pragma unroll
@@ -217,11 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             f[2 * e] = f16_of_codes(uint16_t(w[e]));
             f[2 * e + 1] = f16_of_codes(uint16_t(w[e] >> 16));
           }
-          uint8_t* at = dst + upper * Y::kHalf + row * 128;
-          const int lo = ((c0 ^ (row & 7)) << 4), hi = (((c0 + 1) ^ (row & 7)) << 4);
-          const uint4 f0 = make_uint4(f[0], f[1], f[2], f[3]), f1 = make_uint4(f[4], f[5], f[6], f[7]);
-          *reinterpret_cast<uint4*>(at + (upper ? hi : lo)) = upper ? f1 : f0;
-          *reinterpret_cast<uint4*>(at + (upper ? lo : hi)) = upper ? f0 : f1;
+          uint8_t* at = dst + (x0 + x) % kHalves * Y::kHalf + (x0 + x) / kHalves * 1024;
+          *reinterpret_cast<uint4*>(at + to) = make_uint4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
         }
       }
       tc::fence_async_smem();
@@ -826,8 +833,9 @@ template <int DH, bool BF16> cudaError_t launch_tc(const Kv8AttendArgs& A, const
     const cuuint64_t dims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)(a.pages.n_pages * a.pages.page_size)};
     const cuuint64_t strides[2] = {DH, (cuuint64_t)a.n_kv * DH};
     const cuuint32_t box[3] = {DH, 1, (cuuint32_t)P.box};
-    if (!tma_encode(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !tma_encode(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+    const CUtensorMapSwizzle sw = DH == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (!tma_encode(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.k, dims, strides, box, sw) ||
+        !tma_encode(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.v, dims, strides, box, sw))
       return cudaErrorInvalidValue;
   }
   const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
