@@ -27,8 +27,8 @@ namespace palu {
 namespace {
 
 constexpr int kThreads = 512;            // two softmax warpgroups; two loader warps, MMA and an idle warp; converters
-// Registers: launched with 128 a thread; 256 * 192 + 128 * 80 + 128 * 48 = 512 * 128.
-constexpr int kRegsSoftmax = 192, kRegsOther = 80, kRegsConvert = 48;
+// Registers: launched with 128 a thread; 256 * 192 + 128 * 72 + 128 * 56 = 512 * 128.
+constexpr int kRegsSoftmax = 192, kRegsOther = 72, kRegsConvert = 56;
 constexpr int kBlocks = kTile / kKv8Block;
 
 template <int DH> struct Lay {
@@ -192,6 +192,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&S.code_full[sc], par_c)) break;
       const Info info = S.info[sc];
       if (info.kind == kEnd) break;
+      // the tile's codes are taken while its place is still read by products
+      const uint8_t* src = smem + Y::kOffCode + sc * Y::kCodeB + group0 * 8 * DH;
+      uint4 v[kEach];
+#pragma unroll
+      for (int x = 0; x < kEach; ++x)
+        v[x] = *reinterpret_cast<const uint4*>(src + x / kHalves * 8 * DH + (from ^ (x % kHalves * 64)));
+      if (info.valid != kTile) {
+        const int valid = info.valid - group0 * 8 - a7;                // of this thread's rows, those 8 x below it
+#pragma unroll
+        for (int x = 0; x < kEach; ++x)
+          if (x / kHalves * 8 >= valid) v[x] = make_uint4(0u, 0u, 0u, 0u);
+      }
       if (!wait(&S.empty[st], par)) break;
       if (info.kind == kKeys) {
         if (warp == 12) {
@@ -202,40 +214,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_k;
       }
-      const uint8_t* src = smem + Y::kOffCode + sc * Y::kCodeB + group0 * 8 * DH;
       uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB + group0 * 1024;
-      const int valid = info.valid - group0 * 8 - a7;                  // of this thread's rows, those 8 x below it
-      const bool whole = info.valid == kTile;
 #pragma unroll
-      for (int x0 = 0; x0 < kEach; x0 += 4) {
-        uint4 v[4];
+      for (int x = 0; x < kEach; ++x) {
+        const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+        uint32_t f[8];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          v[x] = *reinterpret_cast<const uint4*>(src + (x0 + x) / kHalves * 8 * DH + (from ^ ((x0 + x) % kHalves * 64)));
-        if (!whole) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if ((x0 + x) / kHalves * 8 >= valid) v[x] = make_uint4(0u, 0u, 0u, 0u);
+        for (int e = 0; e < 4; ++e) {
+          f[2 * e] = f16_of_codes(uint16_t(w[e]));
+          f[2 * e + 1] = f16_of_codes(uint16_t(w[e] >> 16));
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-          uint32_t f[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[2 * e] = f16_of_codes(uint16_t(w[e]));
-            f[2 * e + 1] = f16_of_codes(uint16_t(w[e] >> 16));
-          }
-          uint8_t* at = dst + (x0 + x) % kHalves * Y::kHalf + (x0 + x) / kHalves * 1024;
-          *reinterpret_cast<uint4*>(at + to) = make_uint4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
-        }
+        uint8_t* at = dst + x % kHalves * Y::kHalf + x / kHalves * 1024;
+        *reinterpret_cast<uint4*>(at + to) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(&S.code_empty[sc]);
         tc::mbar_arrive(&S.full[st]);
+        tc::mbar_arrive(&S.code_empty[sc]);
       }
       if (++sc == Y::kCodes) {
         sc = 0;
