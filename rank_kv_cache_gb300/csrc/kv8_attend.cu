@@ -123,48 +123,76 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
     uint8_t* ring = smem + warp * S::kWarp;
     const uint32_t ring_a = smem_u32(ring);
     const int first = t0 + warp * kTok;
-    const int n_it = first < t1 ? (t1 - first + S::kStep - 1) / S::kStep : 0;
     const uint8_t* kb = static_cast<const uint8_t*>(a.pages.k) + h * DH;
     const uint8_t* vb = static_cast<const uint8_t*>(a.pages.v) + h * DH;
     const int64_t tok_stride = (int64_t)a.n_kv * DH;
 
-    // slot of this lane's block of step `it` (-1: past the range, or a page outside the pool)
-    auto slot_of = [&](int it) -> int {
-      const int t = first + it * S::kStep + lane * kKv8Block;
-      if (it >= n_it || lane >= kBlocks || t >= t1) return -1;
-      const int64_t s = kv_slot(R, a.pages, b, t);
-      if (s < 0) record_error(a.err, kCodeDevice, kErrPage, t, b);
-      return int(s);
+    // This lane's block of 16 tokens of the step that is looked up next; its slot, or -1: past the range, or a page
+    // outside the pool. A step is kStep tokens on from the last, so its page is found without a division.
+    const int ps = a.pages.page_size, step_pages = S::kStep / ps, step_rest = S::kStep % ps;
+    int look_t = first + lane * kKv8Block;
+    int look_pg = R.page_table ? look_t / ps : 0, look_off = look_t - look_pg * ps;
+    const int32_t* table = R.page_table ? R.page_table + (int64_t)b * R.table_pages : nullptr;
+    auto slot_next = [&]() -> int {
+      int slot = -1;
+      if (lane < kBlocks && look_t < t1) {
+        int page = b;
+        if (table) page = look_pg < R.table_pages ? table[look_pg] : -1;
+        if (page >= 0 && page < a.pages.n_pages) slot = page * ps + look_off;
+        else record_error(a.err, kCodeDevice, kErrPage, look_t, b);
+      }
+      look_t += S::kStep;
+      if (table) {
+        look_pg += step_pages;
+        look_off += step_rest;
+        if (look_off >= ps) {
+          look_off -= ps;
+          ++look_pg;
+        }
+      } else {
+        look_off += S::kStep;
+      }
+      return slot;
     };
-    auto load = [&](int it, int slot) {
-      if (it < n_it) {
-        const uint32_t st = ring_a + (it % kStages) * 2 * S::kTile;
-        const int rest = t1 - first - it * S::kStep;                 // tokens of the step that are there
-        constexpr int kCh = DH / 16;                                 // 16-byte chunks of a row
+    // a lane copies the 16-byte chunk `ch` of every kRows-th row, from `row0` on: all places are constants apart
+    constexpr int kCh = DH / 16, kRows = 32 / kCh, kPer = kKv8Block / kRows;
+    const int row0_l = lane / kCh, ch = lane % kCh;
+    const int64_t lane_off = (int64_t)row0_l * tok_stride + ch * 16, row_off = kRows * tok_stride;
+    const uint32_t k_to = key_at<DH>(row0_l, ch), v_to = value_at<DH>(row0_l, ch);
+    auto load = [&](int stage, int rest, int slot) {                 // rest: tokens of the step that are there
+      if (rest > 0) {
+        const uint32_t st = ring_a + stage * (2 * S::kTile);
 #pragma unroll
-        for (int x = 0; x < kTok * kCh / 32; ++x) {
-          const int row = (x * 32 + lane) / kCh, ch = lane % kCh;
-          const int s = __shfl_sync(0xffffffffu, slot, row / kKv8Block);
-          const bool in = s >= 0 && row < rest;
-          const int64_t off = in ? (s + row % kKv8Block) * tok_stride + ch * 16 : 0;
-          cp16(st + key_at<DH>(row, ch), kb + off, in ? 16 : 0);
-          cp16(st + S::kTile + value_at<DH>(row, ch), vb + off, in ? 16 : 0);
+        for (int i = 0; i < kBlocks; ++i) {
+          const int s = __shfl_sync(0xffffffffu, slot, i);
+          const int64_t off = s < 0 ? 0 : s * tok_stride + lane_off;
+          const int in = s < 0 ? 0 : rest - i * kKv8Block - row0_l;  // rows of the block that are there, those x kRows below it
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) {
+            const int row = i * kKv8Block + x * kRows;               // and row0_l
+            // the chunk's exchange by the row's low bits: those of row0_l, and for rows of eight chunks bit 2 of 4 x
+            const uint32_t flip = DH == 128 ? uint32_t(row & 4) << 4 : 0u;
+            const int bytes = x * kRows < in ? 16 : 0;
+            const int64_t o = bytes ? off + x * row_off : 0;
+            cp16(st + row * DH + k_to, kb + o, bytes);
+            cp16(st + S::kTile + row * DH + (v_to ^ flip), vb + o, bytes);
+          }
         }
         if (lane < kBlocks) {
           const int64_t off = slot < 0 ? 0 : (int64_t)(slot / kKv8Block) * a.n_kv + h;
-          cp4(smem_u32(&scales[warp][it % kStages][0][lane]), A.k_scale + off, slot < 0 ? 0 : 4);
-          cp4(smem_u32(&scales[warp][it % kStages][1][lane]), A.v_scale + off, slot < 0 ? 0 : 4);
+          cp4(smem_u32(&scales[warp][stage][0][lane]), A.k_scale + off, slot < 0 ? 0 : 4);
+          cp4(smem_u32(&scales[warp][stage][1][lane]), A.v_scale + off, slot < 0 ? 0 : 4);
         }
       }
       cp_commit();
     };
 
-    int next = slot_of(0);
+    int next = slot_next();
 #pragma unroll
     for (int it = 0; it < kStages - 1; ++it) {
       const int cur = next;
-      next = slot_of(it + 1);
-      load(it, cur);
+      next = slot_next();
+      load(it, t1 - first - it * S::kStep, cur);
     }
 
     // Query rows as the A operand: row = lane / 4 and + 8; inner index: lane % 4 has the elements [16 c + 4 w, + 4) of
@@ -209,29 +237,36 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
     }
     const int vis_min = L - n;                                       // every row sees slots up to here
 
-    for (int it = 0; it < n_it; ++it) {
+    int stage = 0;
+    for (int tb = first; tb < t1; tb += S::kStep) {
       {
         const int cur = next;
-        next = slot_of(it + kStages);
-        load(it + kStages - 1, cur);
+        next = slot_next();
+        load(stage == 0 ? kStages - 1 : stage - 1, t1 - tb - (kStages - 1) * S::kStep, cur);
       }
       cp_wait<kStages - 1>();
       __syncwarp();
-      const uint32_t ks = ring_a + (it % kStages) * 2 * S::kTile, vs = ks + S::kTile;
+      const uint32_t ks = ring_a + stage * (2 * S::kTile), vs = ks + S::kTile;
       float s[kNT][4];
 #pragma unroll
-      for (int i = 0; i < kNT; ++i) {
-        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      for (int i = 0; i < kNT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      // four tokens' eights at a time: products in a row belong to different ones
+#pragma unroll
+      for (int i0 = 0; i0 < kNT; i0 += 4) {
 #pragma unroll
         for (int c = 0; c < DH / 64; ++c) {
-          const uint4 v = lds16(ks + key_at<DH>(i * 8 + r0, c * 4 + cp));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = lds16(ks + key_at<DH>((i0 + i) * 8 + r0, c * 4 + cp));
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma<false>(s[i], qf[c * 4 + k], f16_of_codes(uint16_t(w[k])), f16_of_codes(uint16_t(w[k] >> 16)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w = k == 0 ? v[i].x : k == 1 ? v[i].y : k == 2 ? v[i].z : v[i].w;
+              mma<false>(s[i0 + i], qf[c * 4 + k], f16_of_codes(uint16_t(w)), f16_of_codes(uint16_t(w >> 16)));
+            }
         }
       }
-      const int tb = first + it * S::kStep;
       if (tb + kTok > t1 || tb + kTok - 1 > vis_min) {
 #pragma unroll
         for (int i = 0; i < kNT; ++i)
@@ -244,8 +279,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
       float k_s[kBlocks], v_log[kBlocks], v_inv[kBlocks];
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) {
-        k_s[i] = scale_or_one(scales[warp][it % kStages][0][i]);
-        const float z = scale_or_one(scales[warp][it % kStages][1][i]);
+        k_s[i] = scale_or_one(scales[warp][stage][0][i]);
+        const float z = scale_or_one(scales[warp][stage][1][i]);
         v_log[i] = lg2(z);
         v_inv[i] = rcp(z);
       }
@@ -309,6 +344,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
         }
       }
       __syncwarp();
+      stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     cp_wait<0>();
 #pragma unroll
