@@ -22,17 +22,22 @@ namespace palu {
 namespace {
 
 constexpr int kWarps = kFewWarps;
-constexpr int kStages = 3;
 constexpr float kLift = 15.f;            // log2 of the largest weight
 
-template <int DH> struct Sm {
+// RB: the query rows in sixteens, one or two. Two share the fp16 keys and values that a warp has made; their queries stand in
+// shared memory, as the registers hold their outputs.
+template <int DH, int RB> struct Sm {
   static constexpr int kTok = 4096 / DH;                    // tokens a warp takes at once: 32, or 64 of d = 64
   static constexpr int kBlocks = kTok / kKv8Block;
+  static constexpr int kRows = 16 * RB;
+  static constexpr int kStages = 3;
   static constexpr int kStep = kWarps * kTok;
   static constexpr int kTile = kTok * DH;                   // one warp's K (or V) stage
-  static constexpr int kWarp = kStages * 2 * kTile;
-  static constexpr int kBytes = kWarps * kWarp;
-  static_assert(kKvFewRows * 2 * kKvFewMostCtas * 4 <= kBytes && kWarps * kKvFewRows * DH * 4 <= kBytes, "joins");
+  static constexpr int kRing = kStages * 2 * kTile;
+  static constexpr int kOffQ = kWarps * kRing;              // queries in the order of the products' registers
+  static constexpr int kBytes = kOffQ + (RB == 1 ? 0 : RB * DH * 32);
+  // a unit has at most as many pieces as the call aims at CTAs
+  static_assert(kRows * (kKvFewMostCtas + 1) * 4 <= kOffQ && kWarps * kRows * DH * 4 <= kOffQ, "joins");
 };
 
 // Places of 16-byte chunks in a tile. Keys are read as 16 bytes of two tokens by eight lanes, four chunks each; values as
@@ -53,13 +58,14 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-template <int DH, bool BF16>
+template <int DH, bool BF16, int RB>
 __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv8AttendArgs A) {
-  using S = Sm<DH>;
-  constexpr int kTok = S::kTok, kNT = kTok / 8, kBlocks = S::kBlocks;
+  using S = Sm<DH, RB>;
+  constexpr int kTok = S::kTok, kNT = kTok / 8, kBlocks = S::kBlocks, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ FewJoin X;
+  __shared__ FewJoin<kWarps, S::kRows> X;
   __shared__ float scales[kWarps][kStages][2][kBlocks];
+  __shared__ float row_scale[S::kRows];
   const KvAttendArgs& a = A.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const KvRows& R = a.rows;
@@ -113,15 +119,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
     len = (len + np - 1) / np * S::kStep;
     const int t0 = min(L, piece * len), t1 = min(L, t0 + len);
 
-    float o[DH / 16][2][4];
+    float o[RB][DH / 16][2][4], m[RB][2], l[RB][2];
 #pragma unroll
-    for (int i = 0; i < DH / 16; ++i)
+    for (int z = 0; z < RB; ++z) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][0][e] = o[i][1][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[z][i][0][e] = o[z][i][1][e] = 0.f;
+      m[z][0] = m[z][1] = -INFINITY;
+      l[z][0] = l[z][1] = 0.f;
+    }
 
-    uint8_t* ring = smem + warp * S::kWarp;
-    const uint32_t ring_a = smem_u32(ring);
+    const uint32_t ring_a = smem_u32(smem + warp * S::kRing);
     const int first = t0 + warp * kTok;
     const uint8_t* kb = static_cast<const uint8_t*>(a.pages.k) + h * DH;
     const uint8_t* vb = static_cast<const uint8_t*>(a.pages.v) + h * DH;
@@ -198,58 +207,83 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
     // Query rows as the A operand: row = lane / 4 and + 8; inner index: lane % 4 has the elements [16 c + 4 w, + 4) of
     // every 64 in the product w of the four that they take, as a key's chunk gives them.
     const int r0 = lane >> 2, cp = lane & 3;
-    uint32_t qf[DH / 16][4];
-    int vis[2];                                                      // last slot the two query rows see
-    float scale[2];                                                  // log2(e) / sqrt(d), without the row's lift
+    uint32_t qf[DH / 16][4];                                         // RB = 2: of the sixteen that this warp prepares
+    float scale[RB][2];                                              // log2(e) / sqrt(d), without the row's lift
+    uint4* q_s = reinterpret_cast<uint4*>(smem + S::kOffQ) + lane;   // [RB][DH / 16][32 lanes]
+    if (RB == 1 || warp < RB) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int rr = r0 + 8 * x;
-      const bool ok = rr < rows;
-      const int i = rr / a.g, head = h * a.g + rr % a.g;
-      vis[x] = ok ? L - n + i : -1;
-      scale[x] = a.scale_log2;
-      const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
-                                                      (int64_t)(q0 + i) * a.q_stride + head * DH + cp * 16);
+      for (int x = 0; x < 2; ++x) {
+        const int rr = (RB == 1 ? 0 : warp) * 16 + r0 + 8 * x;
+        const bool ok = rr < rows;
+        const int i = rr / a.g, head = h * a.g + rr % a.g;
+        float lift = 1.f;
+        const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
+                                                        (int64_t)(q0 + i) * a.q_stride + head * DH + cp * 16);
 #pragma unroll
-      for (int k = 0; k < DH / 16; ++k) {
-        const uint2 v = ok ? p[k / 4 * 16 + k % 4] : make_uint2(0u, 0u);
-        qf[k][x] = v.x;
-        qf[k][2 + x] = v.y;
+        for (int k = 0; k < DH / 16; ++k) {
+          const uint2 v = ok ? p[k / 4 * 16 + k % 4] : make_uint2(0u, 0u);
+          qf[k][x] = v.x;
+          qf[k][2 + x] = v.y;
+        }
+        if constexpr (BF16) {
+          __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][x])));
+            top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][2 + x])));
+          }
+          float big = fmaxf(__low2float(top), __high2float(top));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          lift = lift_of(big);
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            qf[k][x] = lifted(qf[k][x], lift);
+            qf[k][2 + x] = lifted(qf[k][2 + x], lift);
+          }
+        }
+        scale[0][x] = a.scale_log2 * (1.f / lift);                   // powers of two
+        if (RB > 1 && cp == 0) row_scale[rr] = scale[0][x];
       }
-      if constexpr (BF16) {
-        __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+      if constexpr (RB > 1) {
 #pragma unroll
-        for (int k = 0; k < DH / 16; ++k) {
-          top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][x])));
-          top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][2 + x])));
-        }
-        float big = fmaxf(__low2float(top), __high2float(top));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const float lift = lift_of(big);
-        scale[x] *= 1.f / lift;                                      // powers of two
-#pragma unroll
-        for (int k = 0; k < DH / 16; ++k) {
-          qf[k][x] = lifted(qf[k][x], lift);
-          qf[k][2 + x] = lifted(qf[k][2 + x], lift);
-        }
+        for (int k = 0; k < DH / 16; ++k)
+          q_s[(warp * (DH / 16) + k) * 32] = make_uint4(qf[k][0], qf[k][1], qf[k][2], qf[k][3]);
       }
     }
+    if constexpr (RB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int z = 0; z < RB; ++z) {
+        scale[z][0] = row_scale[z * 16 + r0];
+        scale[z][1] = row_scale[z * 16 + r0 + 8];
+      }
+    }
+    int vis[RB][2];                                                  // last slot the query rows see
+#pragma unroll
+    for (int z = 0; z < RB; ++z)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int rr = z * 16 + r0 + 8 * x;
+        vis[z][x] = rr < rows ? L - n + rr / a.g : -1;
+      }
     const int vis_min = L - n;                                       // every row sees slots up to here
 
     int stage = 0;
     for (int tb = first; tb < t1; tb += S::kStep) {
+      cp_wait<kStages - 2>();
+      __syncwarp();                                                  // the stage is there, the one before it has been read
       {
         const int cur = next;
         next = slot_next();
         load(stage == 0 ? kStages - 1 : stage - 1, t1 - tb - (kStages - 1) * S::kStep, cur);
       }
-      cp_wait<kStages - 1>();
-      __syncwarp();
       const uint32_t ks = ring_a + stage * (2 * S::kTile), vs = ks + S::kTile;
-      float s[kNT][4];
+      float s[RB][kNT][4];
 #pragma unroll
-      for (int i = 0; i < kNT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      for (int z = 0; z < RB; ++z)
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) s[z][i][0] = s[z][i][1] = s[z][i][2] = s[z][i][3] = 0.f;
       // four tokens' eights at a time: products in a row belong to different ones
 #pragma unroll
       for (int i0 = 0; i0 < kNT; i0 += 4) {
@@ -259,142 +293,168 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = lds16(ks + key_at<DH>((i0 + i) * 8 + r0, c * 4 + cp));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k) {
+            uint32_t f[4][2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t w = k == 0 ? v[i].x : k == 1 ? v[i].y : k == 2 ? v[i].z : v[i].w;
-              mma<false>(s[i0 + i], qf[c * 4 + k], f16_of_codes(uint16_t(w)), f16_of_codes(uint16_t(w >> 16)));
+              f[i][0] = f16_of_codes(uint16_t(w));
+              f[i][1] = f16_of_codes(uint16_t(w >> 16));
             }
+#pragma unroll
+            for (int z = 0; z < RB; ++z) {
+              if constexpr (RB == 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma<false>(s[z][i0 + i], qf[c * 4 + k], f[i][0], f[i][1]);
+              } else {
+                const uint4 q4 = q_s[(z * (DH / 16) + c * 4 + k) * 32];
+                const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma<false>(s[z][i0 + i], q, f[i][0], f[i][1]);
+              }
+            }
+          }
         }
       }
       if (tb + kTok > t1 || tb + kTok - 1 > vis_min) {
 #pragma unroll
-        for (int i = 0; i < kNT; ++i)
+        for (int z = 0; z < RB; ++z)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = tb + i * 8 + cp * 2 + (e & 1);
-            if (t >= t1 || t > vis[e >> 1]) s[i][e] = -INFINITY;
-          }
+          for (int i = 0; i < kNT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = tb + i * 8 + cp * 2 + (e & 1);
+              if (t >= t1 || t > vis[z][e >> 1]) s[z][i][e] = -INFINITY;
+            }
       }
       float k_s[kBlocks], v_log[kBlocks], v_inv[kBlocks];
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) {
         k_s[i] = scale_or_one(scales[warp][stage][0][i]);
-        const float z = scale_or_one(scales[warp][stage][1][i]);
-        v_log[i] = lg2(z);
-        v_inv[i] = rcp(z);
+        const float y = scale_or_one(scales[warp][stage][1][i]);
+        v_log[i] = lg2(y);
+        v_inv[i] = rcp(y);
       }
-      float al[2];
+      uint32_t pf[RB][kBlocks][4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float mx = -INFINITY;
+      for (int z = 0; z < RB; ++z) {
+        float al[2];
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-          const float y = fmaxf(fmaxf(s[2 * i][2 * x], s[2 * i][2 * x + 1]), fmaxf(s[2 * i + 1][2 * x], s[2 * i + 1][2 * x + 1]));
-          mx = fmaxf(mx, fmaf(y, scale[x] * k_s[i], v_log[i]));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[x], softmax_base<false>(mx, kLift));
-        const float base = mn == -INFINITY ? 0.f : mn;               // nothing seen yet: every weight is 2^-inf = 0
-        al[x] = ex2(m[x] - base);
-        m[x] = mn;
-        l[x] *= al[x];
+        for (int x = 0; x < 2; ++x) {
+          float mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-          const float c = scale[x] * k_s[i], d = v_log[i] - base;
-          float sum = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[2 * i + e][2 * x] = ex2(fmaf(s[2 * i + e][2 * x], c, d));
-            s[2 * i + e][2 * x + 1] = ex2(fmaf(s[2 * i + e][2 * x + 1], c, d));
-            sum += s[2 * i + e][2 * x] + s[2 * i + e][2 * x + 1];
+          for (int i = 0; i < kBlocks; ++i) {
+            const float y = fmaxf(fmaxf(s[z][2 * i][2 * x], s[z][2 * i][2 * x + 1]),
+                                  fmaxf(s[z][2 * i + 1][2 * x], s[z][2 * i + 1][2 * x + 1]));
+            mx = fmaxf(mx, fmaf(y, scale[z][x] * k_s[i], v_log[i]));
           }
-          l[x] = fmaf(sum, v_inv[i], l[x]);
-        }
-      }
-      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[z][x], softmax_base<false>(mx, kLift));
+          const float base = mn == -INFINITY ? 0.f : mn;             // nothing seen yet: every weight is 2^-inf = 0
+          al[x] = ex2(m[z][x] - base);
+          m[z][x] = mn;
+          l[z][x] *= al[x];
 #pragma unroll
-        for (int i = 0; i < DH / 16; ++i)
+          for (int i = 0; i < kBlocks; ++i) {
+            const float c = scale[z][x] * k_s[i], d = v_log[i] - base;
+            float p[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            o[i][e][0] *= al[0];
-            o[i][e][1] *= al[0];
-            o[i][e][2] *= al[1];
-            o[i][e][3] *= al[1];
+            for (int e = 0; e < 4; ++e) p[e] = ex2(fmaf(s[z][2 * i + e / 2][2 * x + e % 2], c, d));
+            l[z][x] = fmaf((p[0] + p[1]) + (p[2] + p[3]), v_inv[i], l[z][x]);
+            pf[z][i][x] = pack2<false>(p[0], p[1]);
+            pf[z][i][2 + x] = pack2<false>(p[2], p[3]);
           }
+        }
+        if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              o[z][i][e][0] *= al[0];
+              o[z][i][e][1] *= al[0];
+              o[z][i][e][2] *= al[1];
+              o[z][i][e][3] *= al[1];
+            }
+        }
       }
       const int vr = ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
 #pragma unroll
       for (int k = 0; k < kBlocks; ++k) {
-        const uint32_t pf[4] = {pack2<false>(s[2 * k][0], s[2 * k][1]), pack2<false>(s[2 * k][2], s[2 * k][3]),
-                                pack2<false>(s[2 * k + 1][0], s[2 * k + 1][1]),
-                                pack2<false>(s[2 * k + 1][2], s[2 * k + 1][3])};
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) {
           uint32_t f[4];                                             // tokens 0 - 7 and 8 - 15 of two chunks
           ldsm4t(f, vs + value_at<DH>(k * 16 + vr, 2 * i + vc));
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
+          for (int y = 0; y < 2; ++y) {
             // two tokens of an even and an odd column: parted, the even columns are one product, the odd ones another
-            const uint32_t b0 = __byte_perm(f[2 * z], 0u, 0x3120), b1 = __byte_perm(f[2 * z + 1], 0u, 0x3120);
-            mma<false>(o[2 * i + z][0], pf, f16_of_codes(uint16_t(b0)), f16_of_codes(uint16_t(b1)));
-            mma<false>(o[2 * i + z][1], pf, f16_of_codes(uint16_t(b0 >> 16)), f16_of_codes(uint16_t(b1 >> 16)));
+            const uint32_t b0 = __byte_perm(f[2 * y], 0u, 0x3120), b1 = __byte_perm(f[2 * y + 1], 0u, 0x3120);
+            const uint32_t e0 = f16_of_codes(uint16_t(b0)), e1 = f16_of_codes(uint16_t(b1));
+            const uint32_t u0 = f16_of_codes(uint16_t(b0 >> 16)), u1 = f16_of_codes(uint16_t(b1 >> 16));
+#pragma unroll
+            for (int z = 0; z < RB; ++z) {
+              mma<false>(o[z][2 * i + y][0], pf[z][k], e0, e1);
+              mma<false>(o[z][2 * i + y][1], pf[z][k], u0, u1);
+            }
           }
         }
       }
-      __syncwarp();
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     cp_wait<0>();
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-    }
     __syncthreads();
 
     // join the warps: each leaves its output rows in the (now free) ring
-    float* ob = reinterpret_cast<float*>(smem) + warp * kKvFewRows * DH;
-    if (cp == 0) {
-      X.ml[warp][r0] = make_float2(m[0], l[0]);
-      X.ml[warp][r0 + 8] = make_float2(m[1], l[1]);
-    }
+    float* ob = reinterpret_cast<float*>(smem) + warp * S::kRows * DH;
 #pragma unroll
-    for (int i = 0; i < DH / 16; ++i)
+    for (int z = 0; z < RB; ++z)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        *reinterpret_cast<float4*>(ob + (r0 + 8 * x) * DH + i * 16 + cp * 4) =
-            make_float4(o[i][0][2 * x], o[i][1][2 * x], o[i][0][2 * x + 1], o[i][1][2 * x + 1]);
+      for (int x = 0; x < 2; ++x) {
+        const int r = z * 16 + r0 + 8 * x;
+        l[z][x] += __shfl_xor_sync(0xffffffffu, l[z][x], 1);
+        l[z][x] += __shfl_xor_sync(0xffffffffu, l[z][x], 2);
+        if (cp == 0) X.ml[warp][r] = make_float2(m[z][x], l[z][x]);
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i)
+          *reinterpret_cast<float4*>(ob + r * DH + i * 16 + cp * 4) =
+              make_float4(o[z][i][0][2 * x], o[z][i][1][2 * x], o[z][i][0][2 * x + 1], o[z][i][1][2 * x + 1]);
+      }
     __syncthreads();
     finish_piece<DH, BF16>(a, X, smem, q0, rows, h, np, piece, first_slot);
     __syncthreads();                                                 // the joins' space becomes the ring again
   }
 }
 
-template <int DH, bool BF16> cudaError_t prepare_few() {
-  return cudaFuncSetAttribute(kv8_attend_few_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm<DH>::kBytes);
+template <int DH, bool BF16, int RB> cudaError_t prepare_few() {
+  return cudaFuncSetAttribute(kv8_attend_few_kernel<DH, BF16, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Sm<DH, RB>::kBytes);
 }
-template <int DH, bool BF16> cudaError_t launch_few(const Kv8AttendArgs& a, int ctas, cudaStream_t st) {
-  return launch_early(kv8_attend_few_kernel<DH, BF16>, dim3(ctas), kWarps * 32, Sm<DH>::kBytes, st, a);
+template <int DH, bool BF16> cudaError_t prepare_both() {
+  const cudaError_t e = prepare_few<DH, BF16, 1>();
+  return e == cudaSuccess ? prepare_few<DH, BF16, 2>() : e;
+}
+template <int DH, bool BF16, int RB> cudaError_t launch_few(Kv8AttendArgs A, int sm_count, cudaStream_t st) {
+  KvAttendArgs& a = A.a;
+  // the cut aims at the CTAs that the GPU holds; no more are launched than the rows' bounds give steps
+  a.ctas = kKvFewCtas * sm_count < kKvFewMostCtas ? kKvFewCtas * sm_count : kKvFewMostCtas;
+  const int64_t steps = (((int64_t)a.rows.max_kv_len + Sm<DH, RB>::kStep - 1) / Sm<DH, RB>::kStep + 1) * a.rows.batch * a.n_kv;
+  const int grid = steps < a.ctas ? (int)steps : a.ctas;
+  return launch_early(kv8_attend_few_kernel<DH, BF16, RB>, dim3(grid), kWarps * 32, Sm<DH, RB>::kBytes, st, A);
+}
+template <int DH, bool BF16> cudaError_t launch_rows(const Kv8AttendArgs& A, int sm_count, cudaStream_t st) {
+  return A.a.rows.max_new * A.a.g <= 16 ? launch_few<DH, BF16, 1>(A, sm_count, st) : launch_few<DH, BF16, 2>(A, sm_count, st);
 }
 
 }  // namespace
 
 cudaError_t prepare_kv8_attend_few(int head_dim, bool bf16) {
-  if (head_dim == 128) return bf16 ? prepare_few<128, true>() : prepare_few<128, false>();
-  return bf16 ? prepare_few<64, true>() : prepare_few<64, false>();
+  if (head_dim == 128) return bf16 ? prepare_both<128, true>() : prepare_both<128, false>();
+  return bf16 ? prepare_both<64, true>() : prepare_both<64, false>();
 }
 
-cudaError_t launch_kv8_attend_few(Kv8AttendArgs A, int sm_count, cudaStream_t st) {
-  KvAttendArgs& a = A.a;
-  // the cut aims at the CTAs that the GPU holds; no more are launched than the rows' bounds give steps
-  a.ctas = kKvFewCtas * sm_count < kKvFewMostCtas ? kKvFewCtas * sm_count : kKvFewMostCtas;
-  const int step = a.head_dim == 128 ? Sm<128>::kStep : Sm<64>::kStep;
-  const int64_t steps = (((int64_t)a.rows.max_kv_len + step - 1) / step + 1) * a.rows.batch * a.n_kv;
-  const int grid = steps < a.ctas ? (int)steps : a.ctas;
-  if (a.head_dim == 128) return a.bf16 ? launch_few<128, true>(A, grid, st) : launch_few<128, false>(A, grid, st);
-  return a.bf16 ? launch_few<64, true>(A, grid, st) : launch_few<64, false>(A, grid, st);
+cudaError_t launch_kv8_attend_few(const Kv8AttendArgs& A, int sm_count, cudaStream_t st) {
+  if (A.a.head_dim == 128) return A.a.bf16 ? launch_rows<128, true>(A, sm_count, st) : launch_rows<128, false>(A, sm_count, st);
+  return A.a.bf16 ? launch_rows<64, true>(A, sm_count, st) : launch_rows<64, false>(A, sm_count, st);
 }
 
 }  // namespace palu

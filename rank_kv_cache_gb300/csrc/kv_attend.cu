@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attend_few_kernel(const KvA
   using S = Sm<DH>;
   constexpr int kTok = S::kTok, kNT = kTok / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ FewJoin X;
+  __shared__ FewJoin<> X;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvRows& R = a.rows;
   grid_wait();

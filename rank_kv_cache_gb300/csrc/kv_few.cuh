@@ -90,24 +90,25 @@ __device__ __forceinline__ int piece_length(int steps0, int64_t all, int batch, 
 }
 
 constexpr int kFewWarps = 4;             // warps of a CTA
-struct FewJoin {
-  float2 ml[kFewWarps][kKvFewRows];      // of each warp's rows: maximum (log2 units) and sum
-  float wgt[kFewWarps][kKvFewRows];
-  float2 tot[kKvFewRows];
+template <int PARTS = kFewWarps, int ROWS = kKvFewRows> struct FewJoin {
+  float2 ml[PARTS][ROWS];                // of each part's rows: maximum (log2 units) and sum
+  float wgt[PARTS][ROWS];
+  float2 tot[ROWS];
   int last_cta;
 };
 
-// A piece's end: joins the warps' outputs, which stand in shared memory as fp32 [warp][row][d] with their maxima and sums in X
-// (the CTA has met since), and writes the unit's rows or its partial; the last CTA of a cut unit joins its pieces.
-template <int DH, bool BF16>
-__device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin& X, uint8_t* smem, int q0, int rows, int h,
+// A piece's end: joins the outputs of its parts (the warps, or pairs of warps, that took its tokens in turn), which stand in
+// shared memory as fp32 [part][row][d] with their maxima and sums in X (the CTA has met since), and writes the unit's
+// rows or its partial; the last CTA of a cut unit joins its pieces.
+template <int DH, bool BF16, int PARTS, int ROWS>
+__device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin<PARTS, ROWS>& X, uint8_t* smem, int q0, int rows, int h,
                                              int np, int piece, int first_slot) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (threadIdx.x < kKvFewRows) {
+  if (threadIdx.x < ROWS) {
     const int r = threadIdx.x;
     float M = -INFINITY, Lsum = 0.f;
-    for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, X.ml[w][r].x);
-    for (int w = 0; w < kFewWarps; ++w) {
+    for (int w = 0; w < PARTS; ++w) M = fmaxf(M, X.ml[w][r].x);
+    for (int w = 0; w < PARTS; ++w) {
       const float x = M == -INFINITY ? 0.f : ex2(X.ml[w][r].x - M);
       X.wgt[w][r] = x;
       Lsum = fmaf(X.ml[w][r].y, x, Lsum);
@@ -124,13 +125,13 @@ __device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin& X, 
   };
   auto out_at = [&](int r) -> int64_t { return ((int64_t)(q0 + r / a.g) * a.n_heads + h * a.g + r % a.g) * DH; };
   const bool whole = np == 1;
-  float* po = a.part_o + (int64_t)(first_slot + piece) * kKvFewRows * DH;
+  float* po = a.part_o + (int64_t)(first_slot + piece) * ROWS * DH;
   for (int x = tid; x < rows * (DH / 2); x += kFewWarps * 32) {
     const int r = x / (DH / 2), cl = x % (DH / 2) * 2;
     float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int y = 0; y < kFewWarps; ++y) {
-      const float2 u = *reinterpret_cast<const float2*>(of + (y * kKvFewRows + r) * DH + cl);
+    for (int y = 0; y < PARTS; ++y) {
+      const float2 u = *reinterpret_cast<const float2*>(of + (y * ROWS + r) * DH + cl);
       v.x = fmaf(u.x, X.wgt[y][r], v.x);
       v.y = fmaf(u.y, X.wgt[y][r], v.y);
     }
@@ -143,7 +144,7 @@ __device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin& X, 
     }
   }
   if (!whole) {
-    if (tid < rows) a.part_ml[(int64_t)(first_slot + piece) * kKvFewRows + tid] = X.tot[tid];
+    if (tid < rows) a.part_ml[(int64_t)(first_slot + piece) * ROWS + tid] = X.tot[tid];
     __threadfence();
     __syncthreads();
     if (tid == 0) X.last_cta = atomicAdd(&a.counters[first_slot], 1u) == unsigned(np - 1);
@@ -152,7 +153,7 @@ __device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin& X, 
       __threadfence();
       // join the pieces, in their order
       float* wr = reinterpret_cast<float*>(smem);                  // [rows][np] weights
-      auto slot = [&](int k) { return (int64_t)(first_slot + k) * kKvFewRows; };
+      auto slot = [&](int k) { return (int64_t)(first_slot + k) * ROWS; };
       for (int r = warp; r < rows; r += kFewWarps) {
         float M = -INFINITY, Lsum = 0.f;
         for (int k = lane; k < np; k += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot(k) + r]).x);

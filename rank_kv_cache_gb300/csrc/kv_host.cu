@@ -18,7 +18,7 @@ KvLayout kv_layout(const palu_kv_desc& d) {
   L.err = off;
   off = align256(off + 256);
   if (d.dtype != PALU_F32) {
-    const size_t few = (size_t)kPartSlots * kKvFewRows, tc = (size_t)kTcSlots * 2 * kKvTcRows;
+    const size_t few = (size_t)kPartSlots * kKv8FewRows, tc = (size_t)kTcSlots * 2 * kKvTcRows;
     const size_t rows = few > tc ? few : tc;
     L.head = off;
     off = align256(off + sizeof(KvPlanHead));
