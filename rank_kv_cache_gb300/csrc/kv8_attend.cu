@@ -3,11 +3,14 @@
 //   x_t = log2(e) / sqrt(d) s_k(t) q . c_k(t),   o = sum_t 2^x_t s_v(t) c_v(t) / sum_t 2^x_t,   lse = ln sum_t 2^x_t,
 //
 // c the e4m3 codes of slot t, s_k and s_v the scales of its block of 16 slots. The work is cut as for 16-bit caches
-// (kv_attend.cu: units of up to 16 query rows of a key/value head, pieces over all CTAs, four warps with a ring of cp.async
+// (kv_attend.cu: units of up to 32 query rows of a key/value head, pieces over all CTAs, four warps with a ring of cp.async
 // copies each); what differs lies between shared memory and the matrix instructions.
-//   * Codes become fp16 in registers, exactly, two an instruction. The order of a product's inner index is free, so a
-//     lane reads 16 consecutive codes of a key in one access and the queries' registers are loaded to match; of values,
-//     pairs of codes are transposed as if they were 16-bit elements, and each pair parted by one byte permutation.
+//   * The products are turned over: S^T = K Q^T and O^T = V^T P^T, tokens and then columns of the head being the 16 rows of
+//     a matrix instruction (mma.sync m16n8k16) and query rows its 8 columns. So query rows count in eights, one to four
+//     of them (NB), and codes, made fp16 in registers once, serve all.
+//   * Codes become fp16 exactly, two an instruction. The order of a product's inner index is free, so a lane reads 16
+//     consecutive codes of a key in one access and the queries' registers are loaded to match; of values, pairs of codes
+//     are transposed as if they were 16-bit elements, and each pair parted by one byte permutation.
 //   * bf16 queries become fp16, lifted by a power of two of their row so that the largest lies in [2^14, 2^15).
 //   * s_k multiplies 16 scores at once. s_v belongs into the weights of the product with c_v, not into their sum: with
 //     y_t = x_t + log2 s_v(t) and a running maximum M of y, weights are w_t = 2^(y_t - M), o = sum w c_v and
@@ -24,20 +27,19 @@ namespace {
 constexpr int kWarps = kFewWarps;
 constexpr float kLift = 15.f;            // log2 of the largest weight
 
-// RB: the query rows in sixteens, one or two. Two share the fp16 keys and values that a warp has made; their queries stand in
-// shared memory, as the registers hold their outputs.
-template <int DH, int RB> struct Sm {
+// NB: query rows in eights. One leaves registers for three CTAs an SM, whose copies in flight then need fewer stages.
+template <int DH, int NB> struct Sm {
   static constexpr int kTok = 4096 / DH;                    // tokens a warp takes at once: 32, or 64 of d = 64
   static constexpr int kBlocks = kTok / kKv8Block;
-  static constexpr int kRows = 16 * RB;
-  static constexpr int kStages = 3;
+  static constexpr int kRows = 8 * NB;
+  static constexpr int kCtas = NB == 1 ? 3 : 2;             // of an SM
+  static constexpr int kStages = NB == 1 ? 2 : 3;
   static constexpr int kStep = kWarps * kTok;
   static constexpr int kTile = kTok * DH;                   // one warp's K (or V) stage
   static constexpr int kRing = kStages * 2 * kTile;
-  static constexpr int kOffQ = kWarps * kRing;              // queries in the order of the products' registers
-  static constexpr int kBytes = kOffQ + (RB == 1 ? 0 : RB * DH * 32);
+  static constexpr int kBytes = kWarps * kRing;
   // a unit has at most as many pieces as the call aims at CTAs
-  static_assert(kRows * (kKvFewMostCtas + 1) * 4 <= kOffQ && kWarps * kRows * DH * 4 <= kOffQ, "joins");
+  static_assert(kRows * (kKvFewMostCtas + 1) * 4 <= kBytes && kWarps * kRows * DH * 4 <= kBytes, "joins");
 };
 
 // Places of 16-byte chunks in a tile. Keys are read as 16 bytes of two tokens by eight lanes, four chunks each; values as
@@ -58,14 +60,20 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-template <int DH, bool BF16, int RB>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv8AttendArgs A) {
-  using S = Sm<DH, RB>;
-  constexpr int kTok = S::kTok, kNT = kTok / 8, kBlocks = S::kBlocks, kStages = S::kStages;
+// an 8 x 8 matrix of 16-bit elements, two of a row a lane, turned over
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <int DH, bool BF16, int NB>
+__global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_few_kernel(const Kv8AttendArgs A) {
+  using S = Sm<DH, NB>;
+  constexpr int kTok = S::kTok, kBlocks = S::kBlocks, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FewJoin<kWarps, S::kRows> X;
   __shared__ float scales[kWarps][kStages][2][kBlocks];
-  __shared__ float row_scale[S::kRows];
   const KvAttendArgs& a = A.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const KvRows& R = a.rows;
@@ -119,13 +127,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
     len = (len + np - 1) / np * S::kStep;
     const int t0 = min(L, piece * len), t1 = min(L, t0 + len);
 
-    float o[RB][DH / 16][2][4], m[RB][2], l[RB][2];
+    float o[NB][DH / 16][4], m[NB][2], l[NB][2];
 #pragma unroll
-    for (int z = 0; z < RB; ++z) {
+    for (int z = 0; z < NB; ++z) {
 #pragma unroll
-      for (int i = 0; i < DH / 16; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[z][i][0][e] = o[z][i][1][e] = 0.f;
+      for (int i = 0; i < DH / 16; ++i) o[z][i][0] = o[z][i][1] = o[z][i][2] = o[z][i][3] = 0.f;
       m[z][0] = m[z][1] = -INFINITY;
       l[z][0] = l[z][1] = 0.f;
     }
@@ -204,69 +210,49 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
       load(it, t1 - first - it * S::kStep, cur);
     }
 
-    // Query rows as the A operand: row = lane / 4 and + 8; inner index: lane % 4 has the elements [16 c + 4 w, + 4) of
-    // every 64 in the product w of the four that they take, as a key's chunk gives them.
+    // Query rows as the B operand: column lane / 4 of an eight; inner index: lane % 4 has the elements [16 c + 4 w, + 4) of
+    // every 64 in the product w of the four that they take, as a key's chunk gives them. Of scores and outputs a lane has
+    // the columns 2 (lane % 4) and the next.
     const int r0 = lane >> 2, cp = lane & 3;
-    uint32_t qf[DH / 16][4];                                         // RB = 2: of the sixteen that this warp prepares
-    float scale[RB][2];                                              // log2(e) / sqrt(d), without the row's lift
-    uint4* q_s = reinterpret_cast<uint4*>(smem + S::kOffQ) + lane;   // [RB][DH / 16][32 lanes]
-    if (RB == 1 || warp < RB) {
+    uint32_t qf[NB][DH / 16][2];
+    float scale[NB][2];                                              // log2(e) / sqrt(d), without the row's lift
+    int vis[NB][2];                                                  // last slot the query rows see
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int rr = (RB == 1 ? 0 : warp) * 16 + r0 + 8 * x;
-        const bool ok = rr < rows;
-        const int i = rr / a.g, head = h * a.g + rr % a.g;
-        float lift = 1.f;
-        const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
-                                                        (int64_t)(q0 + i) * a.q_stride + head * DH + cp * 16);
+    for (int z = 0; z < NB; ++z) {
+      const int rr = z * 8 + r0;
+      const bool ok = rr < rows;
+      const int head = h * a.g + rr % a.g;
+      const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
+                                                      (int64_t)(q0 + rr / a.g) * a.q_stride + head * DH + cp * 16);
 #pragma unroll
-        for (int k = 0; k < DH / 16; ++k) {
-          const uint2 v = ok ? p[k / 4 * 16 + k % 4] : make_uint2(0u, 0u);
-          qf[k][x] = v.x;
-          qf[k][2 + x] = v.y;
-        }
-        if constexpr (BF16) {
-          __nv_bfloat162 top = __float2bfloat162_rn(0.f);
-#pragma unroll
-          for (int k = 0; k < DH / 16; ++k) {
-            top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][x])));
-            top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][2 + x])));
-          }
-          float big = fmaxf(__low2float(top), __high2float(top));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          lift = lift_of(big);
-#pragma unroll
-          for (int k = 0; k < DH / 16; ++k) {
-            qf[k][x] = lifted(qf[k][x], lift);
-            qf[k][2 + x] = lifted(qf[k][2 + x], lift);
-          }
-        }
-        scale[0][x] = a.scale_log2 * (1.f / lift);                   // powers of two
-        if (RB > 1 && cp == 0) row_scale[rr] = scale[0][x];
+      for (int k = 0; k < DH / 16; ++k) {
+        const uint2 v = ok ? p[k / 4 * 16 + k % 4] : make_uint2(0u, 0u);
+        qf[z][k][0] = v.x;
+        qf[z][k][1] = v.y;
       }
-      if constexpr (RB > 1) {
+      float lift = 1.f;
+      if constexpr (BF16) {
+        __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
         for (int k = 0; k < DH / 16; ++k)
-          q_s[(warp * (DH / 16) + k) * 32] = make_uint4(qf[k][0], qf[k][1], qf[k][2], qf[k][3]);
-      }
-    }
-    if constexpr (RB > 1) {
-      __syncthreads();
 #pragma unroll
-      for (int z = 0; z < RB; ++z) {
-        scale[z][0] = row_scale[z * 16 + r0];
-        scale[z][1] = row_scale[z * 16 + r0 + 8];
-      }
-    }
-    int vis[RB][2];                                                  // last slot the query rows see
+          for (int e = 0; e < 2; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[z][k][e])));
+        float big = fmaxf(__low2float(top), __high2float(top));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        lift = lift_of(big);
 #pragma unroll
-    for (int z = 0; z < RB; ++z)
+        for (int k = 0; k < DH / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) qf[z][k][e] = lifted(qf[z][k][e], lift);
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int rr = z * 16 + r0 + 8 * x;
-        vis[z][x] = rr < rows ? L - n + rr / a.g : -1;
+        const int r = z * 8 + 2 * cp + x;
+        scale[z][x] = a.scale_log2 * (1.f / __shfl_sync(0xffffffffu, lift, (2 * cp + x) * 4));   // powers of two
+        vis[z][x] = r < rows ? L - n + r / a.g : -1;
       }
+    }
     const int vis_min = L - n;                                       // every row sees slots up to here
 
     int stage = 0;
@@ -279,52 +265,48 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
         load(stage == 0 ? kStages - 1 : stage - 1, t1 - tb - (kStages - 1) * S::kStep, cur);
       }
       const uint32_t ks = ring_a + stage * (2 * S::kTile), vs = ks + S::kTile;
-      float s[RB][kNT][4];
+      float s[NB][kBlocks][4];                                       // of tokens r0 and r0 + 8, two query rows each
 #pragma unroll
-      for (int z = 0; z < RB; ++z)
+      for (int z = 0; z < NB; ++z)
 #pragma unroll
-        for (int i = 0; i < kNT; ++i) s[z][i][0] = s[z][i][1] = s[z][i][2] = s[z][i][3] = 0.f;
-      // four tokens' eights at a time: products in a row belong to different ones
+        for (int i = 0; i < kBlocks; ++i) s[z][i][0] = s[z][i][1] = s[z][i][2] = s[z][i][3] = 0.f;
+      // two blocks at a time: products in a row belong to different ones
 #pragma unroll
-      for (int i0 = 0; i0 < kNT; i0 += 4) {
+      for (int i0 = 0; i0 < kBlocks; i0 += 2) {
 #pragma unroll
         for (int c = 0; c < DH / 64; ++c) {
-          uint4 v[4];
+          uint4 v[2][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = lds16(ks + key_at<DH>((i0 + i) * 8 + r0, c * 4 + cp));
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) v[i][x] = lds16(ks + key_at<DH>((i0 + i) * 16 + x * 8 + r0, c * 4 + cp));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t f[4][2];
+            uint32_t f[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t w = k == 0 ? v[i].x : k == 1 ? v[i].y : k == 2 ? v[i].z : v[i].w;
-              f[i][0] = f16_of_codes(uint16_t(w));
-              f[i][1] = f16_of_codes(uint16_t(w >> 16));
-            }
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int z = 0; z < RB; ++z) {
-              if constexpr (RB == 1) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mma<false>(s[z][i0 + i], qf[c * 4 + k], f[i][0], f[i][1]);
-              } else {
-                const uint4 q4 = q_s[(z * (DH / 16) + c * 4 + k) * 32];
-                const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mma<false>(s[z][i0 + i], q, f[i][0], f[i][1]);
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t w = k == 0 ? v[i][x].x : k == 1 ? v[i][x].y : k == 2 ? v[i][x].z : v[i][x].w;
+                f[i][x] = f16_of_codes(uint16_t(w));
+                f[i][2 + x] = f16_of_codes(uint16_t(w >> 16));
               }
-            }
+#pragma unroll
+            for (int z = 0; z < NB; ++z)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) mma<false>(s[z][i0 + i], f[i], qf[z][c * 4 + k][0], qf[z][c * 4 + k][1]);
           }
         }
       }
       if (tb + kTok > t1 || tb + kTok - 1 > vis_min) {
 #pragma unroll
-        for (int z = 0; z < RB; ++z)
+        for (int z = 0; z < NB; ++z)
 #pragma unroll
-          for (int i = 0; i < kNT; ++i)
+          for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int t = tb + i * 8 + cp * 2 + (e & 1);
-              if (t >= t1 || t > vis[z][e >> 1]) s[z][i][e] = -INFINITY;
+              const int t = tb + i * 16 + (e >> 1) * 8 + r0;
+              if (t >= t1 || t > vis[z][e & 1]) s[z][i][e] = -INFINITY;
             }
       }
       float k_s[kBlocks], v_log[kBlocks], v_inv[kBlocks];
@@ -335,21 +317,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
         v_log[i] = lg2(y);
         v_inv[i] = rcp(y);
       }
-      uint32_t pf[RB][kBlocks][4];
+      uint32_t pf[NB][kBlocks][2];
 #pragma unroll
-      for (int z = 0; z < RB; ++z) {
+      for (int z = 0; z < NB; ++z) {
         float al[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < kBlocks; ++i) {
-            const float y = fmaxf(fmaxf(s[z][2 * i][2 * x], s[z][2 * i][2 * x + 1]),
-                                  fmaxf(s[z][2 * i + 1][2 * x], s[z][2 * i + 1][2 * x + 1]));
-            mx = fmaxf(mx, fmaf(y, scale[z][x] * k_s[i], v_log[i]));
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          for (int i = 0; i < kBlocks; ++i)
+            mx = fmaxf(mx, fmaf(fmaxf(s[z][i][x], s[z][i][2 + x]), scale[z][x] * k_s[i], v_log[i]));
+#pragma unroll
+          for (int e = 4; e < 32; e *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
           const float mn = fmaxf(m[z][x], softmax_base<false>(mx, kLift));
           const float base = mn == -INFINITY ? 0.f : mn;             // nothing seen yet: every weight is 2^-inf = 0
           al[x] = ex2(m[z][x] - base);
@@ -358,24 +337,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i) {
             const float c = scale[z][x] * k_s[i], d = v_log[i] - base;
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = ex2(fmaf(s[z][2 * i + e / 2][2 * x + e % 2], c, d));
-            l[z][x] = fmaf((p[0] + p[1]) + (p[2] + p[3]), v_inv[i], l[z][x]);
-            pf[z][i][x] = pack2<false>(p[0], p[1]);
-            pf[z][i][2 + x] = pack2<false>(p[2], p[3]);
+            s[z][i][x] = ex2(fmaf(s[z][i][x], c, d));
+            s[z][i][2 + x] = ex2(fmaf(s[z][i][2 + x], c, d));
+            l[z][x] = fmaf(s[z][i][x] + s[z][i][2 + x], v_inv[i], l[z][x]);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          pf[z][i][0] = turned(pack2<false>(s[z][i][0], s[z][i][1]));
+          pf[z][i][1] = turned(pack2<false>(s[z][i][2], s[z][i][3]));
         }
         if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
-          for (int i = 0; i < DH / 16; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              o[z][i][e][0] *= al[0];
-              o[z][i][e][1] *= al[0];
-              o[z][i][e][2] *= al[1];
-              o[z][i][e][3] *= al[1];
-            }
+          for (int i = 0; i < DH / 16; ++i) {
+            o[z][i][0] *= al[0];
+            o[z][i][1] *= al[1];
+            o[z][i][2] *= al[0];
+            o[z][i][3] *= al[1];
+          }
         }
       }
       const int vr = ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
@@ -387,15 +366,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
           ldsm4t(f, vs + value_at<DH>(k * 16 + vr, 2 * i + vc));
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            // two tokens of an even and an odd column: parted, the even columns are one product, the odd ones another
+            // two tokens of an even and an odd column, parted: the even columns are a product's rows 0 to 7, the odd 8 to 15
             const uint32_t b0 = __byte_perm(f[2 * y], 0u, 0x3120), b1 = __byte_perm(f[2 * y + 1], 0u, 0x3120);
-            const uint32_t e0 = f16_of_codes(uint16_t(b0)), e1 = f16_of_codes(uint16_t(b1));
-            const uint32_t u0 = f16_of_codes(uint16_t(b0 >> 16)), u1 = f16_of_codes(uint16_t(b1 >> 16));
+            const uint32_t v[4] = {f16_of_codes(uint16_t(b0)), f16_of_codes(uint16_t(b0 >> 16)),
+                                   f16_of_codes(uint16_t(b1)), f16_of_codes(uint16_t(b1 >> 16))};
 #pragma unroll
-            for (int z = 0; z < RB; ++z) {
-              mma<false>(o[z][2 * i + y][0], pf[z][k], e0, e1);
-              mma<false>(o[z][2 * i + y][1], pf[z][k], u0, u1);
-            }
+            for (int z = 0; z < NB; ++z) mma<false>(o[z][2 * i + y], v, pf[z][k][0], pf[z][k][1]);
           }
         }
       }
@@ -407,17 +383,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
     // join the warps: each leaves its output rows in the (now free) ring
     float* ob = reinterpret_cast<float*>(smem) + warp * S::kRows * DH;
 #pragma unroll
-    for (int z = 0; z < RB; ++z)
+    for (int z = 0; z < NB; ++z)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int r = z * 16 + r0 + 8 * x;
-        l[z][x] += __shfl_xor_sync(0xffffffffu, l[z][x], 1);
-        l[z][x] += __shfl_xor_sync(0xffffffffu, l[z][x], 2);
-        if (cp == 0) X.ml[warp][r] = make_float2(m[z][x], l[z][x]);
+        const int r = z * 8 + 2 * cp + x;
+#pragma unroll
+        for (int e = 4; e < 32; e *= 2) l[z][x] += __shfl_xor_sync(0xffffffffu, l[z][x], e);
+        if (r0 == 0) X.ml[warp][r] = make_float2(m[z][x], l[z][x]);
 #pragma unroll
         for (int i = 0; i < DH / 16; ++i)
-          *reinterpret_cast<float4*>(ob + r * DH + i * 16 + cp * 4) =
-              make_float4(o[z][i][0][2 * x], o[z][i][1][2 * x], o[z][i][0][2 * x + 1], o[z][i][1][2 * x + 1]);
+          *reinterpret_cast<float2*>(ob + r * DH + i * 16 + 2 * r0) = make_float2(o[z][i][x], o[z][i][2 + x]);
       }
     __syncthreads();
     finish_piece<DH, BF16>(a, X, smem, q0, rows, h, np, piece, first_slot);
@@ -425,31 +400,41 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_attend_few_kernel(const Kv
   }
 }
 
-template <int DH, bool BF16, int RB> cudaError_t prepare_few() {
-  return cudaFuncSetAttribute(kv8_attend_few_kernel<DH, BF16, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Sm<DH, RB>::kBytes);
+template <int DH, bool BF16, int NB> cudaError_t prepare_few() {
+  return cudaFuncSetAttribute(kv8_attend_few_kernel<DH, BF16, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Sm<DH, NB>::kBytes);
 }
-template <int DH, bool BF16> cudaError_t prepare_both() {
-  const cudaError_t e = prepare_few<DH, BF16, 1>();
-  return e == cudaSuccess ? prepare_few<DH, BF16, 2>() : e;
+template <int DH, bool BF16> cudaError_t prepare_all() {
+  cudaError_t e = prepare_few<DH, BF16, 1>();
+  if (e == cudaSuccess) e = prepare_few<DH, BF16, 2>();
+  if (e == cudaSuccess) e = prepare_few<DH, BF16, 3>();
+  if (e == cudaSuccess) e = prepare_few<DH, BF16, 4>();
+  return e;
 }
-template <int DH, bool BF16, int RB> cudaError_t launch_few(Kv8AttendArgs A, int sm_count, cudaStream_t st) {
+template <int DH, bool BF16, int NB> cudaError_t launch_few(Kv8AttendArgs A, int sm_count, cudaStream_t st) {
+  using S = Sm<DH, NB>;
   KvAttendArgs& a = A.a;
   // the cut aims at the CTAs that the GPU holds; no more are launched than the rows' bounds give steps
-  a.ctas = kKvFewCtas * sm_count < kKvFewMostCtas ? kKvFewCtas * sm_count : kKvFewMostCtas;
-  const int64_t steps = (((int64_t)a.rows.max_kv_len + Sm<DH, RB>::kStep - 1) / Sm<DH, RB>::kStep + 1) * a.rows.batch * a.n_kv;
+  a.ctas = S::kCtas * sm_count < kKvFewMostCtas ? S::kCtas * sm_count : kKvFewMostCtas;
+  const int64_t steps = (((int64_t)a.rows.max_kv_len + S::kStep - 1) / S::kStep + 1) * a.rows.batch * a.n_kv;
   const int grid = steps < a.ctas ? (int)steps : a.ctas;
-  return launch_early(kv8_attend_few_kernel<DH, BF16, RB>, dim3(grid), kWarps * 32, Sm<DH, RB>::kBytes, st, A);
+  return launch_early(kv8_attend_few_kernel<DH, BF16, NB>, dim3(grid), kWarps * 32, S::kBytes, st, A);
 }
 template <int DH, bool BF16> cudaError_t launch_rows(const Kv8AttendArgs& A, int sm_count, cudaStream_t st) {
-  return A.a.rows.max_new * A.a.g <= 16 ? launch_few<DH, BF16, 1>(A, sm_count, st) : launch_few<DH, BF16, 2>(A, sm_count, st);
+  switch ((A.a.rows.max_new * A.a.g + 7) / 8) {
+    case 0:
+    case 1: return launch_few<DH, BF16, 1>(A, sm_count, st);
+    case 2: return launch_few<DH, BF16, 2>(A, sm_count, st);
+    case 3: return launch_few<DH, BF16, 3>(A, sm_count, st);
+    default: return launch_few<DH, BF16, 4>(A, sm_count, st);
+  }
 }
 
 }  // namespace
 
 cudaError_t prepare_kv8_attend_few(int head_dim, bool bf16) {
-  if (head_dim == 128) return bf16 ? prepare_both<128, true>() : prepare_both<128, false>();
-  return bf16 ? prepare_both<64, true>() : prepare_both<64, false>();
+  if (head_dim == 128) return bf16 ? prepare_all<128, true>() : prepare_all<128, false>();
+  return bf16 ? prepare_all<64, true>() : prepare_all<64, false>();
 }
 
 cudaError_t launch_kv8_attend_few(const Kv8AttendArgs& A, int sm_count, cudaStream_t st) {
