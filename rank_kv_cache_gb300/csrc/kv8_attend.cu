@@ -3,10 +3,10 @@
 //   x_t = log2(e) / sqrt(d) s_k(t) q . c_k(t),   o = sum_t 2^x_t s_v(t) c_v(t) / sum_t 2^x_t,   lse = ln sum_t 2^x_t,
 //
 // c the e4m3 codes of slot t, s_k and s_v the scales of its block of 16 slots. The work is cut as for 16-bit caches
-// (kv_attend.cu: units of up to 32 query rows of a key/value head, pieces over all CTAs, four warps with a ring of cp.async
+// (kv_attend.cu: units of up to 24 query rows of a key/value head, pieces over all CTAs, four warps with a ring of cp.async
 // copies each); what differs lies between shared memory and the matrix instructions.
 //   * The products are turned over: S^T = K Q^T and O^T = V^T P^T, tokens and then columns of the head being the 16 rows of
-//     a matrix instruction (mma.sync m16n8k16) and query rows its 8 columns. So query rows count in eights, one to four
+//     a matrix instruction (mma.sync m16n8k16) and query rows its 8 columns. So query rows count in eights, one to three
 //     of them (NB), and codes, made fp16 in registers once, serve all.
 //   * Codes become fp16 exactly, two an instruction. The order of a product's inner index is free, so a lane reads 16
 //     consecutive codes of a key in one access and the queries' registers are loaded to match; of values, pairs of codes
@@ -37,9 +37,11 @@ template <int DH, int NB> struct Sm {
   static constexpr int kStep = kWarps * kTok;
   static constexpr int kTile = kTok * DH;                   // one warp's K (or V) stage
   static constexpr int kRing = kStages * 2 * kTile;
-  static constexpr int kBytes = kWarps * kRing;
+  static constexpr int kOffQ = kWarps * kRing;
+  static constexpr bool kQueries = NB > 2;                  // their queries stand in shared memory: registers are short
+  static constexpr int kBytes = kOffQ + (kQueries ? kRows * DH * 2 : 0);
   // a unit has at most as many pieces as the call aims at CTAs
-  static_assert(kRows * (kKvFewMostCtas + 1) * 4 <= kBytes && kWarps * kRows * DH * 4 <= kBytes, "joins");
+  static_assert(kRows * (kKvFewMostCtas + 1) * 4 <= kOffQ && kWarps * kRows * DH * 4 <= kOffQ, "joins");
 };
 
 // Places of 16-byte chunks in a tile. Keys are read as 16 bytes of two tokens by eight lanes, four chunks each; values as
@@ -214,12 +216,13 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
     // every 64 in the product w of the four that they take, as a key's chunk gives them. Of scores and outputs a lane has
     // the columns 2 (lane % 4) and the next.
     const int r0 = lane >> 2, cp = lane & 3;
-    uint32_t qf[NB][DH / 16][2];
+    uint32_t qf[S::kQueries ? 1 : NB][DH / 16][2];
+    uint2* q_s = reinterpret_cast<uint2*>(smem + S::kOffQ) + lane;   // [NB][DH / 16][32 lanes]
     float scale[NB][2];                                              // log2(e) / sqrt(d), without the row's lift
     int vis[NB][2];                                                  // last slot the query rows see
 #pragma unroll
     for (int z = 0; z < NB; ++z) {
-      const int rr = z * 8 + r0;
+      const int rr = z * 8 + r0, zq = S::kQueries ? 0 : z;
       const bool ok = rr < rows;
       const int head = h * a.g + rr % a.g;
       const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
@@ -227,8 +230,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
 #pragma unroll
       for (int k = 0; k < DH / 16; ++k) {
         const uint2 v = ok ? p[k / 4 * 16 + k % 4] : make_uint2(0u, 0u);
-        qf[z][k][0] = v.x;
-        qf[z][k][1] = v.y;
+        qf[zq][k][0] = v.x;
+        qf[zq][k][1] = v.y;
       }
       float lift = 1.f;
       if constexpr (BF16) {
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
 #pragma unroll
         for (int k = 0; k < DH / 16; ++k)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[z][k][e])));
+          for (int e = 0; e < 2; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qf[zq][k][e])));
         float big = fmaxf(__low2float(top), __high2float(top));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -244,7 +247,13 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
 #pragma unroll
         for (int k = 0; k < DH / 16; ++k)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) qf[z][k][e] = lifted(qf[z][k][e], lift);
+          for (int e = 0; e < 2; ++e) qf[zq][k][e] = lifted(qf[zq][k][e], lift);
+      }
+      if constexpr (S::kQueries) {
+        if (warp == z % kWarps) {
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) q_s[(z * (DH / 16) + k) * 32] = make_uint2(qf[0][k][0], qf[0][k][1]);
+        }
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -253,6 +262,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
         vis[z][x] = r < rows ? L - n + r / a.g : -1;
       }
     }
+    if constexpr (S::kQueries) __syncthreads();
     const int vis_min = L - n;                                       // every row sees slots up to here
 
     int stage = 0;
@@ -292,9 +302,13 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
                 f[i][2 + x] = f16_of_codes(uint16_t(w >> 16));
               }
 #pragma unroll
-            for (int z = 0; z < NB; ++z)
+            for (int z = 0; z < NB; ++z) {
+              uint2 q;
+              if constexpr (S::kQueries) q = q_s[(z * (DH / 16) + c * 4 + k) * 32];
+              else q = make_uint2(qf[z][c * 4 + k][0], qf[z][c * 4 + k][1]);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) mma<false>(s[z][i0 + i], f[i], qf[z][c * 4 + k][0], qf[z][c * 4 + k][1]);
+              for (int i = 0; i < 2; ++i) mma<false>(s[z][i0 + i], f[i], q.x, q.y);
+            }
           }
         }
       }
@@ -408,7 +422,6 @@ template <int DH, bool BF16> cudaError_t prepare_all() {
   cudaError_t e = prepare_few<DH, BF16, 1>();
   if (e == cudaSuccess) e = prepare_few<DH, BF16, 2>();
   if (e == cudaSuccess) e = prepare_few<DH, BF16, 3>();
-  if (e == cudaSuccess) e = prepare_few<DH, BF16, 4>();
   return e;
 }
 template <int DH, bool BF16, int NB> cudaError_t launch_few(Kv8AttendArgs A, int sm_count, cudaStream_t st) {
@@ -425,8 +438,7 @@ template <int DH, bool BF16> cudaError_t launch_rows(const Kv8AttendArgs& A, int
     case 0:
     case 1: return launch_few<DH, BF16, 1>(A, sm_count, st);
     case 2: return launch_few<DH, BF16, 2>(A, sm_count, st);
-    case 3: return launch_few<DH, BF16, 3>(A, sm_count, st);
-    default: return launch_few<DH, BF16, 4>(A, sm_count, st);
+    default: return launch_few<DH, BF16, 3>(A, sm_count, st);
   }
 }
 

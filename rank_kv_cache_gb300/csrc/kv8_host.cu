@@ -85,7 +85,7 @@ palu_status_t palu_attend_kv8(palu_kv_t h, const palu_kv8_pages* pages, const pa
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if ((int64_t)a.rows.max_new * a.g <= kKv8FewRows) {
-    // 32 query rows hold every row's tokens: the few-row kernel streams the cache once
+    // 24 query rows hold every row's tokens: the few-row kernel streams the cache once
     e = launch_kv8_attend_few(A, h->sm_count, s);
   } else {
     e = launch_kv8_attend_tc(A, tc_plan(h, *rows), s);
