@@ -9,9 +9,9 @@
 //
 // A group is a row's new tokens of one block. A CTA takes the groups that begin among 16 packed tokens: one or two of a
 // prompt, 16 of a decode step. It computes the sines and cosines of their tokens (31 at most) once, in shared memory;
-// then a warp takes one group and head at a time: the 16 tokens' halves of a head stay in registers (16 elements of a
-// token a lane, as in kv_rope.cu) from the loads over norm, rotation and the maximum to the codes. Old codes are read
-// only where a scale grows.
+// then a warp takes one group and head at a time. The 16 tokens' rows of a head come by cp.async while the warp works at
+// the ones before them; their halves then stay in registers (16 elements of a token a lane, as in kv_rope.cu) over norm,
+// rotation and the maximum to the codes. Old codes are read only where a scale grows.
 //
 // Bound: HBM; each input is read once and each output written once.
 #include "kv8.h"
@@ -20,7 +20,7 @@
 namespace palu {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32, kCtas = 4;   // CTAs of an SM
 constexpr int kChunk = kKv8Block;          // packed tokens whose groups a CTA takes
 
 struct Group {
@@ -29,8 +29,9 @@ struct Group {
   int slot0;        // its slot in the pages, or -1
 };
 
-template <int DH> struct Sm {
+template <int DH, int E> struct Sm {              // E: bytes of an element as it comes
   static constexpr int kHalf = DH / 2, kTokens = 2 * kChunk - 1;
+  uint8_t rows[kWarps][2][kKv8Block * DH * E];    // a warp's task and its next one's
   float cs[kTokens][kHalf], sn[kTokens][kHalf];   // pairs 8 j + e of a token at (e / 4) (kHalf / 2) + 4 j + e % 4
   Group group[kChunk];
   int groups, t0, n;                              // the groups' tokens: t0 .. t0 + n - 1
@@ -70,14 +71,20 @@ __device__ __noinline__ void check_rows(const KvRopeArgs& a) {
   }
 }
 
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
 template <typename TI, typename TO, int DH>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvRopeArgs a, const Kv8Pages P,
-                                                              const __grid_constant__ KvFreq f) {
+__global__ void __launch_bounds__(kThreads, kCtas) kv8_append_kernel(const KvRopeArgs a, const Kv8Pages P,
+                                                                     const __grid_constant__ KvFreq f) {
   constexpr int kLanes = DH / 16;          // lanes of a token's head
   constexpr int kTok = 32 / kLanes;        // tokens that a warp takes at once
   constexpr int kPass = kKv8Block / kTok;
   constexpr int kQuarter = DH / 4;
-  __shared__ __align__(16) Sm<DH> S;
+  constexpr int kRow = DH * sizeof(TI), kCh = kRow / 16;   // bytes and 16-byte chunks of a row
+  extern __shared__ __align__(16) uint8_t smem[];
+  Sm<DH, sizeof(TI)>& S = *reinterpret_cast<Sm<DH, sizeof(TI)>*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane % kLanes, tl = lane / kLanes;
   const KvRows& R = a.rows;
   grid_wait();
@@ -126,7 +133,33 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvRopeArgs a
     }
   }
   __syncthreads();
-  const int groups = S.groups, t0 = S.t0;
+  const int groups = S.groups, t0 = S.t0, tasks = groups * heads;
+  // a task: head h of a side (queries, keys, values) of a group
+  auto side_of = [&](int task, int& h) {
+    h = task % heads;
+    const int side = h < a.heads[0] ? 0 : h < a.heads[0] + a.heads[1] ? 1 : 2;
+    h -= side == 0 ? 0 : side == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
+    return side;
+  };
+  auto fetch = [&](int task, int stage) {
+    if (task < tasks) {
+      const Group& g = S.group[task / heads];
+      int h;
+      const int side = side_of(task, h), n = g.n;
+      const void* src = side == 0 ? a.src[0] : side == 1 ? a.src[1] : a.src[2];
+      const int64_t pitch = (side == 0 ? a.src_stride[0] : side == 1 ? a.src_stride[1] : a.src_stride[2]) * (int64_t)sizeof(TI);
+      const uint8_t* x = static_cast<const uint8_t*>(src) + g.t0 * pitch + h * kRow;
+#pragma unroll
+      for (int i = 0; i < kKv8Block * kCh / 32; ++i) {
+        const int tok = (i * 32 + lane) / kCh, c = (i * 32 + lane) % kCh;
+        if (tok < n) cp16(&S.rows[warp][stage][tok * kRow + c * 16], x + tok * pitch + c * 16);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int step = parts * kWarps;
+  int task = part * kWarps + warp, stage = 0;
+  fetch(task, 0);                                  // under way while the angles are computed
 
   if (a.rotate) {
     const int n = S.n;
@@ -148,28 +181,20 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvRopeArgs a
     __syncthreads();
   }
 
-  for (int task = part * kWarps + warp; task < groups * heads; task += parts * kWarps) {
+  for (; task < tasks; task += step, stage ^= 1) {
     const Group g = S.group[task / heads];
-    int h = task % heads;
-    const int side = h < a.heads[0] ? 0 : h < a.heads[0] + a.heads[1] ? 1 : 2;
-    h -= side == 0 ? 0 : side == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
-    const TI* x = static_cast<const TI*>(a.src[side]) + (int64_t)g.t0 * a.src_stride[side] + (h * DH + j * 8);
-    Vec8<TI> lo[kPass], hi[kPass];
-#pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-      const int tok = p * kTok + tl;
-      if (tok < g.n) {
-        lo[p].load(x + (int64_t)tok * a.src_stride[side], 0);
-        hi[p].load(x + (int64_t)tok * a.src_stride[side], DH / 2);
-      }
-    }
+    int h;
+    const int side = side_of(task, h);
+    __syncwarp();                                  // the other stage has been read
+    fetch(task + step, stage ^ 1);
+    const TI* rows = reinterpret_cast<const TI*>(S.rows[warp][stage]) + j * 8;
     const int64_t block = g.slot0 < 0 ? 0 : g.slot0 / kKv8Block;
     const int older = g.pos0 & (kKv8Block - 1);    // older tokens of the block
-    float* scale = side == 0 ? nullptr : P.scale[side - 1] + block * a.heads[1] + h;
+    float* scale = side == 0 ? nullptr : (side == 1 ? P.scale[0] : P.scale[1]) + block * a.heads[1] + h;
     float was = 0.f;
     if (side != 0 && g.slot0 >= 0 && older > 0) was = *scale;
     uint64_t gl[4], gu[4];                         // this lane's norm weights
-    const void* w = side < 2 ? a.w[side] : nullptr;
+    const void* w = side == 0 ? a.w[0] : side == 1 ? a.w[1] : nullptr;
     if (w) {
       Vec8<TI> v;
       v.load(w, j * 8);
@@ -177,14 +202,19 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvRopeArgs a
       v.load(w, j * 8 + DH / 2);
       v.get(gu);
     }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
     uint64_t l[kPass][4], u[kPass][4];
     float top = 0.f;
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
       const int tok = p * kTok + tl;
       if (p * kTok >= g.n) break;
-      lo[p].get(l[p]);
-      hi[p].get(u[p]);
+      Vec8<TI> x;
+      x.load(rows, tok * DH);
+      x.get(l[p]);
+      x.load(rows, tok * DH + DH / 2);
+      x.get(u[p]);
       if (w) {
         uint64_t ss2 = 0;
 #pragma unroll
@@ -284,10 +314,17 @@ cudaError_t launch_typed(const KvRopeArgs& a, const Kv8Pages& p, const KvFreq& f
   // Few chunks: one head of one group a warp, so that the call takes one load's latency (a chunk of a decode step has up to
   // 16 groups). Many: a CTA keeps its angles for more heads.
   const int most = (min(kChunk, a.n_tokens) * heads + kWarps - 1) / kWarps;
-  const int parts = (int)min((int64_t)most, max((int64_t)1, (int64_t)sm_count * 8 / chunks));
+  const int parts = (int)min((int64_t)most, max((int64_t)1, (int64_t)sm_count * 2 * kCtas / chunks));
   const dim3 grid((unsigned)chunks + 1, (unsigned)parts);              // one to check the rows
-  if (a.head_dim == 128) return launch_early(kv8_append_kernel<TI, TO, 128>, grid, kThreads, 0, st, a, p, f);
-  return launch_early(kv8_append_kernel<TI, TO, 64>, grid, kThreads, 0, st, a, p, f);
+  auto go = [&](auto kernel, size_t smem) -> cudaError_t {
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_early(kernel, grid, kThreads, smem, st, a, p, f);
+  };
+  if (a.head_dim == 128) return go(kv8_append_kernel<TI, TO, 128>, sizeof(Sm<128, sizeof(TI)>));
+  return go(kv8_append_kernel<TI, TO, 64>, sizeof(Sm<64, sizeof(TI)>));
 }
 
 template <typename TI>
