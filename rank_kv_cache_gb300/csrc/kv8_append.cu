@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_append_kernel(const KvRop
     }
   }
   __syncthreads();
-  const int groups = S.groups, t0 = S.t0, tasks = groups * heads;
+  const int t0 = S.t0, tasks = S.groups * heads;
   // a task: head h of a side (queries, keys, values) of a group
   auto side_of = [&](int task, int& h) {
     h = task % heads;
@@ -141,8 +141,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_append_kernel(const KvRop
     h -= side == 0 ? 0 : side == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
     return side;
   };
+  // this CTA's tasks lie in a row, so that few groups' angles serve them
+  const int per = (tasks + parts - 1) / parts, first = part * per, end = min(tasks, first + per);
+  if (first >= end) return;
   auto fetch = [&](int task, int stage) {
-    if (task < tasks) {
+    if (task < end) {
       const Group& g = S.group[task / heads];
       int h;
       const int side = side_of(task, h), n = g.n;
@@ -157,36 +160,37 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv8_append_kernel(const KvRop
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const int step = parts * kWarps;
-  int task = part * kWarps + warp, stage = 0;
+  int task = first + warp, stage = 0;
   fetch(task, 0);                                  // under way while the angles are computed
 
   if (a.rotate) {
-    const int n = S.n;
-    for (int i = tid; i < n * (DH / 2); i += kThreads) {
-      const int tok = i / (DH / 2), k = i % (DH / 2);
+    const int g0 = first / heads, g1 = (end - 1) / heads;
+    const int from = S.group[g0].t0 - t0, n = S.group[g1].t0 + S.group[g1].n - t0 - from;
+    const int k = tid % (DH / 2);                  // this thread's pair: lanes that read different parameters take turns
+    const uint64_t turn = f.turn[k];
+    for (int tok = from + tid / (DH / 2); tok < from + n; tok += kThreads / (DH / 2)) {
       int pos;
       if (a.positions) {
         pos = a.positions[t0 + tok];
       } else {
-        int g = 0;                                 // the group that holds the token: they are in order
-        while (g + 1 < groups && S.group[g + 1].t0 <= t0 + tok) ++g;
+        int g = g0;                                // the group that holds the token: they are in order
+        while (g < g1 && S.group[g + 1].t0 <= t0 + tok) ++g;
         pos = S.group[g].pos0 + t0 + tok - S.group[g].t0;
       }
       // turns * 2^64, in [-1/2, 1/2); half turns: * 2^-63
-      const int64_t phase = (int64_t)(uint64_t((int64_t)pos) * f.turn[k]);
+      const int64_t phase = (int64_t)(uint64_t((int64_t)pos) * turn);
       const int at = (k & 4) / 4 * kQuarter + k / 8 * 4 + (k & 3);
       sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &S.sn[tok][at], &S.cs[tok][at]);
     }
     __syncthreads();
   }
 
-  for (; task < tasks; task += step, stage ^= 1) {
+  for (; task < end; task += kWarps, stage ^= 1) {
     const Group g = S.group[task / heads];
     int h;
     const int side = side_of(task, h);
     __syncwarp();                                  // the other stage has been read
-    fetch(task + step, stage ^ 1);
+    fetch(task + kWarps, stage ^ 1);
     const TI* rows = reinterpret_cast<const TI*>(S.rows[warp][stage]) + j * 8;
     const int64_t block = g.slot0 < 0 ? 0 : g.slot0 / kKv8Block;
     const int older = g.pos0 & (kKv8Block - 1);    // older tokens of the block
@@ -311,10 +315,24 @@ template <typename TI, typename TO>
 cudaError_t launch_typed(const KvRopeArgs& a, const Kv8Pages& p, const KvFreq& f, int sm_count, cudaStream_t st) {
   const int heads = a.heads[0] + a.heads[1] + a.heads[2];
   const int chunks = (int)(((int64_t)a.n_tokens + kChunk - 1) / kChunk);
-  // Few chunks: one head of one group a warp, so that the call takes one load's latency (a chunk of a decode step has up to
-  // 16 groups). Many: a CTA keeps its angles for more heads.
-  const int most = (min(kChunk, a.n_tokens) * heads + kWarps - 1) / kWarps;
-  const int parts = (int)min((int64_t)most, max((int64_t)1, (int64_t)sm_count * 2 * kCtas / chunks));
+  // How many CTAs share a chunk: the waves of them, times a warp's tasks and what a CTA's start costs (kStart tasks). Few
+  // chunks get one head of one group a warp, so that the call takes one load's latency; many keep their angles for more
+  // heads. A chunk has one group of a prompt, 16 of a decode step.
+  constexpr int kStart = 2;
+  const int groups = kChunk / min(kChunk, max(1, a.rows.max_new)), tasks = groups * heads, held = sm_count * kCtas;
+  const int most = (tasks + kWarps - 1) / kWarps;
+  int parts = most;
+  if ((int64_t)chunks * most > held) {
+    int least = INT_MAX;
+    for (int p = 1; p <= min(most, 64) && (p == 1 || chunks <= 4 * held / p); ++p) {
+      const int waves = (int)(((int64_t)chunks * p + held - 1) / held);
+      const int time = waves * ((tasks + p * kWarps - 1) / (p * kWarps) + kStart);
+      if (time < least) {
+        least = time;
+        parts = p;
+      }
+    }
+  }
   const dim3 grid((unsigned)chunks + 1, (unsigned)parts);              // one to check the rows
   auto go = [&](auto kernel, size_t smem) -> cudaError_t {
     if (smem > 48 * 1024) {
