@@ -655,7 +655,7 @@ palu_status_t palu_plan_kv_rows(palu_kv_t h, const palu_kv_pool* pool, const int
  *   kv_len, kv_len_out   device [batch], both NULL or both given (they may be one): lengths with all new tokens in, and
  *                 without the rejected ones out
  * Probabilities are finite; they need not sum to 1, and negative ones and NaN count as 0. Products and differences
- * are exact, sums are carried in twice the bits of fp32 and joined in fp64. Uniforms outside [0, 1) are brought to its
+ * are exact, sums are carried in twice the bits of fp32. Uniforms outside [0, 1) are brought to its
  * ends. A draft outside the vocabulary is rejected, and recorded in the error word; so are a row with more than
  * max_draft drafts (its first max_draft are taken), a decreasing row_start (nothing is done) and a distribution that is
  * zero throughout (the token is -1). vocab <= 2^20. Rows of any alignment; those whose addresses are multiples of

@@ -3,10 +3,10 @@
 //   a = the first draft i with u_i q_i(x_i) >= p_i(x_i) (or all of them);  w = max(p_a - q_a, 0), or p_a where every draft
 //   was accepted, or where that is zero;  token = min { v : sum_{j <= v} w_j > u sum_j w_j }.
 //
-// The comparison of a draft is exact (two fp32 numbers' product in fp64). A token is drawn from sums of up to 2^20
-// numbers, of which fp32 would misplace about vocab 2^-24 of the draws: a difference p - q with its rounding error
-// (exact for p >= q >= 0) is added to a sum of two fp32 numbers (Knuth's two-sum), 512 values at a time; those
-// segments' sums are joined in fp64. fp64 throughout would be bound by that unit, at 2 lanes of an SM a cycle.
+// The comparison of a draft is exact (the product of two fp32 numbers with its rounding error). A token is drawn from sums of
+// up to 2^20 numbers, of which fp32 would misplace about vocab 2^-24 of the draws: every sum is an unevaluated one of two
+// fp32 numbers (Knuth's two-sum), to which a difference p - q with its rounding error (exact for p >= q >= 0) is added;
+// 48 bits misplace about vocab 2^-46. fp64 would be bound by that unit: an instruction of a warp takes it 64 cycles.
 //
 // Bound: HBM, one target and one draft row of each batch row. A cluster of 1 to 8 CTAs takes a row; a warp a segment of
 // 512 values, a lane 16 of them in four loads. The CTAs exchange their sums through distributed shared memory; the one
@@ -28,15 +28,52 @@ constexpr int kMostCtas = 8;
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-struct TwoSum {
+// hi + lo, the second at most half a step of the first
+struct Sum {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float x, float rest) {
     const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
     lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)), rest));
     hi = s;
   }
-  __device__ __forceinline__ double value() const { return double(hi) + double(lo); }
+  __device__ __forceinline__ void carry() {
+    const float s = __fadd_rn(hi, lo);
+    lo = __fsub_rn(lo, __fsub_rn(s, hi));
+    hi = s;
+  }
+  __device__ __forceinline__ Sum plus(const Sum& o) const {
+    Sum r = *this;
+    r.add(o.hi, o.lo);
+    r.carry();
+    return r;
+  }
+  __device__ __forceinline__ Sum times(float u) const {
+    Sum r;
+    r.hi = __fmul_rn(hi, u);
+    r.lo = __fmaf_rn(lo, u, __fmaf_rn(hi, u, -r.hi));
+    r.carry();
+    return r;
+  }
+  __device__ __forceinline__ bool over(const Sum& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
 };
+__device__ __forceinline__ Sum shfl(const Sum& s, int lane) {
+  return Sum{__shfl_sync(0xffffffffu, s.hi, lane), __shfl_sync(0xffffffffu, s.lo, lane)};
+}
+// sums of this and the lanes below
+__device__ __forceinline__ Sum running(Sum s) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum z{__shfl_up_sync(0xffffffffu, s.hi, o), __shfl_up_sync(0xffffffffu, s.lo, o)};
+    if ((threadIdx.x & 31) >= o) s = s.plus(z);
+  }
+  return s;
+}
+// u q < p
+__device__ __forceinline__ bool below_p(float u, float q, float p) {
+  const float x = __fmul_rn(u, q);
+  if (x < 1e-20f) return double(u) * double(q) < double(p);   // the error of so small a product might be cut off
+  return x < p || (x == p && __fmaf_rn(u, q, -x) < 0.f);
+}
 
 // four probabilities at v of a row of `vocab`, those outside as 0; `wide`: the row's loads are aligned
 template <typename T> __device__ __forceinline__ void load4(float (&x)[kVec], const T* row, int v, int vocab, bool wide) {
@@ -85,8 +122,8 @@ template <typename T> struct Source {
 };
 
 template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kernel(const KvVerifyArgs a) {
-  extern __shared__ __align__(16) double seg[];        // sums of the CTA's segments
-  __shared__ double part[kMostCtas];                    // sums of the cluster's CTAs
+  extern __shared__ __align__(16) Sum seg[];            // sums of the CTA's segments
+  __shared__ float2 part[kMostCtas];                    // sums of the cluster's CTAs
   __shared__ int taken_s;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -96,15 +133,18 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
   grid_wait();
   grid_release();
 
-  // the row's drafts
+  // the row's drafts; the first 32 come beside the row's bounds
+  const int32_t* drafts = a.draft_tokens + (int64_t)b * a.max_draft;
+  const float* u = a.uniforms + (int64_t)b * (a.max_draft + 1);
+  const int x0 = lane < a.max_draft ? drafts[lane] : 0;
+  const float u0 = lane < a.max_draft ? u[lane] : 0.f;
+  float u1 = u[a.max_draft];
   const int start = a.row_start[b], end = a.row_start[b + 1];
   const bool row_ok = start >= 0 && end >= start && end <= a.n_tokens;
   int n = row_ok ? end - start : 0;
   if (rank == 0 && tid == 0 && (!row_ok || n - 1 > a.max_draft)) record_error(a.err, kCodeDevice, kErrRows, b, b);
   n = min(n, a.max_draft + 1);
   int32_t* out = a.tokens + (int64_t)b * (a.max_draft + 1);
-  const float* u = a.uniforms + (int64_t)b * (a.max_draft + 1);
-  const int32_t* drafts = a.draft_tokens + (int64_t)b * a.max_draft;
   const T* target = static_cast<const T*>(a.target) + (int64_t)start * a.target_stride;
   const T* draft = a.draft ? static_cast<const T*>(a.draft) + (int64_t)b * a.max_draft * a.draft_stride : nullptr;
   if (n == 0) {                                         // the whole cluster
@@ -124,14 +164,14 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
       const int i = i0 + lane;
       bool no = false;
       if (i < n - 1) {
-        const int x = drafts[i];
+        const int x = i0 == 0 ? x0 : drafts[i];
         no = x < 0 || x >= a.vocab;
         if (no) {
           if (rank == 0) record_error(a.err, kCodeDevice, kErrToken, x, b);
         } else {
           const float p = fmaxf(to_f32(target[(int64_t)i * a.target_stride + x]), 0.f);
           const float q = draft ? fmaxf(to_f32(draft[(int64_t)i * a.draft_stride + x]), 0.f) : 1.f;
-          no = !(double(fmaxf(u[i], 0.f)) * double(q) < double(p));
+          no = !below_p(fmaxf(i0 == 0 ? u0 : u[i], 0.f), q, p);
         }
       }
       const unsigned m = __ballot_sync(0xffffffffu, no);
@@ -165,14 +205,14 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
   const int segs = (a.vocab + kSeg - 1) / kSeg, per = (segs + ctas - 1) / ctas;
   const int s0 = min(segs, rank * per), mine = min(segs, s0 + per) - s0;
 
-  double total, below, own;
+  Sum total, below;
   for (;;) {
     for (int s = warp; s < mine; s += kWarps) {
       const int v0 = (s0 + s) * kSeg + lane * kVec;
       Weights w[kSteps];
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) src.load(w[k], v0 + k * 32 * kVec);
-      TwoSum sum;
+      Sum sum;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         src.finish(w[k], v0 + k * 32 * kVec);
@@ -184,28 +224,28 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
         const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, o), lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
         sum.add(hi, lo);
       }
-      if (lane == 0) seg[s] = sum.value();
+      sum.carry();
+      if (lane == 0) seg[s] = sum;
     }
     __syncthreads();
-    own = 0.0;
     if (warp == 0) {                                    // in the segments' order by lanes, then over the lanes
-      for (int s = lane; s < mine; s += 32) own += seg[s];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-      if (lane < ctas) *cluster.map_shared_rank(&part[rank], lane) = own;
+      Sum own;
+      for (int s = lane; s < mine; s += 32) own = own.plus(seg[s]);
+      own = shfl(running(own), 31);
+      if (lane < ctas) *cluster.map_shared_rank(&part[rank], lane) = make_float2(own.hi, own.lo);
     }
     cluster.sync();
-    total = below = 0.0;
+    total = below = Sum{};
     for (int c = 0; c < ctas; ++c) {
-      if (c < rank) below += part[c];
-      total += part[c];
+      if (c == rank) below = total;
+      total = total.plus(Sum{part[c].x, part[c].y});
     }
-    if (total > 0.0 || (!src.q && src.certain < 0)) break;
+    if (total.hi > 0.f || (!src.q && src.certain < 0)) break;
     src.q = nullptr;                                    // nothing is left of p - q: from p
     src.certain = -1;
     cluster.sync();                                     // every CTA has read the sums
   }
-  if (!(total > 0.0)) {
+  if (!(total.hi > 0.f)) {
     if (rank == 0 && tid == 0) {
       out[taken] = -1;
       record_error(a.err, kCodeDevice, kErrToken, -1, b);
@@ -213,30 +253,25 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
     return;
   }
   // The draw falls to the first CTA whose running sum exceeds it; those are the same numbers in every CTA.
-  float u1 = u[a.max_draft];
   u1 = u1 < 1.f ? fmaxf(u1, 0.f) : 0.99999994f;        // 1 - 2^-24; NaN too
-  const double t = double(u1) * total;
-  if (below + part[rank] <= t || below > t || warp != 0 || mine == 0) return;
+  const Sum t = total.times(u1);
+  const Sum own{part[rank].x, part[rank].y};
+  if (warp != 0 || mine == 0 || below.over(t) || !below.plus(own).over(t)) return;
   // the segment: the first whose running sum exceeds it, or by another order of rounding the last that holds anything
-  double run = below, from = below;
+  Sum run = below, from = below;
   int at = -1;
   for (int i0 = 0; i0 < mine; i0 += 32) {
-    const double x = i0 + lane < mine ? seg[i0 + lane] : 0.0;
-    double y = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    y += run;
-    const unsigned holds = __ballot_sync(0xffffffffu, x > 0.0), over = __ballot_sync(0xffffffffu, x > 0.0 && y > t);
+    const Sum x = i0 + lane < mine ? seg[i0 + lane] : Sum{};
+    const Sum y = run.plus(running(x));
+    const unsigned holds = __ballot_sync(0xffffffffu, x.hi > 0.f), over = __ballot_sync(0xffffffffu, x.hi > 0.f && y.over(t));
     const int pick = over ? __ffs(over) - 1 : 31 - __clz(holds);
     if (holds) {
       at = i0 + pick;
-      from = __shfl_sync(0xffffffffu, y - x, pick);
+      const Sum before = shfl(y, max(pick - 1, 0));     // what lies before the segment
+      from = pick ? before : run;
     }
     if (over) break;
-    run = __shfl_sync(0xffffffffu, y, 31);
+    run = shfl(y, 31);
   }
   // the token within it, alike
   const int v0 = (s0 + at) * kSeg + lane * kVec;
@@ -248,25 +283,21 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
     src.finish(w[k], v0 + k * 32 * kVec);
-    double x[kVec], sum = 0.0;
+    Sum sum;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      sum += double(w[k].d[i]) + double(w[k].e[i]);
-      x[i] = sum;
-    }
-    double y = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    const double before = run + (y - sum);
+    for (int i = 0; i < kVec; ++i) sum.add(w[k].d[i], w[k].e[i]);
+    sum.carry();
+    const Sum to = run.plus(running(sum));              // behind this lane's four; before them: behind the lane below's
+    Sum x{__shfl_up_sync(0xffffffffu, to.hi, 1), __shfl_up_sync(0xffffffffu, to.lo, 1)};
+    if (lane == 0) x = run;
     int first = -1, last = -1;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
+      x.add(w[k].d[i], w[k].e[i]);
+      x.carry();
       if (w[k].d[i] > 0.f) {
         last = i;
-        if (first < 0 && before + x[i] > t) first = i;
+        if (first < 0 && x.over(t)) first = i;
       }
     }
     const unsigned over = __ballot_sync(0xffffffffu, first >= 0), holds = __ballot_sync(0xffffffffu, last >= 0);
@@ -279,7 +310,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
       const int l = 31 - __clz(holds);
       token = (s0 + at) * kSeg + k * 32 * kVec + l * kVec + __shfl_sync(0xffffffffu, last, l);
     }
-    run = __shfl_sync(0xffffffffu, run + y, 31);
+    run = shfl(to, 31);
   }
   if (lane == 0) out[taken] = token;
 }
@@ -298,7 +329,7 @@ template <typename T> cudaError_t launch_typed(const KvVerifyArgs& a, int sm_cou
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.batch * ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(double) * ((segs + ctas - 1) / ctas);   // at most 16 KB
+  cfg.dynamicSmemBytes = sizeof(Sum) * ((segs + ctas - 1) / ctas);   // at most 16 KB
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
