@@ -75,49 +75,58 @@ __device__ __forceinline__ bool below_p(float u, float q, float p) {
   return x < p || (x == p && __fmaf_rn(u, q, -x) < 0.f);
 }
 
-// four probabilities at v of a row of `vocab`, those outside as 0; `wide`: the row's loads are aligned
-template <typename T> __device__ __forceinline__ void load4(float (&x)[kVec], const T* row, int v, int vocab, bool wide) {
-  if (wide && v + kVec <= vocab) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(row + v);
-      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-    } else {
-      const uint2 f = *reinterpret_cast<const uint2*>(row + v);
-      const T* e = reinterpret_cast<const T*>(&f);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = to_f32(e[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = v + i < vocab ? to_f32(row[v + i]) : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) x[i] = fmaxf(x[i], 0.f);   // NaN: 0
-}
-
-// What the token is drawn from: max(p - q, 0) as a difference and its rounding error.
+// What the token is drawn from, of a lane's values of a segment: max(p - q, 0) as a difference and its rounding error.
 struct Weights {
-  float d[kVec], e[kVec];
+  float d[kSteps][kVec], e[kSteps][kVec];
 };
 template <typename T> struct Source {
   const T* p;
   const T* q;        // nullptr: none
   int certain;       // a draft that was certain: its weight is 0 (or -1)
   int vocab;
-  bool wide_p, wide_q;
-  __device__ __forceinline__ void load(Weights& w, int v) const {
-    load4(w.d, p, v, vocab, wide_p);
-    if (q) load4(w.e, q, v, vocab, wide_q);
-  }
-  __device__ __forceinline__ void finish(Weights& w, int v) const {
+  bool wide;         // both rows' loads are aligned
+
+  template <bool WIDE> __device__ __forceinline__ void row(float (&x)[kSteps][kVec], const T* r, int v) const {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float x = w.d[i], y = q ? w.e[i] : 0.f;
-      const bool more = x > y && v + i != certain;
-      const float d = __fsub_rn(x, y);
-      w.d[i] = more ? d : 0.f;
-      w.e[i] = more ? __fsub_rn(__fsub_rn(x, d), y) : 0.f;
+    for (int k = 0; k < kSteps; ++k) {
+      const int at = v + k * 32 * kVec;
+      if constexpr (WIDE) {
+        if constexpr (sizeof(T) == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(r + at);
+          x[k][0] = f.x, x[k][1] = f.y, x[k][2] = f.z, x[k][3] = f.w;
+        } else {
+          const uint2 f = *reinterpret_cast<const uint2*>(r + at);
+          const T* e = reinterpret_cast<const T*>(&f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) x[k][i] = to_f32(e[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[k][i] = at + i < vocab ? to_f32(r[at + i]) : 0.f;
+      }
     }
+  }
+  // A lane's values of the segment at v0: 4 at v0 + 4 lane, and every 128 on. Whole segments of aligned rows come without a
+  // branch between the loads, so that all are under way at once.
+  __device__ __forceinline__ void load(Weights& w, int v0) const {
+    const int v = v0 + (threadIdx.x & 31) * kVec;
+    if (wide && v0 + kSeg <= vocab) {
+      row<true>(w.d, p, v);
+      if (q) row<true>(w.e, q, v);
+    } else {
+      row<false>(w.d, p, v);
+      if (q) row<false>(w.e, q, v);
+    }
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const float x = fmaxf(w.d[k][i], 0.f), y = q ? fmaxf(w.e[k][i], 0.f) : 0.f;   // NaN: 0
+        const float d = __fsub_rn(x, y);
+        const bool more = d > 0.f && v + k * 32 * kVec + i != certain;
+        w.d[k][i] = more ? d : 0.f;
+        w.e[k][i] = more ? __fsub_rn(__fsub_rn(x, d), y) : 0.f;
+      }
   }
 };
 
@@ -200,25 +209,20 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
   src.q = rejected && draft ? draft + (int64_t)taken * a.draft_stride : nullptr;
   src.certain = rejected && !draft ? drafts[taken] : -1;
   src.vocab = a.vocab;
-  src.wide_p = (uintptr_t)src.p % (kVec * sizeof(T)) == 0;
-  src.wide_q = (uintptr_t)src.q % (kVec * sizeof(T)) == 0;
+  src.wide = ((uintptr_t)src.p | (uintptr_t)src.q) % (kVec * sizeof(T)) == 0;
   const int segs = (a.vocab + kSeg - 1) / kSeg, per = (segs + ctas - 1) / ctas;
   const int s0 = min(segs, rank * per), mine = min(segs, s0 + per) - s0;
 
   Sum total, below;
   for (;;) {
     for (int s = warp; s < mine; s += kWarps) {
-      const int v0 = (s0 + s) * kSeg + lane * kVec;
-      Weights w[kSteps];
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) src.load(w[k], v0 + k * 32 * kVec);
+      Weights w;
+      src.load(w, (s0 + s) * kSeg);
       Sum sum;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        src.finish(w[k], v0 + k * 32 * kVec);
+      for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum.add(w[k].d[i], w[k].e[i]);
-      }
+        for (int i = 0; i < kVec; ++i) sum.add(w.d[k][i], w.e[k][i]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, o), lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
@@ -274,18 +278,15 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
     run = shfl(y, 31);
   }
   // the token within it, alike
-  const int v0 = (s0 + at) * kSeg + lane * kVec;
-  Weights w[kSteps];
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) src.load(w[k], v0 + k * 32 * kVec);
+  Weights w;
+  src.load(w, (s0 + at) * kSeg);
   run = from;
   int token = -1;
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    src.finish(w[k], v0 + k * 32 * kVec);
     Sum sum;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) sum.add(w[k].d[i], w[k].e[i]);
+    for (int i = 0; i < kVec; ++i) sum.add(w.d[k][i], w.e[k][i]);
     sum.carry();
     const Sum to = run.plus(running(sum));              // behind this lane's four; before them: behind the lane below's
     Sum x{__shfl_up_sync(0xffffffffu, to.hi, 1), __shfl_up_sync(0xffffffffu, to.lo, 1)};
@@ -293,9 +294,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
     int first = -1, last = -1;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      x.add(w[k].d[i], w[k].e[i]);
+      x.add(w.d[k][i], w.e[k][i]);
       x.carry();
-      if (w[k].d[i] > 0.f) {
+      if (w.d[k][i] > 0.f) {
         last = i;
         if (first < 0 && x.over(t)) first = i;
       }
