@@ -22,7 +22,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSeg = 512, kVec = 4, kSteps = kSeg / (32 * kVec);   // values of a segment, of a lane's load; loads
-constexpr int kMostCtas = 8;
+constexpr int kMostCtas = 8, kCtas = 4;                            // of a cluster; of an SM
 
 // the cluster's CTAs have all started: before that their shared memory is not written
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -130,7 +130,7 @@ template <typename T> struct Source {
   }
 };
 
-template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kernel(const KvVerifyArgs a) {
+template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_verify_kernel(const KvVerifyArgs a) {
   extern __shared__ __align__(16) Sum seg[];            // sums of the CTA's segments
   __shared__ float2 part[kMostCtas];                    // sums of the cluster's CTAs
   __shared__ int taken_s;
@@ -317,9 +317,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads) kv_verify_kern
 }
 
 template <typename T> cudaError_t launch_typed(const KvVerifyArgs& a, int sm_count, cudaStream_t st) {
-  // The row's segments are shared by as many CTAs as the GPU holds at once for all rows, four an SM.
+  // The row's segments are shared by as many CTAs as the GPU holds at once for all rows.
   unsigned ctas = kMostCtas;
-  while (ctas > 1 && (int64_t)a.batch * ctas > (int64_t)sm_count * 4) ctas /= 2;
+  while (ctas > 1 && (int64_t)a.batch * ctas > (int64_t)sm_count * kCtas) ctas /= 2;
   const int segs = (a.vocab + kSeg - 1) / kSeg;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -752,6 +752,8 @@ class PagedAttention:
         self.device = self.workspace.device
         self._index = self.device.index
         self._current = torch._C._cuda_getCurrentRawStream
+        self._int = torch.int32
+        self._kinds = {torch.float32: PALU_F32, torch.float16: PALU_F16, torch.bfloat16: PALU_BF16}
         base = int(self.workspace.data_ptr())
         st, self.handle = palu_kv_create(self.desc, base + (-base) % 256, nbytes, self._stream(stream))
         check(st, "palu_kv_create")
@@ -872,7 +874,7 @@ class PagedAttention:
         return out
 
     def _ints(self, name, t, shape):
-        if t.dtype is not _torch().int32 or t.get_device() != self._index or tuple(t.shape) != shape or not t.is_contiguous():
+        if t.dtype is not self._int or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {self.device}")
         return t.data_ptr()
 
@@ -904,27 +906,29 @@ class PagedAttention:
         draft [batch][K][vocab] their probabilities in target's dtype (None: the drafts were certain), uniforms
         [batch][K + 1] in [0, 1). Returns (tokens [batch][K + 1]: accepted drafts, one drawn token, -1; accepted [batch]).
         kv_len [batch] loses the rejected tokens, into kv_len_out (None: in place)."""
-        torch = _torch()
-        names = {torch.float32: PALU_F32, torch.float16: PALU_F16, torch.bfloat16: PALU_BF16}
-        if target.dim() != 2 or target.dtype not in names or target.get_device() != self._index or \
-                (target.shape[1] > 1 and target.stride(1) != 1):
+        torch, dtype = _torch(), target.dtype
+        kind = self._kinds.get(dtype)
+        if target.dim() != 2 or kind is None or target.get_device() != self._index or \
+                (target.stride(1) != 1 and target.shape[1] > 1):
             raise ValueError(f"target must be [n_tokens][vocab] of float32, float16 or bfloat16 on {self.device}")
         N, V = target.shape
         if draft_tokens.dim() != 2:
             raise ValueError("draft_tokens must be [batch][K]")
         B, K = draft_tokens.shape
-        draft_stride = 0
+        wide = (B, K + 1)
+        draft_ptr, draft_stride = None, 0
         if draft is not None:
-            if draft.dtype != target.dtype or draft.get_device() != self._index or draft.shape != (B, K, V):
-                raise ValueError(f"draft must be [{B}][{K}][{V}] {target.dtype} on {self.device}")
-            draft_stride = draft.stride(1) if K > 1 else draft.stride(0) if B > 1 else V
-            if (V > 1 and draft.stride(2) != 1) or (K > 1 and B > 1 and draft.stride(0) != K * draft_stride):
+            if draft.dtype is not dtype or draft.shape != (B, K, V) or draft.get_device() != self._index:
+                raise ValueError(f"draft must be [{B}][{K}][{V}] {dtype} on {self.device}")
+            s0, s1, s2 = draft.stride()
+            draft_ptr, draft_stride = draft.data_ptr(), s1 if K > 1 else s0 if B > 1 else V
+            if (s2 != 1 and V > 1) or (s0 != K * draft_stride and K > 1 and B > 1):
                 raise ValueError("draft: the rows of probabilities must lie evenly apart")
-        if uniforms.dtype != torch.float32 or uniforms.shape != (B, K + 1) or uniforms.get_device() != self._index or \
+        if uniforms.dtype is not torch.float32 or uniforms.shape != wide or uniforms.get_device() != self._index or \
                 not uniforms.is_contiguous():
             raise ValueError(f"uniforms must be a contiguous [{B}][{K + 1}] float32 tensor on {self.device}")
         if tokens is None:
-            tokens = self._empty((B, K + 1), torch.int32, stream)
+            tokens = self._empty(wide, torch.int32, stream)
         if accepted is None:
             accepted = self._empty((B,), torch.int32, stream)
         if kv_len is None and kv_len_out is not None:
@@ -932,10 +936,9 @@ class PagedAttention:
         lens = None if kv_len is None else self._ints("kv_len", kv_len, (B,))
         lens_out = lens if kv_len_out is None else self._ints("kv_len_out", kv_len_out, (B,))
         check(_lib.palu_verify_drafts(
-            self.handle, target.data_ptr(), target.stride(0) if N > 1 else V, _ptr(draft), draft_stride,
-            names[target.dtype], V, self._ints("row_start", row_start, (B + 1,)), B, N,
-            self._ints("draft_tokens", draft_tokens, (B, K)), K, uniforms.data_ptr(),
-            self._ints("tokens", tokens, (B, K + 1)), self._ints("accepted", accepted, (B,)), lens, lens_out,
+            self.handle, target.data_ptr(), target.stride(0) if N > 1 else V, draft_ptr, draft_stride, kind, V,
+            self._ints("row_start", row_start, (B + 1,)), B, N, self._ints("draft_tokens", draft_tokens, (B, K)), K,
+            uniforms.data_ptr(), self._ints("tokens", tokens, wide), self._ints("accepted", accepted, (B,)), lens, lens_out,
             self._stream(stream)), "palu_verify_drafts")
         return tokens, accepted
 
