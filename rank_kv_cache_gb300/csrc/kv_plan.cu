@@ -4,8 +4,8 @@
 //   pages(b) = max(0, ceil((L_b + n_b) / page) - held_b),  row_start = running sum of the admitted n_b,
 //   admitted: the running sums of pages and tokens, over all rows up to b, stay within what is free.
 //
-// Bound: latency (a step of 64 rows moves a few KB). One launch, one cluster of 1 to 8 CTAs: every CTA loads the rows, 4
-// a thread, and works out the three running sums (pages taken, tokens, pages given back) for itself in shared memory;
+// Bound: latency (a step of 64 rows moves a few KB). One launch, one cluster of 1 to 8 CTAs: every CTA loads the rows, one
+// or four a thread, and works out the three running sums (pages taken, tokens, pages given back) for itself in shared memory;
 // then the CTAs share the writes, each finding its rows by bisection of those sums. Nothing is read that
 // another CTA writes: pages are read from the ring's front and written behind its end, table entries are read below
 // `held` and written from there on, and what is replaced in place (lengths, held, the ring's state) is written behind a
@@ -19,7 +19,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kPer = 4, kRows = kThreads * kPer;   // rows of a chunk
+constexpr int kThreads = 512, kWarps = kThreads / 32, kRows = 4 * kThreads;   // rows of a chunk, at most
 constexpr int kMostCtas = 8;
 // Tokens and pages that a CTA writes alone: past it the work goes to a cluster.
 constexpr int kWritesPerCta = 4096;
@@ -43,13 +43,30 @@ __device__ __forceinline__ int last_at_most(const int* x, int n, int v) {
 }
 
 struct Shared {
-  Sums warp[kThreads / 32];
+  Sums warp[kWarps], most[kWarps];
   // of the chunk's rows: running sums before the row (one more: behind the last), relative to the chunk's beginning
   int tokens[kRows + 1], pages[kRows + 1], back[kRows + 1];
   int len[kRows], held[kRows];
 };
 
-__global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanArgs a) {
+// the sum of this lane's and all lower lanes' numbers
+__device__ __forceinline__ Sums running(Sums s) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sums y{__shfl_up_sync(0xffffffffu, s.pages, o), __shfl_up_sync(0xffffffffu, s.tokens, o),
+                 __shfl_up_sync(0xffffffffu, s.back, o)};
+    if ((threadIdx.x & 31) >= o) s = s + y;
+  }
+  return s;
+}
+__device__ __forceinline__ Sums of_lane(const Sums& s, int lane) {
+  return Sums{__shfl_sync(0xffffffffu, s.pages, lane), __shfl_sync(0xffffffffu, s.tokens, lane),
+              __shfl_sync(0xffffffffu, s.back, lane)};
+}
+
+// kPer: rows of a thread
+template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanArgs a) {
+  constexpr int kRows = kThreads * kPer;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& S = *reinterpret_cast<Shared*>(smem);
   cg::cluster_group cluster = cg::this_cluster();
@@ -105,20 +122,13 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanArgs a) {
       run = run + w[e];
     }
     // the running sums over the CTA
-    Sums scan = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const Sums y{__shfl_up_sync(0xffffffffu, scan.pages, o), __shfl_up_sync(0xffffffffu, scan.tokens, o),
-                   __shfl_up_sync(0xffffffffu, scan.back, o)};
-      if (lane >= o) scan = scan + y;
-    }
+    const Sums scan = running(run);
     if (lane == 31) S.warp[warp] = scan;
     __syncthreads();
-    Sums before{0, 0, 0}, all{0, 0, 0};
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before = before + S.warp[i];
-      all = all + S.warp[i];
-    }
+    const Sums warps = running(lane < kWarps ? S.warp[lane] : Sums{0, 0, 0});
+    Sums all = of_lane(warps, 31);
+    const Sums lower = of_lane(warps, max(warp - 1, 0));
+    Sums before = warp ? lower : Sums{0, 0, 0};
     const bool back_ok = all.back <= a.n_pages;   // else the counts do not add up, and the chunk gives nothing back
     if (!back_ok) {
       if (rank == 0 && tid == 0) record_error(a.err, kCodeDevice, kErrPool, a.n_pages, row0);
@@ -144,13 +154,11 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanArgs a) {
     // what the chunk admits in all: the sums ascend, so the largest that fits is the last
     most_tokens = __reduce_max_sync(0xffffffffu, most_tokens);
     most_pages = __reduce_max_sync(0xffffffffu, most_pages);
+    if (lane == 0) S.most[warp] = Sums{most_pages, most_tokens, 0};
     __syncthreads();
-    if (lane == 0) S.warp[warp] = Sums{most_pages, most_tokens, 0};
-    __syncthreads();
-    for (int i = 0; i < kThreads / 32; ++i) {
-      most_tokens = max(most_tokens, (int)S.warp[i].tokens);
-      most_pages = max(most_pages, (int)S.warp[i].pages);
-    }
+    const Sums top = lane < kWarps ? S.most[lane] : Sums{0, 0, 0};
+    most_tokens = __reduce_max_sync(0xffffffffu, (int)top.tokens);
+    most_pages = __reduce_max_sync(0xffffffffu, (int)top.pages);
     at = before;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
@@ -197,21 +205,56 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanArgs a) {
       const int r = last_at_most(S.back, rows + 1, j);
       a.ring[ring_at(count + wanted.back + j)] = a.table[(int64_t)(row0 + r) * a.table_pages + j - S.back[r]];
     }
-    // the tokens' places, four at a time
+    // the tokens' places, four at a time: their pages' loads are under way together
     if (a.positions || a.slots) {
+      const bool wide = tokens % 4 == 0 && (uintptr_t)a.positions % 16 == 0 && (uintptr_t)a.slots % 16 == 0;
       for (int j0 = me * 4; j0 < most_tokens; j0 += step * 4) {
         int r = last_at_most(S.tokens, rows + 1, j0);
-        for (int j = j0; j < min(j0 + 4, most_tokens); ++j) {
-          while (S.tokens[r + 1] <= j) ++r;
-          const int pos = S.len[r] + j - S.tokens[r];
-          if (a.positions) a.positions[tokens + j] = pos;
-          if (a.slots) {
-            const int pg = pos / a.page_size, more = pg - S.held[r];
-            const int page = more < 0 ? a.table[(int64_t)(row0 + r) * a.table_pages + pg]
-                                      : a.ring[ring_at(taken + S.pages[r] + more)];
-            const bool ok = page >= 0 && page < a.n_pages;
-            a.slots[tokens + j] = ok ? page * a.page_size + (pos - pg * a.page_size) : -1;
-            if (!ok) record_error(a.err, kCodeDevice, kErrPage, page, row0 + r);
+        int pos = S.len[r] + j0 - S.tokens[r], pg = pos / a.page_size, off = pos - pg * a.page_size;
+        int place[4], slot[4];
+        const int32_t* from[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int more = pg - S.held[r];
+          place[e] = pos;
+          slot[e] = off;
+          from[e] = more < 0 ? a.table + (int64_t)(row0 + r) * a.table_pages + pg : a.ring + ring_at(taken + S.pages[r] + more);
+          if (j0 + e + 1 >= most_tokens) continue;               // the last one's is looked up again
+          if (S.tokens[r + 1] > j0 + e + 1) {
+            ++pos;
+            if (++off == a.page_size) {
+              off = 0;
+              ++pg;
+            }
+          } else {
+            do ++r;
+            while (S.tokens[r + 1] <= j0 + e + 1);
+            pos = S.len[r];
+            pg = pos / a.page_size;
+            off = pos - pg * a.page_size;
+          }
+        }
+        const int n = min(4, most_tokens - j0);
+        if (a.slots) {
+          int page[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) page[e] = *from[e];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool ok = page[e] >= 0 && page[e] < a.n_pages;
+            slot[e] = ok ? page[e] * a.page_size + slot[e] : -1;
+            if (!ok) record_error(a.err, kCodeDevice, kErrPage, page[e], row0);
+          }
+        }
+        if (wide && n == 4) {
+          if (a.positions) *reinterpret_cast<int4*>(a.positions + tokens + j0) = make_int4(place[0], place[1], place[2], place[3]);
+          if (a.slots) *reinterpret_cast<int4*>(a.slots + tokens + j0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (e >= n) break;
+            if (a.positions) a.positions[tokens + j0 + e] = place[e];
+            if (a.slots) a.slots[tokens + j0 + e] = slot[e];
           }
         }
       }
@@ -254,7 +297,7 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kv_plan_kernel, a);
+  return a.batch <= kThreads ? cudaLaunchKernelEx(&cfg, kv_plan_kernel<1>, a) : cudaLaunchKernelEx(&cfg, kv_plan_kernel<4>, a);
 }
 
 }  // namespace palu
