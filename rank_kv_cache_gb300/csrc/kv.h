@@ -55,19 +55,23 @@ __device__ __forceinline__ int64_t kv_slot(const KvRows& r, const KvPages& p, in
 // next one may set itself up. A few microseconds of launch latency hide behind the work.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <typename... Params, typename... Args>
+// CTAS: of a cluster.
+template <int CTAS = 1, typename... Params, typename... Args>
 cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
                          const Args&... args) {
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CTAS > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 

@@ -18,6 +18,16 @@
 // each to keep their precision: as many products as in fp16, and the weights' terms in the softmax, which bounds the
 // kernel already.
 //
+// Pairs (heads of 128, see launch_kv8_attend_tc): two CTAs of a cluster, on neighbouring SMs, share each step's keys and values.
+//   * A product then has 256 query rows (tcgen05, cta_group::2), 128 of either CTA. Each holds its own queries, scores,
+//     weights and outputs, and half of the other operand: of a step's 128 keys the 64 of its rank, of the values' 128
+//     columns 64. So it loads, converts, keeps and reads half of what it would alone for as many products; alone, the
+//     converters and the products' operands together keep the shared memory's ports busy.
+//   * The first CTA takes the items and hands their numbers to the other. Its MMA warp issues all products, when both
+//     CTAs' tiles, weights and queries say so at its barriers; what they complete arrives at the barriers of both.
+//   * Whatever happened, the two meet before they end: neither's shared or tensor memory is gone while the other's arrivals
+//     or products may still come.
+//
 // Every wait is bounded; one that gives up records PALU_ERR_TIMEOUT, and all roles wait for their own
 // copies and products in flight before tensor memory is freed.
 #include "kv8.h"
@@ -27,25 +37,28 @@ namespace palu {
 namespace {
 
 constexpr int kThreads = 512;            // two softmax warpgroups; two loader warps, MMA and an idle warp; converters
-// Registers: launched with 128 a thread; 256 * 192 + 128 * 72 + 128 * 56 = 512 * 128.
-constexpr int kRegsSoftmax = 192, kRegsOther = 72, kRegsConvert = 56;
 constexpr int kBlocks = kTile / kKv8Block;
 
-template <int DH> struct Lay {
-  // fp16 tiles: 64 elements (128 bytes) of all rows, then the next 64. Code tiles: rows of DH bytes, those of 128 swizzled.
+template <int DH, bool PAIR> struct Lay {
+  // Registers: launched with 128 a thread; 256 softmax + 128 other + 128 convert = 512 * 128. A pair's loaders hold more.
+  static constexpr int kRegsSoftmax = PAIR ? 184 : 192, kRegsOther = PAIR ? 88 : 72, kRegsConvert = 56;
+  // Query tiles: 64 elements (128 bytes) of all rows, then the next 64. fp16 and code tiles hold the CTA's part: keys as the
+  // queries (of a pair's CTA 64 tokens), values by 64 columns of all tokens. Rows of 128 bytes are swizzled.
   static constexpr int kHalf = kTile * 128;             // 64 elements of 128 rows
   static constexpr int kTileB = kHalf * (DH / 64);
-  static constexpr int kCodeB = kTile * DH;
-  static constexpr int kStages = DH == 128 ? 3 : 5;     // fp16 tiles
-  static constexpr int kCodes = DH == 128 ? 4 : 8;      // code tiles
+  static constexpr int kParts = PAIR ? 2 : 1;           // CTAs that share a tile of keys or values
+  static constexpr int kStageB = kTileB / kParts, kKeyHalf = kHalf / kParts;
+  static constexpr int kCodeB = kTile * DH / kParts;
+  static constexpr int kStages = PAIR ? 6 : DH == 128 ? 3 : 5;   // fp16 tiles
+  static constexpr int kCodes = PAIR ? 7 : DH == 128 ? 4 : 8;    // code tiles
   // Scales of key tiles in use. A tile's are written when its place in the ring of kStages tiles is free, and all
   // tiles whose values' products had not ended then count: of the kStages - 1 places before it, and of the values up to
   // three places behind their keys, at most kStages / 2 + 2.
-  static constexpr int kScales = DH == 128 ? 4 : 8;
+  static constexpr int kScales = DH == 128 && !PAIR ? 4 : 8;
   static constexpr int kOffKv = 2 * kTileB;             // behind two query tiles
-  static constexpr int kOffCode = kOffKv + kStages * kTileB;
+  static constexpr int kOffCode = kOffKv + kStages * kStageB;
   static constexpr int kOffBar = kOffCode + kCodes * kCodeB;
-  static constexpr int kShared = DH == 128 ? 2048 : 3072;   // barriers, items, scales, the units' exchange
+  static constexpr int kShared = DH == 128 && !PAIR ? 2048 : 3072;   // barriers, items, scales, the units' exchange
   static constexpr int kSmem = kOffBar + kShared + 1024;    // and alignment
   static constexpr uint32_t kColO = 2 * kTile;          // tensor memory: S (and P) of the units, then O
   static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
@@ -58,12 +71,15 @@ struct Info {
 constexpr int kKeys = 0, kValues = 1, kEnd = 2;
 constexpr int kScaleLanes = 2 * kBlocks;  // lanes that load a key tile's scales
 
-template <int DH> struct Shared {
-  using Y = Lay<DH>;
+template <int DH, bool PAIR> struct Shared {
+  using Y = Lay<DH, PAIR>;
+  // of a pair: at the first CTA, from both: full, q_ready, p_full, idx_empty; at both, from the first one's products: empty,
+  // q_empty, s_full, o_full, drained; the others from the CTA itself
   uint64_t full[Y::kStages], empty[Y::kStages], code_full[Y::kCodes], code_empty[Y::kCodes], scale_full[Y::kScales];
-  uint64_t q_full, q_ready, q_empty, x_full, x_empty, drained;
+  uint64_t q_full, q_ready, q_empty, lift_full, x_full, x_empty, drained;
   uint64_t s_full[2], o_full[2], p_full[2][2];
-  uint64_t item_full[2], item_empty[2];
+  uint64_t item_full[2], item_empty[2], idx_full[2], idx_empty[2];
+  int idx[2];                             // items' numbers, from the pair's first CTA
   Item item[2];
   Plan plan;
   Info info[Y::kCodes];
@@ -77,8 +93,9 @@ template <int DH> struct Shared {
     float lift[kTile];                    // of the queries' rows where both units share a tile, at its beginning
   };
 };
-static_assert(sizeof(Shared<128>) <= Lay<128>::kShared && sizeof(Shared<64>) <= Lay<64>::kShared, "shared block");
-static_assert(sizeof(JoinShared) <= 2 * Lay<64>::kTileB, "in the queries' space");
+template <int DH, bool PAIR> constexpr bool fits = sizeof(Shared<DH, PAIR>) <= Lay<DH, PAIR>::kShared;
+static_assert(fits<128, false> && fits<64, false> && fits<128, true>, "shared block");
+static_assert(sizeof(JoinShared) <= 2 * Lay<64, false>::kTileB, "in the queries' space");
 
 struct Tc8Params {
   TcParams P;
@@ -101,7 +118,7 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
 // Lifts a row of bf16 queries, as TMA left it (two halves of 64 elements, 128-byte swizzle), to fp16 in place.
 template <int DH> __device__ __forceinline__ float lift_row(uint8_t* tile, int r) {
   auto at = [&](int c) -> uint4* {
-    return reinterpret_cast<uint4*>(tile + c / 8 * Lay<DH>::kHalf + r * 128 + ((c % 8 ^ (r & 7)) << 4));
+    return reinterpret_cast<uint4*>(tile + c / 8 * (kTile * 128) + r * 128 + ((c % 8 ^ (r & 7)) << 4));
   };
   __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
@@ -120,23 +137,106 @@ template <int DH> __device__ __forceinline__ float lift_row(uint8_t* tile, int r
   return lift;
 }
 
+// ------------------------------------------------------------------------------------------- of a pair
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t at_cta(const void* p, uint32_t rank) {   // the same place of a CTA of the cluster
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_peer(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_cta(bar, rank)) : "memory");
+}
+// for what lies in tensor memory alone, ordered by tcgen05's own fences: with release the softmax warps waited 1000 clocks
+__device__ __forceinline__ void arrive_peer_relaxed(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_cta(bar, rank)) : "memory");
+}
+__device__ __forceinline__ void st_peer(int* p, int v, uint32_t rank) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at_cta(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// tc::mbar_wait_short, with the cluster's order
+__device__ __forceinline__ bool wait_pair(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, "
+        "p;\n}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_addr(b)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    const uint64_t t = tc::globaltimer();
+    if (t0 == 0) {
+      t0 = t;
+    } else if (t - t0 > limit_ns) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_addr(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t base, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// the products issued so far arrive at the barrier of both CTAs
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          tc::smem_addr(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR) commit_pair(bar);
+  else tc::umma_commit(bar);
+}
+
 // ------------------------------------------------------------------------------------------- attend
-template <int DH, bool BF16>
+template <int DH, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const Tc8Params P8) {
-  using Y = Lay<DH>;
+  using Y = Lay<DH, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Shared<DH>& S = *reinterpret_cast<Shared<DH>*>(smem + Y::kOffBar);
+  Shared<DH, PAIR>& S = *reinterpret_cast<Shared<DH, PAIR>*>(smem + Y::kOffBar);
   volatile int* abort_flag = &S.abort_flag;
-  const TcParams& P = P8.P;
+  const TcParams& P = P8.P;                    // per_tile: of the rows of a product, 128 or 256
   const KvAttendArgs& a = P.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = PAIR ? (int)cta_rank() : 0;
+  const int per = P.per_tile / Y::kParts;      // tokens of this CTA's rows
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Y::kStages; ++i) {
-      tc::mbar_init(&S.full[i], 4);            // the converters
+      tc::mbar_init(&S.full[i], PAIR && rank == 0 ? 5 : 4);   // the converters; the other CTA's MMA warp
       tc::mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < Y::kCodes; ++i) {
@@ -145,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < Y::kScales; ++i) tc::mbar_init(&S.scale_full[i], 1);
     tc::mbar_init(&S.q_full, 1);
-    tc::mbar_init(&S.q_ready, 8);              // bf16 queries, lifted by the softmax warps
+    tc::mbar_init(&S.q_ready, 8 * Y::kParts);  // the softmax warps have seen, and lifted, the queries
+    tc::mbar_init(&S.lift_full, 4);
     tc::mbar_init(&S.q_empty, 1);              // the products that read the queries
     tc::mbar_init(&S.x_full, 4);
     tc::mbar_init(&S.x_empty, 4);
@@ -153,15 +254,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = 0; u < 2; ++u) {
       tc::mbar_init(&S.s_full[u], 1);
       tc::mbar_init(&S.o_full[u], 1);
-      for (int k = 0; k < 2; ++k) tc::mbar_init(&S.p_full[u][k], 4);
+      for (int k = 0; k < 2; ++k) tc::mbar_init(&S.p_full[u][k], 4 * Y::kParts);
       tc::mbar_init(&S.item_full[u], 1);
       tc::mbar_init(&S.item_empty[u], 10);     // eight softmax warps, the MMA warp, the value loader
+      tc::mbar_init(&S.idx_full[u], 1);
+      tc::mbar_init(&S.idx_empty[u], 1);
     }
     S.abort_flag = 0;
     S.cut = 0;
     tc::fence_barrier_init();
   }
-  if (warp == 9) {
+  if constexpr (PAIR) {                        // both CTAs' barriers are there
+    __syncthreads();
+    cluster_meet();
+    if (warp == 9) tmem_alloc_pair(&S.tmem, 512);
+  } else if (warp == 9) {
     tc::tmem_alloc(&S.tmem, 512);
     tc::tmem_relinquish();
   }
@@ -176,13 +283,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ converters
     // 16 codes a lane and step; a warp takes a group of eight rows and 64 of their columns: eight lanes at a time rows a
     // and a ^ 5, whose 16-byte chunks lie in different banks both as codes (128-byte swizzle; rows of 64 bytes lie
-    // so without one) and as fp16. All places are a thread's base and constants.
-    tc::regs_shrink<kRegsConvert>();
-    constexpr int kHalves = DH / 64, kEach = kTile / 8 * kHalves / 4;   // steps of a warp
+    // so without one) and as fp16. All places are a thread's base and constants. Of a pair's tile a warp has 16 keys with
+    // both halves of their columns, or 64 columns of 32 values.
+    tc::regs_shrink<Y::kRegsConvert>();
+    constexpr int kHalves = DH / 64, kEach = kTile / 8 * kHalves / 4 / Y::kParts;   // steps of a warp
     const int c = lane & 3, a7 = (lane >> 3) ^ (lane & 4 ? 5 : 0);       // a7: row of its group of eight
     const uint32_t from = DH == 128 ? uint32_t(a7 * 128 + ((c ^ a7) << 4)) : uint32_t(a7 * 64 + (c << 4));
+    const uint32_t from_v = PAIR ? uint32_t(a7 * 64 + (c << 4)) : from;
     const uint32_t to = uint32_t(a7 * 128 + ((2 * c ^ a7) << 4));
-    const int group0 = (warp - 12) * (kEach / kHalves);
+    // the warp's first row of a tile of keys, or of values, which a pair's CTA holds by halves
+    const int row_k = (warp - 12) * (kEach / kHalves) * 8, row_v = (warp - 12) * 32;
+    const int tok_k = PAIR ? rank * 64 + row_k : row_k;
     int sc = 0, st = 0, n_k = 0;
     uint32_t par_c = 0, par = 1;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -192,20 +303,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&S.code_full[sc], par_c)) break;
       const Info info = S.info[sc];
       if (info.kind == kEnd) break;
+      const bool keys = info.kind == kKeys, whole = !PAIR || keys;      // rows of whole heads, or of 64 columns
       // the tile's codes are taken while its place is still read by products
-      const uint8_t* src = smem + Y::kOffCode + sc * Y::kCodeB + group0 * 8 * DH;
+      const uint8_t* src = smem + Y::kOffCode + sc * Y::kCodeB + (warp - 12) * (Y::kCodeB / 4);
       uint4 v[kEach];
 #pragma unroll
       for (int x = 0; x < kEach; ++x)
-        v[x] = *reinterpret_cast<const uint4*>(src + x / kHalves * 8 * DH + (from ^ (x % kHalves * 64)));
+        v[x] = *reinterpret_cast<const uint4*>(src + (whole ? x / kHalves * 8 * DH + (from ^ (x % kHalves * 64)) : x * 512 + from_v));
       if (info.valid != kTile) {
-        const int valid = info.valid - group0 * 8 - a7;                // of this thread's rows, those 8 x below it
+        const int valid = info.valid - (keys ? tok_k : row_v) - a7;    // of this thread's rows, those 8 x below it
 #pragma unroll
         for (int x = 0; x < kEach; ++x)
-          if (x / kHalves * 8 >= valid) v[x] = make_uint4(0u, 0u, 0u, 0u);
+          if ((whole ? x / kHalves : x) * 8 >= valid) v[x] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (!wait(&S.empty[st], par)) break;
-      if (info.kind == kKeys) {
+      if (keys) {
         if (warp == 12) {
           if (lane < kBlocks)
             S.scale[n_k % Y::kScales][lane] = make_float2(scale_or_one(S.raw[sc][0][lane]), lg2(scale_or_one(S.raw[sc][1][lane])));
@@ -214,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_k;
       }
-      uint8_t* dst = smem + Y::kOffKv + st * Y::kTileB + group0 * 1024;
+      uint8_t* dst = smem + Y::kOffKv + st * Y::kStageB + (whole ? row_k : row_v) * 128;
 #pragma unroll
       for (int x = 0; x < kEach; ++x) {
         const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
@@ -224,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f[2 * e] = f16_of_codes(uint16_t(w[e]));
           f[2 * e + 1] = f16_of_codes(uint16_t(w[e] >> 16));
         }
-        uint8_t* at = dst + x % kHalves * Y::kHalf + x / kHalves * 1024;
+        uint8_t* at = dst + (whole ? x % kHalves * Y::kKeyHalf + x / kHalves * 1024 : x * 1024);
         *reinterpret_cast<uint4*>(at + to) = make_uint4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
@@ -244,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 8) {
-    tc::regs_shrink<kRegsOther>();
+    tc::regs_shrink<Y::kRegsOther>();
     if (warp == 8 || warp == 10) {
       // ------------------------------------------------------------------ loaders
       // Warp 8 takes the items and loads Q and K, warp 10 V. Both count every stage of the ring, in the order
@@ -260,6 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int total = plan.items * a.n_kv;
       const int box = P.box, n_box = kTile / box;
+      // this CTA's boxes of a tile: of a pair half of the keys, half of the values' columns
+      const int x0 = PAIR && keys ? rank * (n_box / 2) : 0, x1 = PAIR && keys ? x0 + n_box / 2 : n_box;
+      const int row_b = PAIR && !keys ? DH / 2 : DH, col = PAIR && !keys ? rank * (DH / 2) : 0;
       const int ps = a.pages.page_size, tile_pages = kTile / ps, tile_rest = kTile % ps;
       const int table_pages = int(a.rows.table_pages), n_pages = int(a.pages.n_pages);
       const int oob_slot = n_pages * ps;
@@ -272,6 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, phase, abort_flag, P.wait_ns));
         return ok;
       };
+      auto across = [&](uint64_t* bar, uint32_t phase) {   // what the pair's other CTA says
+        ok = __all_sync(0xffffffffu, wait_pair(bar, phase, abort_flag, P.wait_ns));
+        return ok;
+      };
       if (lane == 0) {
         if (keys) tc::tma_prefetch(&tm_q);
         tc::tma_prefetch(map);
@@ -281,7 +400,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (keys) {
           if (!wait(&S.item_empty[i & 1], ((i >> 1) & 1) ^ 1)) break;
           int idx = 0;
-          if (lane == 0) idx = (int)atomicAdd(&P.plan.head->next, 1u);
+          if (rank == 0) {
+            // the peer's place for the number is free when it has read the one two before
+            if (PAIR && i >= 2 && !across(&S.idx_empty[i & 1], ((i >> 1) & 1) ^ 1)) break;
+            if (lane == 0) {
+              idx = (int)atomicAdd(&P.plan.head->next, 1u);
+              if constexpr (PAIR) {
+                st_peer(&S.idx[i & 1], idx, 1);
+                arrive_peer(&S.idx_full[i & 1], 1);
+              }
+            }
+          } else {
+            if (!across(&S.idx_full[i & 1], (i >> 1) & 1)) break;
+            if (lane == 0) {
+              idx = *(volatile int*)&S.idx[i & 1];
+              arrive_peer(&S.idx_empty[i & 1], 0);
+            }
+          }
           idx = __shfl_sync(0xffffffffu, idx, 0);
           if (idx < total) {
             const int e = idx / a.n_kv;    // never less than the one before
@@ -327,11 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (exchanged && !wait(&S.x_empty, n_x++ & 1)) break;
           exchanged = tiles == 1 && kv1 - kv0 > 1;
           if (lane == 0) {
-            tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(tiles) * P.per_tile * a.g * DH * 2);
+            tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(tiles) * per * a.g * DH * 2);
             for (int t = 0; t < tiles; ++t)
               for (int c = 0; c < DH / 64; ++c)
                 tc::tma_load_3d(smem + t * Y::kTileB + c * Y::kHalf, &tm_q, &S.q_full, c * 64, h * a.g,
-                                it.q0 + it.tok0 + t * P.per_tile);
+                                it.q0 + it.tok0 + t * P.per_tile + rank * per);
           }
           ++loads_q;
           __syncwarp();
@@ -382,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           uint8_t* dst = smem + Y::kOffCode + st * Y::kCodeB;
-          for (int x = 0; x < n_box; ++x) {
+          for (int x = x0; x < x1; ++x) {
             const int sx = __shfl_sync(0xffffffffu, slot, x);
-            if (tc::elect_one()) tc::tma_load_3d(dst + x * box * DH, map, &S.code_full[st], 0, h, sx);
+            if (tc::elect_one()) tc::tma_load_3d(dst + (x - x0) * box * row_b, map, &S.code_full[st], col, h, sx);
             __syncwarp();
           }
           mine |= 1u;
@@ -424,8 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The whole warp walks the loop, so that stages and descriptors stay in uniform registers, and one lane
       // issues: from a branch of one thread each product took 80 cycles to issue, longer than it runs. One warp
       // issues for both units, in turn: with a warp each, the units fell into step and waited together.
-      const uint32_t id_qk = tc::idesc_f16(kTile, kTile, false);
-      const uint32_t id_pv = tc::idesc_f16(kTile, DH, false) | tc::kIdescBMajorMN;
+      // Of a pair, the first CTA's issues for both, and the other's hands on what its converters say.
+      const uint32_t id_qk = tc::idesc_f16(kTile * Y::kParts, kTile, false);
+      const uint32_t id_pv = tc::idesc_f16(kTile * Y::kParts, DH, false) | tc::kIdescBMajorMN;
       const uint32_t base = tc::smem_addr(smem);
       const uint64_t dq = tc::sdesc_sw128(base, 16, 1024), dk = tc::sdesc_sw128(base + Y::kOffKv, 16, 1024);
       const uint64_t dv = tc::sdesc_sw128(base + Y::kOffKv, Y::kHalf, 1024);
@@ -438,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto stage = [&]() -> int {        // waits for the next stage of the ring and takes it
         const int s = st;
-        wait(&S.full[s], par);
+        if constexpr (PAIR) wait_pair(&S.full[s], par, abort_flag, P.wait_ns);
+        else wait(&S.full[s], par);
         if (++st == Y::kStages) {
           st = 0;
           par ^= 1;
@@ -447,23 +584,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // S_u = Q K^T of key stage s; `last`: the item's last product that reads the queries
       auto qk = [&](int u, uint64_t q, int s, bool free, bool last) {
-        const uint64_t kd = dk + uint64_t(s) * (Y::kTileB >> 4);
+        const uint64_t kd = dk + uint64_t(s) * (Y::kStageB >> 4);
         __syncwarp();
         tc::tc_fence_after();
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < DH / 16; ++k) {
-            const uint64_t off = ((k / 4) * Y::kHalf + (k % 4) * 32) >> 4;
-            tc::umma_f16(tmem + u * kTile, q + off, kd + off, id_qk, k != 0);
+            const uint64_t qo = ((k / 4) * Y::kHalf + (k % 4) * 32) >> 4, ko = ((k / 4) * Y::kKeyHalf + (k % 4) * 32) >> 4;
+            if constexpr (PAIR) umma_pair(tmem + u * kTile, q + qo, kd + ko, id_qk, k != 0);
+            else tc::umma_f16(tmem + u * kTile, q + qo, kd + ko, id_qk, k != 0);
           }
-          tc::umma_commit(&S.s_full[u]);
-          if (free) tc::umma_commit(&S.empty[s]);
-          if (last) tc::umma_commit(&S.q_empty);
+          commit<PAIR>(&S.s_full[u]);
+          if (free) commit<PAIR>(&S.empty[s]);
+          if (last) commit<PAIR>(&S.q_empty);
         }
       };
       // O_u += P_u V of value stage s, the first half's weights first; `last`: the item's last for the unit
       auto pv = [&](int u, int s, bool first, bool free, bool last) {
-        const uint64_t vd = dv + uint64_t(s) * (Y::kTileB >> 4);
+        const uint64_t vd = dv + uint64_t(s) * (Y::kStageB >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           wait(&S.p_full[u][half], np[u]);
@@ -472,10 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tc::elect_one()) {
 #pragma unroll
             for (int k = half * 4; k < half * 4 + 4; ++k)
-              tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, vd + ((k * 2048) >> 4), id_pv,
-                              !first || k != 0);
-            if (half == 1 && free) tc::umma_commit(&S.empty[s]);
-            if (half == 1 && last) tc::umma_commit(&S.o_full[u]);
+              if constexpr (PAIR)
+                umma_pair_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, vd + ((k * 2048) >> 4), id_pv, !first || k != 0);
+              else
+                tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, vd + ((k * 2048) >> 4), id_pv, !first || k != 0);
+            if (half == 1 && free) commit<PAIR>(&S.empty[s]);
+            if (half == 1 && last) commit<PAIR>(&S.o_full[u]);
           }
         }
         np[u] ^= 1;
@@ -495,7 +635,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it.tiles == 0) break;
         const int n = it.kv1 - it.kv0;
         if (n == 0) continue;
-        wait(BF16 ? &S.q_ready : &S.q_full, loads_q & 1);
+        if (rank != 0) {
+          for (int k = 0; k < 2 * n && !dead(); ++k) {
+            const int s = st;
+            wait(&S.full[s], par);
+            if (++st == Y::kStages) {
+              st = 0;
+              par ^= 1;
+            }
+            if (lane == 0) arrive_peer(&S.full[s], 0);
+          }
+          continue;
+        }
+        if constexpr (PAIR) wait_pair(&S.q_ready, loads_q & 1, abort_flag, P.wait_ns);
+        else wait(&S.q_ready, loads_q & 1);
         ++loads_q;
         if (it.tiles == 2) {
           // both units over each tile; unit 0 may see fewer (it stops first)
@@ -507,11 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < n; ++k) {
             if (dead()) break;
             const int sv = stage();
+            if (PAIR && k + 1 < n) sk = stage();   // before the weights come: a look at the pair's barriers takes 200 clocks
             if (k < n0) pv(0, sv, k == 0, false, k + 1 == n0);
-            if (k + 1 < n) {
-              sk = stage();
-              if (k + 1 < n0) qk(0, dq, sk, false, false);
-            }
+            if (!PAIR && k + 1 < n) sk = stage();
+            if (k + 1 < n0) qk(0, dq, sk, false, false);
             pv(1, sv, k == 0, true, k + 1 == n);
             if (k + 1 < n) qk(1, dq1, sk, true, k + 2 == n);
           }
@@ -524,30 +676,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < n; ++k) {
             if (dead()) break;
             const int sv = stage();
+            int sk = 0;
+            if (PAIR && k + 2 < n) sk = stage();
             pv(k & 1, sv, k < 2, true, k + 2 >= n);
-            if (k + 2 < n) {
-              const int sk = stage();
-              qk(k & 1, dq, sk, true, k + 3 == n);
-            }
+            if (!PAIR && k + 2 < n) sk = stage();
+            if (k + 2 < n) qk(k & 1, dq, sk, true, k + 3 == n);
           }
         }
         __syncwarp();
       }
       __syncwarp();
-      // every product issued has completed once this commit lands
+      // every product issued has completed once this commit lands, at both CTAs
       volatile int quiet = 0;
-      if (tc::elect_one()) tc::umma_commit(&S.drained);
+      if (rank == 0 && tc::elect_one()) commit<PAIR>(&S.drained);
       __syncwarp();
-      tc::mbar_wait_bounded(&S.drained, 0, &quiet, P.wait_ns);
+      tc::mbar_wait_bounded(&S.drained, 0, &quiet, Y::kParts * P.wait_ns);
     }
   } else {
     // ------------------------------------------------------------------ softmax
-    tc::regs_grow<kRegsSoftmax>();
+    tc::regs_grow<Y::kRegsSoftmax>();
     const int u = warp >> 2;
     const int r = (warp & 3) * 32 + lane;                        // query row of the tile = lane of tensor memory
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + u * kTile, t_o = tmem + lanes + Y::kColO + u * DH;
-    int n_s = 0, n_o = 0, n_o0 = 0, n_x = 0, n_q = 0, n_k = 0;
+    int n_s = 0, n_o = 0, n_o0 = 0, n_x = 0, n_q = 0, n_k = 0, n_l = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t par) {
       ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, par, abort_flag, P.wait_ns));
@@ -562,31 +714,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.tiles == 0) break;
       if (threadIdx.x == 0 && it.split >= 0) ++S.cut;
       const int tile = it.tiles == 2 ? u : 0;
-      const int first_tok = it.tok0 + tile * P.per_tile;
+      const int first_tok = it.tok0 + tile * P.per_tile + (PAIR ? (int)cta_rank() * per : 0);
       const int tok = first_tok + r / a.g;
-      const bool live = r < P.per_tile * a.g && tok < it.n;
+      const bool live = r < per * a.g && tok < it.n;
       const int vis = it.L - it.n + tok;                         // last slot this row sees
       const int vis_min = it.L - it.n + first_tok;               // every row of the tile sees slots up to here
       const int steps = unit_steps(it, u, P.per_tile);
       const bool exchange = it.tiles == 1 && it.kv1 - it.kv0 > 1;
 
       float c = a.scale_log2;                                    // of this row's scores: without its lift
-      if (BF16 && it.kv1 > it.kv0) {
-        float lift = 1.f;
+      if (it.kv1 > it.kv0) {
         if (!wait(&S.q_full, n_q & 1)) break;                    // both units: neither arrives for an item to come
-        if (it.tiles == 2 || u == 0) {
-          if (r < P.per_tile * a.g) lift = lift_row<DH>(smem + tile * Y::kTileB, r);
-          if (it.tiles == 1) S.lift[r] = lift;
-          tc::fence_async_smem();
+        if constexpr (BF16) {
+          float lift = 1.f;
+          if (it.tiles == 2 || u == 0) {
+            if (r < per * a.g) lift = lift_row<DH>(smem + tile * Y::kTileB, r);
+            if (it.tiles == 1) S.lift[r] = lift;
+            tc::fence_async_smem();
+          }
+          __syncwarp();
+          if (it.tiles == 1) {
+            if (u == 0 && lane == 0) tc::mbar_arrive(&S.lift_full);
+            if (u == 1) {
+              if (!wait(&S.lift_full, n_l & 1)) break;
+              lift = S.lift[r];
+            }
+            ++n_l;
+          }
+          c *= 1.f / lift;                                       // powers of two
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.q_ready);
-        if (it.tiles == 1 && u == 1 && steps > 0) {
-          if (!wait(&S.q_ready, n_q & 1)) break;
-          lift = S.lift[r];
+        if (lane == 0) {
+          if constexpr (PAIR) arrive_peer(&S.q_ready, 0);
+          else tc::mbar_arrive(&S.q_ready);
         }
         ++n_q;
-        c *= 1.f / lift;                                         // powers of two
       }
 
       float m = -INFINITY, l = 0.f;
@@ -670,7 +832,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_st_wait();
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&S.p_full[u][x >> 1]);
+            if (lane == 0) {
+              if constexpr (PAIR) arrive_peer_relaxed(&S.p_full[u][x >> 1], 0);
+              else tc::mbar_arrive(&S.p_full[u][x >> 1]);
+            }
           }
         }
       }
@@ -716,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mn;
       }
       const int64_t row = (int64_t)(it.q0 + tok) * a.n_heads + it.h * a.g + r % a.g;
-      const int64_t slot = ((int64_t)it.split * a.n_kv + it.h) * 2 + tile;
+      const int64_t slot = (((int64_t)it.split * a.n_kv + it.h) * 2 + tile) * Y::kParts + (PAIR ? (int)cta_rank() : 0);
       if (it.split < 0) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         f0 *= inv;
@@ -778,16 +943,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x == 0) {
         __threadfence();
         atomicAdd(&P.plan.head->pieces, S.cut);
-        ok = pieces_wait(&P.plan.head->pieces, unsigned(S.plan.slots * a.n_kv), P.wait_ns);
+        ok = pieces_wait(&P.plan.head->pieces, unsigned(S.plan.slots * a.n_kv * Y::kParts), P.wait_ns);
         if (!ok) *abort_flag = 1;
       }
       // the queries' space is free: nothing is in flight behind the last item
-      if (!any(!ok)) join_pieces<DH, BF16>(P, S.plan, rows, *reinterpret_cast<JoinShared*>(smem));
+      if (!any(!ok)) join_pieces<DH, BF16, 2 * Y::kParts>(P, S.plan, rows, *reinterpret_cast<JoinShared*>(smem));
     }
   }
 
   tc::tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_meet();
   tc::tc_fence_after();
   if (threadIdx.x == 0) {
     if (*abort_flag) record_error(a.err, kCodeTimeout, kErrWait, blockIdx.x, 0);
@@ -795,14 +961,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __threadfence();
     if (atomicInc(&P.plan.head->done, gridDim.x - 1) == gridDim.x - 1) P.plan.head->next = P.plan.head->pieces = 0;
   }
-  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+  if (warp == 9) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+    else tc::tmem_dealloc(tmem, 512);
+  }
 }
 
-template <int DH, bool BF16> cudaError_t prepare_tc() {
-  return cudaFuncSetAttribute(kv8_attend_tc_kernel<DH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Lay<DH>::kSmem);
+template <int DH, bool BF16, bool PAIR> cudaError_t prepare_tc() {
+  return cudaFuncSetAttribute(kv8_attend_tc_kernel<DH, BF16, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Lay<DH, PAIR>::kSmem);
 }
-template <int DH, bool BF16> cudaError_t launch_tc(const Kv8AttendArgs& A, const KvTcPlan& t, cudaStream_t st) {
+template <int DH, bool BF16, bool PAIR> cudaError_t launch_tc(const Kv8AttendArgs& A, const KvTcPlan& t, cudaStream_t st) {
+  using Y = Lay<DH, PAIR>;
   const KvAttendArgs& a = A.a;
   Tc8Params P8{};
   P8.k_scale = A.k_scale;
@@ -810,47 +980,72 @@ template <int DH, bool BF16> cudaError_t launch_tc(const Kv8AttendArgs& A, const
   TcParams& P = P8.P;
   P.a = a;
   P.plan = t;
-  P.per_tile = kTile / a.g;
+  const int per = kTile / a.g, sms = t.sm_count / Y::kParts;   // tokens of 128 rows; CTAs or pairs
+  P.per_tile = per * Y::kParts;
+  P.plan.sm_count = sms;
+  P.plan.slots = t.slots / Y::kParts;          // a pair's piece stores twice the rows
   P.out_sectors = (uintptr_t)a.out % 32 == 0;
   P.wait_ns = t.wait_ns;
   CUtensorMap tm_q, tm_k, tm_v;
   {
-    // queries [token][head][d]: boxes of 64 columns, one group's heads, a tile's tokens
+    // queries [token][head][d]: boxes of 64 columns, one group's heads, the tokens of 128 rows
     const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t dims[3] = {DH, (cuuint64_t)a.n_heads, (cuuint64_t)a.rows.n_tokens};
     const cuuint64_t strides[2] = {DH * 2, (cuuint64_t)a.q_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)P.per_tile};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)per};
     if (!tma_encode(&tm_q, dt, 3, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
   }
   {
     // codes [slot][kv head][d]. A box lies in one page: the largest power of two (16 and more) that divides a page, and
-    // without a table, where a row's tokens lie in a row, a whole tile.
-    P.box = a.rows.page_table ? a.pages.page_size & -a.pages.page_size : kTile;
-    P.box = P.box > kTile ? kTile : P.box;
+    // without a table, where a row's tokens lie in a row, a whole tile; of a pair, half a tile at most, and of the values
+    // half the columns.
+    constexpr int kBox = kTile / Y::kParts;
+    P.box = a.rows.page_table ? a.pages.page_size & -a.pages.page_size : kBox;
+    P.box = P.box > kBox ? kBox : P.box;
     const cuuint64_t dims[3] = {DH, (cuuint64_t)a.n_kv, (cuuint64_t)(a.pages.n_pages * a.pages.page_size)};
     const cuuint64_t strides[2] = {DH, (cuuint64_t)a.n_kv * DH};
-    const cuuint32_t box[3] = {DH, 1, (cuuint32_t)P.box};
-    const CUtensorMapSwizzle sw = DH == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-    if (!tma_encode(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.k, dims, strides, box, sw) ||
-        !tma_encode(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.v, dims, strides, box, sw))
-      return cudaErrorInvalidValue;
+    auto map = [&](CUtensorMap* m, const void* p, int columns) {
+      const cuuint32_t box[3] = {(cuuint32_t)columns, 1, (cuuint32_t)P.box};
+      const CUtensorMapSwizzle sw = columns == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+      return tma_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p, dims, strides, box, sw);
+    };
+    if (!map(&tm_k, a.pages.k, DH) || !map(&tm_v, a.pages.v, DH / Y::kParts)) return cudaErrorInvalidValue;
   }
-  const int64_t most = ((int64_t)t.tile_cap + t.slots) * a.n_kv;
-  const unsigned grid = (unsigned)(most < t.sm_count ? most : t.sm_count);
-  return launch_early(kv8_attend_tc_kernel<DH, BF16>, dim3(grid), kThreads, Lay<DH>::kSmem, st, tm_q, tm_k, tm_v, P8);
+  const int64_t most = ((int64_t)t.tile_cap + P.plan.slots) * a.n_kv;
+  const unsigned grid = (unsigned)(most < sms ? most : sms) * Y::kParts;
+  return launch_early<Y::kParts>(kv8_attend_tc_kernel<DH, BF16, PAIR>, dim3(grid), kThreads, Y::kSmem, st, tm_q, tm_k, tm_v, P8);
+}
+
+// Pairs take where there is enough work for them and its rows fill their tiles, by the call's averages and bounds (any choice is right).
+//   * An item of a pair is 512 query rows. Its start, its end and the rows that a causal item computes in vain cost more
+//     than an item of 256, so a pair must have at least 24 steps (of two tiles) to do: 128 tokens of 4 heads, 8 key/value
+//     heads, at 32768 (27 steps): 81 us against 88; at 8192 (7): 38 against 36; 16 sequences of 256 such tokens at 4096
+//     (107): 273 against 302; four of 1024 at 1024 (14): 69 against 67.
+//   * Where a sequence's last item is half empty for want of rows, one CTA alone would have skipped that half. A pair's
+//     steps take about 7/8 of the time, which makes up for that from 1536 rows on: 16 sequences at 4096 of 768 rows take
+//     255 us by pairs against 233, of 1792 rows 454 against 474, of 2400 rows 588 against 656.
+bool in_pairs(const KvAttendArgs& a, int sms) {
+  if (a.head_dim != 128) return false;
+  const int64_t rows = ((int64_t)a.rows.n_tokens * a.g + a.rows.batch - 1) / a.rows.batch;
+  const int64_t ones = (rows + 2 * kTile - 1) / (2 * kTile), pairs = (ones + 1) / 2;
+  const int64_t steps = ((int64_t)a.rows.max_kv_len - a.rows.max_new / 2) / kTile;
+  return 14 * pairs <= 8 * ones && a.rows.batch * pairs * a.n_kv * steps >= (int64_t)24 * (sms / 2);
 }
 
 }  // namespace
 
 cudaError_t prepare_kv8_attend_tc(int head_dim, bool bf16) {
-  if (head_dim == 128) return bf16 ? prepare_tc<128, true>() : prepare_tc<128, false>();
-  return bf16 ? prepare_tc<64, true>() : prepare_tc<64, false>();
+  if (head_dim == 64) return bf16 ? prepare_tc<64, true, false>() : prepare_tc<64, false, false>();
+  const cudaError_t e = bf16 ? prepare_tc<128, true, false>() : prepare_tc<128, false, false>();
+  if (e != cudaSuccess) return e;
+  return bf16 ? prepare_tc<128, true, true>() : prepare_tc<128, false, true>();
 }
 
 cudaError_t launch_kv8_attend_tc(const Kv8AttendArgs& a, const KvTcPlan& t, cudaStream_t st) {
   if (!tma_available()) return cudaErrorNotSupported;
-  if (a.a.head_dim == 128) return a.a.bf16 ? launch_tc<128, true>(a, t, st) : launch_tc<128, false>(a, t, st);
-  return a.a.bf16 ? launch_tc<64, true>(a, t, st) : launch_tc<64, false>(a, t, st);
+  if (a.a.head_dim == 64) return a.a.bf16 ? launch_tc<64, true, false>(a, t, st) : launch_tc<64, false, false>(a, t, st);
+  if (in_pairs(a.a, t.sm_count)) return a.a.bf16 ? launch_tc<128, true, true>(a, t, st) : launch_tc<128, false, true>(a, t, st);
+  return a.a.bf16 ? launch_tc<128, true, false>(a, t, st) : launch_tc<128, false, false>(a, t, st);
 }
 
 }  // namespace palu

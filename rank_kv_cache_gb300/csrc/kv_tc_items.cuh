@@ -198,7 +198,8 @@ struct JoinShared {
   float2 ml[kJoinWarps][32];
 };
 
-template <int DH, bool BF16>
+// SUB: tiles of 128 rows that an item has at most.
+template <int DH, bool BF16, int SUB = 2>
 __device__ __forceinline__ void join_pieces(const TcParams& P, const Plan& plan, Rows32& rows, JoinShared& X) {
   const KvAttendArgs& a = P.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -206,11 +207,12 @@ __device__ __forceinline__ void join_pieces(const TcParams& P, const Plan& plan,
   rows_cut(rows, plan.target);
   // unit: columns fastest, then heads, tiles, and last the row groups of which a tile may have none
   constexpr int kParts = DH / 16;
+  const int per = P.per_tile / (SUB / 2);                          // tokens of 128 rows
   const int inner = plan.joins * a.n_kv * kParts;
-  const int live = (min(2 * P.per_tile, a.rows.max_new) * a.g + kJoinRows - 1) / kJoinRows;
+  const int live = (min(SUB * per, a.rows.max_new) * a.g + kJoinRows - 1) / kJoinRows;
   const bool share = plan.slots >= 2 * kJoinWarps * plan.joins && (int64_t)inner * live <= gridDim.x;
   const int first = share ? blockIdx.x : blockIdx.x + gridDim.x * warp, step = gridDim.x * (share ? 1 : kJoinWarps);
-  for (int un = first; un < inner * 2 * (kTile / kJoinRows); un += step) {
+  for (int un = first; un < inner * SUB * (kTile / kJoinRows); un += step) {
     const int group = un / inner, in_group = un % inner, join = in_group / kParts / a.n_kv;
     Rows32 x = rows;                                               // the row of the cut tile
     unsigned at;
@@ -222,15 +224,14 @@ __device__ __forceinline__ void join_pieces(const TcParams& P, const Plan& plan,
     const int q0 = __shfl_sync(0xffffffffu, x.q0, src), n = __shfl_sync(0xffffffffu, x.n, src);
     const int pieces = __shfl_sync(0xffffffffu, x.pieces, src);
     const int slot = __shfl_sync(0xffffffffu, x.slot0, src) + in_row * pieces;
-    const int tok0 = (__shfl_sync(0xffffffffu, x.tiles, src) - 1 - in_row) * 2 * P.per_tile;
-    const int tiles = n - tok0 > P.per_tile ? 2 : 1;
-    const int h = in_group / kParts % a.n_kv, tile = group % 2, r0 = group / 2 * kJoinRows, r = r0 + lane;
+    const int tok0 = (__shfl_sync(0xffffffffu, x.tiles, src) - 1 - in_row) * SUB * per;
+    const int h = in_group / kParts % a.n_kv, tile = group % SUB, r0 = group / SUB * kJoinRows, r = r0 + lane;
     const int c0 = in_group % kParts * 4;
-    if (tile >= tiles || r0 >= P.per_tile * a.g || tok0 + tile * P.per_tile + r0 / a.g >= n) continue;
-    const int i = tok0 + tile * P.per_tile + r / a.g;
-    const bool live_row = r < P.per_tile * a.g && i < n;
-    const int64_t s0 = ((int64_t)slot * a.n_kv + h) * 2 + tile;
-    const int64_t pitch = (int64_t)2 * a.n_kv * kTile;             // rows between two pieces' partials
+    if (r0 >= per * a.g || tok0 + tile * per + r0 / a.g >= n) continue;
+    const int i = tok0 + tile * per + r / a.g;
+    const bool live_row = r < per * a.g && i < n;
+    const int64_t s0 = ((int64_t)slot * a.n_kv + h) * SUB + tile;
+    const int64_t pitch = (int64_t)SUB * a.n_kv * kTile;           // rows between two pieces' partials
     const float2* ml = a.part_ml + s0 * kTile + r;
     const float4* po = reinterpret_cast<const float4*>(a.part_o) + (s0 * (DH / 4) + c0) * kTile + r;
     float M = -INFINITY, L = 0.f;
