@@ -17,7 +17,10 @@
 //     l = sum over blocks of (sum w) / s_v, so that one exponential serves both and the fp16 weights are relative to the
 //     largest weight that enters the product, whatever the scales (up to 2^15 of it, see softmax_base).
 //
-// Bound: HBM; half the bytes of a 16-bit cache in as many copies.
+// Bound: HBM; half the bytes of a 16-bit cache in as many copies (four tokens at 65536, 8 heads of 128, 4 query rows each: 91
+// us, 5.9 TB/s of 6.8; 103 with two CTAs an SM and three stages). With more query rows the warps' own steps bound it: eight
+// rows of 20 at 1600 to 16384 take 65 us at 44 % of the bandwidth. Two warps sharing their tokens took 80 us there, rows as
+// the 16 of a matrix instruction (two blocks of it, half of the second empty) 67.
 #include "kv8.h"
 #include "kv_few.cuh"
 

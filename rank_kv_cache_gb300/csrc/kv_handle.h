@@ -10,7 +10,7 @@ namespace palu {
 
 // Partials of a call: work that is cut takes a slot for each piece. The cuts keep to these numbers, so the
 // workspace does not grow with the call. The two kernels' partials share the space.
-constexpr int kPartSlots = 2 * kKvFewMostCtas;   // few rows: pieces of 16 query rows (32 over 8-bit pages)
+constexpr int kPartSlots = 2 * kKvFewMostCtas;   // few rows: pieces of 16 query rows (24 over 8-bit pages)
 constexpr int kTcSlots = 456;      // tensor-core kernel: pieces x key/value heads, of two 128-row tiles
 
 struct KvLayout {

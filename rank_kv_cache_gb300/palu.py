@@ -723,6 +723,7 @@ class KVRows:
             raise ValueError("positions must hold n_tokens entries")
         self.tensors, self.index = (row_start, kv_len, page_table, positions), row_start.get_device()
         self.batch, self.n_tokens, self.max_new, self.max_kv_len = batch, int(n_tokens), int(max_new), int(max_kv_len)
+        self._ptrs = tuple(_ptr(t) for t in self.tensors)
         self._c = palu_kv_rows(_ptr(row_start), _ptr(kv_len), _ptr(page_table),
                                0 if page_table is None else int(page_table.shape[1]), _ptr(positions), batch,
                                self.n_tokens, self.max_new, self.max_kv_len)
@@ -752,7 +753,7 @@ class PagedAttention:
         self.device = self.workspace.device
         self._index = self.device.index
         self._current = torch._C._cuda_getCurrentRawStream
-        self._int = torch.int32
+        self._int, self._float = torch.int32, torch.float32
         self._kinds = {torch.float32: PALU_F32, torch.float16: PALU_F16, torch.bfloat16: PALU_BF16}
         base = int(self.workspace.data_ptr())
         st, self.handle = palu_kv_create(self.desc, base + (-base) % 256, nbytes, self._stream(stream))
@@ -857,7 +858,6 @@ class PagedAttention:
     def attend(self, pages: KVPages | KVPages8, rows: KVRows, q, *, out=None, lse=None, stream=None):
         """Causal attention of the new tokens' rotated queries q [n_tokens][n_heads][head_dim] over the pages.
         Returns out, of q's shape; lse, when given, is [n_tokens][n_heads] float32."""
-        torch = _torch()
         self._batch(pages, rows)
         N = rows.n_tokens
         qp, qs = self._view("q", q, self.n_heads, self.dtype, N)
@@ -866,8 +866,8 @@ class PagedAttention:
         op, os_ = self._view("out", out, self.n_heads, self.dtype, N)
         if os_ != self.n_heads * self.head_dim:
             raise ValueError("out must be contiguous")
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (N, self.n_heads) or
-                                lse.device != self.device or not lse.is_contiguous()):
+        if lse is not None and (lse.dtype is not self._float or lse.shape != (N, self.n_heads) or
+                                lse.get_device() != self._index or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous [{N}][{self.n_heads}] float32 tensor on {self.device}")
         call = _lib.palu_attend_kv8 if type(pages) is KVPages8 else _lib.palu_attend_kv
         check(call(self.handle, pages._c, rows._c, qp, qs, op, _ptr(lse), self._stream(stream)), call.__name__)
@@ -884,17 +884,19 @@ class PagedAttention:
         pool.page_table: its row_start, kv_len (which may be `kv_len`) and, where it has them, positions are written, and
         slots [n_tokens], the packed tokens' places in the pages. Rows are admitted in order while pages and
         rows.n_tokens last. held_out and state_out take what pool.held and pool.state become (None: in place)."""
-        row_start, kv_out, table, positions = rows.tensors
-        if table is None or table.data_ptr() != pool.page_table.data_ptr() or table.shape != pool.page_table.shape:
+        table = rows.tensors[2]
+        row_start, kv_out, _, positions = rows._ptrs
+        if table is not pool.page_table and (table is None or table.data_ptr() != pool.page_table.data_ptr() or
+                                             table.shape != pool.page_table.shape):
             raise ValueError("rows must stand over the pool's page table")
         if pool.index != self._index or rows.index != self._index:
             raise ValueError(f"pool and rows must be on {self.device}")
         B = rows.batch
         check(_lib.palu_plan_kv_rows(
             self.handle, pool._c, self._ints("new", new, (B,)), self._ints("kv_len", kv_len, (B,)), B, rows.n_tokens,
-            rows.max_new, rows.max_kv_len, row_start.data_ptr(), kv_out.data_ptr(),
+            rows.max_new, rows.max_kv_len, row_start, kv_out,
             None if held_out is None else self._ints("held_out", held_out, (B,)),
-            None if state_out is None else self._ints("state_out", state_out, (2,)), _ptr(positions),
+            None if state_out is None else self._ints("state_out", state_out, (2,)), positions,
             None if slots is None else self._ints("slots", slots, (rows.n_tokens,)), self._stream(stream)),
             "palu_plan_kv_rows")
         return rows
@@ -906,7 +908,7 @@ class PagedAttention:
         draft [batch][K][vocab] their probabilities in target's dtype (None: the drafts were certain), uniforms
         [batch][K + 1] in [0, 1). Returns (tokens [batch][K + 1]: accepted drafts, one drawn token, -1; accepted [batch]).
         kv_len [batch] loses the rejected tokens, into kv_len_out (None: in place)."""
-        torch, dtype = _torch(), target.dtype
+        dtype = target.dtype
         kind = self._kinds.get(dtype)
         if target.dim() != 2 or kind is None or target.get_device() != self._index or \
                 (target.stride(1) != 1 and target.shape[1] > 1):
@@ -924,13 +926,13 @@ class PagedAttention:
             draft_ptr, draft_stride = draft.data_ptr(), s1 if K > 1 else s0 if B > 1 else V
             if (s2 != 1 and V > 1) or (s0 != K * draft_stride and K > 1 and B > 1):
                 raise ValueError("draft: the rows of probabilities must lie evenly apart")
-        if uniforms.dtype is not torch.float32 or uniforms.shape != wide or uniforms.get_device() != self._index or \
+        if uniforms.dtype is not self._float or uniforms.shape != wide or uniforms.get_device() != self._index or \
                 not uniforms.is_contiguous():
             raise ValueError(f"uniforms must be a contiguous [{B}][{K + 1}] float32 tensor on {self.device}")
         if tokens is None:
-            tokens = self._empty(wide, torch.int32, stream)
+            tokens = self._empty(wide, self._int, stream)
         if accepted is None:
-            accepted = self._empty((B,), torch.int32, stream)
+            accepted = self._empty((B,), self._int, stream)
         if kv_len is None and kv_len_out is not None:
             raise ValueError("kv_len_out without kv_len")
         lens = None if kv_len is None else self._ints("kv_len", kv_len, (B,))
