@@ -317,11 +317,15 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
 }
 
 template <typename T> cudaError_t launch_typed(const KvVerifyArgs& a, int sm_count, cudaStream_t st) {
-  // The row's segments are shared by as many CTAs, 8 at most, as the GPU holds at once for all rows. One row over 131072
-  // tokens: 7.3 us by 8 CTAs, 9.9 by 4, 15.9 by 2, 28.3 by one; 128 rows: 23.6 by 4, 27.0 by 2, 40.2 by one.
-  unsigned ctas = kMostCtas;
-  while (ctas > 1 && (int64_t)a.batch * ctas > (int64_t)sm_count * kCtas) ctas /= 2;
+  // The row's segments are shared by 1 to 8 CTAs, of the numbers with which the GPU holds all rows' CTAs at once the least whose
+  // warps take the fewest segments one after the other. One row over 131072 tokens: 7.3 us by 8 CTAs, 9.9 by 4, 15.9 by 2, 28.3
+  // by one; 128 rows: 23.6 by 4, 27.0 by 2, 40.2 by one; 80 rows 18.9 by 7 against 22.3 by 4, 180 rows 30.7 by 3 against 39.4
+  // by 2. 80 rows over 32000: 10.8 by 4, 12.0 by 7, two segments a warp either way.
   const int segs = (a.vocab + kSeg - 1) / kSeg;
+  auto rounds = [&](int c) { return ((segs + c - 1) / c + kWarps - 1) / kWarps; };
+  int ctas = kMostCtas;
+  while (ctas > 1 && (int64_t)a.batch * ctas > (int64_t)sm_count * kCtas) --ctas;
+  while (ctas > 1 && rounds(ctas - 1) == rounds(ctas)) --ctas;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
