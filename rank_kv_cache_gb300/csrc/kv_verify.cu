@@ -56,6 +56,22 @@ struct Sum {
   }
   __device__ __forceinline__ bool over(const Sum& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
 };
+// two such sums, whose numbers are added by packed instructions
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) { return fma2(b, pair(-1.f, -1.f), a); }
+struct Sum2 {
+  uint64_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(uint64_t x, uint64_t rest) {
+    const uint64_t s = add2(hi, x), b = sub2(s, hi);
+    lo = add2(lo, add2(add2(sub2(hi, sub2(s, b)), sub2(x, b)), rest));
+    hi = s;
+  }
+  __device__ __forceinline__ Sum both() const {
+    const float2 h = unpair(hi), l = unpair(lo);
+    Sum r{h.x, l.x};
+    r.add(h.y, l.y);
+    return r;
+  }
+};
 __device__ __forceinline__ Sum shfl(const Sum& s, int lane) {
   return Sum{__shfl_sync(0xffffffffu, s.hi, lane), __shfl_sync(0xffffffffu, s.lo, lane)};
 }
@@ -120,13 +136,22 @@ template <typename T> struct Source {
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const float x = fmaxf(w.d[k][i], 0.f), y = q ? fmaxf(w.e[k][i], 0.f) : 0.f;   // NaN: 0
-        const float d = __fsub_rn(x, y);
-        const bool more = d > 0.f && v + k * 32 * kVec + i != certain;
-        w.d[k][i] = more ? d : 0.f;
-        w.e[k][i] = more ? __fsub_rn(__fsub_rn(x, d), y) : 0.f;
+      for (int i = 0; i < kVec; i += 2) {
+        // NaN: 0. What q is above p does not count: both results are then 0.
+        const float x0 = fmaxf(w.d[k][i], 0.f), x1 = fmaxf(w.d[k][i + 1], 0.f);
+        const float y0 = q ? fminf(fmaxf(w.e[k][i], 0.f), x0) : 0.f, y1 = q ? fminf(fmaxf(w.e[k][i + 1], 0.f), x1) : 0.f;
+        const uint64_t x = pair(x0, x1), y = pair(y0, y1), d = sub2(x, y);
+        const float2 d2 = unpair(d), e2 = unpair(sub2(sub2(x, d), y));
+        w.d[k][i] = d2.x, w.d[k][i + 1] = d2.y;
+        w.e[k][i] = e2.x, w.e[k][i + 1] = e2.y;
       }
+    if (certain >= v0 && certain < v0 + kSeg) {         // a rejected draft's p is below its 1
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          if (v + k * 32 * kVec + i == certain) w.d[k][i] = 0.f;   // and its rounding error is 0, as there is no q
+    }
   }
 };
 
@@ -218,11 +243,12 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
     for (int s = warp; s < mine; s += kWarps) {
       Weights w;
       src.load(w, (s0 + s) * kSeg);
-      Sum sum;
+      Sum2 two;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum.add(w.d[k][i], w.e[k][i]);
+        for (int i = 0; i < kVec; i += 2) two.add(pair(w.d[k][i], w.d[k][i + 1]), pair(w.e[k][i], w.e[k][i + 1]));
+      Sum sum = two.both();
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, o), lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
