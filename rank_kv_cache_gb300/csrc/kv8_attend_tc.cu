@@ -63,7 +63,7 @@ template <int DH, bool PAIR> struct Lay {
   static constexpr int kOffKv = 2 * kTileB;             // behind two query tiles
   static constexpr int kOffCode = kOffKv + kStages * kStageB;
   static constexpr int kOffBar = kOffCode + kCodes * kCodeB;
-  static constexpr int kShared = DH == 128 && !PAIR ? 2048 : 3072;   // barriers, items, scales, the units' exchange
+  static constexpr int kShared = DH == 128 && !PAIR ? 2048 : 4096;   // barriers, items, scales, the units' exchange
   static constexpr int kSmem = kOffBar + kShared + 1024;    // and alignment
   static constexpr uint32_t kColO = 2 * kTile;          // tensor memory: S (and P) of the units, then O
   static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
