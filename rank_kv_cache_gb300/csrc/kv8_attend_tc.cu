@@ -45,8 +45,10 @@ constexpr int kThreads = 512;            // two softmax warpgroups; two loader w
 constexpr int kBlocks = kTile / kKv8Block;
 
 template <int DH, bool PAIR> struct Lay {
-  // Registers: launched with 128 a thread; 256 softmax + 128 other + 128 convert = 512 * 128. A pair's loaders hold more.
-  static constexpr int kRegsSoftmax = PAIR ? 184 : 192, kRegsOther = PAIR ? 88 : 72, kRegsConvert = 56;
+  // Registers: launched with 128 a thread; 256 softmax + 128 other + 128 convert = 512 * 128. 2048 tokens at 32768, 32 / 8
+  // heads, in bf16 and fp16: 876 and 882 us; with 192, 72 and 56 874 and 978; 184, 88 and 56 925 and 959; 200, 56 and 56 909 and
+  // 878; 176, 96 and 64 964 and 1091.
+  static constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsConvert = 64;
   // Query tiles: 64 elements (128 bytes) of all rows, then the next 64. fp16 and code tiles hold the CTA's part: keys as the
   // queries (of a pair's CTA 64 tokens), values by 64 columns of all tokens. Rows of 128 bytes are swizzled.
   static constexpr int kHalf = kTile * 128;             // 64 elements of 128 rows
@@ -782,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) tc::tmem_ld32_nowait(t_s + x * 32, reinterpret_cast<uint32_t*>(s) + x * 32);
         tc::tmem_ld_wait();
+        float2 z[kBlocks];   // of each 16 scores: s_k c and log2 s_v, held (read again for the weights: 578 us against 562 for the prompts)
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
@@ -791,8 +794,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             y0 = max3(y0, s[b * 16 + y], s[b * 16 + y + 1]);
             y1 = max3(y1, s[b * 16 + y + 2], s[b * 16 + y + 3]);
           }
-          const float2 z = sc[b];
-          mx[b & 1] = fmaxf(mx[b & 1], fmaf(fmaxf(y0, y1), z.x * c, z.y));
+          z[b] = sc[b];
+          z[b].x *= c;
+          mx[b & 1] = fmaxf(mx[b & 1], fmaf(fmaxf(y0, y1), z[b].x, z[b].y));
         }
         const float top = softmax_base<false>(fmaxf(mx[0], mx[1]), kLift);
         const bool raise = top > m + kRaise;                     // true on the first finite score
@@ -819,8 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t p[16];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float2 z = sc[x * 2 + b];
-            const uint64_t c2 = pair(z.x * c, z.x * c), n2 = pair(z.y + neg, z.y + neg);
+            const float2 zb = z[x * 2 + b];
+            const uint64_t c2 = pair(zb.x, zb.x), n2 = pair(zb.y + neg, zb.y + neg);
             uint64_t sum2[2] = {0, 0};
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
@@ -830,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[b * 8 + y] = pack2<false>(p0, p1);
             }
             const float2 w = unpair(add2(sum2[0], sum2[1]));
-            l = fmaf(w.x + w.y, ex2(-z.y), l);                   // without the values' scale
+            l = fmaf(w.x + w.y, ex2(-zb.y), l);                   // without the values' scale
           }
           tc::tmem_st16(t_s + x * 16, p);
           if (x & 1) {                                           // 64 tokens' weights: the product may begin
