@@ -62,6 +62,7 @@ template <int DH, bool PAIR> struct Lay {
   // tiles whose values' products had not ended then count: of the kStages - 1 places before it, and of the values up to
   // three places behind their keys, at most kStages / 2 + 2.
   static constexpr int kScales = DH == 128 && !PAIR ? 4 : 8;
+  static constexpr bool kInverse = PAIR;                // room for the inverse scales (heads of 64 gain nothing)
   static constexpr int kOffKv = 2 * kTileB;             // behind two query tiles
   static constexpr int kOffCode = kOffKv + kStages * kStageB;
   static constexpr int kOffBar = kOffCode + kCodes * kCodeB;
@@ -95,6 +96,7 @@ template <int DH, bool PAIR> struct Shared {
   int abort_flag;
   float raw[Y::kCodes][2][kBlocks];       // scales of keys and values, as they arrive
   float2 scale[Y::kScales][kBlocks];      // s_k and log2 s_v
+  float part[Y::kInverse ? Y::kScales : 1][kBlocks];   // 1 / s_v
   union {
     float2 ml[kTile];                     // of the units' exchange, at an item's end
     float lift[kTile];                    // of the queries' rows where both units share a tile, at its beginning
@@ -326,8 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&S.empty[st], par)) break;
       if (keys) {
         if (warp == 12) {
-          if (lane < kBlocks)
-            S.scale[n_k % Y::kScales][lane] = make_float2(scale_or_one(S.raw[sc][0][lane]), lg2(scale_or_one(S.raw[sc][1][lane])));
+          if (lane < kBlocks) {
+            const float s_v = scale_or_one(S.raw[sc][1][lane]);
+            S.scale[n_k % Y::kScales][lane] = make_float2(scale_or_one(S.raw[sc][0][lane]), lg2(s_v));
+            if constexpr (Y::kInverse) S.part[n_k % Y::kScales][lane] = rcp(s_v);
+          }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&S.scale_full[n_k % Y::kScales]);
         }
@@ -765,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&S.s_full[u], n_s & 1)) break;
         ++n_s;
         const float2* sc = S.scale[kk % Y::kScales];
+        const float* part = S.part[Y::kInverse ? kk % Y::kScales : 0];
         const int t0 = tk * kTile;
         if (t0 + kTile - 1 > vis_min) {
           // tokens that a row does not see: masked in tensor memory, so that the common tile's code stays short
@@ -788,12 +794,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-          float y0 = fmaxf(s[b * 16], s[b * 16 + 1]), y1 = fmaxf(s[b * 16 + 2], s[b * 16 + 3]);
-#pragma unroll
-          for (int y = 4; y < 16; y += 4) {
-            y0 = max3(y0, s[b * 16 + y], s[b * 16 + y + 1]);
-            y1 = max3(y1, s[b * 16 + y + 2], s[b * 16 + y + 3]);
-          }
+          float y0 = max3(s[b * 16], s[b * 16 + 1], s[b * 16 + 2]), y1 = max3(s[b * 16 + 3], s[b * 16 + 4], s[b * 16 + 5]);
+          y0 = max3(y0, s[b * 16 + 6], s[b * 16 + 7]);
+          y1 = max3(y1, s[b * 16 + 8], s[b * 16 + 9]);
+          y0 = max3(y0, s[b * 16 + 10], s[b * 16 + 11]);
+          y1 = max3(y1, s[b * 16 + 12], s[b * 16 + 13]);
+          y0 = max3(y0, s[b * 16 + 14], s[b * 16 + 15]);
           z[b] = sc[b];
           z[b].x *= c;
           mx[b & 1] = fmaxf(mx[b & 1], fmaf(fmaxf(y0, y1), z[b].x, z[b].y));
@@ -825,16 +831,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < 2; ++b) {
             const float2 zb = z[x * 2 + b];
             const uint64_t c2 = pair(zb.x, zb.x), n2 = pair(zb.y + neg, zb.y + neg);
-            uint64_t sum2[2] = {0, 0};
+            uint64_t sum2[2];
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const float2 e = unpair(fma2(pair(s[x * 32 + b * 16 + 2 * y], s[x * 32 + b * 16 + 2 * y + 1]), c2, n2));
               const float p0 = ex2(e.x), p1 = ex2(e.y);
-              sum2[y & 1] = add2(sum2[y & 1], pair(p0, p1));
+              sum2[y & 1] = y < 2 ? pair(p0, p1) : add2(sum2[y & 1], pair(p0, p1));
               p[b * 8 + y] = pack2<false>(p0, p1);
             }
             const float2 w = unpair(add2(sum2[0], sum2[1]));
-            l = fmaf(w.x + w.y, ex2(-zb.y), l);                   // without the values' scale
+            l = fmaf(w.x + w.y, Y::kInverse ? part[x * 2 + b] : ex2(-zb.y), l);                   // without the values' scale
           }
           tc::tmem_st16(t_s + x * 16, p);
           if (x & 1) {                                           // 64 tokens' weights: the product may begin
