@@ -96,7 +96,7 @@ template <int DH, bool PAIR> struct Shared {
   int abort_flag;
   float raw[Y::kCodes][2][kBlocks];       // scales of keys and values, as they arrive
   float2 scale[Y::kScales][kBlocks];      // s_k and log2 s_v
-  float part[Y::kInverse ? Y::kScales : 1][kBlocks];   // 1 / s_v
+  float2 part[Y::kInverse ? Y::kScales : 1][Y::kInverse ? kBlocks : 1];   // 1 / s_v, twice
   union {
     float2 ml[kTile];                     // of the units' exchange, at an item's end
     float lift[kTile];                    // of the queries' rows where both units share a tile, at its beginning
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < kBlocks) {
             const float s_v = scale_or_one(S.raw[sc][1][lane]);
             S.scale[n_k % Y::kScales][lane] = make_float2(scale_or_one(S.raw[sc][0][lane]), lg2(s_v));
-            if constexpr (Y::kInverse) S.part[n_k % Y::kScales][lane] = rcp(s_v);
+            if constexpr (Y::kInverse) S.part[n_k % Y::kScales][lane] = make_float2(rcp(s_v), rcp(s_v));
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&S.scale_full[n_k % Y::kScales]);
@@ -763,14 +763,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_q;
       }
 
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY;
+      uint64_t l2 = 0;                                           // the sum, in two parts
       for (int k = 0; k < steps; ++k) {
         const int tk = unit_tile(it, u, k), kk = n_k + tk - it.kv0;
         if (!wait(&S.scale_full[kk % Y::kScales], (kk / Y::kScales) & 1)) break;
         if (!wait(&S.s_full[u], n_s & 1)) break;
         ++n_s;
         const float2* sc = S.scale[kk % Y::kScales];
-        const float* part = S.part[Y::kInverse ? kk % Y::kScales : 0];
+        const float2* part = S.part[Y::kInverse ? kk % Y::kScales : 0];
         const int t0 = tk * kTile;
         if (t0 + kTile - 1 > vis_min) {
           // tokens that a row does not see: masked in tensor memory, so that the common tile's code stays short
@@ -808,9 +809,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool raise = top > m + kRaise;                     // true on the first finite score
         if (__any_sync(0xffffffffu, raise)) {
           const float mn = raise ? top : m;
-          const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - mn);
+          const float f = m == -INFINITY ? 0.f : exp2f(m - mn);    // nothing seen yet: sum and output are 0
           m = mn;
-          l *= f;
+          l2 = mul2(l2, pair(f, f));
           if (k > 0) {   // s_full also says that the product before it, into O, has completed
 #pragma unroll 1
             for (int x = 0; x < DH; x += 16) {
@@ -839,8 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum2[y & 1] = y < 2 ? pair(p0, p1) : add2(sum2[y & 1], pair(p0, p1));
               p[b * 8 + y] = pack2<false>(p0, p1);
             }
-            const float2 w = unpair(add2(sum2[0], sum2[1]));
-            l = fmaf(w.x + w.y, Y::kInverse ? part[x * 2 + b] : ex2(-zb.y), l);                   // without the values' scale
+            float2 r = Y::kInverse ? part[x * 2 + b] : make_float2(ex2(-zb.y), 0.f);
+            if constexpr (!Y::kInverse) r.y = r.x;
+            l2 = fma2(add2(sum2[0], sum2[1]), pair(r.x, r.y), l2);   // without the values' scale
           }
           tc::tmem_st16(t_s + x * 16, p);
           if (x & 1) {                                           // 64 tokens' weights: the product may begin
@@ -856,6 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       n_k += it.kv1 - it.kv0;
+      float l = unpair(l2).x + unpair(l2).y;
 
       // the unit's row: O / l, or its partial
       if (steps > 0) {
