@@ -14,11 +14,13 @@
 //   * s_k multiplies 16 scores of a thread's row at once. With y_t = x_t + log2 s_v(t) and a running maximum of y, the
 //     weights 2^(y_t - M) are what c_v is multiplied by, and the sum takes them divided by s_v: one exponential
 //     serves both, and the fp16 weights are relative to the largest that enters the product, whatever the scales.
-// Bound: the softmax warps' chain from scores to weights to the next scores (2000 and 1100 to 1300 clocks of a step for two
+// Bound: the softmax warps' chain from scores to weights to the next scores (about 2000 and 1100 clocks of a step for two
 // tiles, of which the products need 1024), and what of the converters does not hide behind it: 2048 new tokens at 65536, 8 heads
-// of 128, 4 query rows each, 1783 us and 1.21 of 1.92 PFLOP/s; four prompts of 4096, 32 heads, 578 us. Without the maximum ahead
-// of the weights (raised afterwards where 16 weights' sum had left fp16) steps were no shorter, and first ones twice as
-// long: 806 us for the prompts. Queries loaded behind the next item's first keys: 592.
+// of 128, 4 query rows each, 1626 us and 1.33 of 1.92 PFLOP/s (tensor pipe 50 % busy at 16384); four prompts of 4096, 32
+// heads, 541 us. Each instruction counts: scales held over a step, inverse scales from the converters, three-way maxima
+// and packed sums took these from 1783 and 578. Without the maximum ahead of the weights (raised afterwards where 16 weights'
+// sum had left fp16) steps were no shorter, and first ones twice as long: 806 us for the prompts. Queries loaded behind the
+// next item's first keys: 592 (against 578).
 // A product straight on the codes (kind::f8f6f4) would want the queries and weights in 8 bits too, in two or three terms
 // each to keep their precision: as many products as in fp16, and the weights' terms in the softmax, which bounds the
 // kernel already.
@@ -1037,11 +1039,11 @@ template <int DH, bool BF16, bool PAIR> cudaError_t launch_tc(const Kv8AttendArg
 // Pairs take where there is enough work for them and its rows fill their tiles, by the call's averages and bounds.
 //   * An item of a pair is 512 query rows. Its start, its end and the rows that a causal item computes in vain cost more
 //     than an item of 256, so a pair must have at least 24 steps (of two tiles) to do: 128 tokens of 4 heads, 8 key/value
-//     heads, at 32768 (27 steps): 81 us against 88; at 8192 (7): 38 against 36; 16 sequences of 256 such tokens at 4096
-//     (107): 273 against 302; four of 1024 at 1024 (14): 69 against 67.
+//     heads, at 32768 (27 steps): 77 us against 82; at 8192 (7): 37 against 35; 16 sequences of 256 such tokens at 4096
+//     (107): 259 against 288; four of 1024 at 1024 (14): 69 against 67.
 //   * Where a sequence's last item is half empty for want of rows, one CTA alone would have skipped that half. A pair's
 //     steps take about 7/8 of the time, which makes up for that from 1536 rows on: 16 sequences at 4096 of 768 rows take
-//     255 us by pairs against 233, of 1792 rows 454 against 474, of 2400 rows 588 against 656.
+//     250 us by pairs against 222, of 1792 rows 428 against 441, of 2400 rows 548 against 604.
 bool in_pairs(const KvAttendArgs& a, int sms) {
   if (a.head_dim != 128) return false;
   const int64_t rows = ((int64_t)a.rows.n_tokens * a.g + a.rows.batch - 1) / a.rows.batch;
