@@ -64,11 +64,10 @@ template <int DH, bool PAIR> struct Lay {
   // tiles whose values' products had not ended then count: of the kStages - 1 places before it, and of the values up to
   // three places behind their keys, at most kStages / 2 + 2.
   static constexpr int kScales = DH == 128 && !PAIR ? 4 : 8;
-  static constexpr bool kInverse = PAIR;                // room for the inverse scales (heads of 64 gain nothing)
   static constexpr int kOffKv = 2 * kTileB;             // behind two query tiles
   static constexpr int kOffCode = kOffKv + kStages * kStageB;
   static constexpr int kOffBar = kOffCode + kCodes * kCodeB;
-  static constexpr int kShared = DH == 128 && !PAIR ? 2048 : 4096;   // barriers, items, scales, the units' exchange
+  static constexpr int kShared = DH == 128 && !PAIR ? 2048 : 4096;   // barriers, items, scales, lifts
   static constexpr int kSmem = kOffBar + kShared + 1024;    // and alignment
   static constexpr uint32_t kColO = 2 * kTile;          // tensor memory: S (and P) of the units, then O
   static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
@@ -86,7 +85,7 @@ template <int DH, bool PAIR> struct Shared {
   // of a pair: at the first CTA, from both: full, q_ready, p_full, idx_empty; at both, from the first one's products: empty,
   // q_empty, s_full, o_full, drained; the others from the CTA itself
   uint64_t full[Y::kStages], empty[Y::kStages], code_full[Y::kCodes], code_empty[Y::kCodes], scale_full[Y::kScales];
-  uint64_t q_full, q_ready, q_empty, lift_full, x_full, x_empty, drained;
+  uint64_t q_full, q_ready, q_empty, lift_full, x_full, drained;
   uint64_t s_full[2], o_full[2], p_full[2][2];
   uint64_t item_full[2], item_empty[2], idx_full[2], idx_empty[2];
   int idx[2];                             // items' numbers, from the pair's first CTA
@@ -98,11 +97,8 @@ template <int DH, bool PAIR> struct Shared {
   int abort_flag;
   float raw[Y::kCodes][2][kBlocks];       // scales of keys and values, as they arrive
   float2 scale[Y::kScales][kBlocks];      // s_k and log2 s_v
-  float2 part[Y::kInverse ? Y::kScales : 1][Y::kInverse ? kBlocks : 1];   // 1 / s_v, twice
-  union {
-    float2 ml[kTile];                     // of the units' exchange, at an item's end
-    float lift[kTile];                    // of the queries' rows where both units share a tile, at its beginning
-  };
+  float2 part[Y::kScales][kBlocks];       // 1 / s_v, twice
+  float lift[kTile];                      // of the queries' rows where both units share a tile
 };
 template <int DH, bool PAIR> constexpr bool fits = sizeof(Shared<DH, PAIR>) <= Lay<DH, PAIR>::kShared;
 static_assert(fits<128, false> && fits<64, false> && fits<128, true>, "shared block");
@@ -124,6 +120,19 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_addr(bar)), "r"(n) : "memory");
+}
+
+// two columns of this warp's lanes of tensor memory
+__device__ __forceinline__ void tmem_st2(uint32_t ta, float a, float b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(ta), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ float2 tmem_ld2(uint32_t ta) {
+  float2 v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\ntcgen05.wait::ld.sync.aligned;"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(ta)
+               : "memory");
+  return v;
 }
 
 // Lifts a row of bf16 queries, as TMA left it (two halves of 64 elements, 128-byte swizzle), to fp16 in place.
@@ -260,7 +269,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&S.lift_full, 4);
     tc::mbar_init(&S.q_empty, 1);              // the products that read the queries
     tc::mbar_init(&S.x_full, 4);
-    tc::mbar_init(&S.x_empty, 4);
     tc::mbar_init(&S.drained, 1);
     for (int u = 0; u < 2; ++u) {
       tc::mbar_init(&S.s_full[u], 1);
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < kBlocks) {
             const float s_v = scale_or_one(S.raw[sc][1][lane]);
             S.scale[n_k % Y::kScales][lane] = make_float2(scale_or_one(S.raw[sc][0][lane]), lg2(s_v));
-            if constexpr (Y::kInverse) S.part[n_k % Y::kScales][lane] = make_float2(rcp(s_v), rcp(s_v));
+            S.part[n_k % Y::kScales][lane] = make_float2(rcp(s_v), rcp(s_v));
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&S.scale_full[n_k % Y::kScales]);
@@ -393,8 +401,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int table_pages = int(a.rows.table_pages), n_pages = int(a.pages.n_pages);
       const int oob_slot = n_pages * ps;
       int st = 0, loads_q = 0, seq = 0;    // the ring's next stage; stages counted
-      int n_x = 0;                         // exchanges of the units, and whether the last is still to be waited for
-      bool exchanged = false;
       uint32_t par = 1, mine = 0;          // what `code_empty` is waited for; which of the last stages this warp filled
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -471,10 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kv1 == kv0) continue;
         const int32_t* table = a.rows.page_table ? a.rows.page_table + (int64_t)b * table_pages : nullptr;
         if (keys) {
-          // the queries' space: read by the last item's products and, where its units met there, by warpgroup 0
+          // the queries' space: read by the last item's products
           if (!wait(&S.q_empty, (loads_q & 1) ^ 1)) break;
-          if (exchanged && !wait(&S.x_empty, n_x++ & 1)) break;
-          exchanged = tiles == 1 && kv1 - kv0 > 1;
           if (lane == 0) {
             tc::mbar_arrive_expect_tx(&S.q_full, uint32_t(tiles) * per * a.g * DH * 2);
             for (int t = 0; t < tiles; ++t)
@@ -713,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;                        // query row of the tile = lane of tensor memory
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + u * kTile, t_o = tmem + lanes + Y::kColO + u * DH;
-    int n_s = 0, n_o = 0, n_o0 = 0, n_x = 0, n_q = 0, n_k = 0, n_l = 0;
+    int n_s = 0, n_o = 0, n_x = 0, n_q = 0, n_k = 0, n_l = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t par) {
       ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, par, abort_flag, P.wait_ns));
@@ -773,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&S.s_full[u], n_s & 1)) break;
         ++n_s;
         const float2* sc = S.scale[kk % Y::kScales];
-        const float2* part = S.part[Y::kInverse ? kk % Y::kScales : 0];
+        const float2* part = S.part[kk % Y::kScales];
         const int t0 = tk * kTile;
         if (t0 + kTile - 1 > vis_min) {
           // tokens that a row does not see: masked in tensor memory, so that the common tile's code stays short
@@ -842,9 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum2[y & 1] = y < 2 ? pair(p0, p1) : add2(sum2[y & 1], pair(p0, p1));
               p[b * 8 + y] = pack2<false>(p0, p1);
             }
-            float2 r = Y::kInverse ? part[x * 2 + b] : make_float2(ex2(-zb.y), 0.f);
-            if constexpr (!Y::kInverse) r.y = r.x;
-            l2 = fma2(add2(sum2[0], sum2[1]), pair(r.x, r.y), l2);   // without the values' scale
+            const float2 inv = part[x * 2 + b];
+            l2 = fma2(add2(sum2[0], sum2[1]), pair(inv.x, inv.y), l2);   // without the values' scale
           }
           tc::tmem_st16(t_s + x * 16, p);
           if (x & 1) {                                           // 64 tokens' weights: the product may begin
@@ -867,22 +870,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&S.o_full[u], n_o & 1)) break;
         ++n_o;
       }
-      float* xs = reinterpret_cast<float*>(smem);                // [d / 4][128 rows][4] in the queries' space
-      if (u == 1 && unit_steps(it, 0, P.per_tile) > 0) ++n_o0;
       if (exchange && u == 1) {
-        if (!wait(&S.o_full[0], (n_o0 - 1) & 1)) break;          // unit 0's products read the queries too
-#pragma unroll 1
-        for (int x = 0; x < DH / 32; ++x) {
-          uint32_t o[32];
-          tc::tmem_ld32_nowait(t_o + x * 32, o);
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int y = 0; y < 8; ++y)
-            *reinterpret_cast<uint4*>(xs + ((x * 8 + y) * kTile + r) * 4) =
-                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-        }
-        S.ml[r] = make_float2(m, l);
-        tc::fence_async_smem();
+        // the other unit finds this one's output where it is, and maximum and sum in place of its scores; the next products
+        // into either come behind the other's word that it is ready for another item
+        tmem_st2(t_s, m, l);
+        tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&S.x_full);
@@ -893,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (exchange) {
         if (!wait(&S.x_full, n_x & 1)) break;
         ++n_x;
-        const float2 o1 = S.ml[r];
+        const float2 o1 = tmem_ld2(t_s + kTile);
         const float mn = fmaxf(m, o1.x), b0 = mn == -INFINITY ? 0.f : mn;
         f0 = exp2f(m - b0);
         f1 = exp2f(o1.x - b0);
@@ -923,14 +915,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int y = 0; y < 32; ++y) o[y] = 0.f;
         }
         if (exchange) {
+          float o1[32];
+          tc::tmem_ld32_nowait(t_o + DH + x * 32, reinterpret_cast<uint32_t*>(o1));
+          tc::tmem_ld_wait();
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const float4 v = *reinterpret_cast<const float4*>(xs + ((x * 8 + y) * kTile + r) * 4);
-            o[4 * y] = fmaf(v.x, f1, o[4 * y]);
-            o[4 * y + 1] = fmaf(v.y, f1, o[4 * y + 1]);
-            o[4 * y + 2] = fmaf(v.z, f1, o[4 * y + 2]);
-            o[4 * y + 3] = fmaf(v.w, f1, o[4 * y + 3]);
-          }
+          for (int y = 0; y < 32; ++y) o[y] = fmaf(o1[y], f1, o[y]);
         }
         if (it.split >= 0 && live) {
           float4* po = reinterpret_cast<float4*>(a.part_o) + (slot * (DH / 4) + x * 8) * kTile + r;
@@ -948,11 +937,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::tc_fence_before();
-      if (exchange) {                                            // the queries' space is read: TMA may fill it again
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.x_empty);
-      }
     }
     // The join. Every item has been taken when a CTA comes here, by CTAs that run and wait for none: the wait for
     // their pieces ends whichever CTAs the GPU holds. All warps meet first, also after a wait that gave up.
