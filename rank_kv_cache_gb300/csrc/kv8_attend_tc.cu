@@ -552,11 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             par ^= 1;
           }
         };
-        const int lead = min(tiles == 1 ? 2 : 1, kv1 - kv0);
-        for (int j = kv0; ok && j < kv0 + lead; ++j) step(true, j);
-        for (int j = kv0; ok && j < kv1; ++j) {
-          step(false, j);
-          if (ok && j + lead < kv1) step(true, j + lead);
+        const int lead = tiles == 1 ? 2 : 1;
+#pragma unroll 1
+        for (int jk = kv0, jv = kv0; ok && jv < kv1;) {
+          const bool k_tile = jk < kv1 && jk - jv < lead;
+          step(k_tile, k_tile ? jk++ : jv++);
         }
       }
       if (ok && keys && wait(&S.code_empty[st], par) && lane == 0) {   // the converters' end
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = tc::sdesc_sw128(base, 16, 1024), dk = tc::sdesc_sw128(base + Y::kOffKv, 16, 1024);
       const uint64_t dv = tc::sdesc_sw128(base + Y::kOffKv, Y::kHalf, 1024);
       int st = 0, loads_q = 0;           // the ring's stage that comes next
-      uint32_t par = 0, np[2] = {0, 0};  // its phase; the weights' phases of the units
+      uint32_t par = 0, np = 0;          // its phase; the weights' phases of the units, a bit each
       // A wait that gives up only raises the abort flag, at which every later wait gives up at once; the loop
       // looks at the flag once a tile, so that a wait that need not wait costs little more than its test.
       auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -622,21 +622,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd = dv + uint64_t(s) * (Y::kStageB >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          wait(&S.p_full[u][half], np[u]);
+          wait(&S.p_full[u][half], np >> u & 1);
           __syncwarp();
           tc::tc_fence_after();
           if (tc::elect_one()) {
 #pragma unroll
-            for (int k = half * 4; k < half * 4 + 4; ++k)
-              if constexpr (PAIR)
-                umma_pair_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, vd + ((k * 2048) >> 4), id_pv, !first || k != 0);
-              else
-                tc::umma_f16_ts(tmem + Y::kColO + u * DH, tmem + u * kTile + k * 8, vd + ((k * 2048) >> 4), id_pv, !first || k != 0);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t o = tmem + Y::kColO + u * DH, w = tmem + u * kTile + half * 32 + k * 8;
+              const uint64_t v = vd + half * (8192 >> 4) + ((k * 2048) >> 4);
+              if constexpr (PAIR) umma_pair_ts(o, w, v, id_pv, !first || half + k != 0);
+              else tc::umma_f16_ts(o, w, v, id_pv, !first || half + k != 0);
+            }
             if (half == 1 && free) commit<PAIR>(&S.empty[s]);
             if (half == 1 && last) commit<PAIR>(&S.o_full[u]);
           }
         }
-        np[u] ^= 1;
+        np ^= 1u << u;
       };
       auto dead = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
       for (int i = 0;; ++i) {
@@ -668,38 +669,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (PAIR) wait_pair(&S.q_ready, loads_q & 1, abort_flag, P.wait_ns);
         else wait(&S.q_ready, loads_q & 1);
         ++loads_q;
-        if (it.tiles == 2) {
-          // both units over each tile; unit 0 may see fewer (it stops first)
-          const int n0 = unit_steps(it, 0, P.per_tile);
-          const uint64_t dq1 = dq + (Y::kTileB >> 4);
-          int sk = stage();
-          if (n0 > 0) qk(0, dq, sk, false, false);
-          qk(1, dq1, sk, true, n == 1);
-          for (int k = 0; k < n; ++k) {
-            if (dead()) break;
-            const int sv = stage();
-            if (PAIR && k + 1 < n) sk = stage();   // before the weights come: a look at the pair's barriers takes 200 clocks
-            if (k < n0) pv(0, sv, k == 0, false, k + 1 == n0);
-            if (!PAIR && k + 1 < n) sk = stage();
-            if (k + 1 < n0) qk(0, dq, sk, false, false);
-            pv(1, sv, k == 0, true, k + 1 == n);
-            if (k + 1 < n) qk(1, dq1, sk, true, k + 2 == n);
-          }
-        } else {
-          // the units take the tiles in turn
-          for (int k = 0; k < min(n, 2); ++k) {
-            const int s = stage();
-            qk(k, dq, s, true, k + 1 == n);
-          }
-          for (int k = 0; k < n; ++k) {
-            if (dead()) break;
-            const int sv = stage();
-            int sk = 0;
-            if (PAIR && k + 2 < n) sk = stage();
-            pv(k & 1, sv, k < 2, true, k + 2 >= n);
-            if (!PAIR && k + 2 < n) sk = stage();
-            if (k + 2 < n) qk(k & 1, dq, sk, true, k + 3 == n);
-          }
+        // Two tiles of queries: both units over each tile of the cache; unit 0 may see fewer (it stops first). One: the
+        // units take the cache's tiles in turn. One loop for both, and for the units, keeps the code short: the warps of
+        // other roles on this scheduler wait for their instructions too.
+        const bool two = it.tiles == 2;
+        const int n0 = two ? unit_steps(it, 0, P.per_tile) : 0;
+        int sk = 0, sv = 0;
+#pragma unroll 1
+        for (int u = 0; u < (two ? 2 : min(n, 2)); ++u) {
+          if (!two || u == 0) sk = stage();
+          if (!two || u == 1 || n0 > 0)
+            qk(u, two && u == 1 ? dq + (Y::kTileB >> 4) : dq, sk, !two || u == 1, two ? u == 1 && n == 1 : u + 1 == n);
+        }
+#pragma unroll 1
+        for (int x = 0; x < (two ? 2 * n : n); ++x) {
+          if (dead()) break;
+          const int u = x & 1, k = two ? x >> 1 : x, seen = two && u == 0 ? n0 : n, next = two ? k + 1 : k + 2;
+          const bool second = !two || u == 1, first = !two || u == 0, more = first && next < n;
+          if (first) sv = stage();
+          if (PAIR && more) sk = stage();   // before the weights come: a look at the pair's barriers takes 200 clocks
+          if (k < seen) pv(u, sv, two ? k == 0 : k < 2, second, next >= seen);
+          if (!PAIR && more) sk = stage();
+          if (next < seen) qk(u, two && u == 1 ? dq + (Y::kTileB >> 4) : dq, sk, second, second && next + 1 == n);
         }
         __syncwarp();
       }
