@@ -14,13 +14,14 @@
 //   * s_k multiplies 16 scores of a thread's row at once. With y_t = x_t + log2 s_v(t) and a running maximum of y, the
 //     weights 2^(y_t - M) are what c_v is multiplied by, and the sum takes them divided by s_v: one exponential
 //     serves both, and the fp16 weights are relative to the largest that enters the product, whatever the scales.
-// Bound: the softmax warps' chain from scores to weights to the next scores (about 2000 and 1100 clocks of a step for two
-// tiles, of which the products need 1024), and what of the converters does not hide behind it: 2048 new tokens at 65536, 8 heads
-// of 128, 4 query rows each, 1626 us and 1.33 of 1.92 PFLOP/s (tensor pipe 50 % busy at 16384); four prompts of 4096, 32
-// heads, 541 us. Each instruction counts: scales held over a step, inverse scales from the converters, three-way maxima
-// and packed sums took these from 1783 and 578. Without the maximum ahead of the weights (raised afterwards where 16 weights'
-// sum had left fp16) steps were no shorter, and first ones twice as long: 806 us for the prompts. Queries loaded behind the
-// next item's first keys: 592 (against 578).
+// Bound: the softmax warps' chain from scores to weights to the next scores, of a step for two tiles about 2800 clocks, of which
+// the products need 1024, and what of the converters does not hide behind it: 2048 new tokens at 65536, 8 heads of 128, 4
+// query rows each, 1590 us and 1.36 of 1.92 PFLOP/s; four prompts of 4096, 32 heads, 535 us. Each instruction counts,
+// also in the instruction caches, which the roles share: scales held over a step, inverse scales from the converters, three-way
+// maxima, packed sums, and one loop each for loads and products took these from 1783 and 578. Not kept: without the maximum
+// ahead of the weights (raised afterwards where 16 weights' sum had left fp16) steps were no shorter, and first ones twice as
+// long (806 us for the prompts, against 578); the units' softmax by turns on each scheduler (1831 against 1641, 575 against
+// 554); queries loaded behind the next item's first keys (592 against 578).
 // A product straight on the codes (kind::f8f6f4) would want the queries and weights in 8 bits too, in two or three terms
 // each to keep their precision: as many products as in fp16, and the weights' terms in the softmax, which bounds the
 // kernel already.
@@ -48,8 +49,8 @@ constexpr int kBlocks = kTile / kKv8Block;
 
 template <int DH, bool PAIR> struct Lay {
   // Registers: launched with 128 a thread; 256 softmax + 128 other + 128 convert = 512 * 128. 2048 tokens at 32768, 32 / 8
-  // heads, in bf16 and fp16: 876 and 882 us; with 192, 72 and 56 874 and 978; 184, 88 and 56 925 and 959; 200, 56 and 56 909 and
-  // 878; 176, 96 and 64 964 and 1091.
+  // heads, in bf16 and fp16: 808 and 823 us; with 208, 48 and 48 830 and 828; 184, 72 and 72 836 and 846; with 200, 56 and 56 809
+  // and 817, but loaders that are short of registers: 16 tokens of 16 rows at 4096, pages of 64, take 67 us against 58.
   static constexpr int kRegsSoftmax = 192, kRegsOther = 64, kRegsConvert = 64;
   // Query tiles: 64 elements (128 bytes) of all rows, then the next 64. fp16 and code tiles hold the CTA's part: keys as the
   // queries (of a pair's CTA 64 tokens), values by 64 columns of all tokens. Rows of 128 bytes are swizzled.
@@ -687,7 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int u = x & 1, k = two ? x >> 1 : x, seen = two && u == 0 ? n0 : n, next = two ? k + 1 : k + 2;
           const bool second = !two || u == 1, first = !two || u == 0, more = first && next < n;
           if (first) sv = stage();
-          if (PAIR && more) sk = stage();   // before the weights come: a look at the pair's barriers takes 200 clocks
+          // Before the weights come: a look at a pair's barriers takes 200 clocks. Alone, units in turn over one tile would wait
+          // for keys that are converted behind the values that the weights want.
+          if (PAIR && more) sk = stage();
           if (k < seen) pv(u, sv, two ? k == 0 : k < 2, second, next >= seen);
           if (!PAIR && more) sk = stage();
           if (next < seen) qk(u, two && u == 1 ? dq + (Y::kTileB >> 4) : dq, sk, second, second && next + 1 == n);
@@ -1013,18 +1016,18 @@ template <int DH, bool BF16, bool PAIR> cudaError_t launch_tc(const Kv8AttendArg
 
 // Pairs take where there is enough work for them and its rows fill their tiles, by the call's averages and bounds.
 //   * An item of a pair is 512 query rows. Its start, its end and the rows that a causal item computes in vain cost more
-//     than an item of 256, so a pair must have at least 24 steps (of two tiles) to do: 128 tokens of 4 heads, 8 key/value
-//     heads, at 32768 (27 steps): 77 us against 82; at 8192 (7): 37 against 35; 16 sequences of 256 such tokens at 4096
-//     (107): 259 against 288; four of 1024 at 1024 (14): 69 against 67.
+//     than an item of 256, so a pair must have at least 40 steps (of two tiles) to do, of which steps over the new tokens
+//     themselves count a quarter: 128 tokens of 4 heads, 8 key/value heads, at 8192 (7): 35 us against 33; at 32768 (27): 73 against 75;
+//     16 sequences of 256 such tokens at 4096 (107): 251 against 271; four prompts of 2048, 32 heads (27): 186 against 175.
 //   * Where a sequence's last item is half empty for want of rows, one CTA alone would have skipped that half. A pair's
-//     steps take about 7/8 of the time, which makes up for that from 1536 rows on: 16 sequences at 4096 of 768 rows take
-//     250 us by pairs against 222, of 1792 rows 428 against 441, of 2400 rows 548 against 604.
+//     steps take about 14/15 of the time, which makes up for that from 3584 rows on: 16 sequences at 4096 of 768 rows take
+//     240 us by pairs against 208, of 1024 rows 251 against 271.
 bool in_pairs(const KvAttendArgs& a, int sms) {
   if (a.head_dim != 128) return false;
   const int64_t rows = ((int64_t)a.rows.n_tokens * a.g + a.rows.batch - 1) / a.rows.batch;
   const int64_t ones = (rows + 2 * kTile - 1) / (2 * kTile), pairs = (ones + 1) / 2;
-  const int64_t steps = ((int64_t)a.rows.max_kv_len - a.rows.max_new / 2) / kTile;
-  return 14 * pairs <= 8 * ones && a.rows.batch * pairs * a.n_kv * steps >= (int64_t)24 * (sms / 2);
+  const int64_t steps = ((int64_t)a.rows.max_kv_len - (int64_t)a.rows.max_new * 3 / 4) / kTile;
+  return 28 * pairs <= 15 * ones && a.rows.batch * pairs * a.n_kv * steps >= (int64_t)40 * (sms / 2);
 }
 
 }  // namespace

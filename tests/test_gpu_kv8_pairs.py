@@ -8,7 +8,7 @@ from tests.kv8_cases import Batch8
 
 pytestmark = pytest.mark.gpu
 
-FAR = 1 << 19       # cached tokens by the bound: at least 24 steps for each of 76 pairs, whatever the rows
+FAR = 1 << 19       # cached tokens by the bound: steps enough for 76 pairs, whatever the rows
 
 
 class Wide(Batch8):
@@ -22,7 +22,7 @@ class Wide(Batch8):
         self.rows = P.KVRows(start, lens, page_table=wide, n_tokens=self.N, max_new=self.rows.max_new, max_kv_len=FAR)
 
 
-# query rows of a key/value head: pairs take averages of 257 to 512 rows, and past 1536 all
+# query rows of a key/value head: pairs take averages whose last 512 are more than half full
 @pytest.mark.parametrize("n,m,dtype", [(8, 2, "bf16"), (4, 4, "f16"), (6, 1, "f16"), (7, 1, "bf16"), (3, 3, "bf16")])
 @pytest.mark.parametrize("rows,at", [(384, 0), (510, 0), (300, 1), (430, 2000), (1800, 77)])
 @pytest.mark.parametrize("page", [16, 48])
