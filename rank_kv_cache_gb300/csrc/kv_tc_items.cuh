@@ -227,7 +227,7 @@ __device__ __forceinline__ void join_pieces(const TcParams& P, const Plan& plan,
     const int tok0 = (__shfl_sync(0xffffffffu, x.tiles, src) - 1 - in_row) * SUB * per;
     const int h = in_group / kParts % a.n_kv, tile = group % SUB, r0 = group / SUB * kJoinRows, r = r0 + lane;
     const int c0 = in_group % kParts * 4;
-    if (r0 >= per * a.g || tok0 + tile * per + r0 / a.g >= n) continue;
+    if (tok0 + tile * per >= n || r0 >= per * a.g || tok0 + tile * per + r0 / a.g >= n) continue;
     const int i = tok0 + tile * per + r / a.g;
     const bool live_row = r < per * a.g && i < n;
     const int64_t s0 = ((int64_t)slot * a.n_kv + h) * SUB + tile;

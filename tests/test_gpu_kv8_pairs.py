@@ -131,3 +131,19 @@ def test_bounded_waits_give_up_and_report_a_timeout(cuda_device):
     assert e.value.status == P.PALU_ERR_TIMEOUT
     plain = Wide(n=8, m=2, d=128, dtype="f16", news=[125], lens=[900], page=16, seed=14)
     plain.run_and_check()
+
+
+def test_two_calls_at_once_on_streams_of_their_own(cuda_device):
+    """Pairs of two calls, cut and joined, that share the GPU."""
+    batches = [Wide(n=8, m=2, d=128, dtype="bf16", news=[100, 70, 128], lens=[20000, 500, 9000], page=64, seed=21),
+               Wide(n=32, m=8, d=128, dtype="f16", news=[120, 100], lens=[9000, 30000], page=32, seed=22)]
+    want = [b.attend() for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    got = [[], []]
+    for _ in range(8):
+        for b, s, g in zip(batches, streams, got):
+            g.append(b.layer.attend(b.pages, b.rows, b.qd, stream=s))
+    torch.cuda.synchronize()
+    for b, w, g in zip(batches, want, got):
+        b.layer.check_device()
+        assert all(torch.equal(w[0], x) for x in g)
