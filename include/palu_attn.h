@@ -592,8 +592,9 @@ palu_status_t palu_append_kv8(palu_kv_t h, const palu_kv8_pages* pages, const pa
  * own to fp16, which loses what lies 2^-38 and more below the row's largest; the softmax weights, with their values'
  * scales, are rounded to fp16 relative to the row's largest (steps of 2^-31 of it, or finer).
  * The result does not depend on timing: the same call gives the same bits. max_new * n_heads / n_kv_heads decides the
- * kernel: up to 24 query rows of a key/value head run on the streaming kernel, more on the tensor-core kernel; that
- * one's pairs of CTAs take heads of 128 where n_tokens, batch, max_new and max_kv_len promise work enough (one launch each).
+ * kernel, and for 13 to 24 query rows of a key/value head batch and max_kv_len too: few rows over much cache run on the streaming
+ * kernel, others on the tensor-core kernel; that one's pairs of CTAs take heads of 128 where n_tokens, batch, max_new and
+ * max_kv_len promise work enough (one launch each).
  * What is recorded in the error word, and when outputs are 0 and -inf, is as for palu_attend_kv. PALU_ERR_UNSUPPORTED for F32
  * handles.
  */

@@ -68,9 +68,7 @@ struct Kv8AttendArgs {
   const float* v_scale;
 };
 cudaError_t prepare_kv8_attend_few(int head_dim, bool bf16);
-// Query rows of a unit that the streaming kernel takes. Eight sequences of up to 16384: 20 rows 66 us against 85 to 92 on the
-// tensor-core kernel; 32 rows of 16384 (a fourth eight of rows) 124 against 128, with spills.
-constexpr int kKv8FewRows = 24;
+constexpr int kKv8FewRows = 24;   // query rows of a unit that the streaming kernel holds
 cudaError_t launch_kv8_attend_few(const Kv8AttendArgs& a, int sm_count, cudaStream_t st);   // max_new g <= kKv8FewRows
 cudaError_t prepare_kv8_attend_tc(int head_dim, bool bf16);
 cudaError_t launch_kv8_attend_tc(const Kv8AttendArgs& a, const KvTcPlan& t, cudaStream_t st);

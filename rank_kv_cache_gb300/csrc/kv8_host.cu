@@ -20,6 +20,20 @@ palu_status_t check_pages8(const palu_kv* h, const palu_kv8_pages* p, const palu
 
 KvPages codes_of_pages(const palu_kv8_pages& p) { return KvPages{p.k, p.v, p.n_pages, p.page_size}; }
 
+// Which kernel. The streaming one holds up to 24 query rows and reads the cache at up to the full rate, but its warps take their
+// steps one after the other, the longer the more rows there are: while the call's bounds promise an SM few steps of 128
+// cached tokens, the tensor-core kernel is sooner done. 32 / 8 heads of 128, 24 query rows: one sequence at 4096 (1.7 steps an SM)
+// 34 us against 18, two at 16384 (13.5) 45 against 38, four at 16384 (27) 56 against 64, eight (54) 87 against 110. 16 rows: one
+// at 4096 24 against 18, two 24 against 21, at 16384 34 against 37, four at 4096 (6.7) 25 against 26. Heads of 64, 24 rows: one
+// at 4096 19 against 16, two at 16384 30 against 33, four at 1000 16 against 19.
+bool streams(const KvAttendArgs& a, int sms) {
+  const int64_t rows = (int64_t)a.rows.max_new * a.g, units = (int64_t)a.rows.batch * a.n_kv;
+  const int64_t steps = units * ((a.rows.max_kv_len + 127) / 128);
+  if (rows > kKv8FewRows) return false;
+  if (rows > 16 && a.head_dim == 128) return steps > (int64_t)16 * sms;
+  return rows <= (a.head_dim == 128 ? 12 : 16) || units > 16 || steps > (int64_t)7 * sms;
+}
+
 bool bad_ints(const void* p) { return !p || (uintptr_t)p % 4; }
 
 }  // namespace
@@ -84,8 +98,7 @@ palu_status_t palu_attend_kv8(palu_kv_t h, const palu_kv8_pages* pages, const pa
   a.pages = codes_of_pages(*pages);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if ((int64_t)a.rows.max_new * a.g <= kKv8FewRows) {
-    // 24 query rows hold every row's tokens: the few-row kernel streams the cache once
+  if (streams(a, h->sm_count)) {
     e = launch_kv8_attend_few(A, h->sm_count, s);
   } else {
     e = launch_kv8_attend_tc(A, tc_plan(h, *rows), s);
