@@ -103,6 +103,7 @@ template <typename T> struct Source {
   int certain;       // a draft that was certain: its weight is 0 (or -1)
   int vocab;
   bool wide;         // both rows' loads are aligned
+  float lift;        // a power of two, for sums outside the range
 
   template <bool WIDE> __device__ __forceinline__ void row(float (&x)[kSteps][kVec], const T* r, int v) const {
 #pragma unroll
@@ -153,6 +154,12 @@ template <typename T> struct Source {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
           if (v + k * 32 * kVec + i == certain) w.d[k][i] = 0.f;   // and its rounding error is 0, as there is no q
+    }
+    if (lift != 1.f) {
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w.d[k][i] *= lift, w.e[k][i] *= lift;
     }
   }
 };
@@ -237,6 +244,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
   src.certain = rejected && !draft ? drafts[taken] : -1;
   src.vocab = a.vocab;
   src.wide = ((uintptr_t)src.p | (uintptr_t)src.q) % (kVec * sizeof(T)) == 0;
+  src.lift = 1.f;
   const int segs = (a.vocab + kSeg - 1) / kSeg, per = (segs + ctas - 1) / ctas;
   const int s0 = min(segs, rank * per), mine = min(segs, s0 + per) - s0;
 
@@ -272,9 +280,17 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
       if (c == rank) below = total;
       total = total.plus(Sum{part[c].x, part[c].y});
     }
-    if (total.hi > 0.f || (!src.q && src.certain < 0)) break;
-    src.q = nullptr;                                    // nothing is left of p - q: from p
-    src.certain = -1;
+    if (total.hi == 0.f) {
+      if (!src.q && src.certain < 0) break;
+      src.q = nullptr;                                  // nothing is left of p - q: from p
+      src.certain = -1;
+    } else {
+      // Below 2^-100 the second number's bits would fall under the least subnormal, u times the sum would round to the sum
+      // itself, and nothing would exceed it; past the largest number sums are NaN. Such a row is summed anew, lifted by 2^100
+      // or lowered by 2^32 (2^20 numbers are then in range, and what that rounds lies far below the sum's last bit).
+      if (src.lift != 1.f || (total.hi >= 0x1p-100f && total.hi < INFINITY)) break;
+      src.lift = total.hi < 1.f ? 0x1p100f : 0x1p-32f;
+    }
     cluster.sync();                                     // every CTA has read the sums
   }
   if (!(total.hi > 0.f)) {

@@ -204,3 +204,34 @@ def test_graphs_and_lengths_elsewhere(cuda_device):
     g.replay()
     torch.cuda.synchronize()
     assert np.array_equal(t3.cpu().numpy(), tokens) and np.array_equal(a3.cpu().numpy(), accepted)
+
+
+# Weights whose sum is subnormal, next to it, or past the largest number. The sums' and products' 48 bits decide each of these draws as
+# rational arithmetic does: none lies nearer to a border than 2^-25 of the sum, but those on it (u = 1/2), which are exact.
+@pytest.mark.parametrize("name,dtype,vocab,weights", [
+    ("one-least", "f32", 700, {650: 2.0 ** -149}), ("seventy-least", "f32", 1300, {5: 30 * 2.0 ** -149, 600: 2.0 ** -149, 1299: 39 * 2.0 ** -149}),
+    ("least-normal", "f32", 6000, {3: 2.0 ** -127, 5900: 2.0 ** -127}), ("above-it", "f32", 9000, {1: 3 * 2.0 ** -120, 4100: 2.0 ** -140, 8999: 2.0 ** -119}),
+    ("largest", "f32", 9000, {0: 3.0e38, 2000: 3.25e38, 8999: 1.0e38}), ("largest-one", "f32", 600, {9: 3.4028234663852886e38}),
+    ("bf16-least", "bf16", 700, {4: 2.0 ** -133, 699: 2.0 ** -132}), ("bf16-largest", "bf16", 700, {4: 2.0 ** 127, 699: 2.0 ** 127}),
+    ("f16-least", "f16", 700, {4: 2.0 ** -24, 699: 2.0 ** -23})])
+@pytest.mark.parametrize("residual", [False, True])
+def test_sums_outside_the_range_draw_a_token(cuda_device, name, dtype, vocab, weights, residual):
+    u = np.float32([0.0, 0.25, 0.5, np.nextafter(np.float32(0.5), np.float32(1)), 0.625, 0.75, 0.995, 1 - 2.0 ** -24])
+    B, rows = len(u), 2 if residual else 1
+    p = torch.zeros(B * rows, vocab, dtype=torch.float64)
+    for v, w in weights.items():
+        p[::rows, v] = w
+    draft, drafts = None, np.zeros((B, rows - 1), dtype=np.int32)
+    if residual:                                                              # a draft of token 2, whose p is 0
+        draft = torch.zeros(B, 1, vocab)
+        draft[:, 0, 2] = 1.0
+        draft[:, 0, 8:200] = 2.0 ** -100
+        drafts[:] = 2
+    c = dict(target=p.to(TYPES[dtype]), draft=None if draft is None else draft.to(TYPES[dtype]), drafts=drafts,
+             starts=(rows * np.arange(B + 1)).astype(np.int32), u=np.stack([u] * rows, 1), kv=np.full(B, 9, dtype=np.int32))
+    assert np.array_equal(c["target"].double().numpy(), p.float().double().numpy())
+    tokens = torch.full((B, rows), 12345, dtype=torch.int32, device="cuda")
+    got, accepted, kv, layer = run(c, tokens=tokens)
+    layer.check_device()
+    assert np.all(accepted == 0)
+    check(c, got, accepted, kv)
