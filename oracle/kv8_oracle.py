@@ -119,6 +119,10 @@ def verify(target, draft, draft_tokens, uniforms):
         x = float(x)
         return Fraction(x) if x > 0 else Fraction(0)
 
+    def uniform(x):                                      # the ends of [0, 1) in fp32
+        x = float(x)
+        return Fraction(max(x, 0.0)) if x < 1 else 1 - Fraction(1, 2 ** 24)
+
     n = len(target)
     a = 0
     while a < n - 1:
@@ -126,7 +130,7 @@ def verify(target, draft, draft_tokens, uniforms):
         if not 0 <= x < len(target[a]):
             break
         q = Fraction(1) if draft is None else prob(draft[a][x])
-        if not Fraction(float(uniforms[a])) * q < prob(target[a][x]):
+        if not uniform(uniforms[a]) * q < prob(target[a][x]):
             break
         a += 1
     w = [prob(p) for p in target[a]]
@@ -140,6 +144,6 @@ def verify(target, draft, draft_tokens, uniforms):
     total, run = sum(w), Fraction(0)
     for v, p in enumerate(w):
         run += p
-        if run > Fraction(float(uniforms[-1])) * total:
+        if run > uniform(uniforms[-1]) * total:
             return a, v
     return a, -1

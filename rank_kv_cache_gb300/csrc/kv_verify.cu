@@ -86,6 +86,8 @@ __device__ __forceinline__ Sum running(Sum s) {
   }
   return s;
 }
+// a random number as one of [0, 1): what is not below 1, NaN too, as 1 - 2^-24
+__device__ __forceinline__ float uniform_of(float u) { return u < 1.f ? fmaxf(u, 0.f) : 0.99999994f; }
 // u q < p
 __device__ __forceinline__ bool below_p(float u, float q, float p) {
   const float x = __fmul_rn(u, q);
@@ -181,7 +183,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
   const float* u = a.uniforms + (int64_t)b * (a.max_draft + 1);
   const int x0 = lane < a.max_draft ? drafts[lane] : 0;
   const float u0 = lane < a.max_draft ? u[lane] : 0.f;
-  float u1 = u[a.max_draft];
+  const float u1 = uniform_of(u[a.max_draft]);
   const int start = a.row_start[b], end = a.row_start[b + 1];
   const bool row_ok = start >= 0 && end >= start && end <= a.n_tokens;
   int n = row_ok ? end - start : 0;
@@ -214,7 +216,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
         } else {
           const float p = fmaxf(to_f32(target[(int64_t)i * a.target_stride + x]), 0.f);
           const float q = draft ? fmaxf(to_f32(draft[(int64_t)i * a.draft_stride + x]), 0.f) : 1.f;
-          no = !below_p(fmaxf(i0 == 0 ? u0 : u[i], 0.f), q, p);
+          no = !below_p(uniform_of(i0 == 0 ? u0 : u[i]), q, p);
         }
       }
       const unsigned m = __ballot_sync(0xffffffffu, no);
@@ -301,7 +303,6 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
     return;
   }
   // The draw falls to the first CTA whose running sum exceeds it; those are the same numbers in every CTA.
-  u1 = u1 < 1.f ? fmaxf(u1, 0.f) : 0.99999994f;        // 1 - 2^-24; NaN too
   const Sum t = total.times(u1);
   const Sum own{part[rank].x, part[rank].y};
   if (warp != 0 || mine == 0 || below.over(t) || !below.plus(own).over(t)) return;

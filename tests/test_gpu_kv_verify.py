@@ -235,3 +235,30 @@ def test_sums_outside_the_range_draw_a_token(cuda_device, name, dtype, vocab, we
     layer.check_device()
     assert np.all(accepted == 0)
     check(c, got, accepted, kv)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("certain", [False, True])
+def test_uniforms_outside_the_range_are_brought_to_its_ends(cuda_device, dtype, certain):
+    # two drafts that the target agrees with to the bit (every number below 1 accepts), and one that it gives half as much
+    V = 600
+    odd = np.float32([1.0, np.nextafter(np.float32(1), np.float32(2)), 2.0, 1e30, np.inf, np.nan, -1.0, -np.inf, -0.0, 1 - 2.0 ** -24])
+    B, K = len(odd), 3
+    p = torch.zeros(B, K + 1, V)
+    p[:, :, [5, 300, 599]] = torch.tensor([0.5, 0.25, 0.25])
+    p[:, 2] *= 0.5
+    q = torch.zeros(B, K, V)
+    q[:, :, [5, 599]] = 0.5
+    if certain:
+        p[:, :2, 5] = 1.0                                                     # as much as a certain draft's
+    for col in range(K + 1):
+        u = np.full((B, K + 1), 0.25, dtype=np.float32)
+        u[:, col] = odd
+        c = dict(target=p.view(-1, V).to(TYPES[dtype]), draft=None if certain else q.to(TYPES[dtype]),
+                 drafts=np.full((B, K), 5, dtype=np.int32), starts=((K + 1) * np.arange(B + 1)).astype(np.int32), u=u,
+                 kv=np.full(B, 9, dtype=np.int32))
+        tokens, accepted, kv, layer = run(c)
+        layer.check_device()
+        check(c, tokens, accepted, kv)
+        if col == 0:
+            assert np.all(accepted > 0)

@@ -91,3 +91,12 @@ def test_verified_tokens_are_distributed_as_the_target():
 def test_certain_drafts(u, v, want):
     p = np.array([[0.5, 0.25, 0.25], [1.0, 0.0, 0.0]])
     assert K8.verify(p, None, [0], [u, v]) == want
+
+
+@pytest.mark.parametrize("u,want", [(1.0, 2), (7.5, 2), (float("inf"), 2), (float("nan"), 2), (-1.0, 2), (1 - 2.0 ** -24, 2)])
+def test_uniforms_are_brought_into_range(u, want):
+    # the target and the draft agree, so that every uniform below 1 accepts; behind the drafts 0 draws the first, the largest the last
+    p = np.array([[0.5, 0.5, 0.0], [0.25, 0.75, 0.0], [0.0, 0.125, 0.875]])
+    assert K8.verify(p, p[:2], [0, 1], [u, u, u]) == (want, 1 if u < 0 else 2)
+    # a certain draft of less than all is rejected by the largest
+    assert K8.verify(p[:2], None, [0], [u, 0.0]) == ((1, 0) if u < 0 else (0, 1))
