@@ -662,7 +662,7 @@ palu_status_t palu_plan_kv_rows(palu_kv_t h, const palu_kv_pool* pool, const int
  * Probabilities are finite; they need not sum to 1, and negative ones and NaN count as 0. Products and differences
  * are exact, sums are carried in twice the bits of fp32. Uniforms outside [0, 1) are brought to its
  * ends, 0 and 1 - 2^-24 (NaN to the latter), those of drafts and of the drawn token alike. A draft outside the vocabulary is rejected, and recorded in the error word; so are a row with more than
- * max_draft drafts (its first max_draft are taken), a decreasing row_start (nothing is done) and a distribution that is
+ * max_draft drafts (its first max_draft are taken, the others leave the length as rejected ones do), a decreasing row_start (nothing is done) and a distribution that is
  * zero throughout (the token is -1). vocab <= 2^20. Rows of any alignment; those whose addresses are multiples of
  * 16 bytes are read fastest.
  */

@@ -186,9 +186,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
   const float u1 = uniform_of(u[a.max_draft]);
   const int start = a.row_start[b], end = a.row_start[b + 1];
   const bool row_ok = start >= 0 && end >= start && end <= a.n_tokens;
-  int n = row_ok ? end - start : 0;
-  if (rank == 0 && tid == 0 && (!row_ok || n - 1 > a.max_draft)) record_error(a.err, kCodeDevice, kErrRows, b, b);
-  n = min(n, a.max_draft + 1);
+  const int brought = row_ok ? end - start : 0;         // tokens that are in the cached length
+  if (rank == 0 && tid == 0 && (!row_ok || brought - 1 > a.max_draft)) record_error(a.err, kCodeDevice, kErrRows, b, b);
+  const int n = min(brought, a.max_draft + 1);
   int32_t* out = a.tokens + (int64_t)b * (a.max_draft + 1);
   const T* target = static_cast<const T*>(a.target) + (int64_t)start * a.target_stride;
   const T* draft = a.draft ? static_cast<const T*>(a.draft) + (int64_t)b * a.max_draft * a.draft_stride : nullptr;
@@ -236,7 +236,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
       if (i != taken) out[i] = i < taken ? drafts[i] : -1;
     if (tid == 0) {
       a.accepted[b] = taken;
-      if (a.kv_len_out) a.kv_len_out[b] = a.kv_len[b] - (n - 1 - taken);
+      if (a.kv_len_out) a.kv_len_out[b] = a.kv_len[b] - (brought - 1 - taken);
     }
   }
 

@@ -262,3 +262,24 @@ def test_uniforms_outside_the_range_are_brought_to_its_ends(cuda_device, dtype, 
         check(c, tokens, accepted, kv)
         if col == 0:
             assert np.all(accepted > 0)
+
+
+def test_drafts_past_the_bound_leave_the_length(cuda_device):
+    # six target rows for two drafts: the first two are judged, and what is not judged is not kept
+    from rank_kv_cache_gb300 import palu as P
+    rng = np.random.default_rng(6)
+    c = make(rng, [3, 3], 50, "f32")
+    c["target"] = torch.cat([c["target"], c["target"][:3]])
+    c["starts"] = np.array([0, 6, 9], dtype=np.int32)
+    c["kv"] = np.array([20, 30], dtype=np.int32)
+    for n in (0, 2):                                                          # accepted of the two
+        c["u"][:, :2] = 0.0 if n else 0.75
+        c["target"][[0, 1, 6, 7], c["drafts"].reshape(-1)] = 0.5
+        c["draft"][[0, 0, 1, 1], [0, 1, 0, 1], c["drafts"].reshape(-1)] = 1.0
+        tokens, accepted, kv, layer = run(c)
+        assert list(accepted) == [n, n] and list(kv) == [20 - (5 - n), 30 - (2 - n)]
+        for b, lo in ((0, 0), (1, 6)):
+            a, token = K8.verify(c["target"][lo:lo + 3].double().numpy(), c["draft"][b].double().numpy(), c["drafts"][b], c["u"][b])
+            assert a == n and list(tokens[b]) == [*c["drafts"][b, :a], token] + [-1] * (2 - a)
+        with pytest.raises(P.PaluError):
+            layer.check_device()
