@@ -95,6 +95,8 @@ __device__ __forceinline__ bool below_p(float u, float q, float p) {
   return x < p || (x == p && __fmaf_rn(u, q, -x) < 0.f);
 }
 
+constexpr int kWide = 1;               // both rows' loads are aligned
+constexpr int kUp = 2, kDown = 4;      // weights are lifted by 2^100, lowered by 2^32
 // What the token is drawn from, of a lane's values of a segment: max(p - q, 0) as a difference and its rounding error.
 struct Weights {
   float d[kSteps][kVec], e[kSteps][kVec];
@@ -104,8 +106,7 @@ template <typename T> struct Source {
   const T* q;        // nullptr: none
   int certain;       // a draft that was certain: its weight is 0 (or -1)
   int vocab;
-  bool wide;         // both rows' loads are aligned
-  float lift;        // a power of two, for sums outside the range
+  int flags;         // kWide, and of kUp and kDown one for sums outside the range
 
   template <bool WIDE> __device__ __forceinline__ void row(float (&x)[kSteps][kVec], const T* r, int v) const {
 #pragma unroll
@@ -131,7 +132,7 @@ template <typename T> struct Source {
   // branch between the loads, so that all are under way at once.
   __device__ __forceinline__ void load(Weights& w, int v0) const {
     const int v = v0 + (threadIdx.x & 31) * kVec;
-    if (wide && v0 + kSeg <= vocab) {
+    if ((flags & kWide) && v0 + kSeg <= vocab) {
       row<true>(w.d, p, v);
       if (q) row<true>(w.e, q, v);
     } else {
@@ -157,7 +158,8 @@ template <typename T> struct Source {
         for (int i = 0; i < kVec; ++i)
           if (v + k * 32 * kVec + i == certain) w.d[k][i] = 0.f;   // and its rounding error is 0, as there is no q
     }
-    if (lift != 1.f) {
+    if (flags & (kUp | kDown)) {
+      const float lift = flags & kUp ? 0x1p100f : 0x1p-32f;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
@@ -245,8 +247,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
   src.q = rejected && draft ? draft + (int64_t)taken * a.draft_stride : nullptr;
   src.certain = rejected && !draft ? drafts[taken] : -1;
   src.vocab = a.vocab;
-  src.wide = ((uintptr_t)src.p | (uintptr_t)src.q) % (kVec * sizeof(T)) == 0;
-  src.lift = 1.f;
+  src.flags = ((uintptr_t)src.p | (uintptr_t)src.q) % (kVec * sizeof(T)) == 0 ? kWide : 0;
   const int segs = (a.vocab + kSeg - 1) / kSeg, per = (segs + ctas - 1) / ctas;
   const int s0 = min(segs, rank * per), mine = min(segs, s0 + per) - s0;
 
@@ -290,8 +291,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kCtas) kv_veri
       // Below 2^-100 the second number's bits would fall under the least subnormal, u times the sum would round to the sum
       // itself, and nothing would exceed it; past the largest number sums are NaN. Such a row is summed anew, lifted by 2^100
       // or lowered by 2^32 (2^20 numbers are then in range, and what that rounds lies far below the sum's last bit).
-      if (src.lift != 1.f || (total.hi >= 0x1p-100f && total.hi < INFINITY)) break;
-      src.lift = total.hi < 1.f ? 0x1p100f : 0x1p-32f;
+      if (src.flags >= kUp || (total.hi >= 0x1p-100f && total.hi < INFINITY)) break;
+      src.flags |= total.hi < 1.f ? kUp : kDown;
     }
     cluster.sync();                                     // every CTA has read the sums
   }
