@@ -55,6 +55,16 @@ __device__ __forceinline__ uint32_t lifted(uint32_t bf16x2, float lift) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What the scores of a row and a block are multiplied by: its part of the row (log2(e) / sqrt(d) without the lift) times s_k. A bf16
+// row's part alone reaches from 2^-103 to 2^111, s_k from 2^-64 to 2^64. Their product is kept a normal number, as a masked
+// score, -infinity, times zero and a score of zero times infinity would be NaN; what this moves are scores below 2^-90, and
+// those whose factor fp32 does not hold. fp16 rows are not lifted and need no bounds. 2048 tokens at 65536 take 1604 us with
+// them and 1588 without; with a branch around them, for rows that some s_k leads out of the range, 1609.
+template <bool BF16> __device__ __forceinline__ float factor_of(float row, float s_k) {
+  const float f = row * s_k;
+  return BF16 ? fminf(fmaxf(f, 0x1p-126f), 0x1.fffffep127f) : f;
+}
+
 struct Kv8Pages {
   KvPages codes;
   float* scale[2];              // of keys and values

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
           float mx = -INFINITY;
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i)
-            mx = fmaxf(mx, fmaf(fmaxf(s[z][i][x], s[z][i][2 + x]), scale[z][x] * k_s[i], v_log[i]));
+            mx = fmaxf(mx, fmaf(fmaxf(s[z][i][x], s[z][i][2 + x]), factor_of<BF16>(scale[z][x], k_s[i]), v_log[i]));
 #pragma unroll
           for (int e = 4; e < 32; e *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
           const float mn = fmaxf(m[z][x], softmax_base<false>(mx, kLift));
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
           l[z][x] *= al[x];
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i) {
-            const float c = scale[z][x] * k_s[i], d = v_log[i] - base;
+            const float c = factor_of<BF16>(scale[z][x], k_s[i]), d = v_log[i] - base;
             s[z][i][x] = ex2(fmaf(s[z][i][x], c, d));
             s[z][i][2 + x] = ex2(fmaf(s[z][i][2 + x], c, d));
             l[z][x] = fmaf(s[z][i][x] + s[z][i][2 + x], v_inv[i], l[z][x]);

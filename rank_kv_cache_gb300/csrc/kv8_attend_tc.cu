@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           y1 = max3(y1, s[b * 16 + 12], s[b * 16 + 13]);
           y0 = max3(y0, s[b * 16 + 14], s[b * 16 + 15]);
           z[b] = sc[b];
-          z[b].x *= c;
+          z[b].x = factor_of<BF16>(c, z[b].x);
           mx[b & 1] = fmaxf(mx[b & 1], fmaf(fmaxf(y0, y1), z[b].x, z[b].y));
         }
         const float top = softmax_base<false>(fmaxf(mx[0], mx[1]), kLift);
