@@ -633,8 +633,10 @@ typedef struct palu_kv_pool {
  *   slots       device [n_tokens] or NULL, written: its page * page_size + offset (-1 behind the last)
  * Page table entries are written in place. A row whose length is negative or not covered by its pages, that holds
  * more pages than the table, or that brings more than max_new tokens or past max_kv_len, is recorded in the error word
- * and left as it is, without new tokens (ended rows: freed all the same, if `held` is right); so is a ring whose number
- * is not within 0 .. n_pages, or would be past it with the pages given back, and a page outside the pool (slot -1).
+ * and left as it is, without new tokens (ended rows: freed all the same, if `held` is right). A ring whose first place is
+ * outside it, or whose number is not within 0 .. n_pages or would be past it with the pages given back, is recorded and
+ * left as it is: no page is taken, and ended rows keep their pages and their length. A page outside the pool is
+ * recorded (slot -1).
  * The outputs overlap no input but as said. batch 0: nothing is done.
  */
 palu_status_t palu_plan_kv_rows(palu_kv_t h, const palu_kv_pool* pool, const int32_t* new_tokens, const int32_t* kv_len,

@@ -83,12 +83,16 @@ def values(codes, scales) -> np.ndarray:
 
 def plan(new, kv_len, held, table, ring, state, page_size, n_tokens):
     """(row_start, kv_len, held, state, positions, slots, table, ring) behind the step."""
-    table, ring = np.array(table), np.array(ring)
-    n_pages = len(ring)
-    free = deque(int(ring[(state[0] + i) % n_pages]) for i in range(state[1]))
+    table, ring, state = np.array(table), np.array(ring), [int(x) for x in state]
+    n_pages, per = len(ring), table.shape[1]
+    back = sum(int(h) for n, h in zip(new, held) if n < 0 and 0 <= h <= per)
+    whole = 0 <= state[0] < n_pages and state[1] >= 0 and state[1] + back <= n_pages   # else the ring is left as it is
+    free = deque(int(ring[(state[0] + i) % n_pages]) for i in range(state[1] if whole else 0))
     given, start, lens, hold, pos, slots, shut = [], [0], [], [], [], [], False
     for b, n in enumerate(new):
         L, have = int(kv_len[b]), int(held[b])
+        if n < 0 and not whole:
+            n = 0
         if n < 0:
             given += [int(p) for p in table[b, :have]]
             L = have = n = 0
@@ -109,7 +113,8 @@ def plan(new, kv_len, held, table, ring, state, page_size, n_tokens):
         ring[(end + i) % n_pages] = p
     rest = n_tokens - len(pos)
     head = (state[0] + state[1] - len(free)) % n_pages
-    return start, lens, hold, [head, len(free) + len(given)], pos + [0] * rest, slots + [-1] * rest, table, ring
+    state = [head, len(free) + len(given)] if whole else state
+    return start, lens, hold, state, pos + [0] * rest, slots + [-1] * rest, table, ring
 
 
 def verify(target, draft, draft_tokens, uniforms):

@@ -9,7 +9,8 @@
 // then the CTAs share the writes, each finding its rows by bisection of those sums. Nothing is read that
 // another CTA writes: pages are read from the ring's front and written behind its end, table entries are read below
 // `held` and written from there on, and what is replaced in place (lengths, held, the ring's state) is written behind a
-// barrier of the cluster.
+// barrier of the cluster. A ring in which the pages given back would reach round to its front is known before the first
+// write and left alone.
 #include <cooperative_groups.h>
 
 #include "kv8.h"
@@ -76,14 +77,34 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
   grid_wait();
   grid_release();
   const int head0 = a.state[0], count0 = a.state[1];
-  const bool ring_ok = head0 >= 0 && head0 < a.n_pages && count0 >= 0 && count0 <= a.n_pages;
-  if (!ring_ok && rank == 0 && tid == 0) record_error(a.err, kCodeDevice, kErrPool, count0, head0);
-  const int head = ring_ok ? head0 : 0, count = ring_ok ? count0 : 0;
-  auto ring_at = [&](int64_t i) {
-    int64_t x = head + i;
-    while (x >= a.n_pages) x -= a.n_pages;   // twice at most where the counts add up
-    return (int)x;
+  auto ring_at = [&](int64_t i) {      // of 0 .. n_pages, in a ring that adds up
+    const int64_t x = head0 + i;
+    return (int)(x < a.n_pages ? x : x - a.n_pages);
   };
+  // The ring adds up: its numbers do, and the pages of all ended rows have a place in it. Else no page is taken or given back.
+  auto adds_up = [&](int64_t back) {
+    const bool ok = head0 >= 0 && head0 < a.n_pages && count0 >= 0 && count0 + back <= a.n_pages;
+    if (!ok && rank == 0 && tid == 0)
+      record_error(a.err, kCodeDevice, kErrPool, (int)min(count0 + back, (int64_t)INT32_MAX), head0);
+    return ok;
+  };
+  auto held_right = [&](int held) { return held >= 0 && held <= a.table_pages; };
+  bool ring_ok = true;                 // one chunk: from its sums
+  if (a.batch > kRows) {
+    int64_t back = 0;
+    for (int b = tid; b < a.batch; b += kThreads) {
+      const int held = a.held[b];
+      if (a.fresh[b] < 0 && held_right(held)) back += held;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) back += __shfl_xor_sync(0xffffffffu, back, o);
+    if (lane == 0) S.warp[warp].back = back;
+    __syncthreads();
+    back = 0;
+    for (int w = 0; w < kWarps; ++w) back += S.warp[w].back;
+    ring_ok = adds_up(back);
+    __syncthreads();
+  }
 
   Sums wanted{0, 0, 0};                // of all rows before the chunk, admitted or not
   int64_t taken = 0, tokens = 0;       // of the admitted ones
@@ -106,10 +127,9 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int r = tid * kPer + e, b = row0 + r;
-      const bool held_ok = held[e] >= 0 && held[e] <= a.table_pages;
-      bool bad = !held_ok;
+      bool bad = !held_right(held[e]);
       if (n[e] < 0) {
-        if (held_ok) w[e].back = held[e];
+        if (!bad) w[e].back = held[e];
       } else {
         const int64_t end = (int64_t)L[e] + n[e];
         bad = bad || L[e] < 0 || n[e] > a.max_new || end > a.max_kv_len || L[e] > (int64_t)held[e] * a.page_size;
@@ -130,11 +150,9 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
     Sums all = of_lane(warps, 31);
     const Sums lower = of_lane(warps, max(warp - 1, 0));
     Sums before = warp ? lower : Sums{0, 0, 0};
-    const bool back_ok = all.back <= a.n_pages;   // else the counts do not add up, and the chunk gives nothing back
-    if (!back_ok) {
-      if (rank == 0 && tid == 0) record_error(a.err, kCodeDevice, kErrPool, a.n_pages, row0);
-      all.back = 0;
-    }
+    if (a.batch <= kRows) ring_ok = adds_up(all.back);
+    if (!ring_ok) all.back = 0;
+    const int count = ring_ok ? count0 : 0;
     before = Sums{before.pages + scan.pages - run.pages, before.tokens + scan.tokens - run.tokens,
                   before.back + scan.back - run.back};
     // Admission falls off once: from the first row that does not fit on. Sums of rows behind it are those of the last one
@@ -167,7 +185,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
       if (r < rows) {
         S.tokens[r] = (int)min(at.tokens, (int64_t)most_tokens);
         S.pages[r] = (int)min(at.pages, (int64_t)most_pages);
-        S.back[r] = back_ok ? (int)at.back : 0;
+        S.back[r] = ring_ok ? (int)at.back : 0;
         S.len[r] = L[e];
         S.held[r] = held[e];
       }
@@ -188,9 +206,9 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
       for (int e = 0; e < kPer; ++e) {
         const int r = tid * kPer + e, b = row0 + r;
         if (r >= rows) continue;
-        const bool ended = n[e] < 0;
+        const bool ended = n[e] < 0 && ring_ok;
         a.row_start[b + 1] = (int)tokens + S.tokens[r + 1];
-        a.kv_len_out[b] = ended ? 0 : L[e] + n[e];
+        a.kv_len_out[b] = ended ? 0 : L[e] + max(n[e], 0);
         a.held_out[b] = ended ? 0 : held[e] + S.pages[r + 1] - S.pages[r];
       }
     }
@@ -271,10 +289,8 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
   }
   // The state is written when every CTA has read it: they have met since.
   if (rank == 0 && tid == 0) {
-    const int64_t left = count - taken + wanted.back;
-    if (count + wanted.back > a.n_pages) record_error(a.err, kCodeDevice, kErrPool, (int)min(left, (int64_t)INT32_MAX), 0);
     a.state_out[0] = ring_ok ? ring_at(taken) : head0;
-    a.state_out[1] = ring_ok ? (int)min(left, (int64_t)a.n_pages) : count0;
+    a.state_out[1] = ring_ok ? (int)(count0 - taken + wanted.back) : count0;
   }
 }
 

@@ -160,3 +160,26 @@ def test_without_positions_or_slots(cuda_device):
         got, layer = run(c, n, positions=positions, slots=slots)
         layer.check_device()
         check(c, got, n)
+
+
+@pytest.mark.parametrize("batch", [6, 512, 700, 2048, 5000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_ring_that_does_not_add_up_is_reported_and_left(cuda_device, batch, in_place):
+    """With requests that end, others that need pages, and others that do not."""
+    from rank_kv_cache_gb300 import palu as P
+    rng = np.random.default_rng(batch)
+    base = make(rng, batch, 16, 60, 9, max(2, batch // 10), 5)
+    pages, back = len(base["ring"]), int(base["held"][base["new"] < 0].sum())
+    base["ring"] = rng.permutation(pages).astype(np.int32)
+    n = int(np.maximum(base["new"], 0).sum()) + 3
+    for head, count, whole in ((0, 10 ** 6, False), (3, -1, False), (-1, 4, False), (pages, 4, False), (2, pages + 1, False),
+                               (pages - 1, pages - back + 1, False), (5, pages - back, True), (0, 2 ** 31 - 1, False)):
+        c = {**base, "state": np.array([head, count], dtype=np.int32)}
+        got, layer = run(c, n, in_place)
+        check(c, got, n)
+        if whole:
+            layer.check_device()
+        else:
+            assert np.array_equal(got[7], base["ring"]) and np.array_equal(got[6], base["table"]) and list(got[3]) == [head, count]
+            with pytest.raises(P.PaluError):
+                layer.check_device()

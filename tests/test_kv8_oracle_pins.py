@@ -100,3 +100,17 @@ def test_uniforms_are_brought_into_range(u, want):
     assert K8.verify(p, p[:2], [0, 1], [u, u, u]) == (want, 1 if u < 0 else 2)
     # a certain draft of less than all is rejected by the largest
     assert K8.verify(p[:2], None, [0], [u, 0.0]) == ((1, 0) if u < 0 else (0, 1))
+
+
+@pytest.mark.parametrize("state,whole", [([9, 4], True), ([9, 7], True), ([9, 8], False), ([10, 4], False), ([-1, 4], False), ([9, -1], False)])
+def test_a_ring_that_does_not_add_up_is_left(state, whole):
+    new, lens, held = [3, -1, 0, 20], [14, 33, 7, 0], [1, 3, 1, 0]
+    table = np.full((4, 3), -1)
+    table[0, 0], table[1], table[2, 0] = 9, [1, 2, 3], 4
+    ring = np.array([6, 7, 8, 0, 0, 0, 0, 0, 0, 5])
+    start, kv, hold, after, pos, slots, tab, out = K8.plan(new, lens, held, table, ring, state, 16, 25)
+    if whole:
+        assert kv == [17, 0, 7, 20] and hold == [2, 0, 1, 2] and after == [2, state[1]]
+    else:                                                                     # no page is taken or given back
+        assert start == [0] * 5 and kv == lens and hold == held and after == state
+        assert np.array_equal(tab, table) and np.array_equal(out, ring)
