@@ -91,7 +91,7 @@ def plan(new, kv_len, held, table, ring, state, page_size, n_tokens):
     given, start, lens, hold, pos, slots, shut = [], [0], [], [], [], [], False
     for b, n in enumerate(new):
         L, have = int(kv_len[b]), int(held[b])
-        if n < 0 and not whole:
+        if n < 0 and not (whole and 0 <= have <= per):
             n = 0
         if n < 0:
             given += [int(p) for p in table[b, :have]]

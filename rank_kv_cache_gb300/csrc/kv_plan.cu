@@ -129,7 +129,8 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
       const int r = tid * kPer + e, b = row0 + r;
       bool bad = !held_right(held[e]);
       if (n[e] < 0) {
-        if (!bad) w[e].back = held[e];
+        if (bad) n[e] = 0;
+        else w[e].back = held[e];
       } else {
         const int64_t end = (int64_t)L[e] + n[e];
         bad = bad || L[e] < 0 || n[e] > a.max_new || end > a.max_kv_len || L[e] > (int64_t)held[e] * a.page_size;

@@ -183,3 +183,19 @@ def test_a_ring_that_does_not_add_up_is_reported_and_left(cuda_device, batch, in
             assert np.array_equal(got[7], base["ring"]) and np.array_equal(got[6], base["table"]) and list(got[3]) == [head, count]
             with pytest.raises(P.PaluError):
                 layer.check_device()
+
+
+@pytest.mark.parametrize("batch", [6, 2100])
+def test_ended_rows_that_hold_more_than_the_table_are_left(cuda_device, batch):
+    from rank_kv_cache_gb300 import palu as P
+    rng = np.random.default_rng(batch)
+    for value in (-1, 10 ** 6, 2 ** 31 - 1):
+        c = make(rng, batch, 16, 100, 10, batch // 2, 4)
+        ended = np.flatnonzero(c["new"] < 0)[::2]
+        c["held"][ended] = value
+        n = int(np.maximum(c["new"], 0).sum())
+        got, layer = run(c, n)
+        check(c, got, n)
+        assert np.array_equal(got[1][ended], c["kv_len"][ended]) and np.all(got[2][ended] == value)
+        with pytest.raises(P.PaluError):
+            layer.check_device()

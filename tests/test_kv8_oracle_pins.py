@@ -114,3 +114,6 @@ def test_a_ring_that_does_not_add_up_is_left(state, whole):
     else:                                                                     # no page is taken or given back
         assert start == [0] * 5 and kv == lens and hold == held and after == state
         assert np.array_equal(tab, table) and np.array_equal(out, ring)
+    # an ended row whose pages cannot be right is left
+    start, kv, hold, after, *_ = K8.plan(new, lens, [1, 4, 1, 0], table, ring, [9, 4], 16, 25)
+    assert kv == [17, 33, 7, 20] and hold == [2, 4, 1, 2] and after == [2, 1]
