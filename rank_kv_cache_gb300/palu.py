@@ -801,7 +801,7 @@ class PagedAttention:
         return t.data_ptr()
 
     def _batch(self, pages, rows):
-        if pages.heads != (self.n_kv_heads, self.head_dim) or not (type(pages) is KVPages8 or pages.dtype == self.dtype):
+        if pages.heads != (self.n_kv_heads, self.head_dim) or not (isinstance(pages, KVPages8) or pages.dtype == self.dtype):
             raise ValueError(f"pages must hold {self.n_kv_heads} heads of {self.head_dim} {self.dtype} values, or of codes")
         if pages.index != self._index or rows.index != self._index:
             raise ValueError(f"pages and rows must be on {self.device}")
@@ -850,7 +850,7 @@ class PagedAttention:
                 raise ValueError("q_out must be contiguous")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        call = _lib.palu_append_kv8 if type(pages) is KVPages8 else _lib.palu_append_kv
+        call = _lib.palu_append_kv8 if isinstance(pages, KVPages8) else _lib.palu_append_kv
         check(call(self.handle, pages._c, rows._c, qp, qs, kp, ks, vp, vs, self._weight("q_weight", q_weight),
                    self._weight("k_weight", k_weight), qo, self._stream(stream)), call.__name__)
         return q_out
@@ -869,7 +869,7 @@ class PagedAttention:
         if lse is not None and (lse.dtype is not self._float or lse.shape != (N, self.n_heads) or
                                 lse.get_device() != self._index or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous [{N}][{self.n_heads}] float32 tensor on {self.device}")
-        call = _lib.palu_attend_kv8 if type(pages) is KVPages8 else _lib.palu_attend_kv
+        call = _lib.palu_attend_kv8 if isinstance(pages, KVPages8) else _lib.palu_attend_kv
         check(call(self.handle, pages._c, rows._c, qp, qs, op, _ptr(lse), self._stream(stream)), call.__name__)
         return out
 

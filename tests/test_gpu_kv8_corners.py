@@ -376,3 +376,19 @@ def test_plan_and_append_on_a_side_stream(cuda_device):
     for a, b in zip(*results):
         assert torch.equal(a, b)
     layer.check_device()
+
+
+def test_pages_of_a_derived_class_are_pages(cuda_device):
+    """A program's own class of 8-bit pages, with what it keeps beside them, goes wherever the pages do."""
+    from rank_kv_cache_gb300 import palu as P
+
+    class Layered(P.KVPages8):
+        layer = 3
+
+    a = Appended(n=4, m=2, d=64, dtype="f16", x_dtype="f16", news=[3, 20], lens=[40, 33], page=16, seed=4)
+    a.pages = Layered(a.pages.k, a.pages.v, a.pages.k_scale, a.pages.v_scale)
+    a.run()
+    a.check()
+    b = Batch8(n=4, m=2, d=64, dtype="f16", news=[3, 20], lens=[40, 33], page=16, seed=5)
+    b.pages = Layered(b.pages.k, b.pages.v, b.pages.k_scale, b.pages.v_scale)
+    b.run_and_check()
