@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Sm<DH, NB>::kCtas)) kv8_attend_f
   using S = Sm<DH, NB>;
   constexpr int kTok = S::kTok, kBlocks = S::kBlocks, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ FewJoin<kWarps, S::kRows> X;
+  __shared__ FewJoin<S::kRows> X;
   __shared__ float scales[kWarps][kStages][2][kBlocks];
   const KvAttendArgs& a = A.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

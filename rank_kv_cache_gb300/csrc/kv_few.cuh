@@ -90,25 +90,25 @@ __device__ __forceinline__ int piece_length(int steps0, int64_t all, int batch, 
 }
 
 constexpr int kFewWarps = 4;             // warps of a CTA
-template <int PARTS = kFewWarps, int ROWS = kKvFewRows> struct FewJoin {
-  float2 ml[PARTS][ROWS];                // of each part's rows: maximum (log2 units) and sum
-  float wgt[PARTS][ROWS];
+template <int ROWS = kKvFewRows> struct FewJoin {
+  float2 ml[kFewWarps][ROWS];            // of each warp's rows: maximum (log2 units) and sum
+  float wgt[kFewWarps][ROWS];
   float2 tot[ROWS];
   int last_cta;
 };
 
-// A piece's end: joins the outputs of its parts (the warps, or pairs of warps, that took its tokens in turn), which stand in
-// shared memory as fp32 [part][row][d] with their maxima and sums in X (the CTA has met since), and writes the unit's
+// A piece's end: joins the outputs of the warps, which took its tokens in turn and whose rows stand in
+// shared memory as fp32 [warp][row][d] with their maxima and sums in X (the CTA has met since), and writes the unit's
 // rows or its partial; the last CTA of a cut unit joins its pieces.
-template <int DH, bool BF16, int PARTS, int ROWS>
-__device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin<PARTS, ROWS>& X, uint8_t* smem, int q0, int rows, int h,
-                                             int np, int piece, int first_slot) {
+template <int DH, bool BF16, int ROWS>
+__device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin<ROWS>& X, uint8_t* smem, int q0, int rows, int h, int np,
+                                             int piece, int first_slot) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (threadIdx.x < ROWS) {
     const int r = threadIdx.x;
     float M = -INFINITY, Lsum = 0.f;
-    for (int w = 0; w < PARTS; ++w) M = fmaxf(M, X.ml[w][r].x);
-    for (int w = 0; w < PARTS; ++w) {
+    for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, X.ml[w][r].x);
+    for (int w = 0; w < kFewWarps; ++w) {
       const float x = M == -INFINITY ? 0.f : ex2(X.ml[w][r].x - M);
       X.wgt[w][r] = x;
       Lsum = fmaf(X.ml[w][r].y, x, Lsum);
@@ -130,7 +130,7 @@ __device__ __forceinline__ void finish_piece(const KvAttendArgs& a, FewJoin<PART
     const int r = x / (DH / 2), cl = x % (DH / 2) * 2;
     float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int y = 0; y < PARTS; ++y) {
+    for (int y = 0; y < kFewWarps; ++y) {
       const float2 u = *reinterpret_cast<const float2*>(of + (y * ROWS + r) * DH + cl);
       v.x = fmaf(u.x, X.wgt[y][r], v.x);
       v.y = fmaf(u.y, X.wgt[y][r], v.y);
