@@ -201,7 +201,8 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
     if (ctas > 1) cluster.sync();
     else __syncthreads();
 
-    const int step = ctas * kThreads, me = rank * kThreads + tid;
+    // numbers of pages and tokens reach 2^31 - 1, and a thread's last step past it: unsigned
+    const unsigned step = ctas * kThreads, me = rank * kThreads + tid;
     if (rank == 0) {
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
@@ -214,21 +215,22 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
       }
     }
     // pages taken: from the ring into the table
-    for (int j = me; j < most_pages; j += step) {
+    for (unsigned j = me; j < (unsigned)most_pages; j += step) {
       const int r = last_at_most(S.pages, rows + 1, j);
       const int page = a.ring[ring_at(taken + j)];
       a.table[(int64_t)(row0 + r) * a.table_pages + S.held[r] + j - S.pages[r]] = page;
       if (page < 0 || page >= a.n_pages) record_error(a.err, kCodeDevice, kErrPage, page, row0 + r);
     }
     // pages given back: from the table into the ring
-    for (int j = me; j < (int)all.back; j += step) {
+    for (unsigned j = me; j < (unsigned)all.back; j += step) {
       const int r = last_at_most(S.back, rows + 1, j);
       a.ring[ring_at(count + wanted.back + j)] = a.table[(int64_t)(row0 + r) * a.table_pages + j - S.back[r]];
     }
     // the tokens' places, four at a time: their pages' loads are under way together
     if (a.positions || a.slots) {
       const bool wide = tokens % 4 == 0 && (uintptr_t)a.positions % 16 == 0 && (uintptr_t)a.slots % 16 == 0;
-      for (int j0 = me * 4; j0 < most_tokens; j0 += step * 4) {
+      for (unsigned j = me * 4; j < (unsigned)most_tokens; j += step * 4) {
+        const int j0 = (int)j;
         int r = last_at_most(S.tokens, rows + 1, j0);
         int pos = S.len[r] + j0 - S.tokens[r], pg = pos / a.page_size, off = pos - pg * a.page_size;
         int place[4], slot[4];
@@ -239,7 +241,7 @@ template <int kPer> __global__ void __launch_bounds__(kThreads) kv_plan_kernel(c
           place[e] = pos;
           slot[e] = off;
           from[e] = more < 0 ? a.table + (int64_t)(row0 + r) * a.table_pages + pg : a.ring + ring_at(taken + S.pages[r] + more);
-          if (j0 + e + 1 >= most_tokens) continue;               // the last one's is looked up again
+          if (most_tokens - j0 <= e + 1) continue;                // the last one's is looked up again
           if (S.tokens[r + 1] > j0 + e + 1) {
             ++pos;
             if (++off == a.page_size) {

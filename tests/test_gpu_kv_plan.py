@@ -199,3 +199,26 @@ def test_ended_rows_that_hold_more_than_the_table_are_left(cuda_device, batch):
         assert np.array_equal(got[1][ended], c["kv_len"][ended]) and np.all(got[2][ended] == value)
         with pytest.raises(P.PaluError):
             layer.check_device()
+
+
+def test_as_many_tokens_as_a_pool_has_slots(cuda_device):
+    """Two rows that fill a pool of nearly 2^31 slots in one step: the places' numbers end next to the largest int."""
+    from rank_kv_cache_gb300 import palu as P
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("wants 20 GB")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ps, pages, L = 64, (1 << 25) - 1, (1 << 30) - 64
+    N = 2 * L + 5
+    layer = P.PagedAttention(n_heads=1, n_kv_heads=1, head_dim=64, dtype="f32", max_batch=2, max_tokens=N)
+    pool = P.KVPool.empty(2, 1 << 24, pages, ps)
+    positions, slots = (torch.full((N + 64,), 99, **i32) for _ in range(2))
+    lens = torch.zeros(2, **i32)
+    rows = P.KVRows(torch.zeros(3, **i32), lens, page_table=pool.page_table, positions=positions[:N], n_tokens=N, max_new=L, max_kv_len=L)
+    layer.plan(pool, torch.full((2,), L, **i32), lens, rows, slots=slots[:N])
+    layer.check_device()
+    assert rows.tensors[0].tolist() == [0, L, 2 * L] and lens.tolist() == [L, L] and pool.held.tolist() == [L // ps] * 2
+    assert pool.state.tolist() == [2 * L // ps, pages - 2 * L // ps]
+    for lo in range(0, N, 1 << 28):                                           # pages come in order: a token's slot is its number
+        t = torch.arange(lo, min(lo + (1 << 28), 2 * L), **i32)
+        assert torch.equal(slots[lo:lo + len(t)], t) and torch.equal(positions[lo:lo + len(t)], torch.where(t < L, t, t - L))
+    assert slots[2 * L:].tolist() == [-1] * 5 + [99] * 64 and positions[2 * L:].tolist() == [0] * 5 + [99] * 64
