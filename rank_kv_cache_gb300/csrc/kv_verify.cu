@@ -151,19 +151,16 @@ template <typename T> struct Source {
         w.d[k][i] = d2.x, w.d[k][i + 1] = d2.y;
         w.e[k][i] = e2.x, w.e[k][i + 1] = e2.y;
       }
-    if (certain >= v0 && certain < v0 + kSeg) {         // a rejected draft's p is below its 1
+    if (unsigned(certain - v0) < unsigned(kSeg) || flags >= kUp) {
+      // a rejected draft's p is below its 1, and its rounding error is 0, as there is no q
+      const float lift = flags < kUp ? 1.f : flags & kUp ? 0x1p100f : 0x1p-32f;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          if (v + k * 32 * kVec + i == certain) w.d[k][i] = 0.f;   // and its rounding error is 0, as there is no q
-    }
-    if (flags & (kUp | kDown)) {
-      const float lift = flags & kUp ? 0x1p100f : 0x1p-32f;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) w.d[k][i] *= lift, w.e[k][i] *= lift;
+        for (int i = 0; i < kVec; ++i) {
+          w.d[k][i] = v + k * 32 * kVec + i == certain ? 0.f : w.d[k][i] * lift;
+          w.e[k][i] *= lift;
+        }
     }
   }
 };
