@@ -571,7 +571,8 @@ typedef struct palu_kv8_pages {
 /*
  * palu_append_kv with pages of 8 bits. The new tokens' keys (normed, rotated) and values of a block and head share a
  * scale: the least power of two, from 2^-64 to 2^64, that brings their largest magnitude to 448 or below. Where older
- * tokens stand in the block (its first slot is none of the row's new ones) the scale is at least theirs; when it grows,
+ * tokens stand in the block (its first slot is none of the row's new ones) the scale is at least theirs (brought to 2^-64
+ * .. 2^64; NaN to 2^-64); when it grows,
  * their codes are restated under it, which by a power of two moves the codes' exponents and loses only what falls
  * below the least subnormal. A block that begins with a new token begins anew. Codes are rounded to nearest (even), so
  * a value of at least 2^-6 scales is off by at most 2^-4 of itself. NaN is stored as NaN; values past 448 * 2^64

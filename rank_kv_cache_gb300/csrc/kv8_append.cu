@@ -15,7 +15,7 @@
 //
 // Bound: HBM; each input is read once and each output written once (four prompts, up to 4096 tokens of 32 + 2 x 8 heads of 128:
 // 61 us, 4.7 TB/s of 6.8; one token of eight requests 4.6 us in a graph, latency). 128 threads of 128 registers, four CTAs an
-// SM: with 256 threads the prompts took 104 us at 160 registers and more (one CTA), 91 at 128 (spilled). A token's angles
+// SM (of fp32 heads of 128 two, for their shared memory; the parts of a chunk are chosen as if four): with 256 threads the prompts took 104 us at 160 registers and more (one CTA), 91 at 128 (spilled). A token's angles
 // are worked out a pair a thread: read by lanes from different places, the parameters' frequencies came one after another.
 #include "kv8.h"
 #include "kv_vec.cuh"

@@ -15,10 +15,11 @@
 //     weights 2^(y_t - M) are what c_v is multiplied by, and the sum takes them divided by s_v: one exponential
 //     serves both, and the fp16 weights are relative to the largest that enters the product, whatever the scales.
 // Bound: the softmax warps' chain from scores to weights to the next scores, of a step for two tiles about 2800 clocks, of which
-// the products need 1024, and what of the converters does not hide behind it: 2048 new tokens at 65536, 8 heads of 128, 4
-// query rows each, 1590 us and 1.36 of 1.92 PFLOP/s; four prompts of 4096, 32 heads, 535 us. Each instruction counts,
+// the products (four of 128 x 128 x 128) need 2048, and what of the converters does not hide behind it: 2048 new tokens at 65536,
+// 8 heads of 128, 4 query rows each, 1604 us and 1.35 of 1.87 PFLOP/s; four prompts of 4096, 32 heads, 535 us. Each instruction counts,
 // also in the instruction caches, which the roles share: scales held over a step, inverse scales from the converters, three-way
-// maxima, packed sums, and one loop each for loads and products took these from 1783 and 578. Not kept: without the maximum
+// maxima, packed sums, and one loop each for loads and products took these from 1783 and 578 (to 1590 and 535; bounds of the
+// scores' factors, see kv8.h, take 14 again). Not kept: without the maximum
 // ahead of the weights (raised afterwards where 16 weights' sum had left fp16) steps were no shorter, and first ones twice as
 // long (806 us for the prompts, against 578); the units' softmax by turns on each scheduler (1831 against 1641, 575 against
 // 554); queries loaded behind the next item's first keys (592 against 578).
@@ -172,7 +173,10 @@ __device__ __forceinline__ uint32_t at_cta(const void* p, uint32_t rank) {   // 
 __device__ __forceinline__ void arrive_peer(uint64_t* bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_cta(bar, rank)) : "memory");
 }
-// for what lies in tensor memory alone, ordered by tcgen05's own fences: with release the softmax warps waited 1000 clocks
+// For what lies in tensor memory alone (scores read, weights written). PTX orders those by tcgen05's own fences, whatever the
+// arrival's semantics: fence::before_thread_sync puts the warp's tcgen05 operations, which it has waited for, ahead of the
+// arrival, and fence::after_thread_sync the products behind the wait. No ordinary memory is handed over here: places of scales
+// are written anew three key tiles or more behind the last that reads them. With release the softmax warps waited 1000 clocks.
 __device__ __forceinline__ void arrive_peer_relaxed(uint64_t* bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_cta(bar, rank)) : "memory");
 }

@@ -4,7 +4,7 @@
 //   pages(b) = max(0, ceil((L_b + n_b) / page) - held_b),  row_start = running sum of the admitted n_b,
 //   admitted: the running sums of pages and tokens, over all rows up to b, stay within what is free.
 //
-// Bound: latency (a step of 64 rows moves a few KB: 4.9 us in a graph; 512 rows, 20 of them ended: 9.3). One launch, one cluster of 1 to 8 CTAs: every CTA loads the rows, one
+// Bound: latency (a step of 64 rows moves a few KB: 4.7 us in a graph; 512 rows, 20 of them ended: 9.3). One launch, one cluster of 1 to 8 CTAs: every CTA loads the rows, one
 // or four a thread, and works out the three running sums (pages taken, tokens, pages given back) for itself in shared memory;
 // then the CTAs share the writes, each finding its rows by bisection of those sums. Nothing is read that
 // another CTA writes: pages are read from the ring's front and written behind its end, table entries are read below

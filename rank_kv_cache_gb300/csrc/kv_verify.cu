@@ -9,8 +9,8 @@
 // 48 bits misplace about vocab 2^-46. fp64 would be bound by that unit: an instruction of a warp takes it 64 cycles.
 //
 // Bound: HBM, one target and one draft row of each batch row. A cluster of 1 to 8 CTAs takes a row; a warp a segment of
-// 512 values, a lane 16 of them in four loads (64 rows of 131072 tokens, fp32: 17 us, 4.0 TB/s of 6.8, of which the drafts'
-// look-ups, the exchange and the second look take 5; four rows of 32000 7.4 us in a graph). The CTAs exchange their sums
+// 512 values, a lane 16 of them in four loads (64 rows of 131072 tokens, fp32: 17 us, 3.9 TB/s of 6.8, of which the drafts'
+// look-ups, the exchange and the second look take 5; four rows of 32000 7.5 us in a graph). The CTAs exchange their sums
 // through distributed shared memory; the one that holds the draw finds the segment by its running sums, and one warp reads
 // that segment again (from L2) for the token.
 #include <cooperative_groups.h>
